@@ -368,6 +368,69 @@ PRISM_API prism_status prism_forward_noalloc(int B, int H, int T, int dk, int dv
                                              const float *eta, const void *conv_w, void *out,
                                              struct CUstream_st *stream, int *device_status);
 
+/*
+ * Token operators -- what stands between token ids and the layer, and between the layer and token
+ * probabilities: the embedding, the norm with the residual's addition, the matrix product in 8-bit
+ * floating point and the log probabilities, with their gradients.  They share a handle that holds
+ * the sizes, the workspace and the status word; rows are tokens in any order (batch and time
+ * flattened).
+ *
+ * Common rules.  D is the model width, V the vocabulary.  Activations, tables, weights and the
+ * cotangents of activations have the handle's io dtype; cotangents of parameters, scales and
+ * per-row statistics are float32; token ids and targets are int64.  Logits have the io dtype unless
+ * PRISM_OPT_OUT_DTYPE selects another (prism_tokens_set_option).  Tensors are row-major and
+ * contiguous except where a row stride (ld, in elements) is an argument, and start on 16-byte
+ * boundaries (per-row vectors of float32 on 4, ids on 8); rows need no alignment of their own.
+ * Sums, softmax statistics and norms are held in float32; every output is rounded once.
+ * A negative id or target means "no token".  One that is >= V is treated the same way and recorded:
+ * prism_tokens_last_device_status() then returns PRISM_ERR_DEVICE.  n = 0 rows is a valid call
+ * (the tensors over rows may then be NULL).
+ * Results do not depend on the order in which the device runs anything: equal inputs give equal bits.
+ */
+typedef struct prism_tokens_s *prism_tokens_t;
+
+/*
+ * prism_tokens_plan -- validate the sizes, bind the handle to the current CUDA device and allocate
+ * its workspace (no later call allocates, so every call can be captured into a graph).  max_rows:
+ * the largest n (or M) of a call, 1 .. 2^24; D in 1 .. 65536; V in 1 .. 2^30.  On error *out_tokens
+ * is NULL.  A handle may be used by one stream at a time.
+ */
+PRISM_API prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism_tokens_t *out_tokens);
+
+/* PRISM_OPT_WAIT_NS, PRISM_OPT_TIMING and PRISM_OPT_OUT_DTYPE (the dtype of logits), as for a plan. */
+PRISM_API prism_status prism_tokens_set_option(prism_tokens_t tokens, prism_option opt, long long value);
+
+/* Free the handle and its workspace.  NULL is accepted. */
+PRISM_API prism_status prism_tokens_destroy(prism_tokens_t tokens);
+
+/* Bytes of device workspace the handle holds (informational). */
+PRISM_API size_t prism_tokens_workspace_bytes(prism_tokens_t tokens);
+
+/* Read and clear the handle's device status word, as prism_plan_last_device_status. */
+PRISM_API prism_status prism_tokens_last_device_status(prism_tokens_t tokens);
+
+/* Per-kernel durations of the handle's last call, as prism_plan_kernel_times. */
+PRISM_API int prism_tokens_kernel_times(prism_tokens_t tokens, prism_kernel_time *out, int max);
+
+/*
+ * prism_embed -- out_i = scale table[ids_i] (zeros where there is no token).
+ *   ids [n] int64   table [V, ld_table] io (the first D columns of each row; ld_table >= D)
+ *   out [n, D] io
+ */
+PRISM_API prism_status prism_embed(prism_tokens_t tokens, int n, const long long *ids, const void *table,
+                                   long long ld_table, float scale, void *out, struct CUstream_st *stream);
+
+/*
+ * prism_embed_backward -- dtable[v] = scale sum_{i : ids_i = v} dout_i for every v in 0 .. V-1 (rows
+ * without a token become zero); with accumulate != 0 the sum is added to dtable and rows without a
+ * token are not touched (a table shared with the head product, gradients over several calls).
+ *   dout [n, D] io   dtable [V, D] float32
+ * The tokens are sorted by id (stably) and each row's terms are added in the order of their
+ * positions within fixed runs, so the result is reproducible bit for bit.
+ */
+PRISM_API prism_status prism_embed_backward(prism_tokens_t tokens, int n, const long long *ids, const void *dout,
+                                            float scale, int accumulate, float *dtable, struct CUstream_st *stream);
+
 /* Version of this library, "major.minor.patch". */
 PRISM_API const char *prism_version(void);
 

@@ -36,7 +36,9 @@ EXPORTED = ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forwa
             "prism_plan_destroy", "prism_workspace_bytes", "prism_plan_last_device_status",
             "prism_status_string", "prism_last_error_message", "prism_version", "prism_plan_kernel_times",
             "prism_forward_noalloc", "prism_forward_state", "prism_decode_step", "prism_forward_nonlinear",
-            "prism_project", "prism_backward", "prism_backward_nonlinear")
+            "prism_project", "prism_backward", "prism_backward_nonlinear",
+            "prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy", "prism_tokens_workspace_bytes",
+            "prism_tokens_last_device_status", "prism_tokens_kernel_times", "prism_embed", "prism_embed_backward")
 
 
 class prism_kernel_time(ctypes.Structure):
@@ -91,6 +93,20 @@ def lib():
             L.prism_backward.argtypes = fwd[:11] + [vp, f, f, f] + [f] * 11 + [vp]
             L.prism_backward_nonlinear.argtypes = L.prism_backward.argtypes
             L.prism_plan_kernel_times.restype = ctypes.c_int
+            c_f, ll = ctypes.c_float, ctypes.c_longlong
+            L.prism_tokens_plan.argtypes = [i, i, i, i, ctypes.POINTER(vp)]
+            L.prism_tokens_set_option.argtypes = [vp, i, ll]
+            L.prism_tokens_destroy.argtypes = [vp]
+            L.prism_tokens_workspace_bytes.argtypes = [vp]
+            L.prism_tokens_workspace_bytes.restype = ctypes.c_size_t
+            L.prism_tokens_last_device_status.argtypes = [vp]
+            L.prism_tokens_kernel_times.argtypes = [vp, ctypes.POINTER(prism_kernel_time), i]
+            L.prism_tokens_kernel_times.restype = ctypes.c_int
+            L.prism_embed.argtypes = [vp, i, vp, vp, ll, c_f, vp, vp]
+            L.prism_embed_backward.argtypes = [vp, i, vp, vp, c_f, i, vp, vp]
+            for name in ("prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy",
+                         "prism_tokens_last_device_status", "prism_embed", "prism_embed_backward"):
+                getattr(L, name).restype = ctypes.c_int
             for name in ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forward_host",
                          "prism_plan_destroy", "prism_plan_last_device_status", "prism_forward_state",
                          "prism_decode_step", "prism_forward_nonlinear", "prism_project", "prism_backward",
@@ -232,6 +248,46 @@ def prism_forward_noalloc(B, H, T, dk, dv, L, q, k, v, beta, alpha, u, gamma, et
                                        _addr(alpha), _addr(u), _addr(gamma), _addr(eta), _addr(conv_w), _addr(out),
                                        _stream(stream), ctypes.byref(status) if wait else None))
     return status.value
+
+
+def prism_tokens_plan(max_rows, D, V, io=PRISM_BF16) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().prism_tokens_plan(max_rows, D, V, int(io), ctypes.byref(h)))
+    return h.value
+
+
+def prism_tokens_set_option(tokens, opt, value):
+    return _check(lib().prism_tokens_set_option(tokens, int(opt), int(value)))
+
+
+def prism_tokens_destroy(tokens):
+    return _check(lib().prism_tokens_destroy(tokens))
+
+
+def prism_tokens_workspace_bytes(tokens) -> int:
+    return int(lib().prism_tokens_workspace_bytes(tokens))
+
+
+def prism_tokens_last_device_status(tokens):
+    return _check(lib().prism_tokens_last_device_status(tokens))
+
+
+def prism_tokens_kernel_times(tokens, max_kernels=16):
+    """[(name, ms), ...] of the handle's last call (ms = -1 when timing was off)."""
+    buf = (prism_kernel_time * max_kernels)()
+    n = lib().prism_tokens_kernel_times(tokens, buf, max_kernels)
+    if n < 0:
+        raise PrismError(PRISM_ERR_INVALID_ARG, prism_last_error_message())
+    return [(buf[i].name.decode(), float(buf[i].ms)) for i in range(min(n, max_kernels))]
+
+
+def prism_embed(tokens, n, ids, table, ld_table, scale, out, stream=None):
+    return _check(lib().prism_embed(tokens, n, _addr(ids), _addr(table), ld_table, scale, _addr(out), _stream(stream)))
+
+
+def prism_embed_backward(tokens, n, ids, dout, scale, accumulate, dtable, stream=None):
+    return _check(lib().prism_embed_backward(tokens, n, _addr(ids), _addr(dout), scale, int(accumulate), _addr(dtable),
+                                             _stream(stream)))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -411,6 +467,101 @@ class Plan:
     def close(self):
         if self.handle:
             prism_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *a):
+        self.close()
+
+
+# ------------------------------------------------------------------------------------------------
+class Tokens:
+    """Owns a ``prism_tokens_t``: the operators between token ids and the layer, and between the layer
+    and token probabilities (see the token operators of include/prism.h).
+
+    ``max_rows`` is the largest number of rows of a call, ``D`` the model width, ``V`` the vocabulary,
+    ``io`` the dtype of activations and tables ("bf16" or "f32"), ``logits`` that of logits (``io``
+    unless given).  Rows are tokens; leading axes of the arguments are flattened.  Outputs are
+    allocated unless given.  ``stream`` is torch's current stream unless given.
+    """
+
+    def __init__(self, max_rows, D, V, io="bf16", logits=None):
+        import torch
+        self.max_rows, self.D, self.V, self.io = max_rows, D, V, io
+        self.logits = logits or io
+        dtypes = {"bf16": torch.bfloat16, "f32": torch.float32}
+        self._io, self._logits = dtypes[self.io], dtypes[self.logits]
+        self._current_stream = torch._C._cuda_getCurrentRawStream
+        self.handle = prism_tokens_plan(max_rows, D, V, PRISM_BF16 if io == "bf16" else PRISM_F32)
+        self.device = torch.cuda.current_device()
+        if self.logits != io:
+            self.set_option(PRISM_OPT_OUT_DTYPE, PRISM_BF16 if self.logits == "bf16" else PRISM_F32)
+
+    def set_option(self, opt, value):
+        prism_tokens_set_option(self.handle, opt, value)
+
+    def workspace_bytes(self):
+        return prism_tokens_workspace_bytes(self.handle)
+
+    def kernel_times(self):
+        return prism_tokens_kernel_times(self.handle)
+
+    def last_device_status(self):
+        return prism_tokens_last_device_status(self.handle)
+
+    def _on(self, stream):
+        return self._current_stream(self.device) if stream is None else _stream(stream)
+
+    @staticmethod
+    def _need(name, t, dtype, numel=None, width=None):
+        """Refuses a tensor that the library would misread: its device, type, layout and size."""
+        if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+        if (numel is not None and t.numel() != numel) or (width is not None and t.shape[-1] != width):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not fit the other arguments")
+
+    def embed(self, ids, table, scale=1.0, out=None, stream=None):
+        """scale * table[ids] (see prism_embed): ids [...] int64, table [V, D] whose rows may be
+        padded (a stride); returns [..., D].  Negative ids give rows of zeros."""
+        import torch
+        n = ids.numel()
+        self._need("ids", ids, torch.int64)
+        if table.dtype is not self._io or not table.is_cuda or table.shape != (self.V, self.D) or table.stride(1) != 1:
+            raise ValueError(f"table must be a CUDA tensor [{self.V}, {self.D}] of {self._io} with contiguous rows")
+        if out is None:
+            out = torch.empty(*ids.shape, self.D, dtype=self._io, device=ids.device)
+        else:
+            self._need("out", out, self._io, n * self.D)
+        prism_embed(self.handle, n, ids, table, table.stride(0), scale, out, self._on(stream))
+        return out
+
+    def embed_backward(self, ids, dout, scale=1.0, dtable=None, accumulate=False, stream=None):
+        """The table's gradient [V, D] float32 (see prism_embed_backward); with ``accumulate`` it is
+        added to ``dtable``."""
+        import torch
+        n = ids.numel()
+        self._need("ids", ids, torch.int64)
+        self._need("dout", dout, self._io, n * self.D, self.D)
+        if dtable is None:
+            if accumulate:
+                raise ValueError("accumulate needs a dtable to add to")
+            dtable = torch.empty(self.V, self.D, dtype=torch.float32, device=ids.device)
+        else:
+            self._need("dtable", dtable, torch.float32, self.V * self.D)
+        prism_embed_backward(self.handle, n, ids, dout, scale, accumulate, dtable, self._on(stream))
+        return dtable
+
+    def close(self):
+        if self.handle:
+            prism_tokens_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

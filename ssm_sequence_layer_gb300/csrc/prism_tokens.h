@@ -1,0 +1,58 @@
+// Internal declarations of the token operators (embedding, norm, 8-bit product, log probabilities).
+#pragma once
+
+#include "prism_internal.h"
+
+namespace prism {
+
+// A launch context: where to record the status and the kernels' times.
+struct TokenLaunch {
+    int sm_count;
+    int *d_status;
+    long long wait_ns;
+    KernelTimer *timer;
+};
+
+// ---- embedding (prism_embed.cu) ------------------------------------------------------------------
+struct EmbedArgs {
+    const long long *ids;
+    const void *table;
+    long long ld_table;
+    float scale;
+    void *out;
+    int n, D, V;
+};
+cudaError_t embed_forward(prism_dtype io, const EmbedArgs &a, const TokenLaunch &l);
+
+// Workspace of the gradient: the tokens sorted by id and the sums of runs that cross a tile's edge.
+struct EmbedWorkspace {
+    int *key[2], *pos[2];  // [max_rows] ids (V = no token) and positions, ping-pong of the sort's passes
+    int *hist;             // [kSortPassesMax][kSortBlocks][kSortBins] digit counts
+    float *part;           // [tiles][2][Dp] sums of a tile's first and last run where it crosses the edge
+};
+size_t embed_workspace_bytes(int max_rows, int D);
+void embed_carve(int max_rows, int D, void *base, EmbedWorkspace *w);
+struct EmbedBackwardArgs {
+    const long long *ids;
+    const void *dout;
+    float scale;
+    int accumulate;
+    float *dtable;
+    int n, D, V;
+};
+cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const EmbedWorkspace &w, const TokenLaunch &l);
+
+}  // namespace prism
+
+struct prism_tokens_s {
+    int max_rows, D, V;
+    prism_dtype io, logits;
+    int device, sm_count;
+    long long opt_wait_ns, opt_timing;
+    prism::KernelTimer timer;
+    bool have_events;  // the timer's events exist (created when timing is first switched on)
+    int *d_status;
+    void *ws;  // device memory (owned)
+    size_t ws_bytes;
+    prism::EmbedWorkspace embed;
+};
