@@ -431,6 +431,35 @@ PRISM_API prism_status prism_embed(prism_tokens_t tokens, int n, const long long
 PRISM_API prism_status prism_embed_backward(prism_tokens_t tokens, int n, const long long *ids, const void *dout,
                                             float scale, int accumulate, float *dtable, struct CUstream_st *stream);
 
+/*
+ * prism_norm -- the residual's addition and a root-mean-square norm:
+ *   r = x + residual (r = x when residual is NULL),   y_j = r_j w_j / sqrt(mean_j r_j^2 + eps)
+ *   x, residual [n, D] io   weight [D] io
+ * Outputs, each of which may be NULL (one of y and y8 must not be):
+ *   sum     [n, D] io        r, rounded (the norm is taken of the unrounded sum); may be residual or x
+ *   y       [n, D] io        may be x, or residual when sum is NULL
+ *   y8      [n, D] e4m3      with y_scale [n, ceil(D / 128)] float32: per row and block of 128
+ *                            columns, y_scale = max(max |y| / 448, 2^-126) and y8 = y / y_scale
+ *                            rounded to nearest; y8 and y_scale come together
+ * NaN in a row reaches the whole row of y; an infinite y makes its block's scale infinite.
+ * eps must be finite and >= 0.  A row of zeros with eps = 0 gives NaN, as the formula does.
+ */
+PRISM_API prism_status prism_norm(prism_tokens_t tokens, int n, const void *x, const void *residual,
+                                  const void *weight, float eps, void *sum, void *y, void *y8, float *y_scale,
+                                  struct CUstream_st *stream);
+
+/*
+ * prism_norm_backward -- the cotangents of prism_norm's inputs.  With r = sum (the forward's output,
+ * or x where there was no residual), q = 1 / sqrt(mean r^2 + eps), rh = r q:
+ *   dx      = q (w dy - rh mean_j(w_j dy_j rh_j)) + dsum      dweight = sum over rows of dy rh
+ * dx is the cotangent of x and of residual alike; dsum [n, D] io (may be NULL) is the cotangent that
+ * reaches the sum by itself (the residual stream).  dy, dx [n, D] io (dx may be dy or dsum);
+ * dweight [D] float32, overwritten.
+ */
+PRISM_API prism_status prism_norm_backward(prism_tokens_t tokens, int n, const void *sum, const void *weight,
+                                           float eps, const void *dy, const void *dsum, void *dx, float *dweight,
+                                           struct CUstream_st *stream);
+
 /* Version of this library, "major.minor.patch". */
 PRISM_API const char *prism_version(void);
 

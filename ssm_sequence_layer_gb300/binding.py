@@ -38,7 +38,8 @@ EXPORTED = ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forwa
             "prism_forward_noalloc", "prism_forward_state", "prism_decode_step", "prism_forward_nonlinear",
             "prism_project", "prism_backward", "prism_backward_nonlinear",
             "prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy", "prism_tokens_workspace_bytes",
-            "prism_tokens_last_device_status", "prism_tokens_kernel_times", "prism_embed", "prism_embed_backward")
+            "prism_tokens_last_device_status", "prism_tokens_kernel_times", "prism_embed", "prism_embed_backward",
+            "prism_norm", "prism_norm_backward")
 
 
 class prism_kernel_time(ctypes.Structure):
@@ -104,8 +105,11 @@ def lib():
             L.prism_tokens_kernel_times.restype = ctypes.c_int
             L.prism_embed.argtypes = [vp, i, vp, vp, ll, c_f, vp, vp]
             L.prism_embed_backward.argtypes = [vp, i, vp, vp, c_f, i, vp, vp]
+            L.prism_norm.argtypes = [vp, i, vp, vp, vp, c_f, vp, vp, vp, vp, vp]
+            L.prism_norm_backward.argtypes = [vp, i, vp, vp, c_f, vp, vp, vp, vp, vp]
             for name in ("prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy",
-                         "prism_tokens_last_device_status", "prism_embed", "prism_embed_backward"):
+                         "prism_tokens_last_device_status", "prism_embed", "prism_embed_backward", "prism_norm",
+                         "prism_norm_backward"):
                 getattr(L, name).restype = ctypes.c_int
             for name in ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forward_host",
                          "prism_plan_destroy", "prism_plan_last_device_status", "prism_forward_state",
@@ -288,6 +292,16 @@ def prism_embed(tokens, n, ids, table, ld_table, scale, out, stream=None):
 def prism_embed_backward(tokens, n, ids, dout, scale, accumulate, dtable, stream=None):
     return _check(lib().prism_embed_backward(tokens, n, _addr(ids), _addr(dout), scale, int(accumulate), _addr(dtable),
                                              _stream(stream)))
+
+
+def prism_norm(tokens, n, x, residual, weight, eps, sum, y, y8, y_scale, stream=None):
+    return _check(lib().prism_norm(tokens, n, _addr(x), _addr(residual), _addr(weight), eps, _addr(sum), _addr(y), _addr(y8),
+                                   _addr(y_scale), _stream(stream)))
+
+
+def prism_norm_backward(tokens, n, sum, weight, eps, dy, dsum, dx, dweight, stream=None):
+    return _check(lib().prism_norm_backward(tokens, n, _addr(sum), _addr(weight), eps, _addr(dy), _addr(dsum), _addr(dx),
+                                            _addr(dweight), _stream(stream)))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -558,6 +572,63 @@ class Tokens:
             self._need("dtable", dtable, torch.float32, self.V * self.D)
         prism_embed_backward(self.handle, n, ids, dout, scale, accumulate, dtable, self._on(stream))
         return dtable
+
+    def norm(self, x, weight, residual=None, eps=1e-6, want=("y",), out=None, stream=None):
+        """The norm of x + residual (see prism_norm): x, residual [..., D], weight [D].  Returns a dict
+        of the outputs that ``want`` names -- "sum" and "y" [..., D], "y8" (float8_e4m3fn) with its
+        "y_scale" [..., ceil(D/128)] -- or fills and returns ``out``, a dict of them."""
+        import torch
+        D = self.D
+        n = x.numel() // D
+        need = self._need
+        need("x", x, self._io, n * D, D)
+        need("weight", weight, self._io, D)
+        if residual is not None:
+            need("residual", residual, self._io, n * D)
+        if out is None:
+            out, lead = {}, x.shape[:-1]
+            for key in want:
+                if key in ("sum", "y"):
+                    out[key] = torch.empty_like(x)
+                elif key == "y8":
+                    out["y8"] = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+                    out["y_scale"] = torch.empty(*lead, -(-D // 128), dtype=torch.float32, device=x.device)
+                else:
+                    raise ValueError(f"prism_norm has no output {key!r}")
+        else:
+            for key, t in out.items():
+                if key in ("sum", "y"):
+                    need(key, t, self._io, n * D)
+                elif key == "y8":
+                    need(key, t, torch.float8_e4m3fn, n * D)
+                elif key == "y_scale":
+                    need(key, t, torch.float32, n * -(-D // 128))
+                else:
+                    raise ValueError(f"prism_norm has no output {key!r}")
+        get = out.get
+        prism_norm(self.handle, n, x, residual, weight, eps, get("sum"), get("y"), get("y8"), get("y_scale"), self._on(stream))
+        return out
+
+    def norm_backward(self, sum, weight, dy, dsum=None, eps=1e-6, out=None, stream=None):
+        """The norm's gradient (see prism_norm_backward): ``sum`` is the forward's "sum" (x itself
+        where there was no residual), dsum the cotangent that reaches it besides the norm's.
+        Returns {"dx" [..., D], "dweight" [D] float32}."""
+        import torch
+        D = self.D
+        n = sum.numel() // D
+        need = self._need
+        need("sum", sum, self._io, n * D, D)
+        need("weight", weight, self._io, D)
+        need("dy", dy, self._io, n * D)
+        if dsum is not None:
+            need("dsum", dsum, self._io, n * D)
+        if out is None:
+            out = {"dx": torch.empty_like(sum), "dweight": torch.empty(D, dtype=torch.float32, device=sum.device)}
+        else:
+            need("dx", out["dx"], self._io, n * D)
+            need("dweight", out["dweight"], torch.float32, D)
+        prism_norm_backward(self.handle, n, sum, weight, eps, dy, dsum, out["dx"], out["dweight"], self._on(stream))
+        return out
 
     def close(self):
         if self.handle:

@@ -101,7 +101,8 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
     t->device = device;
     t->sm_count = sms;
     // one allocation: the status word, then the operators' workspaces
-    t->ws_bytes = 256 + prism::embed_workspace_bytes(max_rows, D);
+    const size_t embed_bytes = prism::embed_workspace_bytes(max_rows, D);
+    t->ws_bytes = 256 + embed_bytes + prism::norm_workspace_bytes(max_rows, D);
     if ((e = cudaMalloc(&t->ws, t->ws_bytes)) != cudaSuccess) {
         delete t;
         return cuda_fail(e, "workspace allocation");
@@ -113,6 +114,7 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
         return cuda_fail(e, "status word init");
     }
     prism::embed_carve(max_rows, D, (char *)t->ws + 256, &t->embed);
+    prism::norm_carve(max_rows, D, (char *)t->ws + 256 + embed_bytes, &t->norm);
     *out_tokens = t;
     return PRISM_OK;
 }
@@ -212,6 +214,36 @@ prism_status prism_embed_backward(prism_tokens_t t, int n, const long long *ids,
         return st;
     const prism::TokenLaunch l = begin(t, stream);
     return launched(prism::embed_backward(t->io, {ids, dout, scale, accumulate != 0, dtable, n, t->D, t->V}, t->embed, l));
+}
+
+prism_status prism_norm(prism_tokens_t t, int n, const void *x, const void *residual, const void *weight, float eps, void *sum,
+                        void *y, void *y8, float *y_scale, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, n, "n");
+    if (st != PRISM_OK) return st;
+    if ((st = check_pointers<7>({{"x", x, 16, n > 0}, {"residual", residual, 16, false}, {"weight", weight, 16, true},
+                                 {"sum", sum, 16, false}, {"y", y, 16, false}, {"y8", y8, 16, false},
+                                 {"y_scale", y_scale, 4, false}})) != PRISM_OK)
+        return st;
+    if (n > 0 && !y && !y8) return fail(PRISM_ERR_INVALID_ARG, "y and y8 must not both be NULL");
+    if (!y8 != !y_scale) return fail(PRISM_ERR_INVALID_ARG, "y8 and y_scale come together");
+    if (!std::isfinite(eps) || eps < 0.f) return fail(PRISM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const prism::TokenLaunch l = begin(t, stream);
+    if (n == 0) return PRISM_OK;
+    return launched(prism::norm_forward(t->io, {x, residual, weight, eps, sum, y, y8, y_scale, n, t->D}, l));
+}
+
+prism_status prism_norm_backward(prism_tokens_t t, int n, const void *sum, const void *weight, float eps, const void *dy,
+                                 const void *dsum, void *dx, float *dweight, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, n, "n");
+    if (st != PRISM_OK) return st;
+    if ((st = check_pointers<6>({{"sum", sum, 16, n > 0}, {"weight", weight, 16, true}, {"dy", dy, 16, n > 0},
+                                 {"dsum", dsum, 16, false}, {"dx", dx, 16, n > 0}, {"dweight", dweight, 4, true}})) != PRISM_OK)
+        return st;
+    if (!std::isfinite(eps) || eps < 0.f) return fail(PRISM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const prism::TokenLaunch l = begin(t, stream);
+    return launched(prism::norm_backward(t->io, {sum, weight, dy, dsum, eps, dx, dweight, n, t->D}, t->norm, l));
 }
 
 }  // extern "C"

@@ -42,6 +42,31 @@ struct EmbedBackwardArgs {
 };
 cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const EmbedWorkspace &w, const TokenLaunch &l);
 
+// ---- norm (prism_norm.cu) -------------------------------------------------------------------------
+struct NormArgs {
+    const void *x, *residual, *weight;
+    float eps;
+    void *sum, *y, *y8;
+    float *y_scale;
+    int n, D;
+};
+cudaError_t norm_forward(prism_dtype io, const NormArgs &a, const TokenLaunch &l);
+
+struct NormWorkspace {
+    float2 *stats;  // [max_rows] 1 / rms and mean(w dy rh) of each row
+    float *part;    // [slabs][D] parts of the weight's gradient
+};
+size_t norm_workspace_bytes(int max_rows, int D);
+void norm_carve(int max_rows, int D, void *base, NormWorkspace *w);
+struct NormBackwardArgs {
+    const void *sum, *weight, *dy, *dsum;
+    float eps;
+    void *dx;
+    float *dweight;
+    int n, D;
+};
+cudaError_t norm_backward(prism_dtype io, const NormBackwardArgs &a, const NormWorkspace &w, const TokenLaunch &l);
+
 }  // namespace prism
 
 struct prism_tokens_s {
@@ -55,4 +80,5 @@ struct prism_tokens_s {
     void *ws;  // device memory (owned)
     size_t ws_bytes;
     prism::EmbedWorkspace embed;
+    prism::NormWorkspace norm;
 };

@@ -39,3 +39,5 @@ def test_null_handle(lib):
     assert lib.prism_tokens_kernel_times(None, None, 0) == -1
     assert lib.prism_embed(None, 1, 16, 16, 64, 1.0, 16, None) == B.PRISM_ERR_INVALID_ARG
     assert lib.prism_embed_backward(None, 1, 16, 16, 1.0, 0, 16, None) == B.PRISM_ERR_INVALID_ARG
+    assert lib.prism_norm(None, 1, 16, None, 16, 1e-6, None, 16, None, None, None) == B.PRISM_ERR_INVALID_ARG
+    assert lib.prism_norm_backward(None, 1, 16, 16, 1e-6, 16, None, 16, 16, None) == B.PRISM_ERR_INVALID_ARG
