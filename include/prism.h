@@ -460,6 +460,39 @@ PRISM_API prism_status prism_norm_backward(prism_tokens_t tokens, int n, const v
                                            float eps, const void *dy, const void *dsum, void *dx, float *dweight,
                                            struct CUstream_st *stream);
 
+/*
+ * prism_token_logprobs -- per row of logits [n, V] (row stride ld >= V), with z = inv_temperature
+ * logits and p = softmax(z):
+ *   lse      [n] float32   log sum_j exp z_j
+ *   logprob  [n] float32   z_t - lse at the target t (0 where there is no target); needs targets
+ *   entropy  [n] float32   -sum_j p_j log p_j
+ *   top_ids  [n, k] int64, top_logprob [n, k] float32: the k most likely tokens, by falling logit and
+ *            at equal logits by rising id; top_logprob = z - lse
+ * targets [n] int64 may be NULL; each output may be NULL; k in 0 .. 32 (k = 0: no top).
+ * Masked tokens: a logit of -inf or of the lowest bfloat16 value and below (either is how masks are
+ * written), and a product that overflows to -inf, counts as z = -inf: its probability is zero, it adds
+ * nothing to the entropy and is never among the top (missing places hold id -1 and -inf).  Where a whole row is masked, lse is -inf,
+ * entropy 0 and logprob -inf.  NaN or +inf in a row gives NaN lse, logprob and entropy, as the
+ * formulas do; NaN logits come first among the top.  inv_temperature must be finite and > 0.
+ */
+PRISM_API prism_status prism_token_logprobs(prism_tokens_t tokens, int n, const void *logits, long long ld,
+                                            const long long *targets, float inv_temperature, int k, float *lse,
+                                            float *logprob, float *entropy, long long *top_ids, float *top_logprob,
+                                            struct CUstream_st *stream);
+
+/*
+ * prism_token_logprobs_backward -- the cotangent of the logits, given lse and entropy from the forward:
+ *   dlogits_j = inv_temperature (dlogprob (1_{j=t} - p_j) - dentropy p_j (log p_j + entropy))
+ *   dlogprob, dentropy [n] float32 (each may be NULL, not both; dlogprob needs targets, dentropy needs
+ *   entropy); dlogits [n, V] with row stride ld_d >= V, dtype of the logits, may be the logits
+ *   themselves when ld_d = ld.  Masked tokens and wholly masked rows get zero.
+ */
+PRISM_API prism_status prism_token_logprobs_backward(prism_tokens_t tokens, int n, const void *logits, long long ld,
+                                                     const long long *targets, float inv_temperature,
+                                                     const float *lse, const float *entropy, const float *dlogprob,
+                                                     const float *dentropy, void *dlogits, long long ld_d,
+                                                     struct CUstream_st *stream);
+
 /* Version of this library, "major.minor.patch". */
 PRISM_API const char *prism_version(void);
 

@@ -52,3 +52,60 @@ def norm_backward(r, weight, eps, dy, dsum=None):
     rh = r * q
     dx = q * (w * dy - rh * np.mean(w * dy * rh, axis=1, keepdims=True))
     return dx + (0 if dsum is None else np.asarray(dsum, dtype=np.float64)), np.sum(dy * rh, axis=0)
+
+
+LOWEST = -3.38953139e38  # bfloat16's: a logit at or below it is masked
+
+
+def z_of(logits, c):
+    return np.where(logits <= LOWEST * (1 - 1e-9), -np.inf, c * logits.astype(np.float64))
+
+
+def token_logprobs(logits, targets, c, k):
+    """lse, logprob, entropy, top ids and top log probabilities, row by row."""
+    z = z_of(logits, c)
+    n, V = z.shape
+    out = {"lse": np.zeros(n), "logprob": np.zeros(n), "entropy": np.zeros(n), "top_ids": np.full((n, k), -1, dtype=np.int64),
+           "top_logprob": np.full((n, k), -np.inf)}
+    for i in range(n):
+        row = z[i]
+        live = np.nonzero(row != -np.inf)[0]
+        with np.errstate(invalid="ignore"):
+            m, logs = 0.0, -np.inf
+            if live.size == 0:
+                h = 0.0
+            elif np.isnan(row).any() or np.isposinf(row).any():
+                logs, h = np.nan, np.nan
+            else:
+                m = row[live].max()
+                e = np.exp(row[live] - m)
+                logs = np.log(e.sum())
+                h = logs - np.sum(e * (row[live] - m)) / e.sum()
+            out["lse"][i], out["entropy"][i] = m + logs, h
+            if targets is not None and 0 <= targets[i] < V:
+                out["logprob"][i] = -np.inf if live.size == 0 else (row[targets[i]] - m) - logs
+            nan = np.isnan(row[live])
+            order = live[np.lexsort((live, np.where(nan, 0.0, -row[live]), ~nan))][:k]
+            out["top_ids"][i, :order.size] = order
+            out["top_logprob"][i, :order.size] = (row[order] - m) - logs
+    return out
+
+
+def token_logprobs_backward(logits, targets, c, lse, entropy, dlogprob, dentropy):
+    z = z_of(logits, c)
+    g = np.zeros_like(z)
+    for i in range(z.shape[0]):
+        if lse[i] == -np.inf:
+            continue
+        live = z[i] != -np.inf
+        lp = z[i][live] - lse[i]
+        p = np.exp(lp)
+        t = targets[i] if targets is not None and dlogprob is not None and 0 <= targets[i] < z.shape[1] else -1
+        d = dlogprob[i] if t >= 0 else 0.0
+        row = -d * p
+        if dentropy is not None:
+            row = row - dentropy[i] * p * (lp + entropy[i])
+        g[i][live] = row
+        if t >= 0 and live[t]:
+            g[i, t] += d
+    return c * g

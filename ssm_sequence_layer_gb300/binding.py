@@ -39,7 +39,7 @@ EXPORTED = ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forwa
             "prism_project", "prism_backward", "prism_backward_nonlinear",
             "prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy", "prism_tokens_workspace_bytes",
             "prism_tokens_last_device_status", "prism_tokens_kernel_times", "prism_embed", "prism_embed_backward",
-            "prism_norm", "prism_norm_backward")
+            "prism_norm", "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward")
 
 
 class prism_kernel_time(ctypes.Structure):
@@ -107,9 +107,11 @@ def lib():
             L.prism_embed_backward.argtypes = [vp, i, vp, vp, c_f, i, vp, vp]
             L.prism_norm.argtypes = [vp, i, vp, vp, vp, c_f, vp, vp, vp, vp, vp]
             L.prism_norm_backward.argtypes = [vp, i, vp, vp, c_f, vp, vp, vp, vp, vp]
+            L.prism_token_logprobs.argtypes = [vp, i, vp, ll, vp, c_f, i, vp, vp, vp, vp, vp, vp]
+            L.prism_token_logprobs_backward.argtypes = [vp, i, vp, ll, vp, c_f, vp, vp, vp, vp, vp, ll, vp]
             for name in ("prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy",
                          "prism_tokens_last_device_status", "prism_embed", "prism_embed_backward", "prism_norm",
-                         "prism_norm_backward"):
+                         "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward"):
                 getattr(L, name).restype = ctypes.c_int
             for name in ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forward_host",
                          "prism_plan_destroy", "prism_plan_last_device_status", "prism_forward_state",
@@ -302,6 +304,20 @@ def prism_norm(tokens, n, x, residual, weight, eps, sum, y, y8, y_scale, stream=
 def prism_norm_backward(tokens, n, sum, weight, eps, dy, dsum, dx, dweight, stream=None):
     return _check(lib().prism_norm_backward(tokens, n, _addr(sum), _addr(weight), eps, _addr(dy), _addr(dsum), _addr(dx),
                                             _addr(dweight), _stream(stream)))
+
+
+def prism_token_logprobs(tokens, n, logits, ld, targets, inv_temperature, k, lse, logprob, entropy, top_ids, top_logprob,
+                         stream=None):
+    return _check(lib().prism_token_logprobs(tokens, n, _addr(logits), ld, _addr(targets), inv_temperature, k, _addr(lse),
+                                             _addr(logprob), _addr(entropy), _addr(top_ids), _addr(top_logprob),
+                                             _stream(stream)))
+
+
+def prism_token_logprobs_backward(tokens, n, logits, ld, targets, inv_temperature, lse, entropy, dlogprob, dentropy, dlogits,
+                                  ld_d, stream=None):
+    return _check(lib().prism_token_logprobs_backward(tokens, n, _addr(logits), ld, _addr(targets), inv_temperature, _addr(lse),
+                                                      _addr(entropy), _addr(dlogprob), _addr(dentropy), _addr(dlogits), ld_d,
+                                                      _stream(stream)))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -629,6 +645,71 @@ class Tokens:
             need("dweight", out["dweight"], torch.float32, D)
         prism_norm_backward(self.handle, n, sum, weight, eps, dy, dsum, out["dx"], out["dweight"], self._on(stream))
         return out
+
+    def _logit_rows(self, name, t):
+        """(rows, row stride) of logits [..., V], or [n, V] with padded rows."""
+        V = self.V
+        if t.dtype is not self._logits or not t.is_cuda or t.shape[-1] != V:
+            raise ValueError(f"{name} must be a CUDA tensor [..., {V}] of {self._logits}")
+        if t.is_contiguous():
+            return t.numel() // V, V
+        if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < V:
+            raise ValueError(f"{name} must be contiguous, or [n, {V}] with contiguous rows")
+        return t.shape[0], t.stride(0)
+
+    def token_logprobs(self, logits, targets=None, inv_temperature=1.0, k=0, out=None, stream=None):
+        """Log probabilities of ``targets`` [...] int64 under softmax(inv_temperature * logits) with
+        entropy and the k most likely tokens (see prism_token_logprobs).  Returns a dict of "lse",
+        "entropy" [...], with targets "logprob" [...], with k > 0 "top_ids" [..., k] int64 and
+        "top_logprob" [..., k]; or fills and returns ``out``, a dict of those that are wanted."""
+        import torch
+        n, ld = self._logit_rows("logits", logits)
+        need, f32, i64 = self._need, torch.float32, torch.int64
+        if targets is not None:
+            need("targets", targets, i64, n)
+        if out is None:
+            lead, dev = logits.shape[:-1], logits.device
+            out = {key: torch.empty(lead, dtype=f32, device=dev) for key in ("lse", "entropy")}
+            if targets is not None:
+                out["logprob"] = torch.empty(lead, dtype=f32, device=dev)
+            if k > 0:
+                out["top_ids"] = torch.empty(*lead, k, dtype=i64, device=dev)
+                out["top_logprob"] = torch.empty(*lead, k, dtype=f32, device=dev)
+        else:
+            for key, t in out.items():
+                if key in ("lse", "entropy", "logprob"):
+                    need(key, t, f32, n)
+                elif key in ("top_ids", "top_logprob"):
+                    need(key, t, i64 if key == "top_ids" else f32, n * k)
+                else:
+                    raise ValueError(f"prism_token_logprobs has no output {key!r}")
+        get = out.get
+        prism_token_logprobs(self.handle, n, logits, ld, targets, inv_temperature, k, get("lse"), get("logprob"), get("entropy"),
+                             get("top_ids"), get("top_logprob"), self._on(stream))
+        return out
+
+    def token_logprobs_backward(self, logits, targets, lse, entropy, dlogprob, dentropy=None, inv_temperature=1.0, dlogits=None,
+                                stream=None):
+        """The logits' cotangent (see prism_token_logprobs_backward), given the forward's lse and
+        entropy (may be None without dentropy); dlogits may be the logits themselves."""
+        import torch
+        n, ld = self._logit_rows("logits", logits)
+        need, f32 = self._need, torch.float32
+        for name, t in (("lse", lse), ("entropy", entropy), ("dlogprob", dlogprob), ("dentropy", dentropy)):
+            if t is not None:
+                need(name, t, f32, n)
+        if targets is not None:
+            need("targets", targets, torch.int64, n)
+        if dlogits is None:
+            dlogits = torch.empty(logits.shape, dtype=self._logits, device=logits.device)
+            ld_d = self.V
+        else:
+            rows, ld_d = self._logit_rows("dlogits", dlogits)
+            if rows != n:
+                raise ValueError("dlogits must have the logits' rows")
+        prism_token_logprobs_backward(self.handle, n, logits, ld, targets, inv_temperature, lse, entropy, dlogprob, dentropy,
+                                      dlogits, ld_d, self._on(stream))
+        return dlogits
 
     def close(self):
         if self.handle:

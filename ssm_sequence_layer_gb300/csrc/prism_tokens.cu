@@ -246,4 +246,46 @@ prism_status prism_norm_backward(prism_tokens_t t, int n, const void *sum, const
     return launched(prism::norm_backward(t->io, {sum, weight, dy, dsum, eps, dx, dweight, n, t->D}, t->norm, l));
 }
 
+prism_status prism_token_logprobs(prism_tokens_t t, int n, const void *logits, long long ld, const long long *targets,
+                                  float inv_temperature, int k, float *lse, float *logprob, float *entropy, long long *top_ids,
+                                  float *top_logprob, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, n, "n");
+    if (st != PRISM_OK) return st;
+    if ((st = check_pointers<7>({{"logits", logits, 16, n > 0}, {"targets", targets, 8, n > 0 && logprob}, {"lse", lse, 4, false},
+                                 {"logprob", logprob, 4, false}, {"entropy", entropy, 4, false}, {"top_ids", top_ids, 8, false},
+                                 {"top_logprob", top_logprob, 4, false}})) != PRISM_OK)
+        return st;
+    if (ld < t->V) return fail(PRISM_ERR_INVALID_ARG, "ld must be >= V = %d (got %lld)", t->V, ld);
+    if (k < 0 || k > 32) return fail(PRISM_ERR_INVALID_ARG, "k must be in 0 .. 32 (got %d)", k);
+    if (!std::isfinite(inv_temperature) || inv_temperature <= 0.f)
+        return fail(PRISM_ERR_INVALID_ARG, "inv_temperature must be finite and > 0");
+    if (!top_ids && !top_logprob) k = 0;
+    const prism::TokenLaunch l = begin(t, stream);
+    if (n == 0) return PRISM_OK;
+    return launched(prism::logprobs_forward(
+        t->logits, {logits, ld, targets, inv_temperature, lse, logprob, entropy, top_ids, top_logprob, n, t->V, k}, l));
+}
+
+prism_status prism_token_logprobs_backward(prism_tokens_t t, int n, const void *logits, long long ld, const long long *targets,
+                                           float inv_temperature, const float *lse, const float *entropy, const float *dlogprob,
+                                           const float *dentropy, void *dlogits, long long ld_d, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, n, "n");
+    if (st != PRISM_OK) return st;
+    if ((st = check_pointers<7>({{"logits", logits, 16, n > 0}, {"targets", targets, 8, n > 0 && dlogprob}, {"lse", lse, 4, n > 0},
+                                 {"entropy", entropy, 4, n > 0 && dentropy}, {"dlogprob", dlogprob, 4, false},
+                                 {"dentropy", dentropy, 4, false}, {"dlogits", dlogits, 16, n > 0}})) != PRISM_OK)
+        return st;
+    if (n > 0 && !dlogprob && !dentropy) return fail(PRISM_ERR_INVALID_ARG, "dlogprob and dentropy must not both be NULL");
+    if (ld < t->V || ld_d < t->V) return fail(PRISM_ERR_INVALID_ARG, "ld and ld_d must be >= V = %d (got %lld, %lld)", t->V, ld, ld_d);
+    if (logits == dlogits && ld != ld_d) return fail(PRISM_ERR_INVALID_ARG, "in place, ld_d must equal ld");
+    if (!std::isfinite(inv_temperature) || inv_temperature <= 0.f)
+        return fail(PRISM_ERR_INVALID_ARG, "inv_temperature must be finite and > 0");
+    const prism::TokenLaunch l = begin(t, stream);
+    if (n == 0) return PRISM_OK;
+    return launched(prism::logprobs_backward(
+        t->logits, {logits, ld, targets, inv_temperature, lse, entropy, dlogprob, dentropy, dlogits, ld_d, n, t->V}, l));
+}
+
 }  // extern "C"

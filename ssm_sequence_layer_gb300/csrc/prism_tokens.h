@@ -67,6 +67,30 @@ struct NormBackwardArgs {
 };
 cudaError_t norm_backward(prism_dtype io, const NormBackwardArgs &a, const NormWorkspace &w, const TokenLaunch &l);
 
+// ---- log probabilities (prism_logprobs.cu) ---------------------------------------------------------
+struct LogprobArgs {
+    const void *logits;
+    long long ld;
+    const long long *targets;
+    float inv_temperature;
+    float *lse, *logprob, *entropy;
+    long long *top_ids;
+    float *top_logprob;
+    int n, V, k;
+};
+cudaError_t logprobs_forward(prism_dtype logits, const LogprobArgs &a, const TokenLaunch &l);
+struct LogprobBackwardArgs {
+    const void *logits;
+    long long ld;
+    const long long *targets;
+    float inv_temperature;
+    const float *lse, *entropy, *dlogprob, *dentropy;
+    void *dlogits;
+    long long ld_d;
+    int n, V;
+};
+cudaError_t logprobs_backward(prism_dtype logits, const LogprobBackwardArgs &a, const TokenLaunch &l);
+
 }  // namespace prism
 
 struct prism_tokens_s {
