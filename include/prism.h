@@ -461,6 +461,28 @@ PRISM_API prism_status prism_norm_backward(prism_tokens_t tokens, int n, const v
                                            struct CUstream_st *stream);
 
 /*
+ * prism_matmul8 -- a matrix product of e4m3 operands whose values share a scale in blocks of 128:
+ *   out[m, j] = sum_b a_scale[m, b] w_scale[j / 128, b] sum_{k in block b} a8[m, k] w8[j, k]
+ *   a8 [M, K] e4m3   a_scale [M, ceil(K/128)] float32          (prism_norm's y8 and y_scale)
+ *   w8 [N, K] e4m3   w_scale [ceil(N/128), ceil(K/128)] float32 (prism_matmul8_weights)
+ *   out [M, N], the handle's logits dtype (io, or PRISM_OPT_OUT_DTYPE)
+ * K is a multiple of 16, at most 65536; N at most 2^30; M at most max_rows.  N and K need not be the
+ * handle's V and D: the product also serves projections.  Products are exact, sums are float32.  An
+ * expired device wait is reported by prism_tokens_last_device_status.
+ */
+PRISM_API prism_status prism_matmul8(prism_tokens_t tokens, int M, int N, int K, const void *a8,
+                                     const float *a_scale, const void *w8, const float *w_scale, void *out,
+                                     struct CUstream_st *stream);
+
+/*
+ * prism_matmul8_weights -- lay weights W [N, K] (io dtype) out for prism_matmul8, once: per block of
+ * 128 x 128, w_scale = max(max |W| / 448, 2^-126) and w8 = W / w_scale rounded to nearest.
+ * Weights must be finite.
+ */
+PRISM_API prism_status prism_matmul8_weights(prism_tokens_t tokens, int N, int K, const void *W, void *w8,
+                                             float *w_scale, struct CUstream_st *stream);
+
+/*
  * prism_token_logprobs -- per row of logits [n, V] (row stride ld >= V), with z = inv_temperature
  * logits and p = softmax(z):
  *   lse      [n] float32   log sum_j exp z_j

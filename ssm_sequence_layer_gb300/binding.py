@@ -39,7 +39,8 @@ EXPORTED = ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forwa
             "prism_project", "prism_backward", "prism_backward_nonlinear",
             "prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy", "prism_tokens_workspace_bytes",
             "prism_tokens_last_device_status", "prism_tokens_kernel_times", "prism_embed", "prism_embed_backward",
-            "prism_norm", "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward")
+            "prism_norm", "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward",
+            "prism_matmul8", "prism_matmul8_weights")
 
 
 class prism_kernel_time(ctypes.Structure):
@@ -109,9 +110,12 @@ def lib():
             L.prism_norm_backward.argtypes = [vp, i, vp, vp, c_f, vp, vp, vp, vp, vp]
             L.prism_token_logprobs.argtypes = [vp, i, vp, ll, vp, c_f, i, vp, vp, vp, vp, vp, vp]
             L.prism_token_logprobs_backward.argtypes = [vp, i, vp, ll, vp, c_f, vp, vp, vp, vp, vp, ll, vp]
+            L.prism_matmul8.argtypes = [vp, i, i, i, vp, vp, vp, vp, vp, vp]
+            L.prism_matmul8_weights.argtypes = [vp, i, i, vp, vp, vp, vp]
             for name in ("prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy",
                          "prism_tokens_last_device_status", "prism_embed", "prism_embed_backward", "prism_norm",
-                         "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward"):
+                         "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward",
+                         "prism_matmul8", "prism_matmul8_weights"):
                 getattr(L, name).restype = ctypes.c_int
             for name in ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forward_host",
                          "prism_plan_destroy", "prism_plan_last_device_status", "prism_forward_state",
@@ -304,6 +308,15 @@ def prism_norm(tokens, n, x, residual, weight, eps, sum, y, y8, y_scale, stream=
 def prism_norm_backward(tokens, n, sum, weight, eps, dy, dsum, dx, dweight, stream=None):
     return _check(lib().prism_norm_backward(tokens, n, _addr(sum), _addr(weight), eps, _addr(dy), _addr(dsum), _addr(dx),
                                             _addr(dweight), _stream(stream)))
+
+
+def prism_matmul8(tokens, M, N, K, a8, a_scale, w8, w_scale, out, stream=None):
+    return _check(lib().prism_matmul8(tokens, M, N, K, _addr(a8), _addr(a_scale), _addr(w8), _addr(w_scale), _addr(out),
+                                      _stream(stream)))
+
+
+def prism_matmul8_weights(tokens, N, K, W, w8, w_scale, stream=None):
+    return _check(lib().prism_matmul8_weights(tokens, N, K, _addr(W), _addr(w8), _addr(w_scale), _stream(stream)))
 
 
 def prism_token_logprobs(tokens, n, logits, ld, targets, inv_temperature, k, lse, logprob, entropy, top_ids, top_logprob,
@@ -645,6 +658,35 @@ class Tokens:
             need("dweight", out["dweight"], torch.float32, D)
         prism_norm_backward(self.handle, n, sum, weight, eps, dy, dsum, out["dx"], out["dweight"], self._on(stream))
         return out
+
+    def matmul8(self, a8, a_scale, w8, w_scale, out=None, stream=None):
+        """The 8-bit product (see prism_matmul8): a8 [..., K] float8_e4m3fn with a_scale
+        [..., ceil(K/128)] (norm's "y8" and "y_scale"), w8 [N, K] with w_scale
+        [ceil(N/128), ceil(K/128)] (matmul8_weights); returns [..., N] in the logits' dtype."""
+        import torch
+        need, f8, f32 = self._need, torch.float8_e4m3fn, torch.float32
+        N, K = w8.shape
+        M, kb = a8.numel() // K, -(-K // 128)
+        need("a8", a8, f8, M * K, K)
+        need("a_scale", a_scale, f32, M * kb, kb)
+        need("w8", w8, f8)
+        need("w_scale", w_scale, f32, -(-N // 128) * kb, kb)
+        if out is None:
+            out = torch.empty(*a8.shape[:-1], N, dtype=self._logits, device=a8.device)
+        else:
+            need("out", out, self._logits, M * N)
+        prism_matmul8(self.handle, M, N, K, a8, a_scale, w8, w_scale, out, self._on(stream))
+        return out
+
+    def matmul8_weights(self, W, stream=None):
+        """Weights W [N, K] (io dtype) laid out once for matmul8: (w8, w_scale)."""
+        import torch
+        N, K = W.shape
+        self._need("W", W, self._io)
+        w8 = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=W.device)
+        w_scale = torch.empty(-(-N // 128), -(-K // 128), dtype=torch.float32, device=W.device)
+        prism_matmul8_weights(self.handle, N, K, W, w8, w_scale, self._on(stream))
+        return w8, w_scale
 
     def _logit_rows(self, name, t):
         """(rows, row stride) of logits [..., V], or [n, V] with padded rows."""

@@ -60,6 +60,14 @@ prism_status check_call(const prism_tokens_s *t, int n, const char *rows)
     return PRISM_OK;
 }
 
+prism_status check_sizes8(int N, int K)
+{
+    if (N < 1 || K < 1) return fail(PRISM_ERR_INVALID_ARG, "N and K must be >= 1 (got %d, %d)", N, K);
+    if (K % 16 != 0 || K > 65536 || N > (1 << 30))
+        return fail(PRISM_ERR_UNSUPPORTED, "K must be a multiple of 16, at most 65536, and N at most 2^30 (got K=%d, N=%d)", K, N);
+    return PRISM_OK;
+}
+
 prism::TokenLaunch begin(prism_tokens_s *t, struct CUstream_st *stream)
 {
     t->timer.on = t->opt_timing != 0;
@@ -244,6 +252,31 @@ prism_status prism_norm_backward(prism_tokens_t t, int n, const void *sum, const
     if (!std::isfinite(eps) || eps < 0.f) return fail(PRISM_ERR_INVALID_ARG, "eps must be finite and >= 0");
     const prism::TokenLaunch l = begin(t, stream);
     return launched(prism::norm_backward(t->io, {sum, weight, dy, dsum, eps, dx, dweight, n, t->D}, t->norm, l));
+}
+
+prism_status prism_matmul8(prism_tokens_t t, int M, int N, int K, const void *a8, const float *a_scale, const void *w8,
+                           const float *w_scale, void *out, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, M, "M");
+    if (st != PRISM_OK) return st;
+    if ((st = check_sizes8(N, K)) != PRISM_OK) return st;
+    if ((st = check_pointers<5>({{"a8", a8, 16, M > 0}, {"a_scale", a_scale, 4, M > 0}, {"w8", w8, 16, true},
+                                 {"w_scale", w_scale, 4, true}, {"out", out, 16, M > 0}})) != PRISM_OK)
+        return st;
+    const prism::TokenLaunch l = begin(t, stream);
+    if (M == 0) return PRISM_OK;
+    return launched(prism::matmul8(t->logits, {a8, a_scale, w8, w_scale, out, M, N, K}, l));
+}
+
+prism_status prism_matmul8_weights(prism_tokens_t t, int N, int K, const void *W, void *w8, float *w_scale,
+                                   struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, 0, "n");
+    if (st != PRISM_OK) return st;
+    if ((st = check_sizes8(N, K)) != PRISM_OK) return st;
+    if ((st = check_pointers<3>({{"W", W, 16, true}, {"w8", w8, 16, true}, {"w_scale", w_scale, 4, true}})) != PRISM_OK) return st;
+    const prism::TokenLaunch l = begin(t, stream);
+    return launched(prism::matmul8_weights(t->io, N, K, W, w8, w_scale, l));
 }
 
 prism_status prism_token_logprobs(prism_tokens_t t, int n, const void *logits, long long ld, const long long *targets,

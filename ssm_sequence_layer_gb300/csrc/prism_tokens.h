@@ -67,6 +67,18 @@ struct NormBackwardArgs {
 };
 cudaError_t norm_backward(prism_dtype io, const NormBackwardArgs &a, const NormWorkspace &w, const TokenLaunch &l);
 
+// ---- 8-bit product (prism_matmul8.cu) --------------------------------------------------------------
+struct Matmul8Args {
+    const void *a8;
+    const float *a_scale;
+    const void *w8;
+    const float *w_scale;
+    void *out;
+    int M, N, K;
+};
+cudaError_t matmul8(prism_dtype out, const Matmul8Args &a, const TokenLaunch &l);
+cudaError_t matmul8_weights(prism_dtype io, int N, int K, const void *W, void *w8, float *w_scale, const TokenLaunch &l);
+
 // ---- log probabilities (prism_logprobs.cu) ---------------------------------------------------------
 struct LogprobArgs {
     const void *logits;

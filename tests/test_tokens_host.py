@@ -43,3 +43,5 @@ def test_null_handle(lib):
     assert lib.prism_norm_backward(None, 1, 16, 16, 1e-6, 16, None, 16, 16, None) == B.PRISM_ERR_INVALID_ARG
     assert lib.prism_token_logprobs(None, 1, 16, 10, 16, 1.0, 0, 16, 16, 16, None, None, None) == B.PRISM_ERR_INVALID_ARG
     assert lib.prism_token_logprobs_backward(None, 1, 16, 10, 16, 1.0, 16, 16, 16, None, 16, 10, None) == B.PRISM_ERR_INVALID_ARG
+    assert lib.prism_matmul8(None, 1, 16, 16, 16, 16, 16, 16, 16, None) == B.PRISM_ERR_INVALID_ARG
+    assert lib.prism_matmul8_weights(None, 16, 16, 16, 16, 16, None) == B.PRISM_ERR_INVALID_ARG
