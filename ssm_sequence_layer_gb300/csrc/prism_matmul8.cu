@@ -2,23 +2,20 @@
 //
 //   out[m, j] = sum_b a_scale[m, b] w_scale[j / 128, b] c_b[m, j],   c_b[m, j] = sum_{k in block b} a8[m, k] w8[j, k]
 //
-// Products of e4m3 values are exact in fp32; the sum over a block is scaled and added in fp32 once per block.
+// Products of e4m3 values are exact in fp32; the sum over a block is scaled and added in fp32 once per
+// block.  Few rows are bound by the weights' bytes (skinny_kernel), many by the tensor cores and by the
+// output's bytes (product_kernel).
+#include <cudaTypedefs.h>
+
 #include "io_util.h"
 #include "prism_tokens.h"
+#include "tc_ptx.h"
 
 namespace prism {
 namespace mm8 {
 
 constexpr int kBlock = 128;
 constexpr float kMaxE4M3 = 448.f, kMinScale = 1.17549435e-38f;
-
-// two e4m3 values (the first in the low byte) as floats
-__device__ __forceinline__ float2 two_e4m3(uint16_t v)
-{
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
 
 template <typename out_t>
 struct Params {
@@ -28,58 +25,406 @@ struct Params {
     int M, N, K, KB;
 };
 
-constexpr int TM = 64, TN = 64;
+// ---------------------------------------------------------------------------------------------
+// Few rows (M <= 32): the weights' bytes bound the product, every weight is used M times at most.  A
+// warp takes 16 rows of w8 as the A operand of m16n8k32 products straight from global memory to
+// registers (16 bytes of a row per lane and load, four loads for a block of 16 x 128), and 8 NT rows
+// of a8 as B operands.  The products' k order is a free choice as long as both operands share it: the
+// four words of a lane's 16 bytes serve as the k slots (lane % 4) 4 .. + 3 and 16 + (lane % 4) 4 .. + 3 of
+// two products.  KS warps of a CTA share a row tile and split the blocks of 128 among them, so that
+// narrow products still fill the machine; their sums are added in a fixed order.
+constexpr int kSkinnyWarps = 8;
 
-template <typename out_t>
-__global__ void __launch_bounds__(256) product_any_kernel(const Params<out_t> p)
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    __shared__ float as[16][TM + 1], ws[16][TN + 1];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int n0 = blockIdx.x * TN;
-    for (int m0 = blockIdx.y * TM; m0 < p.M; m0 += gridDim.y * TM) {
-    float total[4][4] = {};
-    for (int b = 0; b < p.KB; ++b) {
-        float c[4][4] = {};
-        for (int k0 = b * kBlock; k0 < min(p.K, (b + 1) * kBlock); k0 += 16) {
-            const int r = tid >> 2, q = (tid & 3) * 4;  // 64 rows, 4 values each
-            uint32_t va = 0, vw = 0;
-            if (m0 + r < p.M) va = *reinterpret_cast<const uint32_t *>(p.a + (size_t)(m0 + r) * p.K + k0 + q);
-            if (n0 + r < p.N) vw = *reinterpret_cast<const uint32_t *>(p.w + (size_t)(n0 + r) * p.K + k0 + q);
-            __syncthreads();
-            const float2 a0 = two_e4m3((uint16_t)va), a1 = two_e4m3((uint16_t)(va >> 16));
-            const float2 w0 = two_e4m3((uint16_t)vw), w1 = two_e4m3((uint16_t)(vw >> 16));
-            as[q][r] = a0.x, as[q + 1][r] = a0.y, as[q + 2][r] = a1.x, as[q + 3][r] = a1.y;
-            ws[q][r] = w0.x, ws[q + 1][r] = w0.y, ws[q + 2][r] = w1.x, ws[q + 3][r] = w1.y;
-            __syncthreads();
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename out_t, int NT, int KS>
+__global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const Params<out_t> p)
+{
+    constexpr int RT = kSkinnyWarps / KS;  // row tiles of a CTA
+    constexpr int AHEAD = 2;               // blocks of 128 in flight
+    __shared__ float parts[KS > 1 ? kSkinnyWarps : 1][16][8 * NT + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const int ks = warp % KS, n0 = (blockIdx.x * RT + warp / KS) * 16;
+    float total[NT][4];
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) total[t][i] = 0.f;
+    if (n0 < p.N) {
+        // rows beyond the operands' last are read as the last and not stored
+        const uint8_t *wr[2] = {p.w + (size_t)min(n0 + g, p.N - 1) * p.K, p.w + (size_t)min(n0 + g + 8, p.N - 1) * p.K};
+        const float *ws = p.w_scale + (size_t)(n0 / kBlock) * p.KB;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        uint4 w[AHEAD][2][2];
+        auto load = [&](int slot, int b) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) c[i][j] = fmaf(as[k][ty * 4 + i], ws[k][tx * 4 + j], c[i][j]);
-        }
+            for (int h = 0; h < 2; ++h) {
+                const int k = b * kBlock + h * 64 + q * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = m0 + ty * 4 + i;
-            const float sa = m < p.M ? p.a_scale[(size_t)m * p.KB + b] : 0.f;
+                for (int r = 0; r < 2; ++r)
+                    w[slot][r][h] = k < p.K ? __ldcs(reinterpret_cast<const uint4 *>(wr[r] + k)) : zero;
+            }
+        };
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx * 4 + j;
-                const float sw = n < p.N ? p.w_scale[(size_t)(n / kBlock) * p.KB + b] : 0.f;
-                total[i][j] = fmaf(c[i][j], sa * sw, total[i][j]);
+        for (int s = 0; s < AHEAD; ++s) load(s, ks + s * KS);
+        for (int b0 = ks; b0 < p.KB; b0 += AHEAD * KS) {
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) {
+                const int b = b0 + s * KS;
+                if (b >= p.KB) break;
+                uint4 a[NT][2];
+                float sa[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint8_t *ar = p.a + (size_t)min(8 * t + g, p.M - 1) * p.K;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = b * kBlock + h * 64 + q * 16;
+                        a[t][h] = k < p.K ? __ldg(reinterpret_cast<const uint4 *>(ar + k)) : zero;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) sa[t][i] = p.a_scale[(size_t)min(8 * t + 2 * q + i, p.M - 1) * p.KB + b];
+                }
+                const float sw = ws[b];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mma_e4m3(c, w[s][0][h].x, w[s][1][h].x, w[s][0][h].y, w[s][1][h].y, a[t][h].x, a[t][h].y);
+                        mma_e4m3(c, w[s][0][h].z, w[s][1][h].z, w[s][0][h].w, w[s][1][h].w, a[t][h].z, a[t][h].w);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) total[t][i] = fmaf(c[i], sa[t][i & 1] * sw, total[t][i]);
+                }
+                load(s, b + AHEAD * KS);
             }
         }
     }
+    if constexpr (KS > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m < p.M && n < p.N) io::st(p.out + (size_t)m * p.N + n, total[i][j]);
-        }
+            for (int i = 0; i < 4; ++i) parts[warp][g + 8 * (i >> 1)][8 * t + 2 * q + (i & 1)] = total[t][i];
+        __syncthreads();
+        if (ks != 0) return;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                for (int o = 1; o < KS; ++o) total[t][i] += parts[warp + o][g + 8 * (i >> 1)][8 * t + 2 * q + (i & 1)];
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 8 * t + 2 * q + (i & 1), n = n0 + g + 8 * (i >> 1);
+            if (m < p.M && n < p.N) io::st(p.out + (size_t)m * p.N + n, total[t][i]);
+        }
 }
 
+template <typename out_t, int NT>
+void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
+{
+    // enough warps to keep each SM's loads in flight (16 a SM), as far as the blocks of 128 reach
+    const int tiles = (p.N + 15) / 16;
+    int ks = 1;
+    while (ks < 8 && ks < p.KB && tiles * ks < 16 * sm_count) ks *= 2;
+    const int rt = kSkinnyWarps / ks;
+    const unsigned grid = (tiles + rt - 1) / rt;
+    if (ks == 1) skinny_kernel<out_t, NT, 1><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
+    else if (ks == 2) skinny_kernel<out_t, NT, 2><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
+    else if (ks == 4) skinny_kernel<out_t, NT, 4><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
+    else skinny_kernel<out_t, NT, 8><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
+}
+
+// ---------------------------------------------------------------------------------------------
+// More rows: tcgen05 (kind::f8f6f4), persistent.  A tile of 128 rows x BN columns per CTA; each block
+// of 128 in k is one stage of the operand ring (TMA, 128-byte swizzle: a row of a stage is 128 e4m3
+// values) and four tcgen05.mma (K = 32) into one of two accumulators of BN columns in tensor memory.
+// The accumulator holds c_b of one block only: the eight epilogue warps read it, scale it by
+// a_scale[m, b] w_scale[j / 128, b] and add it to the sums in their registers (one row and BN / 2
+// columns per thread) while the next block's products run into the other accumulator.  Per block the
+// tensor core needs 128 BN 128 / 8192 cycles and the scaled addition 128 BN / 128: half as many.
+using namespace prism::tc;
+
+constexpr int BM = 128, STAGE_ROWS = 128;
+constexpr int kEpilogueWarps = 8, kThreads = 64 + 32 * kEpilogueWarps;
+
+template <int BN>
+struct Layout {
+    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr uint32_t A_BYTES = BM * kBlock, B_BYTES = BN * kBlock, STAGE = A_BYTES + B_BYTES;
+    static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging of 32 rows x 128 bytes of output
+    static constexpr uint32_t OFF_OUT = STAGES * STAGE;
+    static constexpr uint32_t SMEM = OFF_OUT + kEpilogueWarps * OUT_WARP + 1024;  // + alignment slack
+    static_assert(SMEM <= 232448 && OFF_OUT % 1024 == 0, "layout");
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum));
+}
+
+// K-major 128B-swizzled operand: 16-byte core-matrix rows, 1024-byte groups of 8 rows
+__device__ __forceinline__ uint64_t operand(uint32_t addr) { return sdesc(addr, 16, 1024); }
+
+// instruction descriptor: e4m3 A and B (format 0), fp32 accumulator
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+struct Waits {
+    int *status;
+    unsigned long long ns;
+};
+
+template <typename out_t, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_out, const Params<out_t> p, const Waits wt, int tiled_out)
+{
+    using L = Layout<BN>;
+    constexpr int STAGES = L::STAGES, HALF = BN / 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ uint32_t tmem_base_s;
+    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2];
+    __shared__ int abort_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+    const long long tiles = (long long)tiles_m * tiles_n;
+    const int my_tiles = tiles > blockIdx.x ? (int)((tiles - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
+    const long long total = (long long)my_tiles * p.KB;
+    const uint32_t sbase = smem_u32(sm);
+
+    if (tid == 0) {
+        abort_s = 0;
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&freed[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&acc_full[s]), 1);
+            mbar_init(smem_u32(&acc_empty[s]), kEpilogueWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tm_a);
+        prefetch_tmap(&tm_w);
+        if (tiled_out) prefetch_tmap(&tm_out);
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_base_s), 2 * BN);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = tmem_base_s;
+
+    // tiles of one column of tiles run at the same time on neighbouring CTAs and share w8 in L2
+    auto tile_at = [&](int i, int &m0, int &n0) {
+        const long long t = (long long)blockIdx.x + (long long)i * gridDim.x;
+        m0 = (int)(t % tiles_m) * BM;
+        n0 = (int)(t / tiles_m) * BN;
+    };
+    auto give_up = [&] {
+        atomicCAS(wt.status, 0, kDevTimeout);
+        *(volatile int *)&abort_s = 1;
+    };
+    long long issued = 0;  // the issuing threads' counts of steps, for the drain
+    if (tid == 32) {  // ---- operand loads ----
+        int s = 0, i = 0, b = 0, m0 = 0, n0 = 0;
+        uint32_t round = 0;
+        for (long long g = 0; g < total; ++g) {
+            if (b == 0) tile_at(i, m0, n0);
+            if (round > 0 && !mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns)) {
+                give_up();
+                break;
+            }
+            if (*(volatile int *)&abort_s) break;
+            const uint32_t mb = smem_u32(&full[s]), at = sbase + s * L::STAGE;
+            mbar_expect_tx(mb, L::STAGE);
+            tma_load_2d(at, &tm_a, mb, b * kBlock, m0);
+#pragma unroll
+            for (int h = 0; h < BN / STAGE_ROWS; ++h)
+                tma_load_2d(at + L::A_BYTES + h * STAGE_ROWS * kBlock, &tm_w, mb, b * kBlock, n0 + h * STAGE_ROWS);
+            issued = g + 1;
+            if (++s == STAGES) s = 0, ++round;
+            if (++b == p.KB) b = 0, ++i;
+        }
+    } else if (tid == 0) {  // ---- products ----
+        int s = 0;
+        uint32_t round = 0;
+        for (long long g = 0; g < total; ++g) {
+            const int buf = (int)(g & 1);
+            bool ok = g < 2 || mbar_wait(smem_u32(&acc_empty[buf]), (uint32_t)((g - 2) >> 1) & 1, wt.ns);
+            ok = ok && mbar_wait(smem_u32(&full[s]), round & 1, wt.ns);
+            if (!ok) {
+                give_up();
+                break;
+            }
+            if (*(volatile int *)&abort_s) break;
+            fence_after_sync();
+            const uint64_t da = operand(sbase + s * L::STAGE), db = operand(sbase + s * L::STAGE + L::A_BYTES);
+#pragma unroll
+            for (int j = 0; j < kBlock / 32; ++j)
+                mma_f8(tmem + buf * BN, da + 2 * j, db + 2 * j, idesc_e4m3(BM, BN), j > 0);
+            mma_commit(smem_u32(&freed[s]));
+            mma_commit(smem_u32(&acc_full[buf]));
+            issued = g + 1;
+            if (++s == STAGES) s = 0, ++round;
+        }
+    } else if (warp >= 2) {  // ---- scaled sums: lane quarter warp % 4, columns of half (warp - 2) / 4 ----
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t from = ((uint32_t)(quarter * 32) << 16) + half * HALF;
+        uint8_t *stage = sm + L::OFF_OUT + (warp - 2) * L::OUT_WARP;
+        const uint32_t stage_u32 = smem_u32(stage);
+        long long g = 0;
+        bool ok = true;
+        for (int i = 0; i < my_tiles && ok; ++i) {
+            int m0, n0;
+            tile_at(i, m0, n0);
+            n0 += half * HALF;
+            const int m = m0 + quarter * 32 + lane;
+            const float *sa = p.a_scale + (size_t)min(m, p.M - 1) * p.KB;
+            const float *sw = p.w_scale + (size_t)(min(n0, p.N - 1) / kBlock) * p.KB;
+            float acc[HALF];
+#pragma unroll
+            for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
+            float scale = sa[0] * sw[0];
+            for (int b = 0; b < p.KB; ++b, ++g) {
+                const int buf = (int)(g & 1);
+                const float next = b + 1 < p.KB ? sa[b + 1] * sw[b + 1] : 0.f;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[buf]), (uint32_t)(g >> 1) & 1, wt.ns));
+                if (!ok) break;
+                fence_after_sync();
+#pragma unroll
+                for (int ch = 0; ch < HALF / 16; ++ch) {
+                    float v[16];
+                    tmem_ld(tmem + buf * BN + from + 16 * ch, v);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) acc[16 * ch + c] = fmaf(v[c], scale, acc[16 * ch + c]);
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+                scale = next;
+            }
+            if (!ok) {
+                if (lane == 0) give_up();  // products may still be in flight: the drain below waits for them
+                break;
+            }
+            // the warp's 32 rows leave in pieces of 128 bytes of columns
+            constexpr int PIECE = 128 / (int)sizeof(out_t);
+#pragma unroll
+            for (int c0 = 0; c0 < HALF; c0 += PIECE) {
+                if (n0 + c0 >= p.N) break;
+                if (tiled_out) {
+                    bulk_wait_read();  // the previous piece has left the staging (lane 0's own copies)
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        uint4 w;
+                        if constexpr (sizeof(out_t) == 2) {
+                            io::Unit<__nv_bfloat16, 8> x;
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = acc[c0 + 8 * u + e];
+                            x.set(f);
+                            w = x.w;
+                        } else {
+                            w = make_uint4(__float_as_uint(acc[c0 + 4 * u]), __float_as_uint(acc[c0 + 4 * u + 1]),
+                                           __float_as_uint(acc[c0 + 4 * u + 2]), __float_as_uint(acc[c0 + 4 * u + 3]));
+                        }
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = w;
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && m0 + quarter * 32 < p.M) {
+                        tma_store_2d(&tm_out, stage_u32, n0 + c0, m0 + quarter * 32);
+                        bulk_commit();
+                    }
+                } else {  // rows whose stride is no multiple of 16 bytes: transposed through the staging
+                    __syncwarp();
+                    float *t = reinterpret_cast<float *>(stage);
+#pragma unroll
+                    for (int q = 0; q < PIECE; q += 32) {
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) t[lane * 32 + (c ^ lane)] = acc[c0 + q + c];
+                        __syncwarp();
+                        const int n = n0 + c0 + q + lane;
+                        for (int r = 0; r < 32; ++r) {
+                            const int row = m0 + quarter * 32 + r;
+                            if (row < p.M && n < p.N) io::st(p.out + (size_t)row * p.N + n, t[r * 32 + (lane ^ r)]);
+                        }
+                    }
+                }
+            }
+        }
+        if (tiled_out) bulk_wait_read();  // before the staging goes
+    }
+    // drain: after an expired wait, the copies and products in flight land before the CTA exits
+    __syncthreads();
+    if (abort_s && issued > 0) {
+        const long long last = issued - 1;
+        if (tid == 0)  // products complete in order
+            (void)mbar_wait(smem_u32(&freed[last % STAGES]), (uint32_t)(last / STAGES) & 1, 1000000000ull);
+        if (tid == 32)
+            for (long long g = last >= STAGES ? last - STAGES + 1 : 0; g <= last; ++g)
+                (void)mbar_wait(smem_u32(&full[g % STAGES]), (uint32_t)(g / STAGES) & 1, 1000000000ull);
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 2 * BN);
+}
+
+bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, long long cols, long long rows, long long stride, int box_cols,
+            int box_rows)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)ptr;
+    }();
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    return fn && fn(map, type, 2, const_cast<void *>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename out_t, int BN>
+cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l)
+{
+    CUtensorMap ma, mw, mo;
+    if (!encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a, p.K, p.M, p.K, kBlock, BM) ||
+        !encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.K, p.N, p.K, kBlock, STAGE_ROWS))
+        return cudaErrorInvalidValue;
+    const long long stride = (long long)p.N * sizeof(out_t);
+    const bool tiled = stride % 16 == 0;
+    if (!tiled) mo = ma;  // not used
+    else if (!encode(&mo, sizeof(out_t) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.out, p.N, p.M,
+                     stride, 128 / (int)sizeof(out_t), 32))
+        return cudaErrorInvalidValue;
+    const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+    const Waits wt{l.d_status, l.wait_ns > 0 ? (unsigned long long)l.wait_ns : 100000000ull};
+    product_kernel<out_t, BN><<<(unsigned)(tiles < l.sm_count ? tiles : l.sm_count), kThreads, Layout<BN>::SMEM, l.timer->stream>>>(
+        ma, mw, mo, p, wt, tiled ? 1 : 0);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------------------------
 // A block lays out 128 rows of one block of 128 columns: their largest magnitude, then the values.
 template <typename io_t>
 __global__ void __launch_bounds__(256) weights_kernel(const io_t *__restrict__ W, uint8_t *__restrict__ w8,
@@ -114,13 +459,38 @@ cudaError_t product(const Matmul8Args &a, const TokenLaunch &l)
 {
     const Params<out_t> p{(const uint8_t *)a.a8, (const uint8_t *)a.w8, a.a_scale, a.w_scale, (out_t *)a.out, a.M, a.N, a.K,
                           (a.K + kBlock - 1) / kBlock};
+    cudaError_t e;
     l.timer->begin("matmul8");
-    product_any_kernel<out_t><<<dim3((a.N + TN - 1) / TN, min((a.M + TM - 1) / TM, 65535)), 256, 0, l.timer->stream>>>(p);
+    if (a.M <= 32) {
+        if (a.M <= 8) launch_skinny<out_t, 1>(p, l.sm_count, l.timer->stream);
+        else if (a.M <= 16) launch_skinny<out_t, 2>(p, l.sm_count, l.timer->stream);
+        else launch_skinny<out_t, 4>(p, l.sm_count, l.timer->stream);
+        e = cudaGetLastError();
+    } else {
+        // wide tiles halve the reads of a8; narrow ones where wide ones would leave SMs without a tile
+        const long long wide = (long long)((a.M + BM - 1) / BM) * ((a.N + 255) / 256);
+        e = wide >= l.sm_count ? launch_product<out_t, 256>(p, l) : launch_product<out_t, 128>(p, l);
+    }
     l.timer->end();
-    return cudaGetLastError();
+    return e;
+}
+
+template <typename out_t, int BN>
+cudaError_t prepare()
+{
+    return cudaFuncSetAttribute(product_kernel<out_t, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<BN>::SMEM);
 }
 
 }  // namespace mm8
+
+cudaError_t matmul8_prepare()
+{
+    cudaError_t e = mm8::prepare<float, 128>();
+    if (e == cudaSuccess) e = mm8::prepare<float, 256>();
+    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 128>();
+    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 256>();
+    return e;
+}
 
 cudaError_t matmul8(prism_dtype out, const Matmul8Args &a, const TokenLaunch &l)
 {

@@ -76,6 +76,7 @@ struct Matmul8Args {
     void *out;
     int M, N, K;
 };
+cudaError_t matmul8_prepare();
 cudaError_t matmul8(prism_dtype out, const Matmul8Args &a, const TokenLaunch &l);
 cudaError_t matmul8_weights(prism_dtype io, int N, int K, const void *W, void *w8, float *w_scale, const TokenLaunch &l);
 

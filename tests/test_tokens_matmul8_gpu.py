@@ -69,6 +69,38 @@ def test_matmul8(out, M, N, K):
     assert np.all(np.abs(f64(got[:M]) - ref) <= e + half)
 
 
+def test_sums_keep_32_bits():
+    """One large product among small ones: 448 * 448 = 200704 < 2^18 and 127 times 2^-6.  Every partial
+    sum is a multiple of 2^-6 below 2^18, so it has 24 bits: sums held in fp32 are exact in any order, and
+    sums held in fewer bits would drop small products."""
+    M, N, K = 130, 256, 128
+    a8 = torch.full((M, K), 0.125).to(torch.float8_e4m3fn)
+    w8 = torch.full((N, K), 0.125).to(torch.float8_e4m3fn)
+    a8[:, 77] = 448.0
+    w8[:, 77] = 448.0
+    for rows in (1, 8, 16, 40, 130):
+        with B.Tokens(M, 64, 64, io="f32") as t:
+            got = t.matmul8(a8[:rows].cuda(), torch.ones(rows, 1, device="cuda"), w8.cuda(), torch.ones(2, 1, device="cuda"))
+        assert torch.all(got == 448.0 * 448.0 + 127 / 64), rows
+
+
+def test_an_expired_wait_is_reported():
+    """With a bound of 1 ns every wait runs out: the status says so, and the handle works again after it."""
+    a8, sa, w8, sw = draw(600, 1000, 768, 1)
+    with B.Tokens(600, 64, 64, io="f32") as t:
+        ref = t.matmul8(a8, sa, w8, sw)
+        torch.empty(1 << 28, device="cuda").zero_()  # operands out of L2, so that loads take longer than the bound
+        t.set_option(B.PRISM_OPT_WAIT_NS, 1)
+        t.matmul8(a8, sa, w8, sw)
+        torch.cuda.synchronize()
+        with pytest.raises(B.PrismError) as ei:
+            t.last_device_status()
+        assert ei.value.status == B.PRISM_ERR_TIMEOUT
+        t.set_option(B.PRISM_OPT_WAIT_NS, 0)
+        assert torch.equal(t.matmul8(a8, sa, w8, sw), ref)
+        t.last_device_status()
+
+
 def test_special_values():
     """NaN stays in its row or column; an infinite scale gives infinities and NaN as the formula does; zeros give zeros."""
     M, N, K = 140, 300, 256
