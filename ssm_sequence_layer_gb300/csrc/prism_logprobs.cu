@@ -1,55 +1,128 @@
 // Log probabilities of given tokens with entropy and top alternatives, and the gradient.
 //
 // With z = inv_temperature logits, m = max_j z_j, s = sum_j exp(z_j - m), t = sum_j exp(z_j - m) (z_j - m):
-//   lse = m + log s,   logprob = z_target - lse,   entropy = log s - t / s
+//   lse = m + log s,   logprob = (z_target - m) - log s,   entropy = log s - t / s
 //   dlogits_j = inv_temperature (dlogprob (1_{j = target} - p_j) - dentropy p_j (log p_j + entropy))
-// One pass over the row with a running maximum: m, s and t of two parts join as
+// One pass over the row with a running maximum; two parts of a row join as
 //   m = max(m1, m2),  f_i = exp(m_i - m),  s = sum f_i s_i,  t = sum f_i (t_i + s_i (m_i - m))
-// HBM bounds both directions (a few operations and one exponential per value).
+// The differences are taken between logits (exact where they are near, and no finite logit overflows)
+// and scaled by c2 = inv_temperature log2 e, so that an exponential is one ex2; t is kept in base 2.
+// A few operations and one exponential per value: HBM bounds both directions.
 //
 // A logit of -inf or of the lowest value (of bfloat16, or below) marks a masked token, and so does a
 // product that overflows to -inf: z = -inf there.
 #include "io_util.h"
 #include "prism_tokens.h"
+#include "tc_ptx.h"
 
 namespace prism {
 namespace logp {
 
-constexpr int kThreads = 512;
-constexpr float kLog2e = 1.4426950408889634f;
-
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kAhead = 4;             // 16-byte units in flight per thread
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.38953139e38f;  // the lowest bfloat16 value
+constexpr float kFar = -1e4f;         // 2^kFar = 0, and kFar times anything in range is finite
+constexpr int kClusterMax = 8, kTopMax = 32;
+constexpr int kCandidates = 1024;
+constexpr size_t kKeepMax = 200 * 1024;  // shared memory for a row's slice
 
-// z of a logit; -inf for a masked token (NaN stays NaN)
-__device__ __forceinline__ float z_of(float x, float c) { return x <= kLowest ? -INFINITY : x * c; }
-
-struct Running {
-    float m, s, t;
-};
-__device__ __forceinline__ Running join(const Running a, const Running b)
+__device__ __forceinline__ float ex2(float x)
 {
-    Running r;
-    r.m = fmaxf(a.m, b.m);
-    // a part that holds nothing (m = -inf) has s = t = 0: its factor must be a number
-    const float da = a.m == r.m ? 0.f : a.m - r.m, db = b.m == r.m ? 0.f : b.m - r.m;
-    const float fa = __expf(da), fb = __expf(db);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b)  // NaN if either is
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+template <typename logit_t>
+struct Row;
+template <>
+struct Row<__nv_bfloat16> {
+    static constexpr int VEC = 8;
+    using U = io::Unit<__nv_bfloat16, 8>;
+    static __device__ __forceinline__ U nothing()
+    {
+        U u;
+        u.w = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+        return u;
+    }
+    // the larger of two numbers; NaN only if both are
+    static __device__ __forceinline__ float largest(const U &u)
+    {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u.w);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+};
+template <>
+struct Row<float> {
+    static constexpr int VEC = 4;
+    using U = io::Unit<float, 4>;
+    static __device__ __forceinline__ U nothing()
+    {
+        U u;
+        u.w = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+        return u;
+    }
+    static __device__ __forceinline__ float largest(const U &u)
+    {
+        float f[4];
+        u.get(f);
+        return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+    }
+};
+
+// A part of a row: its largest logit (-inf: no live token), s and t relative to it
+struct Part {
+    float top, s, t;
+};
+__device__ __forceinline__ Part join(const Part a, const Part b, float c2)
+{
+    Part r;
+    r.top = fmaxf(a.top, b.top);
+    const float da = a.top == r.top ? 0.f : (a.top - r.top) * c2, db = b.top == r.top ? 0.f : (b.top - r.top) * c2;
+    const float fa = ex2(da), fb = ex2(db);
     r.s = a.s * fa + b.s * fb;
-    r.t = fa * (fa > 0.f ? a.t + a.s * da : 0.f) + fb * (fb > 0.f ? b.t + b.s * db : 0.f);
+    r.t = (fa > 0.f ? fa * (a.t + a.s * da) : 0.f) + (fb > 0.f ? fb * (b.t + b.s * db) : 0.f);
     return r;
 }
-__device__ __forceinline__ void add(Running &r, float z)
-{
-    if (z == -INFINITY) return;  // a masked token
-    if (z > r.m) {
-        const float d = r.m == -INFINITY ? 0.f : r.m - z, f = r.m == -INFINITY ? 0.f : __expf(d);
-        r.t = f > 0.f ? f * (r.t + r.s * d) : 0.f;
-        r.s *= f;
-        r.m = z;
+
+// A thread's share of a row; top = kLowest: no live token so far (then s = t = 0, or NaN)
+struct Share {
+    float top = kLowest, s = 0.f, t = 0.f;
+
+    template <typename R, int N>
+    __device__ __forceinline__ void add(const typename R::U (&x)[N], float c2)
+    {
+        float now = top;
+#pragma unroll
+        for (int i = 0; i < N; ++i) now = fmaxf(now, R::largest(x[i]));
+        const float d = fmaxf((top - now) * c2, kFar), f = ex2(d);
+        t = f * fmaf(s, d, t);
+        s *= f;
+        top = now;
+        const float from = now > kLowest ? now : 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v[R::VEC];
+            x[i].get(v);
+#pragma unroll
+            for (int e = 0; e < R::VEC; ++e) {
+                // masked tokens end at kFar, where p = 0; NaN (and +inf against itself) goes into the sums
+                const float z = max_nan((v[e] - from) * c2, kFar), p = ex2(z);
+                s += p;
+                t = fmaf(p, z, t);
+            }
+        }
     }
-    const float d = z - r.m, e = __expf(d);  // NaN and +inf give NaN here, as the formulas do
-    r.s += e;
-    r.t = e == 0.f ? r.t : fmaf(e, d, r.t);
-}
+    __device__ __forceinline__ Part part() const { return {top > kLowest ? top : -INFINITY, s, t}; }
+};
 
 // A logit's place in the order of the top: by value (NaN first), then by lowest id.  Larger keys come
 // first; 0 stands for nothing (masked tokens never become keys).
@@ -59,6 +132,12 @@ __device__ __forceinline__ unsigned long long key_of(float x, int id)
     b = x != x ? 0xffffffffu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
     return ((unsigned long long)b << 32) | (uint32_t)~id;
 }
+__device__ __forceinline__ float value_of(unsigned long long key)
+{
+    const uint32_t b = (uint32_t)(key >> 32);
+    return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);  // 0xffffffff gives a NaN
+}
+__device__ __forceinline__ int id_of(unsigned long long key) { return (int)~(uint32_t)key; }
 
 template <typename logit_t>
 struct ForwardParams {
@@ -72,65 +151,244 @@ struct ForwardParams {
     int *status;
 };
 
+// A row's slice for one CTA of its cluster: single values up to the first 16-byte boundary (first CTA),
+// units, single values behind the last unit (last CTA).
 template <typename logit_t>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardParams<logit_t> p)
+struct Slice {
+    const logit_t *x;
+    int head, u0, u1, tail0, tail1;  // singles [0, head), units [u0, u1) behind them, singles [tail0, tail1)
+    __device__ Slice(const logit_t *row, int V, int rank, int size)
+    {
+        constexpr int VEC = Row<logit_t>::VEC;
+        x = row;
+        const int off = (int)(((uintptr_t)row & 15) / sizeof(logit_t)), before = min(V, off ? VEC - off : 0);
+        const int units = (V - before) / VEC;
+        u0 = (int)((long long)units * rank / size);
+        u1 = (int)((long long)units * (rank + 1) / size);
+        tail0 = before + units * VEC;
+        tail1 = rank == size - 1 ? V : tail0;
+        first = before;
+        head = rank == 0 ? before : 0;
+    }
+    int first;  // id of unit 0's first value
+    // the single value that thread tid holds: its id, or -1
+    __device__ __forceinline__ int single(int tid) const
+    {
+        if (tid < head) return tid;
+        if (tid >= 32 && tail0 + tid - 32 < tail1) return tail0 + tid - 32;
+        return -1;
+    }
+    __device__ __forceinline__ const uint4 *units() const { return reinterpret_cast<const uint4 *>(x + first); }
+};
+
+template <typename logit_t, bool TOP, bool KEEP>
+__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParams<logit_t> p, int cluster)
 {
-    __shared__ Running parts[kThreads / 32];
-    __shared__ unsigned long long best[kThreads / 32];
-    __shared__ float m_s, logs_s;
+    using R = Row<logit_t>;
+    using U = typename R::U;
+    extern __shared__ uint4 kept[];  // the slice's units, for the second look at them
+    __shared__ Part parts[kWarps];
+    __shared__ Part mine;                                    // this CTA's part
+    __shared__ unsigned long long best[TOP ? kTopMax : 1];   // its first k keys
+    __shared__ unsigned long long cand[TOP ? kCandidates : 1];
+    __shared__ float group_top[32];
+    __shared__ int found;
+    __shared__ float threshold;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long row = blockIdx.x;
-    const logit_t *x = p.logits + row * p.ld;
-    Running r{-INFINITY, 0.f, 0.f};
-    for (int j = tid; j < p.V; j += kThreads) add(r, z_of(io::ld(x + j), p.inv_temperature));
+    const int rank = cluster > 1 ? (int)(blockIdx.x % cluster) : 0;
+    const long long row = blockIdx.x / cluster;
+    const Slice<logit_t> sl(p.logits + row * p.ld, p.V, rank, cluster);
+    const float c2 = p.inv_temperature * kLog2e;
+    const uint4 *units = sl.units();
+
+    Share sh;
+    for (int u = sl.u0 + tid; u < sl.u1; u += kAhead * kThreads) {
+        U x[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            x[a] = R::nothing();
+            if (u + a * kThreads < sl.u1) x[a].w = __ldg(units + u + a * kThreads);
+        }
+        if constexpr (TOP && KEEP) {
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                if (u + a * kThreads < sl.u1) kept[u + a * kThreads - sl.u0] = x[a].w;
+        }
+        sh.template add<R, kAhead>(x, c2);
+    }
+    const int single = sl.single(tid);
+    if (single >= 0) {
+        U x[1] = {R::nothing()};
+        *reinterpret_cast<logit_t *>(&x[0].w) = sl.x[single];
+        sh.template add<R, 1>(x, c2);
+    }
+    Part r = sh.part();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const Running other{__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o),
-                            __shfl_xor_sync(0xffffffffu, r.t, o)};
-        r = lane & o ? join(other, r) : join(r, other);
+        const Part other{__shfl_xor_sync(0xffffffffu, r.top, o), __shfl_xor_sync(0xffffffffu, r.s, o),
+                         __shfl_xor_sync(0xffffffffu, r.t, o)};
+        r = lane & o ? join(other, r, c2) : join(r, other, c2);
     }
     if (lane == 0) parts[warp] = r;
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) r = join(r, parts[w]);
-        // logprob = (z - m) - log s rather than z - lse: the difference is exact where z and m are near
-        const bool none = r.m == -INFINITY && r.s == 0.f;
-        const float m = none ? 0.f : r.m, logs = none ? -INFINITY : logf(r.s);
-        m_s = m;
-        logs_s = logs;
-        if (p.lse) p.lse[row] = m + logs;
-        if (p.entropy) p.entropy[row] = none ? 0.f : logs - r.t / r.s;
-        if (p.logprob) {
-            const long long t = p.targets[row];
-            if (t >= p.V) atomicCAS(p.status, 0, kDevBounds);
-            float v = 0.f;
-            if (t >= 0 && t < p.V) v = none ? -INFINITY : (z_of(io::ld(x + t), p.inv_temperature) - m) - logs;
-            p.logprob[row] = v;
-        }
-    }
-    __syncthreads();
-    unsigned long long last = ~0ull;
-    for (int i = 0; i < p.k; ++i) {
-        unsigned long long b = 0;
-        for (int j = tid; j < p.V; j += kThreads) {
-            const float v = io::ld(x + j);
-            if (z_of(v, p.inv_temperature) == -INFINITY) continue;
-            const unsigned long long key = key_of(v, j);
-            if (key < last && key > b) b = key;
-        }
+    if constexpr (TOP) {  // the largest logit of each half warp
+        float g = sh.top;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
-        if (lane == 0) best[warp] = b;
+        for (int o = 8; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if ((lane & 15) == 0) group_top[warp * 2 + (lane >> 4)] = g;
+        if (tid == 0) found = 0;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        r = lane < kWarps ? parts[lane] : Part{-INFINITY, 0.f, 0.f};
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            const Part other{__shfl_xor_sync(0xffffffffu, r.top, o), __shfl_xor_sync(0xffffffffu, r.s, o),
+                             __shfl_xor_sync(0xffffffffu, r.t, o)};
+            r = lane & o ? join(other, r, c2) : join(r, other, c2);
+        }
+        if (lane == 0) mine = r;
+    }
+    if constexpr (TOP) {
+        // The k-th largest of the 32 groups' largest logits: at least k of the slice's logits reach it, and
+        // few more.  Those are collected and ordered by counting.
+        if (warp == 1) {
+            const float g = group_top[lane];
+            int above = 0;
+            for (int o = 0; o < 32; ++o) {
+                const float other = group_top[o];
+                above += other > g || (other == g && o < lane);
+            }
+            if (above == p.k - 1) threshold = g;
+        }
         __syncthreads();
-        for (int w = 0; w < kThreads / 32; ++w) b = max(b, best[w]);
+        const float least = threshold;
+        auto offer = [&](float v, int id) {
+            if (v < least || v <= kLowest || v * p.inv_temperature == -INFINITY) return;  // NaN passes
+            const int at = atomicAdd(&found, 1);
+            if (at < kCandidates) cand[at] = key_of(v, id);
+        };
+        for (int u = sl.u0 + tid; u < sl.u1; u += kThreads) {
+            U x;
+            x.w = KEEP ? kept[u - sl.u0] : __ldg(units + u);
+            float v[R::VEC];
+            x.get(v);
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < R::VEC; ++e) any |= !(v[e] < least);
+            if (any)
+#pragma unroll
+                for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + u * R::VEC + e);
+        }
+        if (single >= 0) offer(io::ld(sl.x + single), single);
+        if (tid < kTopMax) best[tid] = 0;
         __syncthreads();
-        last = b;
-        if (tid == 0) {
-            const int id = (int)~(uint32_t)b;
-            if (p.top_ids) p.top_ids[row * p.k + i] = b ? id : -1;
-            if (p.top_logprob) p.top_logprob[row * p.k + i] = b ? (io::ld(x + id) * p.inv_temperature - m_s) - logs_s : -INFINITY;
+        const int count = found;
+        if (count <= kCandidates) {
+            for (int i = tid; i < count; i += kThreads) {
+                const unsigned long long key = cand[i];
+                int above = 0;
+                for (int o = 0; o < count; ++o) above += cand[o] > key;
+                if (above < p.k) best[above] = key;
+            }
+        } else {
+            // many equal logits, or an order that the groups miss: the largest key below the last one, k times
+            unsigned long long last = ~0ull;
+            for (int i = 0; i < p.k; ++i) {
+                unsigned long long b = 0;
+                auto look = [&](float v, int id) {
+                    if (v <= kLowest || v * p.inv_temperature == -INFINITY) return;
+                    const unsigned long long key = key_of(v, id);
+                    if (key < last && key > b) b = key;
+                };
+                for (int u = sl.u0 + tid; u < sl.u1; u += kThreads) {
+                    U x;
+                    x.w = KEEP ? kept[u - sl.u0] : __ldg(units + u);
+                    float v[R::VEC];
+                    x.get(v);
+#pragma unroll
+                    for (int e = 0; e < R::VEC; ++e) look(v[e], sl.first + u * R::VEC + e);
+                }
+                if (single >= 0) look(io::ld(sl.x + single), single);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+                __syncthreads();  // cand is free: the round before has been read
+                if (lane == 0) cand[warp] = b;
+                __syncthreads();
+                for (int w = 0; w < kWarps; ++w) b = max(b, cand[w]);
+                last = b;
+                if (tid == 0) best[i] = b;
+                if (b == 0) break;
+            }
         }
     }
+    // the cluster's parts and keys join in its first CTA
+    if (cluster > 1) {
+        asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+    if (rank == 0) {
+        auto remote = [&](const void *local, int cta) {
+            uint32_t a;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(local)), "r"(cta));
+            return a;
+        };
+        auto far_float = [&](const float *local, int cta) {
+            float v;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote(local, cta)) : "memory");
+            return v;
+        };
+        Part all = mine;
+        for (int o = 1; o < cluster; ++o)  // every thread joins them: the top needs the row's sum as well
+            all = join(all, {far_float(&mine.top, o), far_float(&mine.s, o), far_float(&mine.t, o)}, c2);
+        const float c = p.inv_temperature;
+        const bool none = all.s == all.s && all.top * c == -INFINITY;
+        const float top = none ? 0.f : all.top, logs = none ? -INFINITY : logf(all.s);
+        if (tid == 0) {
+            if (p.lse) p.lse[row] = fmaf(top, c, logs);
+            if (p.entropy) p.entropy[row] = none ? 0.f : logs - all.t / all.s * kLn2;
+            if (p.logprob) {
+                const long long t = p.targets[row];
+                if (t >= p.V) atomicCAS(p.status, 0, kDevBounds);
+                float v = 0.f;
+                if (t >= 0 && t < p.V) {
+                    const float x = io::ld(sl.x + t);
+                    v = none || x <= kLowest ? -INFINITY : (x - top) * c - logs;
+                    if (all.s != all.s) v = all.s;
+                }
+                p.logprob[row] = v;
+            }
+        }
+        if constexpr (TOP) {
+            unsigned long long key = 0;
+            int place = tid;
+            if (cluster > 1) {
+                const int total = cluster * p.k;
+                __syncthreads();  // cand is free
+                if (tid < total) {
+                    unsigned long long v;
+                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(&best[tid % p.k], tid / p.k)) : "memory");
+                    cand[tid] = v;
+                }
+                __syncthreads();
+                place = p.k;
+                if (tid < total) {
+                    key = cand[tid];
+                    place = 0;  // empty places (key 0) keep their order behind the keys
+                    for (int o = 0; o < total; ++o) place += cand[o] > key || (cand[o] == key && o < tid);
+                }
+            } else if (tid < p.k) {
+                key = best[tid];
+            }
+            if (place < p.k && (cluster > 1 ? tid < cluster * p.k : tid < p.k)) {
+                const float x = value_of(key);
+                if (p.top_ids) p.top_ids[row * p.k + place] = key ? id_of(key) : -1;
+                if (p.top_logprob) p.top_logprob[row * p.k + place] = key ? (x - top) * c - logs : -INFINITY;
+            }
+        }
+    }
+    // the other CTAs' shared memory stays until the first one has read it
+    if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 template <typename logit_t>
@@ -145,29 +403,83 @@ struct BackwardParams {
     int *status;
 };
 
+// A CTA takes kAhead units per thread of one row.  dlogits_j = p_j (B - dentropy log p_j), plus dlogprob at the
+// target, with inv_temperature in dlogprob and dentropy, and B = -dlogprob - dentropy entropy.
 template <typename logit_t>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const BackwardParams<logit_t> p)
+__global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardParams<logit_t> p, int chunks)
 {
-    const long long row = blockIdx.x;
-    const logit_t *x = p.logits + row * p.ld;
-    logit_t *d = p.dlogits + row * p.ld_d;
-    const float lse = p.lse[row];
+    using R = Row<logit_t>;
+    using U = typename R::U;
+    const int tid = threadIdx.x;
+    const long long row = blockIdx.x / chunks;
+    const int chunk = (int)(blockIdx.x % chunks);
+    const Slice<logit_t> sl(p.logits + row * p.ld, p.V, 0, 1);
+    logit_t *out = p.dlogits + row * p.ld_d;
+    const uint4 *units = sl.units();
+    const int u0 = chunk * kAhead * kThreads + tid;
+    U x[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+        if (u0 + a * kThreads < sl.u1) x[a].w = units[u0 + a * kThreads];
+    const float lse = p.lse[row], c = p.inv_temperature;
     long long t = p.dlogprob ? p.targets[row] : -1;
     if (t >= p.V) {
-        if (threadIdx.x == 0) atomicCAS(p.status, 0, kDevBounds);
+        if (tid == 0) atomicCAS(p.status, 0, kDevBounds);
         t = -1;
     }
-    const float dlp = t >= 0 ? p.dlogprob[row] : 0.f;
-    const float dh = p.dentropy ? p.dentropy[row] : 0.f, h = p.dentropy ? p.entropy[row] : 0.f;
-    for (int j = threadIdx.x; j < p.V; j += kThreads) {
-        const float z = z_of(io::ld(x + j), p.inv_temperature);
-        float g = 0.f;
-        if (z != -INFINITY && lse != -INFINITY) {
-            const float lp = z - lse, pr = __expf(lp);
-            g = (j == t ? dlp : 0.f) - pr * dlp - (pr == 0.f ? 0.f : dh * pr * (lp + h));
+    const bool none = lse == -INFINITY;
+    const float dlp = t >= 0 && !none ? p.dlogprob[row] * c : 0.f;
+    const float dh = p.dentropy && !none ? p.dentropy[row] * c : 0.f, h = p.dentropy && !none ? p.entropy[row] : 0.f;
+    const float minus_lse = none ? 0.f : -lse, Bc = fmaf(-dh, h, -dlp);
+    auto grad = [&](float v) {
+        const float z = max_nan(fmaf(v, c, minus_lse), kFar), pr = ex2(z * kLog2e);
+        return pr * fmaf(-dh, z, Bc);
+    };
+    auto at_target = [&](float v) { return v <= kLowest ? 0.f : dlp; };  // a masked target has no gradient
+    const bool aligned = (((uintptr_t)(out + sl.first)) & 15) == 0;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+        const int u = u0 + a * kThreads;
+        if (u >= sl.u1) break;
+        const int id = sl.first + u * R::VEC;
+        float v[R::VEC];
+        x[a].get(v);
+        const int hit = t >= id && t < id + R::VEC ? (int)t - id : -1;
+#pragma unroll
+        for (int e = 0; e < R::VEC; ++e) {
+            const float g = grad(v[e]);
+            v[e] = e == hit ? g + at_target(v[e]) : g;
         }
-        io::st(d + j, g * p.inv_temperature);
+        if (aligned) {
+            x[a].set(v);
+            *reinterpret_cast<uint4 *>(out + id) = x[a].w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < R::VEC; ++e) io::st(out + id + e, v[e]);
+        }
     }
+    const int single = chunk == 0 ? sl.single(tid) : -1;
+    if (single >= 0) {
+        const float v = io::ld(sl.x + single), g = grad(v);
+        io::st(out + single, single == t ? g + at_target(v) : g);
+    }
+}
+
+template <typename logit_t, bool TOP, bool KEEP>
+cudaError_t launch_forward(const ForwardParams<logit_t> &p, int cluster, size_t smem, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.n * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, forward_kernel<logit_t, TOP, KEEP>, p, cluster);
 }
 
 template <typename logit_t>
@@ -175,10 +487,24 @@ cudaError_t forward(const LogprobArgs &a, const TokenLaunch &l)
 {
     const ForwardParams<logit_t> p{(const logit_t *)a.logits, a.targets, a.lse, a.logprob, a.entropy, a.top_logprob, a.top_ids,
                                    a.ld, a.inv_temperature, a.n, a.V, a.k, l.d_status};
+    // Few rows are split over a cluster, down to one unit per thread.  With alternatives the slice also
+    // has to fit shared memory, two CTAs to an SM if a cluster can make it that small.
+    const long long units = a.V / Row<logit_t>::VEC + 1;
+    int cluster = 1;
+    while (cluster < kClusterMax && (long long)a.n * cluster < 2 * l.sm_count && units / cluster > kThreads) cluster *= 2;
+    auto slice = [&] { return (size_t)(units / cluster + 1) * 16; };
+    if (a.k > 0)
+        while (cluster < kClusterMax && slice() > kKeepMax / 2) cluster *= 2;
     l.timer->begin("token_logprobs");
-    forward_kernel<logit_t><<<a.n, kThreads, 0, l.timer->stream>>>(p);
+    cudaError_t e;
+    if (a.k == 0)
+        e = launch_forward<logit_t, false, false>(p, cluster, 0, l.timer->stream);
+    else if (slice() <= kKeepMax)
+        e = launch_forward<logit_t, true, true>(p, cluster, slice(), l.timer->stream);
+    else
+        e = launch_forward<logit_t, true, false>(p, cluster, 0, l.timer->stream);
     l.timer->end();
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename logit_t>
@@ -186,13 +512,25 @@ cudaError_t backward(const LogprobBackwardArgs &a, const TokenLaunch &l)
 {
     const BackwardParams<logit_t> p{(const logit_t *)a.logits, a.targets, a.lse, a.entropy, a.dlogprob, a.dentropy,
                                     (logit_t *)a.dlogits, a.ld, a.ld_d, a.inv_temperature, a.n, a.V, l.d_status};
+    const int units = a.V / Row<logit_t>::VEC, per = kAhead * kThreads, chunks = units > per ? (units + per - 1) / per : 1;
     l.timer->begin("token_logprobs_backward");
-    backward_kernel<logit_t><<<a.n, kThreads, 0, l.timer->stream>>>(p);
+    // n chunks: below 2^31 for any logits that fit the device's memory
+    backward_kernel<logit_t><<<(unsigned)((long long)a.n * chunks), kThreads, 0, l.timer->stream>>>(p, chunks);
     l.timer->end();
     return cudaGetLastError();
 }
 
 }  // namespace logp
+
+cudaError_t logprobs_prepare()
+{
+    cudaError_t e = cudaFuncSetAttribute(logp::forward_kernel<float, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)logp::kKeepMax);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(logp::forward_kernel<__nv_bfloat16, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)logp::kKeepMax);
+    return e;
+}
 
 cudaError_t logprobs_forward(prism_dtype logits, const LogprobArgs &a, const TokenLaunch &l)
 {

@@ -100,7 +100,9 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
     if (major != 10 || minor != 3)
         return fail(PRISM_ERR_ARCH, "device %d is sm_%d%d; this library is built for sm_103 only", device, major, minor);
 
-    if ((e = prism::matmul8_prepare()) != cudaSuccess) return cuda_fail(e, "kernel attribute setup");
+    e = prism::matmul8_prepare();
+    if (e == cudaSuccess) e = prism::logprobs_prepare();
+    if (e != cudaSuccess) return cuda_fail(e, "kernel attribute setup");
     prism_tokens_s *t = new (std::nothrow) prism_tokens_s();
     if (!t) return fail(PRISM_ERR_INVALID_ARG, "out of host memory");
     t->max_rows = max_rows;

@@ -91,6 +91,7 @@ struct LogprobArgs {
     float *top_logprob;
     int n, V, k;
 };
+cudaError_t logprobs_prepare();
 cudaError_t logprobs_forward(prism_dtype logits, const LogprobArgs &a, const TokenLaunch &l);
 struct LogprobBackwardArgs {
     const void *logits;
