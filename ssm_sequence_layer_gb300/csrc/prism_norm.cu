@@ -5,6 +5,8 @@
 //   dx = q (w dy - rh mean_j(w_j dy_j rh_j)) + dsum,   rh = r q,   dweight = sum over rows of dy rh
 //
 // A few operations per value read: HBM bounds both directions.
+#include <type_traits>
+
 #include "io_util.h"
 #include "prism_tokens.h"
 
@@ -36,6 +38,15 @@ __device__ __forceinline__ uint16_t e4m3x2(float a, float b)
     return r;
 }
 
+// A block's scale from its largest magnitude, and what the values are multiplied with: a product with
+// the reciprocal is within one unit in the last place of the quotient, far inside e4m3's rounding.
+__device__ __forceinline__ float scale_of(float peak, float &inverse)
+{
+    const float s = fmaxf(peak / kMaxE4M3, kMinScale);
+    inverse = 1.f / s;
+    return s;
+}
+
 template <typename io_t>
 struct ForwardParams {
     const io_t *x, *residual, *weight;
@@ -45,6 +56,103 @@ struct ForwardParams {
     float eps;
     int n, D;
 };
+
+// Rows of 16-byte units, held in registers: WPR warps per row, UPL units per lane (unit t + 32 WPR j of a row
+// belongs to thread t, so a block of 128 columns is the same j of 16 (bf16) or 32 (fp32) neighbouring
+// lanes).  Warps walk over the rows; the next row's loads are in flight while a row is worked on, which
+// keeps about 60 KB outstanding per SM.
+template <typename io_t, int WPR, int UPL>
+__global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel(const ForwardParams<io_t> p)
+{
+    constexpr int VEC = 16 / (int)sizeof(io_t), G = 32 * WPR, ROWS = WPR == 1 ? kThreads / 32 : 1;
+    constexpr int PER = kBlock / VEC;  // lanes that share a scale
+    using U = io::Unit<io_t, VEC>;
+    __shared__ float parts[2][WPR];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = WPR == 1 ? lane : (int)threadIdx.x;
+    const int units = p.D / VEC, blocks = (p.D + kBlock - 1) / kBlock;
+    const long long step = (long long)gridDim.x * ROWS;
+    U w[UPL], x[UPL], a[UPL];
+    auto load = [&](long long row) {
+#pragma unroll
+        for (int j = 0; j < UPL; ++j)
+            if (t + G * j < units) {
+                const size_t at = (size_t)row * p.D + (size_t)(t + G * j) * VEC;
+                x[j] = io::load_unit<io_t, VEC>(p.x + at);
+                if (p.residual) a[j] = io::load_unit<io_t, VEC>(p.residual + at);
+            }
+    };
+    long long row = (long long)blockIdx.x * ROWS + (WPR == 1 ? warp : 0);
+    if (row < p.n) load(row);
+#pragma unroll
+    for (int j = 0; j < UPL; ++j)
+        if (t + G * j < units) w[j] = io::load_unit<io_t, VEC>(p.weight + (size_t)(t + G * j) * VEC);
+    for (int turn = 0; row < p.n; row += step, turn ^= 1) {
+        float r[UPL][VEC], ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < UPL; ++j) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) r[j][e] = 0.f;
+            if (t + G * j >= units) continue;
+            x[j].get(r[j]);
+            if (p.residual) {
+                float f[VEC];
+                a[j].get(f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) r[j][e] += f[e];
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) ss = fmaf(r[j][e], r[j][e], ss);
+        }
+        if (row + step < p.n) load(row + step);
+        ss = warp_sum(ss);
+        if constexpr (WPR > 1) {
+            if (lane == 0) parts[turn][warp] = ss;
+            __syncthreads();
+            ss = 0.f;
+#pragma unroll
+            for (int o = 0; o < WPR; ++o) ss += parts[turn][o];
+        }
+        const float q = rsqrtf(ss / (float)p.D + p.eps);
+#pragma unroll
+        for (int j = 0; j < UPL; ++j) {
+            const int u = t + G * j;
+            const bool mine = u < units;
+            const size_t at = (size_t)row * p.D + (size_t)u * VEC;
+            float y[VEC], peak = 0.f;
+            if (mine) w[j].get(y);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                y[e] = mine ? r[j][e] * q * y[e] : 0.f;
+                peak = fmaxf(peak, fabsf(y[e]));
+            }
+            U o;
+            if (mine && p.sum) {
+                o.set(r[j]);
+                io::store_unit<io_t, VEC>(p.sum + at, o);
+            }
+            if (mine && p.y) {
+                o.set(y);
+                io::store_unit<io_t, VEC>(p.y + at, o);
+            }
+            if (p.y8) {
+#pragma unroll
+                for (int o2 = PER / 2; o2 > 0; o2 >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o2));
+                float inverse;
+                const float scale = scale_of(peak, inverse);
+                if (mine) {
+                    if (lane % PER == 0) p.y_scale[(size_t)row * blocks + u / PER] = scale;
+                    uint16_t b[VEC / 2];
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 2) b[e / 2] = e4m3x2(y[e] * inverse, y[e + 1] * inverse);
+                    if constexpr (VEC == 8)
+                        *reinterpret_cast<uint2 *>(p.y8 + at) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+                    else
+                        *reinterpret_cast<uint32_t *>(p.y8 + at) = b[0] | (uint32_t)b[1] << 16;
+                }
+            }
+        }
+    }
+}
 
 // Any width and alignment: a warp per row, one value per lane at a time, two passes over the row (the
 // second one comes from the caches).  Nothing is written before the row has been read to its end, and
@@ -79,12 +187,13 @@ __global__ void __launch_bounds__(kThreads) forward_any_kernel(const ForwardPara
             }
         }
         if (p.y8) {
-            const float scale = fmaxf(warp_max(peak) / kMaxE4M3, kMinScale);
+            float inverse;
+            const float scale = scale_of(warp_max(peak), inverse);
             if (lane == 0) p.y_scale[(size_t)row * blocks + b] = scale;
 #pragma unroll
             for (int i = 0; i < kBlock / 32; ++i) {
                 const int c = b * kBlock + 32 * i + lane;
-                if (c < p.D) p.y8[at + c] = (uint8_t)e4m3x2(y[i] / scale, 0.f);
+                if (c < p.D) p.y8[at + c] = (uint8_t)e4m3x2(y[i] * inverse, 0.f);
             }
         }
     }
@@ -101,7 +210,108 @@ struct BackwardParams {
     int n, D, slabs;
 };
 
-// Per row: q = 1 / rms and mean_j(w dy rh)
+// Rows of 16-byte units in registers, as in forward_kernel: one pass gives dx and this block's part of
+// the weight's gradient, which each thread holds for its own columns over all rows of the block.
+template <typename io_t, int WPR, int UPL>
+__global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) backward_kernel(const BackwardParams<io_t> p)
+{
+    constexpr int VEC = 16 / (int)sizeof(io_t), G = 32 * WPR, ROWS = WPR == 1 ? kThreads / 32 : 1;
+    using U = io::Unit<io_t, VEC>;
+    __shared__ float2 parts[2][WPR];
+    __shared__ float columns[WPR == 1 ? ROWS : 1][WPR == 1 ? G * UPL * VEC : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = WPR == 1 ? lane : (int)threadIdx.x;
+    const int units = p.D / VEC;
+    const long long step = (long long)gridDim.x * ROWS;
+    U w[UPL], x[UPL], a[UPL], b[UPL];
+    float acc[UPL][VEC];
+    auto load = [&](long long row) {
+#pragma unroll
+        for (int j = 0; j < UPL; ++j)
+            if (t + G * j < units) {
+                const size_t at = (size_t)row * p.D + (size_t)(t + G * j) * VEC;
+                x[j] = io::load_unit<io_t, VEC>(p.sum + at);
+                a[j] = io::load_unit<io_t, VEC>(p.dy + at);
+                if (p.dsum) b[j] = io::load_unit<io_t, VEC>(p.dsum + at);
+            }
+    };
+    long long row = (long long)blockIdx.x * ROWS + (WPR == 1 ? warp : 0);
+    if (row < p.n) load(row);
+#pragma unroll
+    for (int j = 0; j < UPL; ++j) {
+        if (t + G * j < units) w[j] = io::load_unit<io_t, VEC>(p.weight + (size_t)(t + G * j) * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+    }
+    for (int turn = 0; row < p.n; row += step, turn ^= 1) {
+        float r[UPL][VEC], dy[UPL][VEC];
+        U ds[UPL];
+        float2 s = make_float2(0.f, 0.f);  // sum r^2, sum w dy r
+#pragma unroll
+        for (int j = 0; j < UPL; ++j) {
+            if (t + G * j >= units) continue;
+            x[j].get(r[j]);
+            a[j].get(dy[j]);
+            ds[j] = b[j];
+            float f[VEC];
+            w[j].get(f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                s.x = fmaf(r[j][e], r[j][e], s.x);
+                s.y = fmaf(f[e] * dy[j][e], r[j][e], s.y);
+            }
+        }
+        if (row + step < p.n) load(row + step);
+        s.x = warp_sum(s.x);
+        s.y = warp_sum(s.y);
+        if constexpr (WPR > 1) {
+            if (lane == 0) parts[turn][warp] = s;
+            __syncthreads();
+            s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int o = 0; o < WPR; ++o) s.x += parts[turn][o].x, s.y += parts[turn][o].y;
+        }
+        const float q = rsqrtf(s.x / (float)p.D + p.eps), mean = s.y * q / (float)p.D;
+#pragma unroll
+        for (int j = 0; j < UPL; ++j) {
+            if (t + G * j >= units) continue;
+            float f[VEC], d[VEC];
+            w[j].get(f);
+            if (p.dsum) ds[j].get(d);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float rh = r[j][e] * q;
+                acc[j][e] = fmaf(dy[j][e], rh, acc[j][e]);
+                const float g = q * (f[e] * dy[j][e] - rh * mean);
+                d[e] = p.dsum ? g + d[e] : g;
+            }
+            U o;
+            o.set(d);
+            io::store_unit<io_t, VEC>(p.dx + (size_t)row * p.D + (size_t)(t + G * j) * VEC, o);
+        }
+    }
+    float *part = p.part + (size_t)blockIdx.x * p.D;
+    if constexpr (WPR == 1) {  // the block's warps add up in order
+#pragma unroll
+        for (int j = 0; j < UPL; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) columns[warp][(lane + 32 * j) * VEC + e] = acc[j][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.D; c += kThreads) {
+            float v = 0.f;
+#pragma unroll
+            for (int o = 0; o < ROWS; ++o) v += columns[o][c];
+            part[c] = v;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < UPL; ++j)
+            if (t + G * j < units)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) part[(size_t)(t + G * j) * VEC + e] = acc[j][e];
+    }
+}
+
+// Any width and alignment, in three steps.  Per row: q = 1 / rms and mean_j(w dy rh)
 template <typename io_t>
 __global__ void __launch_bounds__(kThreads) stats_any_kernel(const BackwardParams<io_t> p)
 {
@@ -158,16 +368,69 @@ __global__ void __launch_bounds__(kThreads) dweight_part_kernel(const BackwardPa
     }
 }
 
-__global__ void __launch_bounds__(kThreads) dweight_kernel(const float *part, float *dweight, int slabs, int D)
+// The slabs' parts added up: 32 columns per block, the slabs split over 32 warps and joined in order
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) dweight_kernel(const float *__restrict__ part, float *dweight, int slabs, int D)
 {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= D) return;
+    __shared__ float sums[kJoinThreads / 32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float acc = 0.f;
-    for (int s = 0; s < slabs; ++s) acc += part[(size_t)s * D + c];
-    dweight[c] = acc;
+    if (c < D) {
+#pragma unroll 4
+        for (int s = warp; s < slabs; s += kJoinThreads / 32) acc += part[(size_t)s * D + c];
+    }
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && c < D) {
+        for (int w = 1; w < kJoinThreads / 32; ++w) acc += sums[w][lane];
+        dweight[c] = acc;
+    }
 }
 
-constexpr int kSlabs = 64;
+constexpr int kSlabs = 320;    // blocks of backward_kernel, at most
+constexpr int kSlabsAny = 64;  // slabs of rows of dweight_part_kernel
+
+// The variant of a width: WPR warps per row and UPL units per lane hold a row of D / VEC units.
+// f(WPR, UPL) is called with the smallest that does; false if none does, or rows are not made of units.
+// WIDEST: the units per lane of the widest variant (the gradient's registers hold two, the norm's four).
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <int WIDEST, typename F>
+bool pick(int D, int vec, F f)
+{
+    if (D % vec != 0) return false;
+    const int units = D / vec;
+    if (units <= 32) f(Int<1>(), Int<1>());
+    else if (units <= 64) f(Int<1>(), Int<2>());
+    else if (units <= 96) f(Int<1>(), Int<3>());
+    else if (units <= 128) f(Int<1>(), Int<4>());
+    else if (units <= 256) f(Int<4>(), Int<2>());
+    else if (units <= 384) f(Int<4>(), Int<3>());
+    else if (units <= 512) f(Int<4>(), Int<4>());
+    else if (units <= 1024) f(Int<16>(), Int<2>());
+    else {
+        if constexpr (WIDEST >= 4) {
+            if (units <= 2048) {
+                f(Int<16>(), Int<4>());
+                return true;
+            }
+        }
+        return false;
+    }
+    return true;
+}
+
+// Blocks of a kernel that walks over the rows: as many as the device holds at a time, no more than rows.
+template <auto kernel>
+unsigned resident_blocks(int threads, int rows_per_block, int n, int sm_count, int most)
+{
+    static const int per_sm = [&] {
+        int b = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, 0) == cudaSuccess && b > 0 ? b : 1;
+    }();
+    const long long all = ((long long)n + rows_per_block - 1) / rows_per_block;
+    return (unsigned)min(all, min((long long)per_sm * sm_count, (long long)most));
+}
 
 template <typename io_t>
 cudaError_t forward(const NormArgs &a, const TokenLaunch &l)
@@ -175,7 +438,13 @@ cudaError_t forward(const NormArgs &a, const TokenLaunch &l)
     const ForwardParams<io_t> p{(const io_t *)a.x, (const io_t *)a.residual, (const io_t *)a.weight, (io_t *)a.sum,
                                 (io_t *)a.y, (uint8_t *)a.y8, a.y_scale, a.eps, a.n, a.D};
     l.timer->begin("norm");
-    forward_any_kernel<io_t><<<(a.n + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, l.timer->stream>>>(p);
+    const bool held = pick<4>(a.D, 16 / (int)sizeof(io_t), [&](auto wpr, auto upl) {
+        constexpr int WPR = decltype(wpr)::value, UPL = decltype(upl)::value, threads = WPR == 1 ? kThreads : 32 * WPR;
+        const unsigned blocks =
+            resident_blocks<forward_kernel<io_t, WPR, UPL>>(threads, WPR == 1 ? kThreads / 32 : 1, a.n, l.sm_count, 1 << 30);
+        forward_kernel<io_t, WPR, UPL><<<blocks, threads, 0, l.timer->stream>>>(p);
+    });
+    if (!held) forward_any_kernel<io_t><<<(a.n + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, l.timer->stream>>>(p);
     l.timer->end();
     return cudaGetLastError();
 }
@@ -183,25 +452,33 @@ cudaError_t forward(const NormArgs &a, const TokenLaunch &l)
 template <typename io_t>
 cudaError_t backward(const NormBackwardArgs &a, const NormWorkspace &w, const TokenLaunch &l)
 {
-    const BackwardParams<io_t> p{(const io_t *)a.sum, (const io_t *)a.weight, (const io_t *)a.dy, (const io_t *)a.dsum,
-                                 (io_t *)a.dx, w.stats, w.part, a.dweight, a.eps, a.n, a.D, kSlabs};
+    BackwardParams<io_t> p{(const io_t *)a.sum, (const io_t *)a.weight, (const io_t *)a.dy, (const io_t *)a.dsum,
+                           (io_t *)a.dx, w.stats, w.part, a.dweight, a.eps, a.n, a.D, 0};
     cudaStream_t s = l.timer->stream;
-    const unsigned rows = (a.n + kThreads / 32 - 1) / (kThreads / 32);
-    if (a.n > 0) {
+    const bool held = a.n > 0 && pick<2>(a.D, 16 / (int)sizeof(io_t), [&](auto wpr, auto upl) {
+        constexpr int WPR = decltype(wpr)::value, UPL = decltype(upl)::value, threads = WPR == 1 ? kThreads : 32 * WPR;
+        const unsigned blocks =
+            resident_blocks<backward_kernel<io_t, WPR, UPL>>(threads, WPR == 1 ? kThreads / 32 : 1, a.n, l.sm_count, kSlabs);
+        p.slabs = (int)blocks;
+        l.timer->begin("norm_backward");
+        backward_kernel<io_t, WPR, UPL><<<blocks, threads, 0, s>>>(p);
+        l.timer->end();
+    });
+    if (!held && a.n > 0) {
+        const unsigned rows = (a.n + kThreads / 32 - 1) / (kThreads / 32);
+        p.slabs = min(kSlabsAny, a.n);
         l.timer->begin("norm_stats");
         stats_any_kernel<io_t><<<rows, kThreads, 0, s>>>(p);
         l.timer->end();
-    }
-    l.timer->begin("norm_dweight_part");
-    dweight_part_kernel<io_t><<<dim3((a.D + 31) / 32, kSlabs), kThreads, 0, s>>>(p);
-    l.timer->end();
-    if (a.n > 0) {
+        l.timer->begin("norm_dweight_part");
+        dweight_part_kernel<io_t><<<dim3((a.D + 31) / 32, p.slabs), kThreads, 0, s>>>(p);
+        l.timer->end();
         l.timer->begin("norm_dx");
         dx_any_kernel<io_t><<<rows, kThreads, 0, s>>>(p);
         l.timer->end();
     }
     l.timer->begin("norm_dweight");
-    dweight_kernel<<<(a.D + kThreads - 1) / kThreads, kThreads, 0, s>>>(w.part, a.dweight, kSlabs, a.D);
+    dweight_kernel<<<(a.D + 31) / 32, kJoinThreads, 0, s>>>(w.part, a.dweight, p.slabs, a.D);
     l.timer->end();
     return cudaGetLastError();
 }
@@ -217,7 +494,7 @@ cudaError_t norm_forward(prism_dtype io, const NormArgs &a, const TokenLaunch &l
 
 size_t norm_workspace_bytes(int max_rows, int D)
 {
-    return norm::up256((size_t)max_rows * 8) + norm::up256((size_t)norm::kSlabs * D * 4);
+    return norm::up256((size_t)max_rows * 8) + norm::up256((size_t)min(norm::kSlabs, max_rows) * D * 4);
 }
 
 void norm_carve(int max_rows, int D, void *base, NormWorkspace *w)
