@@ -17,6 +17,7 @@
 // most frequent ones of a text do, is spread over eight warps there).
 #include "io_util.h"
 #include "prism_tokens.h"
+#include "tc_ptx.h"
 
 namespace prism {
 namespace embed {
@@ -28,7 +29,7 @@ constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32, kSteps = 8;
 constexpr int kSub = kSortThreads * kSteps;  // keys that a block ranks at a time
 
 constexpr int kThreads = 256;
-constexpr int kTile = 16;  // sorted tokens per warp, at least (tile_of)
+constexpr int kTile = 32;  // sorted tokens per warp, at least (tile_of)
 
 // ---------------------------------------------------------------------------------------------
 // lookup: a warp takes 32 UPL units of one row
@@ -108,11 +109,43 @@ __device__ __forceinline__ void scan_bins(int &a, int &b, int *warp_sums)
 }
 static_assert(kBins == 2 * kSortThreads, "scan_bins");
 
+// Counts per warp and digit to each warp's first place among its digit's keys; sum: the digits' counts
+// (thread t: digits 2 t and 2 t + 1).
+__device__ __forceinline__ void prefix_over_warps(uint16_t (&count)[kSortWarps][kBins], int (&sum)[2])
+{
+    sum[0] = sum[1] = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int c = count[w][2 * threadIdx.x + e];
+            count[w][2 * threadIdx.x + e] = (uint16_t)sum[e];
+            sum[e] += c;
+        }
+}
+
+// The sort leaves most SMs and all of HBM idle, so the blocks behind a sort kernel's own clear a share of
+// the table meanwhile (rows that have tokens are written again by the sums, which run after the sort).
+struct Fill {
+    float *dtable;
+    size_t from, to;  // floats, multiples of 4 except the table's end
+};
+__device__ __forceinline__ void fill_share(const Fill &f, int block, int blocks)
+{
+    float4 *d = reinterpret_cast<float4 *>(f.dtable);
+    const size_t end = f.to / 4, step = (size_t)blocks * kSortThreads;
+    for (size_t i = f.from / 4 + (size_t)block * kSortThreads + threadIdx.x; i < end; i += step)
+        d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (block == 0 && threadIdx.x < f.to % 4) f.dtable[end * 4 + threadIdx.x] = 0.f;
+}
+
 // Digit counts of each block's chunk of the tokens, for the first pass; clears the later passes' counts.
 __global__ void __launch_bounds__(kSortThreads) count_kernel(const long long *__restrict__ ids, int n, int V, int chunk,
-                                                            int mask, int passes, int *hist, int *status)
+                                                            int mask, int passes, int nb, int *hist, int *status, const Fill f)
 {
     __shared__ int bins[kBins];
+    tc::allow_dependent_launch();
+    if ((int)blockIdx.x >= nb) return fill_share(f, blockIdx.x - nb, gridDim.x - nb);
     for (int d = threadIdx.x; d < kBins; d += kSortThreads) bins[d] = 0;
     __syncthreads();
     const int i1 = min((long long)n, ((long long)blockIdx.x + 1) * chunk);
@@ -132,28 +165,37 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const long long *__
 
 // One pass: block b places the keys of its chunk; hist holds the counts per block and digit.  The
 // next pass's counts are taken here (hist_next): where a key lands decides which block will read it.
+struct Pass {
+    const long long *ids;       // the first pass reads these ...
+    const int *key_in, *pos_in;  // ... the later ones these
+    int *key_out, *pos_out;
+    const int *hist;
+    int *hist_next;
+    int n, V, chunk, nb, shift, mask, next_shift;
+};
+
 template <bool FIRST>
-__global__ void __launch_bounds__(kSortThreads) scatter_kernel(const long long *__restrict__ ids, const int *__restrict__ key_in,
-                                                              const int *__restrict__ pos_in, int *__restrict__ key_out,
-                                                              int *__restrict__ pos_out, int n, int V, int chunk, int shift,
-                                                              int mask, int next_shift, int next_mask,
-                                                              const int *__restrict__ hist, int *hist_next)
+__global__ void __launch_bounds__(kSortThreads) scatter_kernel(const Pass p, const Fill f)
 {
     __shared__ uint16_t count[kSortWarps][kBins];
     __shared__ int base[kBins];
     __shared__ int warp_sums[kSortWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x, nb = gridDim.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+    tc::allow_dependent_launch();
+    if (b >= p.nb) return fill_share(f, b - p.nb, gridDim.x - p.nb);
+    tc::grid_dependency_wait();
     int total[2] = {0, 0}, before[2] = {0, 0};
-    for (int o = 0; o < nb; ++o) {
-        const int2 h = *reinterpret_cast<const int2 *>(hist + (size_t)o * kBins + 2 * tid);
+#pragma unroll 8
+    for (int o = 0; o < p.nb; ++o) {
+        const int2 h = *reinterpret_cast<const int2 *>(p.hist + (size_t)o * kBins + 2 * tid);
         total[0] += h.x, total[1] += h.y;
         if (o < b) before[0] += h.x, before[1] += h.y;
     }
     scan_bins(total[0], total[1], warp_sums);
     base[2 * tid] = total[0] + before[0];
     base[2 * tid + 1] = total[1] + before[1];
-    const int i1 = min((long long)n, ((long long)b + 1) * chunk);
-    for (int i0 = b * chunk; i0 < i1; i0 += kSub) {
+    const int i1 = min((long long)p.n, ((long long)b + 1) * p.chunk);
+    for (int i0 = b * p.chunk; i0 < i1; i0 += kSub) {
         for (int d = lane; d < kBins; d += 32) count[warp][d] = 0;
         __syncwarp();
         int key[kSteps], pos[kSteps], rank[kSteps];
@@ -163,36 +205,98 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const long long *
             key[s] = 0x7fffffff;  // behind every key of its digit, and not stored
             pos[s] = i;
             if (i < i1) {
-                key[s] = FIRST ? key_of(ids[i], V) : key_in[i];
-                if (!FIRST) pos[s] = pos_in[i];
+                key[s] = FIRST ? key_of(p.ids[i], p.V) : p.key_in[i];
+                if (!FIRST) pos[s] = p.pos_in[i];
             }
         }
-        rank_in_warp<kSteps>(key, shift, mask, count[warp], rank);
+        rank_in_warp<kSteps>(key, p.shift, p.mask, count[warp], rank);
         __syncthreads();
-        int sum[2] = {0, 0};  // of this tile, for the next one's base
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int c = count[w][2 * tid + e];
-                count[w][2 * tid + e] = (uint16_t)sum[e];
-                sum[e] += c;
-            }
+        int sum[2];  // of this tile, for the next one's base
+        prefix_over_warps(count, sum);
         __syncthreads();
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int i = i0 + warp * 32 * kSteps + 32 * s + lane;
-            if (i >= i1) continue;
-            const int d = (key[s] >> shift) & mask;
+            const bool live = i < i1;
+            const int d = (key[s] >> p.shift) & p.mask;
             const int to = base[d] + count[warp][d] + rank[s];
-            key_out[to] = key[s];
-            pos_out[to] = pos[s];
-            if (hist_next) atomicAdd(&hist_next[(size_t)(to / chunk) * kBins + ((key[s] >> next_shift) & next_mask)], 1);
+            if (live) {
+                p.key_out[to] = key[s];
+                p.pos_out[to] = pos[s];
+            }
+            if (p.hist_next) {  // one addition per warp and counter: frequent tokens share theirs
+                const int at = live ? to / p.chunk * kBins + ((key[s] >> p.next_shift) & p.mask) : -1;
+                const uint32_t peers = __match_any_sync(0xffffffffu, at);
+                if (live && (peers & ((1u << lane) - 1u)) == 0) atomicAdd(&p.hist_next[at], __popc(peers));
+            }
         }
         __syncthreads();
         base[2 * tid] += sum[0];
         base[2 * tid + 1] += sum[1];
         __syncthreads();
+    }
+}
+
+// All passes in one block, the keys in registers and shared memory: for at most kSub tokens.
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const long long *__restrict__ ids, int n, int V, int width, int passes,
+                                                           int *__restrict__ key_out, int *__restrict__ pos_out, int *status,
+                                                           const Fill f)
+{
+    __shared__ uint16_t count[kSortWarps][kBins];
+    __shared__ int base[kBins];
+    __shared__ int warp_sums[kSortWarps];
+    __shared__ int keys[kSub];
+    __shared__ uint16_t places[kSub];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, mask = (1 << width) - 1;
+    tc::allow_dependent_launch();
+    if (blockIdx.x > 0) return fill_share(f, blockIdx.x - 1, gridDim.x - 1);
+    int key[kSteps], pos[kSteps], rank[kSteps];
+    bool bad = false;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int i = warp * 32 * kSteps + 32 * s + lane;
+        key[s] = 0x7fffffff;
+        pos[s] = i;
+        if (i < n) {
+            const long long id = ids[i];
+            bad |= id >= V;
+            key[s] = key_of(id, V);
+        }
+    }
+    if (bad) atomicCAS(status, 0, kDevBounds);
+    for (int p = 0; p < passes; ++p) {
+        for (int d = lane; d < kBins; d += 32) count[warp][d] = 0;
+        __syncwarp();
+        rank_in_warp<kSteps>(key, p * width, mask, count[warp], rank);
+        __syncthreads();
+        int sum[2];
+        prefix_over_warps(count, sum);
+        scan_bins(sum[0], sum[1], warp_sums);
+        base[2 * tid] = sum[0];
+        base[2 * tid + 1] = sum[1];
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int d = (key[s] >> (p * width)) & mask, to = base[d] + count[warp][d] + rank[s];
+            keys[to] = key[s];
+            places[to] = (uint16_t)pos[s];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int i = warp * 32 * kSteps + 32 * s + lane;
+            key[s] = keys[i];
+            pos[s] = places[i];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int i = warp * 32 * kSteps + 32 * s + lane;
+        if (i < n) {
+            key_out[i] = key[s];
+            pos_out[i] = pos[s];
+        }
     }
 }
 
@@ -208,14 +312,17 @@ struct SumParams {
 template <typename io_t, int VEC, int UPL>
 __global__ void __launch_bounds__(kThreads) sum_kernel(const io_t *__restrict__ dout, const SumParams p)
 {
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = 8 / UPL;
     const int lane = threadIdx.x & 31;
     const int tile = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    tc::allow_dependent_launch();
+    tc::grid_dependency_wait();
     if (tile >= p.tiles) return;
     const int s0 = tile * p.tile, s1 = min(p.n, s0 + p.tile), units = p.D / VEC;
     const int u0 = blockIdx.y * 32 * UPL + lane;
-    const int first = p.key[s0], last = p.key[s1 - 1];
-    const bool from_before = s0 > 0 && p.key[s0 - 1] == first, goes_on = s1 < p.n && p.key[s1] == last;
+    const int before = s0 > 0 ? p.key[s0 - 1] : -1, behind = s1 < p.n ? p.key[s1] : -1;
+    const int first = p.key[s0];
+    const bool from_before = before == first;
     float acc[UPL][VEC];
 #pragma unroll
     for (int j = 0; j < UPL; ++j)
@@ -226,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const io_t *__restrict__ 
     auto flush = [&](bool in_last) {
         if (cur != p.V) {
             float *to;
-            const bool partial = (in_first && from_before) || (in_last && goes_on);
+            const bool partial = (in_first && from_before) || (in_last && behind == cur);
             if (partial)
                 to = p.part + ((size_t)tile * 2 + (in_first && from_before ? 0 : 1)) * p.Dp;
             else
@@ -261,35 +368,40 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const io_t *__restrict__ 
             for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
         in_first = false;
     };
-    for (int s = s0; s < s1; s += AHEAD) {
-        io::Unit<io_t, VEC> x[AHEAD][UPL];
-        int key[AHEAD];
+    for (int c0 = s0; c0 < s1; c0 += 32) {  // 32 tokens: their keys and positions in one load each
+        const int key32 = c0 + lane < s1 ? p.key[c0 + lane] : p.V, pos32 = c0 + lane < s1 ? p.pos[c0 + lane] : 0;
+        const int here = min(32, s1 - c0);
+        for (int s = 0; s < here; s += AHEAD) {
+            io::Unit<io_t, VEC> x[AHEAD][UPL];
+            int key[AHEAD];
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            key[a] = s + a < s1 ? p.key[s + a] : p.V;
-            if (key[a] != p.V) {
-                const io_t *src = dout + (size_t)p.pos[s + a] * p.D;
+            for (int a = 0; a < AHEAD; ++a) {
+                key[a] = __shfl_sync(0xffffffffu, key32, s + a);  // AHEAD divides 32; p.V behind the tile's end
+                const int pos = __shfl_sync(0xffffffffu, pos32, s + a);
+                if (key[a] != p.V) {
+                    const io_t *src = dout + (size_t)pos * p.D;
+#pragma unroll
+                    for (int j = 0; j < UPL; ++j)
+                        if (u0 + 32 * j < units) x[a][j] = io::load_unit<io_t, VEC>(src + (size_t)(u0 + 32 * j) * VEC);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) {
+                if (s + a >= here) break;
+                if (key[a] != cur) {
+                    flush(false);
+                    cur = key[a];
+                }
+                if (cur == p.V) continue;
 #pragma unroll
                 for (int j = 0; j < UPL; ++j)
-                    if (u0 + 32 * j < units) x[a][j] = io::load_unit<io_t, VEC>(src + (size_t)(u0 + 32 * j) * VEC);
+                    if (u0 + 32 * j < units) {
+                        float f[VEC];
+                        x[a][j].get(f);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) acc[j][e] += f[e];
+                    }
             }
-        }
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            if (s + a >= s1) break;
-            if (key[a] != cur) {
-                flush(false);
-                cur = key[a];
-            }
-            if (cur == p.V) continue;
-#pragma unroll
-            for (int j = 0; j < UPL; ++j)
-                if (u0 + 32 * j < units) {
-                    float f[VEC];
-                    x[a][j].get(f);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[j][e] += f[e];
-                }
         }
     }
     flush(true);
@@ -301,20 +413,31 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const io_t *__restrict__ 
 __global__ void __launch_bounds__(kThreads) join_kernel(const SumParams p)
 {
     __shared__ float4 sums[kThreads / 32][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ int starts[kThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int col = blockIdx.y * 128 + lane * 4;
-    for (int t = 0; t < 8; ++t) {
-        const int a = blockIdx.x * 8 + t;
-        if (a >= p.tiles - 1) break;
-        const int e = (a + 1) * p.tile;  // the first token of the next tile (a is not the last tile)
-        const int key = p.key[e];
-        if (key == p.V || p.key[e - 1] != key) continue;               // no run crosses this edge
-        if (a > 0 && p.key[e - p.tile - 1] == key) continue;           // ... or it started before tile a
-        int b0 = a + 1, b1 = p.tiles;                                  // the first tile that does not begin with the key
-        while (b0 < b1) {
-            const int m = (b0 + b1) >> 1;
-            if (p.key[m * p.tile] == key) b0 = m + 1;
-            else b1 = m;
+    tc::grid_dependency_wait();
+    if (lane == 0) {  // warp w looks at the edge behind the block's tile w
+        const int a = blockIdx.x * (kThreads / 32) + warp;
+        int key = -1;
+        if (a < p.tiles - 1) {
+            const int e = (a + 1) * p.tile;  // the first token of the next tile
+            const int last = p.key[e - 1], next = p.key[e], earlier = a > 0 ? p.key[e - p.tile - 1] : -1;
+            // a run crosses this edge, and did not start before tile a
+            if (next != p.V && last == next && earlier != next) key = next;
+        }
+        starts[warp] = key;
+    }
+    __syncthreads();
+    for (int t = 0; t < kThreads / 32; ++t) {
+        const int a = blockIdx.x * (kThreads / 32) + t, key = starts[t];
+        if (key < 0) continue;
+        int b0 = a + 1;  // the first tile that does not begin with the key: keys are sorted, so count those that do
+        for (;;) {
+            const int i = b0 + tid;
+            const int same = __syncthreads_count(i < p.tiles && p.key[(size_t)i * p.tile] == key);
+            b0 += same;
+            if (same < kThreads) break;
         }
         const int parts = b0 - a;  // part 0: the last one of tile a; part i: the first one of tile a + i
         const int per = (parts + kThreads / 32 - 1) / (kThreads / 32);
@@ -345,8 +468,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumParams p)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Tokens per tile: 16, so that 16K tokens make 1024 warps; longer ones for more tokens than 8192
-// tiles hold, which bounds the workspace.
+// Tokens per tile: 32, the lanes of a warp; longer ones for more tokens than 8192 tiles hold, which
+// bounds the workspace.
 constexpr int kTilesMax = 8193;
 int tile_of(int n)
 {
@@ -355,18 +478,31 @@ int tile_of(int n)
     return t;
 }
 
-template <typename io_t, int VEC>
-cudaError_t launch_sum(const io_t *dout, const SumParams &p, cudaStream_t s)
+// A launch that may begin while the kernel before it in the stream ends (it waits for that kernel's
+// results itself); the first kernel of a call is launched plainly.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
 {
-    const int units = p.D / VEC;
-    const unsigned gx = (p.tiles + kThreads / 32 - 1) / (kThreads / 32);
-    if (units > 64)
-        sum_kernel<io_t, VEC, 4><<<dim3(gx, (units + 127) / 128), kThreads, 0, s>>>(dout, p);
-    else if (units > 32)
-        sum_kernel<io_t, VEC, 2><<<dim3(gx, 1), kThreads, 0, s>>>(dout, p);
-    else
-        sum_kernel<io_t, VEC, 1><<<dim3(gx, 1), kThreads, 0, s>>>(dout, p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Columns are split over warps (32 units each, 64 for the narrow units of unaligned rows): tiles are few
+// when tokens are, and a warp with one unit per lane keeps eight rows in flight.
+template <typename io_t, int VEC>
+cudaError_t launch_sum(const void *dout, const SumParams &p, cudaStream_t s)
+{
+    constexpr int UPL = VEC > 1 ? 1 : 2;
+    const unsigned gx = (p.tiles + kThreads / 32 - 1) / (kThreads / 32), gy = (p.D / VEC + 32 * UPL - 1) / (32 * UPL);
+    return launch_behind(sum_kernel<io_t, VEC, UPL>, dim3(gx, gy), kThreads, s, (const io_t *)dout, p);
 }
 
 template <typename io_t, int VEC>
@@ -434,34 +570,44 @@ cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const Emb
 {
     cudaStream_t s = l.timer->stream;
     cudaError_t e;
-    if (!a.accumulate && (e = cudaMemsetAsync(a.dtable, 0, (size_t)a.V * a.D * 4, s)) != cudaSuccess) return e;
-    if (a.n == 0) return cudaSuccess;
     int bits = 1;
     while ((1LL << bits) <= a.V) ++bits;  // keys 0 .. V
     const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes, mask = (1 << width) - 1;
-    // at most kBlocksMax blocks, of whole tiles of kSub keys
-    const int chunk = (int)((((long long)a.n + kBlocksMax - 1) / kBlocksMax + kSub - 1) / kSub * kSub);
-    const int nb = (a.n + chunk - 1) / chunk;
-    auto hist = [&](int pass) { return w.hist + (size_t)pass * kBlocksMax * kBins; };
-    l.timer->begin("embed_count");
-    count_kernel<<<nb, kSortThreads, 0, s>>>(a.ids, a.n, a.V, chunk, mask, passes, w.hist, l.d_status);
-    l.timer->end();
-    for (int p = 0; p < passes; ++p) {
-        const int to = p & 1, from = to ^ 1;
-        l.timer->begin("embed_scatter");
-        int *next = p + 1 < passes ? hist(p + 1) : nullptr;
-        if (p == 0)
-            scatter_kernel<true><<<nb, kSortThreads, 0, s>>>(a.ids, nullptr, nullptr, w.key[to], w.pos[to], a.n, a.V, chunk, 0,
-                                                             mask, width, mask, hist(0), next);
-        else
-            scatter_kernel<false><<<nb, kSortThreads, 0, s>>>(nullptr, w.key[from], w.pos[from], w.key[to], w.pos[to], a.n, a.V,
-                                                              chunk, p * width, mask, (p + 1) * width, mask, hist(p), next);
+    // the table is cleared in equal shares beside the sort's kernels
+    const int kernels = a.n <= kSub ? 1 : passes + 1, fill_blocks = a.accumulate ? 0 : 4 * l.sm_count;
+    const size_t floats = (size_t)a.V * a.D;
+    auto share = [&](int i) {
+        const size_t quads = floats / 4;
+        return Fill{a.dtable, quads * i / kernels * 4, i == kernels - 1 ? floats : quads * (i + 1) / kernels * 4};
+    };
+    int result = 0;  // which of the two buffers holds the sorted tokens
+    if (a.n <= kSub) {
+        l.timer->begin("embed_sort");
+        sort_kernel<<<1 + fill_blocks, kSortThreads, 0, s>>>(a.ids, a.n, a.V, width, passes, w.key[0], w.pos[0], l.d_status, share(0));
         l.timer->end();
+    } else {
+        // at most kBlocksMax blocks, of whole tiles of kSub keys
+        const int chunk = (int)((((long long)a.n + kBlocksMax - 1) / kBlocksMax + kSub - 1) / kSub * kSub);
+        const int nb = (a.n + chunk - 1) / chunk;
+        auto hist = [&](int pass) { return w.hist + (size_t)pass * kBlocksMax * kBins; };
+        l.timer->begin("embed_count");
+        count_kernel<<<nb + fill_blocks, kSortThreads, 0, s>>>(a.ids, a.n, a.V, chunk, mask, passes, nb, w.hist, l.d_status, share(0));
+        l.timer->end();
+        for (int p = 0; p < passes; ++p) {
+            const int to = p & 1, from = to ^ 1;
+            const Pass ps{a.ids, w.key[from], w.pos[from], w.key[to], w.pos[to], hist(p), p + 1 < passes ? hist(p + 1) : nullptr,
+                          a.n, a.V, chunk, nb, p * width, mask, (p + 1) * width};
+            l.timer->begin("embed_scatter");
+            e = launch_behind(p == 0 ? scatter_kernel<true> : scatter_kernel<false>, dim3(nb + fill_blocks), kSortThreads, s, ps, share(p + 1));
+            l.timer->end();
+            if (e != cudaSuccess) return e;
+            result = to;
+        }
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || a.n == 0) return e;
     SumParams sp;
-    sp.key = w.key[(passes - 1) & 1];
-    sp.pos = w.pos[(passes - 1) & 1];
+    sp.key = w.key[result];
+    sp.pos = w.pos[result];
     sp.dtable = a.dtable;
     sp.part = w.part;
     sp.scale = a.scale;
@@ -474,16 +620,15 @@ cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const Emb
     sp.accumulate = a.accumulate;
     l.timer->begin("embed_sum");
     if (io == PRISM_BF16)
-        e = a.D % 8 == 0 ? launch_sum<__nv_bfloat16, 8>((const __nv_bfloat16 *)a.dout, sp, s)
-                         : launch_sum<__nv_bfloat16, 1>((const __nv_bfloat16 *)a.dout, sp, s);
+        e = a.D % 8 == 0 ? launch_sum<__nv_bfloat16, 8>(a.dout, sp, s) : launch_sum<__nv_bfloat16, 1>(a.dout, sp, s);
     else
-        e = a.D % 4 == 0 ? launch_sum<float, 4>((const float *)a.dout, sp, s) : launch_sum<float, 1>((const float *)a.dout, sp, s);
+        e = a.D % 4 == 0 ? launch_sum<float, 4>(a.dout, sp, s) : launch_sum<float, 1>(a.dout, sp, s);
     l.timer->end();
     if (e != cudaSuccess || sp.tiles < 2) return e;
     l.timer->begin("embed_join");
-    join_kernel<<<dim3((sp.tiles + 7) / 8, (a.D + 127) / 128), kThreads, 0, s>>>(sp);
+    e = launch_behind(join_kernel, dim3((sp.tiles + kThreads / 32 - 1) / (kThreads / 32), (a.D + 127) / 128), kThreads, s, sp);
     l.timer->end();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace prism
