@@ -15,6 +15,8 @@
 // registers, writing a sum whenever the id changes.  Runs that cross a tile's edge leave their part
 // in the workspace; a last kernel adds those parts in order (a token that fills many tiles, as the
 // most frequent ones of a text do, is spread over eight warps there).
+#include <type_traits>
+
 #include "io_util.h"
 #include "prism_tokens.h"
 #include "tc_ptx.h"
@@ -29,6 +31,10 @@ constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32, kSteps = 8;
 constexpr int kSub = kSortThreads * kSteps;  // keys that a block ranks at a time
 
 constexpr int kThreads = 256;
+// Bytes of the table that one sort kernel clears: what the L2 takes while the sort runs.  Measured for 16384 x
+// 768 of 50021 (bf16) and 32768 x 256 of 200003 (fp32): 16 MB 51 and 73 us, 48 MB 48 and 65 us, 80 MB 48 and
+// 57 us, 112 MB 52 and 53 us, all of it 53 and 56 us.
+constexpr long long kBesideSort = 96 << 20;
 constexpr int kTile = 32;  // sorted tokens per warp, at least (tile_of)
 
 // ---------------------------------------------------------------------------------------------
@@ -71,14 +77,28 @@ __device__ __forceinline__ int key_of(long long id, int V) { return id >= 0 && i
 
 // Ranks of a tile's keys: warp w holds keys w 32 STEPS + 32 s + lane.  count[w][d] is the number of
 // the warp's keys with digit d so far; rank[s] the number of them before this lane's key.
-template <int STEPS>
-__device__ __forceinline__ void rank_in_warp(const int (&key)[STEPS], int shift, int mask, uint16_t *count, int (&rank)[STEPS])
+// The lanes that share a digit are found with one vote per bit: match_any took about 360 cycles a step
+// here (it goes through the distinct values), the votes take a tenth of that.
+__device__ __forceinline__ uint32_t peers_of(int d, int width)
 {
+    uint32_t peers = 0xffffffffu;
+    for (int b = 0; b < width; ++b) {
+        const bool bit = (d >> b) & 1;
+        const uint32_t set = __ballot_sync(0xffffffffu, bit);
+        peers &= bit ? set : ~set;
+    }
+    return peers;
+}
+
+template <int STEPS>
+__device__ __forceinline__ void rank_in_warp(const int (&key)[STEPS], int shift, int width, uint16_t *count, int (&rank)[STEPS])
+{
+    const int mask = (1 << width) - 1;
     const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
         const int d = (key[s] >> shift) & mask;
-        const uint32_t peers = __match_any_sync(0xffffffffu, d);
+        const uint32_t peers = peers_of(d, width);
         const int before = count[d];
         rank[s] = before + __popc(peers & below);
         __syncwarp();
@@ -126,6 +146,7 @@ __device__ __forceinline__ void prefix_over_warps(uint16_t (&count)[kSortWarps][
 
 // The sort leaves most SMs and all of HBM idle, so the blocks behind a sort kernel's own clear a share of
 // the table meanwhile (rows that have tokens are written again by the sums, which run after the sort).
+// What the sort's few microseconds cannot hide is cleared beside the sums (clear_absent).
 struct Fill {
     float *dtable;
     size_t from, to;  // floats, multiples of 4 except the table's end
@@ -133,21 +154,23 @@ struct Fill {
 __device__ __forceinline__ void fill_share(const Fill &f, int block, int blocks)
 {
     float4 *d = reinterpret_cast<float4 *>(f.dtable);
-    const size_t end = f.to / 4, step = (size_t)blocks * kSortThreads;
-    for (size_t i = f.from / 4 + (size_t)block * kSortThreads + threadIdx.x; i < end; i += step)
+    const size_t end = f.to / 4, step = (size_t)blocks * blockDim.x;
+    for (size_t i = f.from / 4 + (size_t)block * blockDim.x + threadIdx.x; i < end; i += step)
         d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (block == 0 && threadIdx.x < f.to % 4) f.dtable[end * 4 + threadIdx.x] = 0.f;
 }
 
 // Digit counts of each block's chunk of the tokens, for the first pass; clears the later passes' counts.
 __global__ void __launch_bounds__(kSortThreads) count_kernel(const long long *__restrict__ ids, int n, int V, int chunk,
-                                                            int mask, int passes, int nb, int *hist, int *status, const Fill f)
+                                                            int mask, int passes, int nb, int *hist, uint32_t *present, int *status,
+                                                            const Fill f)
 {
     __shared__ int bins[kBins];
     tc::allow_dependent_launch();
     if ((int)blockIdx.x >= nb) return fill_share(f, blockIdx.x - nb, gridDim.x - nb);
     for (int d = threadIdx.x; d < kBins; d += kSortThreads) bins[d] = 0;
     __syncthreads();
+    for (int i = blockIdx.x * kSortThreads + threadIdx.x; i <= V / 32; i += nb * kSortThreads) present[i] = 0;
     const int i1 = min((long long)n, ((long long)blockIdx.x + 1) * chunk);
     bool bad = false;
     for (int i = blockIdx.x * chunk + threadIdx.x; i < i1; i += kSortThreads) {
@@ -171,7 +194,8 @@ struct Pass {
     int *key_out, *pos_out;
     const int *hist;
     int *hist_next;
-    int n, V, chunk, nb, shift, mask, next_shift;
+    uint32_t *present;  // set by the first pass
+    int n, V, chunk, nb, shift, width, mask, next_shift;
 };
 
 template <bool FIRST>
@@ -202,14 +226,14 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const Pass p, con
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int i = i0 + warp * 32 * kSteps + 32 * s + lane;
-            key[s] = 0x7fffffff;  // behind every key of its digit, and not stored
+            key[s] = -1;  // no token: the last digit in every pass, behind that digit's keys; not stored
             pos[s] = i;
             if (i < i1) {
                 key[s] = FIRST ? key_of(p.ids[i], p.V) : p.key_in[i];
                 if (!FIRST) pos[s] = p.pos_in[i];
             }
         }
-        rank_in_warp<kSteps>(key, p.shift, p.mask, count[warp], rank);
+        rank_in_warp<kSteps>(key, p.shift, p.width, count[warp], rank);
         __syncthreads();
         int sum[2];  // of this tile, for the next one's base
         prefix_over_warps(count, sum);
@@ -223,6 +247,8 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const Pass p, con
             if (live) {
                 p.key_out[to] = key[s];
                 p.pos_out[to] = pos[s];
+                const uint32_t bit = 1u << (key[s] & 31);  // frequent ids find it set
+                if (FIRST && !(*(volatile uint32_t *)&p.present[key[s] >> 5] & bit)) atomicOr(&p.present[key[s] >> 5], bit);
             }
             if (p.hist_next) {  // one addition per warp and counter: frequent tokens share theirs
                 const int at = live ? to / p.chunk * kBins + ((key[s] >> p.next_shift) & p.mask) : -1;
@@ -237,68 +263,138 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(const Pass p, con
     }
 }
 
-// All passes in one block, the keys in registers and shared memory: for at most kSub tokens.
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const long long *__restrict__ ids, int n, int V, int width, int passes,
-                                                           int *__restrict__ key_out, int *__restrict__ pos_out, int *status,
-                                                           const Fill f)
+// All passes in one cluster of CS CTAs (one CTA for few tokens), the keys in registers and in shared
+// memory: CTA c holds the sorted places [c per, (c + 1) per) of a pass, reads the other CTAs' digit
+// counts and writes each key straight to the shared memory of the CTA that holds its place.  A pass
+// costs two cluster barriers instead of two launches.  At most CS kClusterThreads STEPS tokens.
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kCluster = 8, kClusterSteps = 8;
+
+struct ClusterShared {
+    uint16_t count[kClusterWarps][kBins];
+    int total[kBins];  // this CTA's keys by digit; read by the others
+    int base[kBins];
+    int warp_sums[16];
+    int2 sorted[1];    // [STEPS kClusterThreads] key and position
+};
+
+template <int CS>
+__device__ __forceinline__ void cluster_sync()
 {
-    __shared__ uint16_t count[kSortWarps][kBins];
-    __shared__ int base[kBins];
-    __shared__ int warp_sums[kSortWarps];
-    __shared__ int keys[kSub];
-    __shared__ uint16_t places[kSub];
+    if constexpr (CS > 1)
+        asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+    else
+        __syncthreads();
+}
+
+template <int CS, int STEPS>
+__global__ void __launch_bounds__(kClusterThreads) cluster_sort_kernel(const long long *__restrict__ ids, int n, int per, int V,
+                                                                      int width, int passes, int *__restrict__ key_out,
+                                                                      int *__restrict__ pos_out, uint32_t *present, int *status,
+                                                                      const Fill f)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    ClusterShared &sh = *reinterpret_cast<ClusterShared *>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, mask = (1 << width) - 1;
     tc::allow_dependent_launch();
-    if (blockIdx.x > 0) return fill_share(f, blockIdx.x - 1, gridDim.x - 1);
-    int key[kSteps], pos[kSteps], rank[kSteps];
+    if (blockIdx.x >= CS) return fill_share(f, blockIdx.x - CS, gridDim.x - CS);
+    const int rank = blockIdx.x, i0 = rank * per, mine = max(0, min(n - i0, per));
+    int key[STEPS], pos[STEPS], place[STEPS];
     bool bad = false;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int i = warp * 32 * kSteps + 32 * s + lane;
-        key[s] = 0x7fffffff;
-        pos[s] = i;
-        if (i < n) {
-            const long long id = ids[i];
+    for (int s = 0; s < STEPS; ++s) {
+        const int i = warp * 32 * STEPS + 32 * s + lane;
+        key[s] = -1;  // no token: the last digit in every pass, behind that digit's keys; not stored
+        pos[s] = i0 + i;
+        if (i < mine) {
+            const long long id = ids[i0 + i];
             bad |= id >= V;
             key[s] = key_of(id, V);
         }
     }
     if (bad) atomicCAS(status, 0, kDevBounds);
+    for (int i = rank * kClusterThreads + tid; i <= V / 32; i += CS * kClusterThreads) present[i] = 0;
     for (int p = 0; p < passes; ++p) {
-        for (int d = lane; d < kBins; d += 32) count[warp][d] = 0;
+        for (int d = lane; d < kBins; d += 32) sh.count[warp][d] = 0;
         __syncwarp();
-        rank_in_warp<kSteps>(key, p * width, mask, count[warp], rank);
+        rank_in_warp<STEPS>(key, p * width, width, sh.count[warp], place);
         __syncthreads();
-        int sum[2];
-        prefix_over_warps(count, sum);
-        scan_bins(sum[0], sum[1], warp_sums);
-        base[2 * tid] = sum[0];
-        base[2 * tid + 1] = sum[1];
-        __syncthreads();
+        if (tid < kBins) {  // to each warp's first place among its digit's keys; the padding has the last digit
+            int sum = 0;
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const int c = sh.count[w][tid];
+                sh.count[w][tid] = (uint16_t)sum;
+                sum += c;
+            }
+            sh.total[tid] = sum - (tid == mask ? STEPS * kClusterThreads - mine : 0);
+        }
+        cluster_sync<CS>();
+        int all = 0, before = 0;
+        if (tid < kBins) {
+            if constexpr (CS > 1) {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int d = (key[s] >> (p * width)) & mask, to = base[d] + count[warp][d] + rank[s];
-            keys[to] = key[s];
-            places[to] = (uint16_t)pos[s];
+                for (int c = 0; c < CS; ++c) {
+                    uint32_t a;
+                    int v;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(&sh.total[tid])), "r"(c));
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+                    all += v;
+                    if (c < rank) before += v;
+                }
+            } else {
+                all = sh.total[tid];
+            }
+            int run = all;  // exclusive sum over the digits
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += x;
+            }
+            if (lane == 31) sh.warp_sums[warp] = run;
+            all = run - all;
+        }
+        __syncthreads();
+        if (tid < kBins) {
+            for (int w = 0; w < warp; ++w) all += sh.warp_sums[w];
+            sh.base[tid] = all + before;
         }
         __syncthreads();
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int i = warp * 32 * kSteps + 32 * s + lane;
-            key[s] = keys[i];
-            pos[s] = places[i];
+        for (int s = 0; s < STEPS; ++s) {
+            const int i = warp * 32 * STEPS + 32 * s + lane;
+            if (i >= mine) continue;
+            const int d = (key[s] >> (p * width)) & mask, to = sh.base[d] + sh.count[warp][d] + place[s];
+            if constexpr (CS > 1) {
+                uint32_t a;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(&sh.sorted[to % per])), "r"(to / per));
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(key[s]), "r"(pos[s]) : "memory");
+            } else {
+                sh.sorted[to] = make_int2(key[s], pos[s]);
+            }
+        }
+        cluster_sync<CS>();
+        if (p == passes - 1) break;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int i = warp * 32 * STEPS + 32 * s + lane;
+            key[s] = -1;
+            if (i < mine) {
+                const int2 v = sh.sorted[i];
+                key[s] = v.x;
+                pos[s] = v.y;
+            }
         }
         __syncthreads();
     }
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int i = warp * 32 * kSteps + 32 * s + lane;
-        if (i < n) {
-            key_out[i] = key[s];
-            pos_out[i] = pos[s];
-        }
+    // (the last barrier also keeps every CTA until the others have read its counts)
+    for (int i = tid; i < mine; i += kClusterThreads) {
+        const int2 v = sh.sorted[i];
+        key_out[i0 + i] = v.x;
+        pos_out[i0 + i] = v.y;
+        if (i == 0 || sh.sorted[i - 1].x != v.x) atomicOr(&present[v.x >> 5], 1u << (v.x & 31));
     }
 }
+static_assert(kBins <= 16 * 32, "warp_sums");
 
 // ---------------------------------------------------------------------------------------------
 // sums: a warp adds up the rows of one tile of sorted tokens, 32 UPL units of the columns
@@ -307,19 +403,48 @@ struct SumParams {
     float *dtable, *part;
     float scale;
     int n, D, Dp, V, tile, tiles, accumulate;
+    int cleared;  // rows [0, cleared) are zero already; V when there is nothing to clear
+    const uint32_t *present;  // a bit for each id that has a token
 };
 
+// Clears the rows without a token among those that the sort's kernels left.  The warps of all clearing
+// blocks sweep over the table side by side; a lane reads the presence bit of one of its warp's next 32 rows.
+__device__ __forceinline__ void clear_absent(const SumParams &p, int block, int blocks)
+{
+    const int lane = threadIdx.x & 31, warps = blocks * (kThreads / 32);
+    for (long long r0 = p.cleared + block * (kThreads / 32) + (threadIdx.x >> 5); r0 < p.V; r0 += 32LL * warps) {
+        const long long mine = r0 + (long long)lane * warps;
+        const bool absent = mine < p.V && !(p.present[mine >> 5] >> (mine & 31) & 1);
+        for (uint32_t left = __ballot_sync(0xffffffffu, absent); left; left &= left - 1) {
+            float *d = p.dtable + (size_t)(r0 + (long long)(__ffs(left) - 1) * warps) * p.D;
+            if (p.D % 4 == 0)
+                for (int c = lane; c < p.D / 4; c += 32) reinterpret_cast<float4 *>(d)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            else
+                for (int c = lane; c < p.D; c += 32) d[c] = 0.f;
+        }
+    }
+}
+
+// Adds onto the table without waiting for its old value.  Each element gets one addition in a call, so
+// the order of these operations cannot change a result.
+__device__ __forceinline__ void add_onto(float *p, const float4 v)
+{
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
 template <typename io_t, int VEC, int UPL>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const io_t *__restrict__ dout, const SumParams p)
+__global__ void __launch_bounds__(kThreads, 3) sum_kernel(const io_t *__restrict__ dout, const SumParams p, int chunks)
 {
     constexpr int AHEAD = 8 / UPL;
     const int lane = threadIdx.x & 31;
-    const int tile = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int sums = (p.tiles + kThreads / 32 - 1) / (kThreads / 32) * chunks;  // blocks that add; the others clear
     tc::allow_dependent_launch();
     tc::grid_dependency_wait();
+    if ((int)blockIdx.x >= sums) return clear_absent(p, blockIdx.x - sums, gridDim.x - sums);
+    const int tile = blockIdx.x / chunks * (kThreads / 32) + (threadIdx.x >> 5);
     if (tile >= p.tiles) return;
     const int s0 = tile * p.tile, s1 = min(p.n, s0 + p.tile), units = p.D / VEC;
-    const int u0 = blockIdx.y * 32 * UPL + lane;
+    const int u0 = blockIdx.x % chunks * 32 * UPL + lane;
     const int before = s0 > 0 ? p.key[s0 - 1] : -1, behind = s1 < p.n ? p.key[s1] : -1;
     const int first = p.key[s0];
     const bool from_before = before == first;
@@ -346,18 +471,17 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const io_t *__restrict__ 
                     for (int e = 0; e < VEC; e += (VEC >= 4 ? 4 : 1)) {
                         if constexpr (VEC >= 4) {
                             float4 v = make_float4(acc[j][e], acc[j][e + 1], acc[j][e + 2], acc[j][e + 3]);
-                            if (!partial) {
-                                v.x *= p.scale, v.y *= p.scale, v.z *= p.scale, v.w *= p.scale;
-                                if (p.accumulate) {
-                                    const float4 o = *reinterpret_cast<const float4 *>(q + e);
-                                    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-                                }
-                            }
-                            *reinterpret_cast<float4 *>(q + e) = v;
+                            if (!partial) v.x *= p.scale, v.y *= p.scale, v.z *= p.scale, v.w *= p.scale;
+                            if (!partial && p.accumulate)
+                                add_onto(q + e, v);
+                            else
+                                *reinterpret_cast<float4 *>(q + e) = v;
                         } else {
-                            float v = acc[j][e];
-                            if (!partial) v = p.accumulate ? fmaf(v, p.scale, q[e]) : v * p.scale;
-                            q[e] = v;
+                            const float v = partial ? acc[j][e] : acc[j][e] * p.scale;
+                            if (!partial && p.accumulate)
+                                atomicAdd(q + e, v);
+                            else
+                                q[e] = v;
                         }
                     }
                 }
@@ -413,35 +537,12 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const io_t *__restrict__ 
 __global__ void __launch_bounds__(kThreads) join_kernel(const SumParams p)
 {
     __shared__ float4 sums[kThreads / 32][32];
-    __shared__ int starts[kThreads / 32];
+    __shared__ int long_key[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int col = blockIdx.y * 128 + lane * 4;
     tc::grid_dependency_wait();
-    if (lane == 0) {  // warp w looks at the edge behind the block's tile w
-        const int a = blockIdx.x * (kThreads / 32) + warp;
-        int key = -1;
-        if (a < p.tiles - 1) {
-            const int e = (a + 1) * p.tile;  // the first token of the next tile
-            const int last = p.key[e - 1], next = p.key[e], earlier = a > 0 ? p.key[e - p.tile - 1] : -1;
-            // a run crosses this edge, and did not start before tile a
-            if (next != p.V && last == next && earlier != next) key = next;
-        }
-        starts[warp] = key;
-    }
-    __syncthreads();
-    for (int t = 0; t < kThreads / 32; ++t) {
-        const int a = blockIdx.x * (kThreads / 32) + t, key = starts[t];
-        if (key < 0) continue;
-        int b0 = a + 1;  // the first tile that does not begin with the key: keys are sorted, so count those that do
-        for (;;) {
-            const int i = b0 + tid;
-            const int same = __syncthreads_count(i < p.tiles && p.key[(size_t)i * p.tile] == key);
-            b0 += same;
-            if (same < kThreads) break;
-        }
-        const int parts = b0 - a;  // part 0: the last one of tile a; part i: the first one of tile a + i
-        const int per = (parts + kThreads / 32 - 1) / (kThreads / 32);
-        const int i0 = min(parts, warp * per), i1 = min(parts, i0 + per);
+    // part 0: the last one of tile a; part i: the first one of tile a + i
+    auto add_parts = [&](int a, int i0, int i1) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col < p.Dp) {
 #pragma unroll 8
@@ -450,18 +551,51 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumParams p)
                 acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
             }
         }
+        return acc;
+    };
+    auto finish = [&](int key, const float4 acc) {
+        const float f[4] = {acc.x, acc.y, acc.z, acc.w};
+        float *to = p.dtable + (size_t)key * p.D + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < p.D) to[i] = p.accumulate ? fmaf(f[i], p.scale, to[i]) : f[i] * p.scale;
+    };
+    // A warp takes the edge behind one tile: does a run cross it that did not start before tile a?
+    const int a = blockIdx.x * (kThreads / 32) + warp;
+    int key = -1, more = 0;
+    if (a < p.tiles - 1) {
+        const int e = (a + 1) * p.tile;  // the first token of the next tile
+        const int last = p.key[e - 1], next = p.key[e], earlier = a > 0 ? p.key[e - p.tile - 1] : -1;
+        // keys are sorted, so the tiles that begin with the key follow each other
+        const int i = a + 1 + lane;
+        const bool same = i < p.tiles && p.key[(size_t)i * p.tile] == next;
+        more = __popc(__ballot_sync(0xffffffffu, same));
+        if (next != p.V && last == next && earlier != next) key = next;
+    }
+    const bool fits = more < 32;
+    if (key >= 0 && fits) finish(key, add_parts(a, 0, more + 1));
+    if (lane == 0) long_key[warp] = fits ? -1 : key;
+    __syncthreads();
+    for (int t = 0; t < kThreads / 32; ++t) {  // runs of more tiles: the whole block
+        const int from = blockIdx.x * (kThreads / 32) + t, k = long_key[t];
+        if (k < 0) continue;
+        int b = from + 33;  // the first tile that does not begin with the key
+        for (;;) {
+            const int i = b + tid;
+            const int same = __syncthreads_count(i < p.tiles && p.key[(size_t)i * p.tile] == k);
+            b += same;
+            if (same < kThreads) break;
+        }
+        const int parts = b - from, per = (parts + kThreads / 32 - 1) / (kThreads / 32);
+        float4 acc = add_parts(from, min(parts, warp * per), min(parts, warp * per + per));
         sums[warp][lane] = acc;
         __syncthreads();
-        if (warp == 0 && col < p.D) {
-            const int used = (parts + per - 1) / per;
-            for (int w = 1; w < used; ++w) {
+        if (warp == 0) {
+            for (int w = 1; w < kThreads / 32; ++w) {
                 const float4 v = sums[w][lane];
                 acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
             }
-            const float f[4] = {acc.x, acc.y, acc.z, acc.w};
-            float *to = p.dtable + (size_t)key * p.D + col;
-            for (int i = 0; i < 4; ++i)
-                if (col + i < p.D) to[i] = p.accumulate ? fmaf(f[i], p.scale, to[i]) : f[i] * p.scale;
+            finish(k, acc);
         }
         __syncthreads();
     }
@@ -477,6 +611,10 @@ int tile_of(int n)
     while (n / t >= kTilesMax) t *= 2;
     return t;
 }
+
+constexpr int kSmall = 2048;  // tokens that one CTA sorts
+
+constexpr size_t cluster_smem(int steps) { return sizeof(ClusterShared) + (size_t)steps * kClusterThreads * sizeof(int2); }
 
 // A launch that may begin while the kernel before it in the stream ends (it waits for that kernel's
 // results itself); the first kernel of a call is launched plainly.
@@ -498,11 +636,11 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStre
 // Columns are split over warps (32 units each, 64 for the narrow units of unaligned rows): tiles are few
 // when tokens are, and a warp with one unit per lane keeps eight rows in flight.
 template <typename io_t, int VEC>
-cudaError_t launch_sum(const void *dout, const SumParams &p, cudaStream_t s)
+cudaError_t launch_sum(const void *dout, const SumParams &p, int clear_blocks, cudaStream_t s)
 {
     constexpr int UPL = VEC > 1 ? 1 : 2;
     const unsigned gx = (p.tiles + kThreads / 32 - 1) / (kThreads / 32), gy = (p.D / VEC + 32 * UPL - 1) / (32 * UPL);
-    return launch_behind(sum_kernel<io_t, VEC, UPL>, dim3(gx, gy), kThreads, s, (const io_t *)dout, p);
+    return launch_behind(sum_kernel<io_t, VEC, UPL>, dim3(gx * gy + clear_blocks), kThreads, s, (const io_t *)dout, p, (int)gy);
 }
 
 template <typename io_t, int VEC>
@@ -533,6 +671,22 @@ int padded(int D) { return (D + 3) & ~3; }
 
 using namespace embed;
 
+template <int CS, int STEPS>
+static cudaError_t prepare_sort()
+{
+    return cudaFuncSetAttribute(cluster_sort_kernel<CS, STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cluster_smem(STEPS));
+}
+
+cudaError_t embed_prepare()
+{
+    cudaError_t e = prepare_sort<1, 2>();
+    if (e == cudaSuccess) e = prepare_sort<kCluster, 1>();
+    if (e == cudaSuccess) e = prepare_sort<kCluster, 2>();
+    if (e == cudaSuccess) e = prepare_sort<kCluster, 4>();
+    if (e == cudaSuccess) e = prepare_sort<kCluster, kClusterSteps>();
+    return e;
+}
+
 cudaError_t embed_forward(prism_dtype io, const EmbedArgs &a, const TokenLaunch &l)
 {
     // 16-byte units where every row of both tensors starts on a 16-byte boundary
@@ -543,14 +697,15 @@ cudaError_t embed_forward(prism_dtype io, const EmbedArgs &a, const TokenLaunch 
     return units ? launch_lookup<float, 4>(a, l) : launch_lookup<float, 1>(a, l);
 }
 
-size_t embed_workspace_bytes(int max_rows, int D)
+size_t embed_workspace_bytes(int max_rows, int D, int V)
 {
     const size_t all = ((size_t)max_rows + kTile - 1) / kTile, tiles = all < kTilesMax ? all : kTilesMax;
     return 4 * up256((size_t)max_rows * 4) + up256((size_t)kPassesMax * kBlocksMax * kBins * 4) +
+           up256(((size_t)V / 32 + 1) * 4) +
            up256(tiles * 2 * padded(D) * 4);
 }
 
-void embed_carve(int max_rows, int D, void *base, EmbedWorkspace *w)
+void embed_carve(int max_rows, int V, void *base, EmbedWorkspace *w)
 {
     char *p = (char *)base;
     auto take = [&](size_t bytes) {
@@ -563,6 +718,7 @@ void embed_carve(int max_rows, int D, void *base, EmbedWorkspace *w)
         w->pos[i] = (int *)take((size_t)max_rows * 4);
     }
     w->hist = (int *)take((size_t)kPassesMax * kBlocksMax * kBins * 4);
+    w->present = (uint32_t *)take(((size_t)V / 32 + 1) * 4);
     w->part = (float *)take(0);
 }
 
@@ -573,30 +729,56 @@ cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const Emb
     int bits = 1;
     while ((1LL << bits) <= a.V) ++bits;  // keys 0 .. V
     const int passes = (bits + 8) / 9, width = (bits + passes - 1) / passes, mask = (1 << width) - 1;
-    // the table is cleared in equal shares beside the sort's kernels
-    const int kernels = a.n <= kSub ? 1 : passes + 1, fill_blocks = a.accumulate ? 0 : 4 * l.sm_count;
-    const size_t floats = (size_t)a.V * a.D;
+    // The sort's kernels clear the table's first rows in equal shares, as many as fit beside them (without
+    // tokens there are no sums, and they clear everything).
+    const bool in_cluster = a.n <= kCluster * kClusterThreads * kClusterSteps;
+    const int kernels = in_cluster ? 1 : passes + 1, fill_blocks = a.accumulate ? 0 : (in_cluster ? 2 : 4) * l.sm_count;
+    const long long beside = kernels * kBesideSort / ((long long)a.D * 4);
+    const int cleared = a.accumulate || a.n == 0 || beside >= a.V ? a.V : (int)beside;
+    const size_t floats = (size_t)cleared * a.D;
     auto share = [&](int i) {
         const size_t quads = floats / 4;
         return Fill{a.dtable, quads * i / kernels * 4, i == kernels - 1 ? floats : quads * (i + 1) / kernels * 4};
     };
     int result = 0;  // which of the two buffers holds the sorted tokens
-    if (a.n <= kSub) {
+    if (in_cluster) {
         l.timer->begin("embed_sort");
-        sort_kernel<<<1 + fill_blocks, kSortThreads, 0, s>>>(a.ids, a.n, a.V, width, passes, w.key[0], w.pos[0], l.d_status, share(0));
+        const int per = a.n <= kSmall ? a.n : (a.n + kCluster - 1) / kCluster;
+        auto go = [&](auto cs, auto steps) {
+            constexpr int CS = decltype(cs)::value, STEPS = decltype(steps)::value;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(CS + fill_blocks / kCluster * kCluster);
+            cfg.blockDim = dim3(kClusterThreads);
+            cfg.dynamicSmemBytes = cluster_smem(STEPS);
+            cfg.stream = s;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = CS;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = CS > 1 ? 1 : 0;
+            e = cudaLaunchKernelEx(&cfg, cluster_sort_kernel<CS, STEPS>, a.ids, a.n, per, a.V, width, passes, w.key[0], w.pos[0],
+                                   w.present, l.d_status, share(0));
+        };
+        if (a.n <= kSmall) go(std::integral_constant<int, 1>(), std::integral_constant<int, 2>());
+        else if (per <= kClusterThreads) go(std::integral_constant<int, kCluster>(), std::integral_constant<int, 1>());
+        else if (per <= 2 * kClusterThreads) go(std::integral_constant<int, kCluster>(), std::integral_constant<int, 2>());
+        else if (per <= 4 * kClusterThreads) go(std::integral_constant<int, kCluster>(), std::integral_constant<int, 4>());
+        else go(std::integral_constant<int, kCluster>(), std::integral_constant<int, kClusterSteps>());
         l.timer->end();
+        if (e != cudaSuccess) return e;
     } else {
         // at most kBlocksMax blocks, of whole tiles of kSub keys
         const int chunk = (int)((((long long)a.n + kBlocksMax - 1) / kBlocksMax + kSub - 1) / kSub * kSub);
         const int nb = (a.n + chunk - 1) / chunk;
         auto hist = [&](int pass) { return w.hist + (size_t)pass * kBlocksMax * kBins; };
         l.timer->begin("embed_count");
-        count_kernel<<<nb + fill_blocks, kSortThreads, 0, s>>>(a.ids, a.n, a.V, chunk, mask, passes, nb, w.hist, l.d_status, share(0));
+        count_kernel<<<nb + fill_blocks, kSortThreads, 0, s>>>(a.ids, a.n, a.V, chunk, mask, passes, nb, w.hist, w.present, l.d_status, share(0));
         l.timer->end();
         for (int p = 0; p < passes; ++p) {
             const int to = p & 1, from = to ^ 1;
-            const Pass ps{a.ids, w.key[from], w.pos[from], w.key[to], w.pos[to], hist(p), p + 1 < passes ? hist(p + 1) : nullptr,
-                          a.n, a.V, chunk, nb, p * width, mask, (p + 1) * width};
+            const Pass ps{a.ids, w.key[from], w.pos[from], w.key[to], w.pos[to], hist(p), p + 1 < passes ? hist(p + 1) : nullptr, w.present,
+                          a.n, a.V, chunk, nb, p * width, width, mask, (p + 1) * width};
             l.timer->begin("embed_scatter");
             e = launch_behind(p == 0 ? scatter_kernel<true> : scatter_kernel<false>, dim3(nb + fill_blocks), kSortThreads, s, ps, share(p + 1));
             l.timer->end();
@@ -618,11 +800,14 @@ cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const Emb
     sp.tile = tile_of(a.n);
     sp.tiles = (a.n + sp.tile - 1) / sp.tile;
     sp.accumulate = a.accumulate;
+    sp.cleared = cleared;
+    sp.present = w.present;
+    const int clear_blocks = cleared < a.V ? 2 * l.sm_count : 0;
     l.timer->begin("embed_sum");
     if (io == PRISM_BF16)
-        e = a.D % 8 == 0 ? launch_sum<__nv_bfloat16, 8>(a.dout, sp, s) : launch_sum<__nv_bfloat16, 1>(a.dout, sp, s);
+        e = a.D % 8 == 0 ? launch_sum<__nv_bfloat16, 8>(a.dout, sp, clear_blocks, s) : launch_sum<__nv_bfloat16, 1>(a.dout, sp, clear_blocks, s);
     else
-        e = a.D % 4 == 0 ? launch_sum<float, 4>(a.dout, sp, s) : launch_sum<float, 1>(a.dout, sp, s);
+        e = a.D % 4 == 0 ? launch_sum<float, 4>(a.dout, sp, clear_blocks, s) : launch_sum<float, 1>(a.dout, sp, clear_blocks, s);
     l.timer->end();
     if (e != cudaSuccess || sp.tiles < 2) return e;
     l.timer->begin("embed_join");

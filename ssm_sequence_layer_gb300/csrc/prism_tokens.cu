@@ -100,7 +100,8 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
     if (major != 10 || minor != 3)
         return fail(PRISM_ERR_ARCH, "device %d is sm_%d%d; this library is built for sm_103 only", device, major, minor);
 
-    e = prism::matmul8_prepare();
+    e = prism::embed_prepare();
+    if (e == cudaSuccess) e = prism::matmul8_prepare();
     if (e == cudaSuccess) e = prism::logprobs_prepare();
     if (e != cudaSuccess) return cuda_fail(e, "kernel attribute setup");
     prism_tokens_s *t = new (std::nothrow) prism_tokens_s();
@@ -112,7 +113,7 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
     t->device = device;
     t->sm_count = sms;
     // one allocation: the status word, then the operators' workspaces
-    const size_t embed_bytes = prism::embed_workspace_bytes(max_rows, D);
+    const size_t embed_bytes = prism::embed_workspace_bytes(max_rows, D, V);
     t->ws_bytes = 256 + embed_bytes + prism::norm_workspace_bytes(max_rows, D);
     if ((e = cudaMalloc(&t->ws, t->ws_bytes)) != cudaSuccess) {
         delete t;
@@ -124,7 +125,7 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
         delete t;
         return cuda_fail(e, "status word init");
     }
-    prism::embed_carve(max_rows, D, (char *)t->ws + 256, &t->embed);
+    prism::embed_carve(max_rows, V, (char *)t->ws + 256, &t->embed);
     prism::norm_carve(max_rows, D, (char *)t->ws + 256 + embed_bytes, &t->norm);
     *out_tokens = t;
     return PRISM_OK;

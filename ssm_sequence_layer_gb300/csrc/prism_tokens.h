@@ -22,16 +22,18 @@ struct EmbedArgs {
     void *out;
     int n, D, V;
 };
+cudaError_t embed_prepare();
 cudaError_t embed_forward(prism_dtype io, const EmbedArgs &a, const TokenLaunch &l);
 
 // Workspace of the gradient: the tokens sorted by id and the sums of runs that cross a tile's edge.
 struct EmbedWorkspace {
     int *key[2], *pos[2];  // [max_rows] ids (V = no token) and positions, ping-pong of the sort's passes
     int *hist;             // [kSortPassesMax][kSortBlocks][kSortBins] digit counts
+    uint32_t *present;     // [V / 32 + 1] a bit for each id that has a token (and for "no token")
     float *part;           // [tiles][2][Dp] sums of a tile's first and last run where it crosses the edge
 };
-size_t embed_workspace_bytes(int max_rows, int D);
-void embed_carve(int max_rows, int D, void *base, EmbedWorkspace *w);
+size_t embed_workspace_bytes(int max_rows, int D, int V);
+void embed_carve(int max_rows, int V, void *base, EmbedWorkspace *w);
 struct EmbedBackwardArgs {
     const long long *ids;
     const void *dout;

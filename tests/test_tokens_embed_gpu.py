@@ -69,7 +69,8 @@ def check_gradient(got, ids, dout, scale, V, onto=None):
 @pytest.mark.parametrize("n,D,V,kind", [
     (1, 64, 10, "zipf"), (16, 768, 50, "zipf"), (17, 8, 3, "zipf"), (333, 257, 1000, "zipf"), (2048, 64, 511, "zipf"),
     (2049, 64, 512, "zipf"), (5000, 40, 70001, "zipf"), (5000, 128, 7, "one"), (300, 136, 20, "none"),
-    (4000, 72, 4000, "distinct"), (12000, 1032, 300, "zipf"), (3000, 1, 300000, "zipf"), (270000, 16, 90, "zipf")])
+    (4000, 72, 4000, "distinct"), (12000, 1032, 300, "zipf"), (3000, 1, 300000, "zipf"), (270000, 16, 90, "zipf"),
+    (20000, 24, 40000, "zipf"), (40000, 8, 600000, "zipf"), (65537, 8, 1000, "one"), (70000, 12, 262144, "zipf"), (2500, 520, 9000, "one")])
 def test_embed_backward(io, n, D, V, kind):
     g = torch.Generator().manual_seed(n * 3 + D)
     ids = draw_ids(n, V, 5, kind)
@@ -88,6 +89,28 @@ def test_embed_backward(io, n, D, V, kind):
     d64 = dout.double().numpy()
     check_gradient(first.double().cpu().numpy(), ids.numpy(), d64, 0.75, V)
     check_gradient(added.double().cpu().numpy(), ids.numpy(), d64, 0.75, V, onto.double().cpu().numpy())
+
+
+def test_ids_of_the_largest_vocabulary():
+    """Ids of up to 30 bits, the sort's four passes, on both sides of the cluster sort's capacity; the table
+    itself does not fit, so the gradient goes onto ids that are the last rows of nothing: D = 1, 2^28 rows."""
+    V = 1 << 28
+    for n in (100, 5000, 70000):
+        g = torch.Generator().manual_seed(n)
+        ids = torch.randint(0, V, (n,), generator=g)
+        ids[: n // 2] = V - 1 - torch.randint(0, 50, (n // 2,), generator=g)
+        dout = torch.randn(n, 1, generator=g)
+        with B.Tokens(n, 1, V, io="f32") as t:
+            d = t.embed_backward(ids.cuda(), dout.cuda())
+            torch.cuda.synchronize()
+            t.last_device_status()
+        rows, inverse = torch.unique(ids, return_inverse=True)
+        ref = torch.zeros(rows.numel(), dtype=torch.float64).index_add_(0, inverse, dout[:, 0].double())
+        size = torch.zeros(rows.numel(), dtype=torch.float64).index_add_(0, inverse, dout[:, 0].double().abs())
+        count = torch.bincount(inverse)
+        assert torch.all((d[rows.cuda(), 0].cpu().double() - ref).abs() <= 2.0 ** -24 * (count + 2) * size)
+        assert torch.count_nonzero(d).item() == torch.count_nonzero(ref.float()).item()
+        del d
 
 
 def test_embed_gradient_is_the_lookup_transposed():
