@@ -23,7 +23,7 @@ constexpr int kAhead = 4;             // 16-byte units in flight per thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.38953139e38f;  // the lowest bfloat16 value
 constexpr float kFar = -1e4f;         // 2^kFar = 0, and kFar times anything in range is finite
-constexpr int kClusterMax = 8, kTopMax = 32;
+constexpr int kLogClusterMax = 3, kTopMax = 32;
 constexpr int kCandidates = 1024;
 constexpr size_t kKeepMax = 200 * 1024;  // shared memory for a row's slice
 
@@ -40,6 +40,29 @@ __device__ __forceinline__ float max_nan(float a, float b)  // NaN if either is
     return y;
 }
 
+// Two fp32 operations in one instruction (the kernels are close to the issue limit at HBM's rate)
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r)) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(r)) : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 template <typename logit_t>
 struct Row;
 template <>
@@ -52,12 +75,19 @@ struct Row<__nv_bfloat16> {
         u.w = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
         return u;
     }
-    // the larger of two numbers; NaN only if both are
+    // the largest number
     static __device__ __forceinline__ float largest(const U &u)
     {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u.w);
         const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
         return fmaxf(__low2float(m), __high2float(m));
+    }
+    // ... or NaN if there is one
+    static __device__ __forceinline__ float largest_nan(const U &u)
+    {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u.w);
+        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+        return max_nan(__low2float(m), __high2float(m));
     }
 };
 template <>
@@ -75,6 +105,12 @@ struct Row<float> {
         float f[4];
         u.get(f);
         return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+    }
+    static __device__ __forceinline__ float largest_nan(const U &u)
+    {
+        float f[4];
+        u.get(f);
+        return max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]));
     }
 };
 
@@ -95,33 +131,43 @@ __device__ __forceinline__ Part join(const Part a, const Part b, float c2)
 
 // A thread's share of a row; top = kLowest: no live token so far (then s = t = 0, or NaN)
 struct Share {
-    float top = kLowest, s = 0.f, t = 0.f;
+    float top = kLowest;
+    float2 s = {0.f, 0.f}, t = {0.f, 0.f};  // even and odd values
 
+    // n: how many of the units are there (the others are R::nothing())
     template <typename R, int N>
-    __device__ __forceinline__ void add(const typename R::U (&x)[N], float c2)
+    __device__ __forceinline__ void add(const typename R::U (&x)[N], int n, float c2)
     {
         float now = top;
 #pragma unroll
         for (int i = 0; i < N; ++i) now = fmaxf(now, R::largest(x[i]));
-        const float d = fmaxf((top - now) * c2, kFar), f = ex2(d);
-        t = f * fmaf(s, d, t);
-        s *= f;
+        const float2 d = both(fmaxf((top - now) * c2, kFar)), f = both(ex2(d.x));
+        t = mul2(f, fma2(s, d, t));
+        s = mul2(f, s);
         top = now;
-        const float from = now > kLowest ? now : 0.f;
+        const float2 minus_from = both(now > kLowest ? -now : 0.f), cc = both(c2);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            if (i >= n) break;
             float v[R::VEC];
             x[i].get(v);
 #pragma unroll
-            for (int e = 0; e < R::VEC; ++e) {
+            for (int e = 0; e < R::VEC; e += 2) {
                 // masked tokens end at kFar, where p = 0; NaN (and +inf against itself) goes into the sums
-                const float z = max_nan((v[e] - from) * c2, kFar), p = ex2(z);
-                s += p;
-                t = fmaf(p, z, t);
+                float2 z = mul2(add2(make_float2(v[e], v[e + 1]), minus_from), cc);
+                z.x = max_nan(z.x, kFar), z.y = max_nan(z.y, kFar);
+                const float2 p = make_float2(ex2(z.x), ex2(z.y));
+                s = add2(s, p);
+                t = fma2(p, z, t);
             }
         }
     }
-    __device__ __forceinline__ Part part() const { return {top > kLowest ? top : -INFINITY, s, t}; }
+    // the share relative to a larger logit (kLowest: nobody has a live token)
+    __device__ __forceinline__ Part part(float onto, float c2) const
+    {
+        const float d = fmaxf((top - onto) * c2, kFar), f = ex2(d), sum = s.x + s.y;
+        return {onto > kLowest ? onto : -INFINITY, f * sum, f * fmaf(sum, d, t.x + t.y)};
+    }
 };
 
 // A logit's place in the order of the top: by value (NaN first), then by lowest id.  Larger keys come
@@ -157,16 +203,16 @@ template <typename logit_t>
 struct Slice {
     const logit_t *x;
     int head, u0, u1, tail0, tail1;  // singles [0, head), units [u0, u1) behind them, singles [tail0, tail1)
-    __device__ Slice(const logit_t *row, int V, int rank, int size)
+    __device__ Slice(const logit_t *row, int V, int rank, int log_size)
     {
         constexpr int VEC = Row<logit_t>::VEC;
         x = row;
         const int off = (int)(((uintptr_t)row & 15) / sizeof(logit_t)), before = min(V, off ? VEC - off : 0);
         const int units = (V - before) / VEC;
-        u0 = (int)((long long)units * rank / size);
-        u1 = (int)((long long)units * (rank + 1) / size);
+        u0 = (int)((long long)units * rank >> log_size);
+        u1 = (int)((long long)units * (rank + 1) >> log_size);
         tail0 = before + units * VEC;
-        tail1 = rank == size - 1 ? V : tail0;
+        tail1 = rank + 1 == 1 << log_size ? V : tail0;
         first = before;
         head = rank == 0 ? before : 0;
     }
@@ -182,7 +228,7 @@ struct Slice {
 };
 
 template <typename logit_t, bool TOP, bool KEEP>
-__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParams<logit_t> p, int cluster)
+__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParams<logit_t> p, int log_cluster)
 {
     using R = Row<logit_t>;
     using U = typename R::U;
@@ -195,9 +241,9 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParam
     __shared__ int found;
     __shared__ float threshold;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = cluster > 1 ? (int)(blockIdx.x % cluster) : 0;
-    const long long row = blockIdx.x / cluster;
-    const Slice<logit_t> sl(p.logits + row * p.ld, p.V, rank, cluster);
+    const int cluster = 1 << log_cluster, rank = blockIdx.x & (cluster - 1);
+    const long long row = blockIdx.x >> log_cluster;
+    const Slice<logit_t> sl(p.logits + row * p.ld, p.V, rank, log_cluster);
     const float c2 = p.inv_temperature * kLog2e;
     const uint4 *units = sl.units();
 
@@ -214,36 +260,38 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParam
             for (int a = 0; a < kAhead; ++a)
                 if (u + a * kThreads < sl.u1) kept[u + a * kThreads - sl.u0] = x[a].w;
         }
-        sh.template add<R, kAhead>(x, c2);
+        sh.template add<R, kAhead>(x, (sl.u1 - u + kThreads - 1) / kThreads, c2);
     }
     const int single = sl.single(tid);
     if (single >= 0) {
         U x[1] = {R::nothing()};
         *reinterpret_cast<logit_t *>(&x[0].w) = sl.x[single];
-        sh.template add<R, 1>(x, c2);
+        sh.template add<R, 1>(x, 1, c2);
     }
-    Part r = sh.part();
+    // The warp's largest logit, the thread's sums brought onto it, and the warp's sums.  On the way, the
+    // largest logit of each half warp.
+    float warp_top = sh.top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Part other{__shfl_xor_sync(0xffffffffu, r.top, o), __shfl_xor_sync(0xffffffffu, r.s, o),
-                         __shfl_xor_sync(0xffffffffu, r.t, o)};
-        r = lane & o ? join(other, r, c2) : join(r, other, c2);
-    }
-    if (lane == 0) parts[warp] = r;
-    if constexpr (TOP) {  // the largest logit of each half warp
-        float g = sh.top;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        if ((lane & 15) == 0) group_top[warp * 2 + (lane >> 4)] = g;
+    for (int o = 1; o < 16; o <<= 1) warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, o));
+    if constexpr (TOP) {
+        if ((lane & 15) == 0) group_top[warp * 2 + (lane >> 4)] = warp_top;
         if (tid == 0) found = 0;
     }
+    warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, 16));
+    Part r = sh.part(warp_top, c2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
+        r.t += __shfl_xor_sync(0xffffffffu, r.t, o);
+    }
+    if (lane == 0) parts[warp] = r;
     __syncthreads();
     if (warp == 0) {
         r = lane < kWarps ? parts[lane] : Part{-INFINITY, 0.f, 0.f};
 #pragma unroll
         for (int o = kWarps / 2; o > 0; o >>= 1) {
             const Part other{__shfl_xor_sync(0xffffffffu, r.top, o), __shfl_xor_sync(0xffffffffu, r.s, o),
-                             __shfl_xor_sync(0xffffffffu, r.t, o)};
+                            __shfl_xor_sync(0xffffffffu, r.t, o)};
             r = lane & o ? join(other, r, c2) : join(r, other, c2);
         }
         if (lane == 0) mine = r;
@@ -270,14 +318,11 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParam
         for (int u = sl.u0 + tid; u < sl.u1; u += kThreads) {
             U x;
             x.w = KEEP ? kept[u - sl.u0] : __ldg(units + u);
+            if (R::largest_nan(x) < least) continue;
             float v[R::VEC];
             x.get(v);
-            bool any = false;
 #pragma unroll
-            for (int e = 0; e < R::VEC; ++e) any |= !(v[e] < least);
-            if (any)
-#pragma unroll
-                for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + u * R::VEC + e);
+            for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + u * R::VEC + e);
         }
         if (single >= 0) offer(io::ld(sl.x + single), single);
         if (tid < kTopMax) best[tid] = 0;
@@ -413,14 +458,14 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardPar
     const int tid = threadIdx.x;
     const long long row = blockIdx.x / chunks;
     const int chunk = (int)(blockIdx.x % chunks);
-    const Slice<logit_t> sl(p.logits + row * p.ld, p.V, 0, 1);
+    const Slice<logit_t> sl(p.logits + row * p.ld, p.V, 0, 0);
     logit_t *out = p.dlogits + row * p.ld_d;
     const uint4 *units = sl.units();
-    const int u0 = chunk * kAhead * kThreads + tid;
+    const int per = (sl.u1 + chunks - 1) / chunks, u0 = chunk * per + tid, u1 = min(sl.u1, chunk * per + per);
     U x[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
-        if (u0 + a * kThreads < sl.u1) x[a].w = units[u0 + a * kThreads];
+        if (u0 + a * kThreads < u1) x[a].w = units[u0 + a * kThreads];
     const float lse = p.lse[row], c = p.inv_temperature;
     long long t = p.dlogprob ? p.targets[row] : -1;
     if (t >= p.V) {
@@ -431,24 +476,33 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardPar
     const float dlp = t >= 0 && !none ? p.dlogprob[row] * c : 0.f;
     const float dh = p.dentropy && !none ? p.dentropy[row] * c : 0.f, h = p.dentropy && !none ? p.entropy[row] : 0.f;
     const float minus_lse = none ? 0.f : -lse, Bc = fmaf(-dh, h, -dlp);
-    auto grad = [&](float v) {
-        const float z = max_nan(fmaf(v, c, minus_lse), kFar), pr = ex2(z * kLog2e);
-        return pr * fmaf(-dh, z, Bc);
+    auto grad = [&](float2 v) {
+        float2 z = fma2(v, both(c), both(minus_lse));
+        z.x = max_nan(z.x, kFar), z.y = max_nan(z.y, kFar);
+        const float2 y = mul2(z, both(kLog2e));
+        return mul2(make_float2(ex2(y.x), ex2(y.y)), fma2(both(-dh), z, both(Bc)));
     };
     auto at_target = [&](float v) { return v <= kLowest ? 0.f : dlp; };  // a masked target has no gradient
     const bool aligned = (((uintptr_t)(out + sl.first)) & 15) == 0;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
         const int u = u0 + a * kThreads;
-        if (u >= sl.u1) break;
+        if (u >= u1) break;
         const int id = sl.first + u * R::VEC;
-        float v[R::VEC];
+        float v[R::VEC], at_hit = 0.f;
         x[a].get(v);
         const int hit = t >= id && t < id + R::VEC ? (int)t - id : -1;
 #pragma unroll
-        for (int e = 0; e < R::VEC; ++e) {
-            const float g = grad(v[e]);
-            v[e] = e == hit ? g + at_target(v[e]) : g;
+        for (int e = 0; e < R::VEC; e += 2) {
+            const float2 x2 = make_float2(v[e], v[e + 1]), g = grad(x2);
+            if (e == hit) at_hit = at_target(x2.x);
+            if (e + 1 == hit) at_hit = at_target(x2.y);
+            v[e] = g.x, v[e + 1] = g.y;
+        }
+        if (hit >= 0) {
+#pragma unroll
+            for (int e = 0; e < R::VEC; ++e)
+                if (e == hit) v[e] += at_hit;
         }
         if (aligned) {
             x[a].set(v);
@@ -460,14 +514,15 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardPar
     }
     const int single = chunk == 0 ? sl.single(tid) : -1;
     if (single >= 0) {
-        const float v = io::ld(sl.x + single), g = grad(v);
+        const float v = io::ld(sl.x + single), g = grad(both(v)).x;
         io::st(out + single, single == t ? g + at_target(v) : g);
     }
 }
 
 template <typename logit_t, bool TOP, bool KEEP>
-cudaError_t launch_forward(const ForwardParams<logit_t> &p, int cluster, size_t smem, cudaStream_t s)
+cudaError_t launch_forward(const ForwardParams<logit_t> &p, int log_cluster, size_t smem, cudaStream_t s)
 {
+    const int cluster = 1 << log_cluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.n * cluster));
     cfg.blockDim = dim3(kThreads);
@@ -479,7 +534,7 @@ cudaError_t launch_forward(const ForwardParams<logit_t> &p, int cluster, size_t 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, forward_kernel<logit_t, TOP, KEEP>, p, cluster);
+    return cudaLaunchKernelEx(&cfg, forward_kernel<logit_t, TOP, KEEP>, p, log_cluster);
 }
 
 template <typename logit_t>
@@ -490,19 +545,19 @@ cudaError_t forward(const LogprobArgs &a, const TokenLaunch &l)
     // Few rows are split over a cluster, down to one unit per thread.  With alternatives the slice also
     // has to fit shared memory, two CTAs to an SM if a cluster can make it that small.
     const long long units = a.V / Row<logit_t>::VEC + 1;
-    int cluster = 1;
-    while (cluster < kClusterMax && (long long)a.n * cluster < 2 * l.sm_count && units / cluster > kThreads) cluster *= 2;
-    auto slice = [&] { return (size_t)(units / cluster + 1) * 16; };
+    int log_cluster = 0;
+    while (log_cluster < kLogClusterMax && ((long long)a.n << log_cluster) < 2 * l.sm_count && units >> log_cluster > kThreads) ++log_cluster;
+    auto slice = [&] { return (size_t)((units >> log_cluster) + 1) * 16; };
     if (a.k > 0)
-        while (cluster < kClusterMax && slice() > kKeepMax / 2) cluster *= 2;
+        while (log_cluster < kLogClusterMax && slice() > kKeepMax / 2) ++log_cluster;
     l.timer->begin("token_logprobs");
     cudaError_t e;
     if (a.k == 0)
-        e = launch_forward<logit_t, false, false>(p, cluster, 0, l.timer->stream);
+        e = launch_forward<logit_t, false, false>(p, log_cluster, 0, l.timer->stream);
     else if (slice() <= kKeepMax)
-        e = launch_forward<logit_t, true, true>(p, cluster, slice(), l.timer->stream);
+        e = launch_forward<logit_t, true, true>(p, log_cluster, slice(), l.timer->stream);
     else
-        e = launch_forward<logit_t, true, false>(p, cluster, 0, l.timer->stream);
+        e = launch_forward<logit_t, true, false>(p, log_cluster, 0, l.timer->stream);
     l.timer->end();
     return e;
 }
