@@ -18,14 +18,15 @@
 namespace prism {
 namespace logp {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kAhead = 4;             // 16-byte units in flight per thread
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kAhead = 4;             // 16-byte units in flight per thread: a batch
+constexpr int kBatch = kAhead * kThreads;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.38953139e38f;  // the lowest bfloat16 value
 constexpr float kFar = -1e4f;         // 2^kFar = 0, and kFar times anything in range is finite
 constexpr int kLogClusterMax = 3, kTopMax = 32;
 constexpr int kCandidates = 1024;
-constexpr size_t kKeepMax = 200 * 1024;  // shared memory for a row's slice
+constexpr int kBatchesMax = 96;       // batches of a slice whose largest logits are kept
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -134,13 +135,14 @@ struct Share {
     float top = kLowest;
     float2 s = {0.f, 0.f}, t = {0.f, 0.f};  // even and odd values
 
-    // n: how many of the units are there (the others are R::nothing())
+    // returns the units' largest logit
     template <typename R, int N>
-    __device__ __forceinline__ void add(const typename R::U (&x)[N], int n, float c2)
+    __device__ __forceinline__ float add(const typename R::U (&x)[N], float c2)
     {
-        float now = top;
+        float most = R::largest(x[0]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) now = fmaxf(now, R::largest(x[i]));
+        for (int i = 1; i < N; ++i) most = fmaxf(most, R::largest(x[i]));
+        const float now = fmaxf(top, most);
         const float2 d = both(fmaxf((top - now) * c2, kFar)), f = both(ex2(d.x));
         t = mul2(f, fma2(s, d, t));
         s = mul2(f, s);
@@ -148,7 +150,6 @@ struct Share {
         const float2 minus_from = both(now > kLowest ? -now : 0.f), cc = both(c2);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (i >= n) break;
             float v[R::VEC];
             x[i].get(v);
 #pragma unroll
@@ -161,6 +162,7 @@ struct Share {
                 t = fma2(p, z, t);
             }
         }
+        return most;
     }
     // the share relative to a larger logit (kLowest: nobody has a live token)
     __device__ __forceinline__ Part part(float onto, float c2) const
@@ -227,12 +229,12 @@ struct Slice {
     __device__ __forceinline__ const uint4 *units() const { return reinterpret_cast<const uint4 *>(x + first); }
 };
 
-template <typename logit_t, bool TOP, bool KEEP>
-__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParams<logit_t> p, int log_cluster)
+template <typename logit_t, bool TOP>
+__global__ void __launch_bounds__(kThreads, 4) forward_kernel(const ForwardParams<logit_t> p, int log_cluster, int kept)
 {
     using R = Row<logit_t>;
     using U = typename R::U;
-    extern __shared__ uint4 kept[];  // the slice's units, for the second look at them
+    extern __shared__ float batch_top[];                     // [kept][kThreads] the largest logit of each thread's batches
     __shared__ Part parts[kWarps];
     __shared__ Part mine;                                    // this CTA's part
     __shared__ unsigned long long best[TOP ? kTopMax : 1];   // its first k keys
@@ -248,36 +250,48 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParam
     const uint4 *units = sl.units();
 
     Share sh;
-    for (int u = sl.u0 + tid; u < sl.u1; u += kAhead * kThreads) {
+    int u = sl.u0, batch = 0;
+    for (; u + kBatch <= sl.u1; u += kBatch, ++batch) {
         U x[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) x[a].w = __ldg(units + u + a * kThreads + tid);
+        const float most = sh.template add<R, kAhead>(x, c2);
+        if (TOP && batch < kept) batch_top[batch * kThreads + tid] = most;
+    }
+    {  // the last batch is not full
+        U x[kAhead];
+        float most = kLowest;
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
             x[a] = R::nothing();
-            if (u + a * kThreads < sl.u1) x[a].w = __ldg(units + u + a * kThreads);
+            if (u + a * kThreads + tid < sl.u1) x[a].w = __ldg(units + u + a * kThreads + tid);
         }
-        if constexpr (TOP && KEEP) {
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-                if (u + a * kThreads < sl.u1) kept[u + a * kThreads - sl.u0] = x[a].w;
+        for (int a = 0; a < kAhead; ++a) {
+            if (u + a * kThreads >= sl.u1) break;
+            const U one[1] = {x[a]};
+            most = fmaxf(most, sh.template add<R, 1>(one, c2));
         }
-        sh.template add<R, kAhead>(x, (sl.u1 - u + kThreads - 1) / kThreads, c2);
+        if (TOP && batch < kept) batch_top[batch * kThreads + tid] = most;
     }
     const int single = sl.single(tid);
     if (single >= 0) {
         U x[1] = {R::nothing()};
         *reinterpret_cast<logit_t *>(&x[0].w) = sl.x[single];
-        sh.template add<R, 1>(x, 1, c2);
+        sh.template add<R, 1>(x, c2);
     }
     // The warp's largest logit, the thread's sums brought onto it, and the warp's sums.  On the way, the
-    // largest logit of each half warp.
+    // largest logit of each of 32 groups of threads.
+    constexpr int GROUP = kThreads / 32;
     float warp_top = sh.top;
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, o));
-    if constexpr (TOP) {
-        if ((lane & 15) == 0) group_top[warp * 2 + (lane >> 4)] = warp_top;
-        if (tid == 0) found = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+        if (TOP && o == GROUP) {
+            if (lane % GROUP == 0) group_top[tid / GROUP] = warp_top;
+            if (tid == 0) found = 0;
+        }
+        warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, o));
     }
-    warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, 16));
     Part r = sh.part(warp_top, c2);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -315,26 +329,40 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParam
             const int at = atomicAdd(&found, 1);
             if (at < kCandidates) cand[at] = key_of(v, id);
         };
-        for (int u = sl.u0 + tid; u < sl.u1; u += kThreads) {
-            U x;
-            x.w = KEEP ? kept[u - sl.u0] : __ldg(units + u);
-            if (R::largest_nan(x) < least) continue;
-            float v[R::VEC];
-            x.get(v);
+        // only batches that reach the threshold are looked at again (from L2); a thread whose sum is NaN looks
+        // at all of its own
+        const bool all = sh.s.x + sh.s.y != sh.s.x + sh.s.y;
+        batch = 0;
+        for (u = sl.u0; u < sl.u1; u += kBatch, ++batch) {
+            if (!all && batch < kept && batch_top[batch * kThreads + tid] < least) continue;
 #pragma unroll
-            for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + u * R::VEC + e);
+            for (int a = 0; a < kAhead; ++a) {
+                const int at = u + a * kThreads + tid;
+                if (at >= sl.u1) break;
+                U x;
+                x.w = __ldg(units + at);
+                if (R::largest_nan(x) < least) continue;
+                float v[R::VEC];
+                x.get(v);
+#pragma unroll
+                for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + at * R::VEC + e);
+            }
         }
         if (single >= 0) offer(io::ld(sl.x + single), single);
         if (tid < kTopMax) best[tid] = 0;
         __syncthreads();
         const int count = found;
         if (count <= kCandidates) {
-            for (int i = tid; i < count; i += kThreads) {
-                const unsigned long long key = cand[i];
-                int above = 0;
-                for (int o = 0; o < count; ++o) above += cand[o] > key;
-                if (above < p.k) best[above] = key;
-            }
+            // order by counting; few candidates need one warp only
+            if (count > 32 || warp == 0)
+                for (int i = tid; i < count; i += kThreads) {
+                    const unsigned long long key = cand[i];
+                    int above = 0;
+                    for (int o = 0; o < count; ++o) above += cand[o] > key;
+                    if (above < p.k) best[above] = key;
+                }
+            if (count > 32) __syncthreads();
+            __syncwarp();
         } else {
             // many equal logits, or an order that the groups miss: the largest key below the last one, k times
             unsigned long long last = ~0ull;
@@ -345,13 +373,13 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParam
                     const unsigned long long key = key_of(v, id);
                     if (key < last && key > b) b = key;
                 };
-                for (int u = sl.u0 + tid; u < sl.u1; u += kThreads) {
+                for (int at = sl.u0 + tid; at < sl.u1; at += kThreads) {
                     U x;
-                    x.w = KEEP ? kept[u - sl.u0] : __ldg(units + u);
+                    x.w = __ldg(units + at);
                     float v[R::VEC];
                     x.get(v);
 #pragma unroll
-                    for (int e = 0; e < R::VEC; ++e) look(v[e], sl.first + u * R::VEC + e);
+                    for (int e = 0; e < R::VEC; ++e) look(v[e], sl.first + at * R::VEC + e);
                 }
                 if (single >= 0) look(io::ld(sl.x + single), single);
 #pragma unroll
@@ -364,14 +392,16 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const ForwardParam
                 if (tid == 0) best[i] = b;
                 if (b == 0) break;
             }
+            __syncwarp();
         }
     }
-    // the cluster's parts and keys join in its first CTA
-    if (cluster > 1) {
+    // The cluster's parts and keys join in its first CTA; without a cluster the rest is one warp's work
+    // (warp 0 wrote mine and, but for the barriers above, best).
+    if (cluster > 1)
         asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-    } else {
-        __syncthreads();
-    }
+    else if (warp > 0)
+        return;
+    __syncwarp();
     if (rank == 0) {
         auto remote = [&](const void *local, int cta) {
             uint32_t a;
@@ -451,7 +481,7 @@ struct BackwardParams {
 // A CTA takes kAhead units per thread of one row.  dlogits_j = p_j (B - dentropy log p_j), plus dlogprob at the
 // target, with inv_temperature in dlogprob and dentropy, and B = -dlogprob - dentropy entropy.
 template <typename logit_t>
-__global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardParams<logit_t> p, int chunks)
+__global__ void __launch_bounds__(kThreads, 6) backward_kernel(const BackwardParams<logit_t> p, int chunks)
 {
     using R = Row<logit_t>;
     using U = typename R::U;
@@ -519,14 +549,14 @@ __global__ void __launch_bounds__(kThreads, 3) backward_kernel(const BackwardPar
     }
 }
 
-template <typename logit_t, bool TOP, bool KEEP>
-cudaError_t launch_forward(const ForwardParams<logit_t> &p, int log_cluster, size_t smem, cudaStream_t s)
+template <typename logit_t, bool TOP>
+cudaError_t launch_forward(const ForwardParams<logit_t> &p, int log_cluster, int kept, cudaStream_t s)
 {
     const int cluster = 1 << log_cluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.n * cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = (size_t)kept * kThreads * 4;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -534,7 +564,7 @@ cudaError_t launch_forward(const ForwardParams<logit_t> &p, int log_cluster, siz
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, forward_kernel<logit_t, TOP, KEEP>, p, log_cluster);
+    return cudaLaunchKernelEx(&cfg, forward_kernel<logit_t, TOP>, p, log_cluster, kept);
 }
 
 template <typename logit_t>
@@ -542,22 +572,15 @@ cudaError_t forward(const LogprobArgs &a, const TokenLaunch &l)
 {
     const ForwardParams<logit_t> p{(const logit_t *)a.logits, a.targets, a.lse, a.logprob, a.entropy, a.top_logprob, a.top_ids,
                                    a.ld, a.inv_temperature, a.n, a.V, a.k, l.d_status};
-    // Few rows are split over a cluster, down to one unit per thread.  With alternatives the slice also
-    // has to fit shared memory, two CTAs to an SM if a cluster can make it that small.
+    // Few rows are split over a cluster, down to one unit per thread.
     const long long units = a.V / Row<logit_t>::VEC + 1;
     int log_cluster = 0;
     while (log_cluster < kLogClusterMax && ((long long)a.n << log_cluster) < 2 * l.sm_count && units >> log_cluster > kThreads) ++log_cluster;
-    auto slice = [&] { return (size_t)((units >> log_cluster) + 1) * 16; };
-    if (a.k > 0)
-        while (log_cluster < kLogClusterMax && slice() > kKeepMax / 2) ++log_cluster;
+    const long long batches = (units >> log_cluster) / kBatch + 1;
     l.timer->begin("token_logprobs");
-    cudaError_t e;
-    if (a.k == 0)
-        e = launch_forward<logit_t, false, false>(p, log_cluster, 0, l.timer->stream);
-    else if (slice() <= kKeepMax)
-        e = launch_forward<logit_t, true, true>(p, log_cluster, slice(), l.timer->stream);
-    else
-        e = launch_forward<logit_t, true, false>(p, log_cluster, 0, l.timer->stream);
+    const cudaError_t e =
+        a.k == 0 ? launch_forward<logit_t, false>(p, log_cluster, 0, l.timer->stream)
+                 : launch_forward<logit_t, true>(p, log_cluster, (int)(batches < kBatchesMax ? batches : kBatchesMax), l.timer->stream);
     l.timer->end();
     return e;
 }
@@ -579,11 +602,10 @@ cudaError_t backward(const LogprobBackwardArgs &a, const TokenLaunch &l)
 
 cudaError_t logprobs_prepare()
 {
-    cudaError_t e = cudaFuncSetAttribute(logp::forward_kernel<float, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)logp::kKeepMax);
+    const int smem = logp::kBatchesMax * logp::kThreads * 4;
+    cudaError_t e = cudaFuncSetAttribute(logp::forward_kernel<float, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(logp::forward_kernel<__nv_bfloat16, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)logp::kKeepMax);
+        e = cudaFuncSetAttribute(logp::forward_kernel<__nv_bfloat16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     return e;
 }
 
