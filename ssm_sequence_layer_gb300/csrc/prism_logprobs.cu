@@ -230,7 +230,7 @@ struct Slice {
 };
 
 template <typename logit_t, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) forward_kernel(const ForwardParams<logit_t> p, int log_cluster, int kept)
+__global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParams<logit_t> p, int log_cluster, int kept)
 {
     using R = Row<logit_t>;
     using U = typename R::U;
@@ -335,17 +335,19 @@ __global__ void __launch_bounds__(kThreads, 4) forward_kernel(const ForwardParam
         batch = 0;
         for (u = sl.u0; u < sl.u1; u += kBatch, ++batch) {
             if (!all && batch < kept && batch_top[batch * kThreads + tid] < least) continue;
+            U x[kAhead];
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                const int at = u + a * kThreads + tid;
-                if (at >= sl.u1) break;
-                U x;
-                x.w = __ldg(units + at);
-                if (R::largest_nan(x) < least) continue;
-                float v[R::VEC];
-                x.get(v);
+                x[a] = R::nothing();
+                if (u + a * kThreads + tid < sl.u1) x[a].w = __ldg(units + u + a * kThreads + tid);
+            }
 #pragma unroll
-                for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + at * R::VEC + e);
+            for (int a = 0; a < kAhead; ++a) {
+                if (R::largest_nan(x[a]) < least) continue;
+                float v[R::VEC];
+                x[a].get(v);
+#pragma unroll
+                for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + (u + a * kThreads + tid) * R::VEC + e);
             }
         }
         if (single >= 0) offer(io::ld(sl.x + single), single);
