@@ -150,18 +150,23 @@ void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
 // values) and four tcgen05.mma (K = 32) into one of two accumulators of BN columns in tensor memory.
 // The accumulator holds c_b of one block only: the eight epilogue warps read it, scale it by
 // a_scale[m, b] w_scale[j / 128, b] and add it to the sums in their registers (one row and BN / 2
-// columns per thread) while the next block's products run into the other accumulator.  Per block the
-// tensor core needs 128 BN 128 / 8192 cycles and the scaled addition 128 BN / 128: half as many.
+// columns per thread, two columns per instruction) while the next block's products run into the other
+// accumulator.  Per block the tensor core needs 128 BN 128 / 8192 cycles and the scaled additions
+// 128 BN / 256.  The sums take more registers than an even share, so the four warps of the
+// issuing group hand theirs over.
 using namespace prism::tc;
 
 constexpr int BM = 128, STAGE_ROWS = 128;
-constexpr int kEpilogueWarps = 8, kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;  // three warpgroups
+// 384 threads launch with 168 registers each; 128 x 56 + 256 x 224 is the same number
+constexpr int kIssueRegs = 56, kEpilogueRegs = 224;
+static_assert(128 * kIssueRegs + 256 * kEpilogueRegs <= kThreads * 168, "registers handed over");
 
 template <int BN>
 struct Layout {
     static constexpr int STAGES = BN == 256 ? 4 : 6;
     static constexpr uint32_t A_BYTES = BM * kBlock, B_BYTES = BN * kBlock, STAGE = A_BYTES + B_BYTES;
-    static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging of 32 rows x 128 bytes of output
+    static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging of 32 x 32 sums, for rows that are not aligned
     static constexpr uint32_t OFF_OUT = STAGES * STAGE;
     static constexpr uint32_t SMEM = OFF_OUT + kEpilogueWarps * OUT_WARP + 1024;  // + alignment slack
     static_assert(SMEM <= 232448 && OFF_OUT % 1024 == 0, "layout");
@@ -189,10 +194,55 @@ struct Waits {
     unsigned long long ns;
 };
 
+// Lanes x 32 columns of an accumulator; the values may be used after ld_wait, which takes them as
+// operands so that no use moves in front of it.
+__device__ __forceinline__ void ld_issue(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+
+// acc += c s for the 32 values, two at a time
+__device__ __forceinline__ void add_scaled(float2 *acc, const uint32_t (&r)[32], float s)
+{
+    const float2 s2 = make_float2(s, s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 c = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        acc[i] = io::fma2(c, s2, acc[i]);
+    }
+}
+
+// 16 or 32 bytes to global memory
+__device__ __forceinline__ void store16(void *p, uint4 a) { *reinterpret_cast<uint4 *>(p) = a; }
+__device__ __forceinline__ void store32(void *p, uint4 a, uint4 b)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+                 "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 template <typename out_t, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                   const __grid_constant__ CUtensorMap tm_out, const Params<out_t> p, const Waits wt, int tiled_out)
+    product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Params<out_t> p,
+                   const Waits wt, int store_bytes)
 {
     using L = Layout<BN>;
     constexpr int STAGES = L::STAGES, HALF = BN / 2;
@@ -221,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_tmap(&tm_a);
         prefetch_tmap(&tm_w);
-        if (tiled_out) prefetch_tmap(&tm_out);
     }
     if (warp == 0) tmem_alloc(smem_u32(&tmem_base_s), 2 * BN);
     fence_before_sync();
@@ -240,6 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         *(volatile int *)&abort_s = 1;
     };
     long long issued = 0;  // the issuing threads' counts of steps, for the drain
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (tid == 32) {  // ---- operand loads ----
         int s = 0, i = 0, b = 0, m0 = 0, n0 = 0;
         uint32_t round = 0;
@@ -282,11 +333,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             issued = g + 1;
             if (++s == STAGES) s = 0, ++round;
         }
-    } else if (warp >= 2) {  // ---- scaled sums: lane quarter warp % 4, columns of half (warp - 2) / 4 ----
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+    }
+    } else {  // ---- scaled sums: lane quarter warp % 4, columns of half (warp - 4) / 4 ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t from = ((uint32_t)(quarter * 32) << 16) + half * HALF;
-        uint8_t *stage = sm + L::OFF_OUT + (warp - 2) * L::OUT_WARP;
-        const uint32_t stage_u32 = smem_u32(stage);
+        float *stage = reinterpret_cast<float *>(sm + L::OFF_OUT + (warp - 4) * L::OUT_WARP);
         long long g = 0;
         bool ok = true;
         for (int i = 0; i < my_tiles && ok; ++i) {
@@ -296,9 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int m = m0 + quarter * 32 + lane;
             const float *sa = p.a_scale + (size_t)min(m, p.M - 1) * p.KB;
             const float *sw = p.w_scale + (size_t)(min(n0, p.N - 1) / kBlock) * p.KB;
-            float acc[HALF];
+            float2 acc[HALF / 2];
 #pragma unroll
-            for (int c = 0; c < HALF; ++c) acc[c] = 0.f;
+            for (int c = 0; c < HALF / 2; ++c) acc[c] = make_float2(0.f, 0.f);
             float scale = sa[0] * sw[0];
             for (int b = 0; b < p.KB; ++b, ++g) {
                 const int buf = (int)(g & 1);
@@ -306,71 +358,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[buf]), (uint32_t)(g >> 1) & 1, wt.ns));
                 if (!ok) break;
                 fence_after_sync();
+                const uint32_t at = tmem + buf * BN + from;
+                uint32_t r[2][32];
+                ld_issue(at, r[0]);
 #pragma unroll
-                for (int ch = 0; ch < HALF / 16; ++ch) {
-                    float v[16];
-                    tmem_ld(tmem + buf * BN + from + 16 * ch, v);
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) acc[16 * ch + c] = fmaf(v[c], scale, acc[16 * ch + c]);
+                for (int ch = 0; ch < HALF / 32; ++ch) {  // the next columns load while these are added
+                    ld_wait(r[ch & 1]);
+                    if (ch + 1 < HALF / 32) ld_issue(at + 32 * (ch + 1), r[(ch + 1) & 1]);
+                    if (ch + 1 == HALF / 32) {
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+                    }
+                    add_scaled(acc + 16 * ch, r[ch & 1], scale);
                 }
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
                 scale = next;
             }
             if (!ok) {
                 if (lane == 0) give_up();  // products may still be in flight: the drain below waits for them
                 break;
             }
-            // the warp's 32 rows leave in pieces of 128 bytes of columns
-            constexpr int PIECE = 128 / (int)sizeof(out_t);
+            if (store_bytes >= 16) {  // a thread's row of HALF columns, in whole sectors where rows allow it
+                constexpr int PER = 16 / (int)sizeof(out_t);
+                if (m < p.M) {
+                    out_t *to = p.out + (size_t)m * p.N + n0;
 #pragma unroll
-            for (int c0 = 0; c0 < HALF; c0 += PIECE) {
-                if (n0 + c0 >= p.N) break;
-                if (tiled_out) {
-                    bulk_wait_read();  // the previous piece has left the staging (lane 0's own copies)
-                    __syncwarp();
+                    for (int c = 0; c < HALF; c += 2 * PER) {
+                        io::Unit<out_t, PER> x[2];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        uint4 w;
-                        if constexpr (sizeof(out_t) == 2) {
-                            io::Unit<__nv_bfloat16, 8> x;
-                            float f[8];
+                        for (int h = 0; h < 2; ++h) {
+                            float f[PER];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = acc[c0 + 8 * u + e];
-                            x.set(f);
-                            w = x.w;
-                        } else {
-                            w = make_uint4(__float_as_uint(acc[c0 + 4 * u]), __float_as_uint(acc[c0 + 4 * u + 1]),
-                                           __float_as_uint(acc[c0 + 4 * u + 2]), __float_as_uint(acc[c0 + 4 * u + 3]));
+                            for (int e = 0; e < PER; e += 2)
+                                f[e] = acc[(c + h * PER + e) / 2].x, f[e + 1] = acc[(c + h * PER + e) / 2].y;
+                            x[h].set(f);
                         }
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = w;
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && m0 + quarter * 32 < p.M) {
-                        tma_store_2d(&tm_out, stage_u32, n0 + c0, m0 + quarter * 32);
-                        bulk_commit();
-                    }
-                } else {  // rows whose stride is no multiple of 16 bytes: transposed through the staging
-                    __syncwarp();
-                    float *t = reinterpret_cast<float *>(stage);
-#pragma unroll
-                    for (int q = 0; q < PIECE; q += 32) {
-                        __syncwarp();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) t[lane * 32 + (c ^ lane)] = acc[c0 + q + c];
-                        __syncwarp();
-                        const int n = n0 + c0 + q + lane;
-                        for (int r = 0; r < 32; ++r) {
-                            const int row = m0 + quarter * 32 + r;
-                            if (row < p.M && n < p.N) io::st(p.out + (size_t)row * p.N + n, t[r * 32 + (lane ^ r)]);
+                        if (store_bytes == 32 && n0 + c + 2 * PER <= p.N) {
+                            store32(to + c, x[0].w, x[1].w);
+                        } else {  // N is a multiple of PER
+                            if (n0 + c < p.N) store16(to + c, x[0].w);
+                            if (n0 + c + PER < p.N) store16(to + c + PER, x[1].w);
                         }
                     }
                 }
+            } else {  // rows that are not aligned: 32 x 32 sums at a time, transposed through shared memory
+#pragma unroll
+                for (int q = 0; q < HALF; q += 32) {
+                    if (n0 + q >= p.N) break;
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) stage[lane * 32 + (c ^ lane)] = c & 1 ? acc[(q + c) / 2].y : acc[(q + c) / 2].x;
+                    __syncwarp();
+                    const int n = n0 + q + lane;
+                    out_t *to = p.out + (size_t)(m0 + quarter * 32) * p.N + n;
+                    const int rows = n < p.N ? min(32, p.M - m0 - quarter * 32) : 0;
+#pragma unroll 8
+                    for (int r = 0; r < rows; ++r) io::st(to + (size_t)r * p.N, stage[r * 32 + (lane ^ r)]);
+                }
             }
         }
-        if (tiled_out) bulk_wait_read();  // before the staging goes
     }
     // drain: after an expired wait, the copies and products in flight land before the CTA exits
     __syncthreads();
@@ -387,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, 2 * BN);
 }
 
-bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, long long cols, long long rows, long long stride, int box_cols,
-            int box_rows)
+// e4m3 rows of K values as boxes of 128 rows x 128 values
+bool encode(CUtensorMap *map, const void *base, int K, int rows)
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *ptr = nullptr;
@@ -398,29 +444,23 @@ bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, long l
             ptr = nullptr;
         return (PFN_cuTensorMapEncodeTiled_v12000)ptr;
     }();
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, steps[2] = {1, 1};
-    return fn && fn(map, type, 2, const_cast<void *>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)K};
+    const cuuint32_t box[2] = {kBlock, STAGE_ROWS}, steps[2] = {1, 1};
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, steps,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename out_t, int BN>
 cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l)
 {
-    CUtensorMap ma, mw, mo;
-    if (!encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a, p.K, p.M, p.K, kBlock, BM) ||
-        !encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.K, p.N, p.K, kBlock, STAGE_ROWS))
-        return cudaErrorInvalidValue;
-    const long long stride = (long long)p.N * sizeof(out_t);
-    const bool tiled = stride % 16 == 0;
-    if (!tiled) mo = ma;  // not used
-    else if (!encode(&mo, sizeof(out_t) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.out, p.N, p.M,
-                     stride, 128 / (int)sizeof(out_t), 32))
-        return cudaErrorInvalidValue;
-    const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+    CUtensorMap ma, mw;
+    if (!encode(&ma, p.a, p.K, p.M) || !encode(&mw, p.w, p.K, p.N)) return cudaErrorInvalidValue;
+    const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN), stride = (long long)p.N * sizeof(out_t);
+    const int store_bytes = stride % 32 == 0 && (uintptr_t)p.out % 32 == 0 ? 32 : stride % 16 == 0 ? 16 : 1;
     const Waits wt{l.d_status, l.wait_ns > 0 ? (unsigned long long)l.wait_ns : 100000000ull};
     product_kernel<out_t, BN><<<(unsigned)(tiles < l.sm_count ? tiles : l.sm_count), kThreads, Layout<BN>::SMEM, l.timer->stream>>>(
-        ma, mw, mo, p, wt, tiled ? 1 : 0);
+        ma, mw, p, wt, store_bytes);
     return cudaGetLastError();
 }
 
