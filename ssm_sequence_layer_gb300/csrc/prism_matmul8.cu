@@ -164,9 +164,9 @@ static_assert(128 * kIssueRegs + 256 * kEpilogueRegs <= kThreads * 168, "registe
 
 template <int BN>
 struct Layout {
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int STAGES = BN == 256 ? 3 : 5;
     static constexpr uint32_t A_BYTES = BM * kBlock, B_BYTES = BN * kBlock, STAGE = A_BYTES + B_BYTES;
-    static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging of 32 x 32 sums, for rows that are not aligned
+    static constexpr uint32_t PIECE = 4096, OUT_WARP = 2 * PIECE;  // a warp's staging: pieces of 32 rows x 128 bytes of output
     static constexpr uint32_t OFF_OUT = STAGES * STAGE;
     static constexpr uint32_t SMEM = OFF_OUT + kEpilogueWarps * OUT_WARP + 1024;  // + alignment slack
     static_assert(SMEM <= 232448 && OFF_OUT % 1024 == 0, "layout");
@@ -230,19 +230,10 @@ __device__ __forceinline__ void add_scaled(float2 *acc, const uint32_t (&r)[32],
     }
 }
 
-// 16 or 32 bytes to global memory
-__device__ __forceinline__ void store16(void *p, uint4 a) { *reinterpret_cast<uint4 *>(p) = a; }
-__device__ __forceinline__ void store32(void *p, uint4 a, uint4 b)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
-                 "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
-}
-
 template <typename out_t, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Params<out_t> p,
-                   const Waits wt, int store_bytes)
+    product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_out, const Params<out_t> p, const Waits wt, int tiled_out)
 {
     using L = Layout<BN>;
     constexpr int STAGES = L::STAGES, HALF = BN / 2;
@@ -271,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_tmap(&tm_a);
         prefetch_tmap(&tm_w);
+        if (tiled_out) prefetch_tmap(&tm_out);
     }
     if (warp == 0) tmem_alloc(smem_u32(&tmem_base_s), 2 * BN);
     fence_before_sync();
@@ -338,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t from = ((uint32_t)(quarter * 32) << 16) + half * HALF;
-        float *stage = reinterpret_cast<float *>(sm + L::OFF_OUT + (warp - 4) * L::OUT_WARP);
+        uint8_t *stage = sm + L::OFF_OUT + (warp - 4) * L::OUT_WARP;
+        const uint32_t stage_u32 = smem_u32(stage);
         long long g = 0;
         bool ok = true;
         for (int i = 0; i < my_tiles && ok; ++i) {
@@ -378,45 +371,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) give_up();  // products may still be in flight: the drain below waits for them
                 break;
             }
-            if (store_bytes >= 16) {  // a thread's row of HALF columns, in whole sectors where rows allow it
-                constexpr int PER = 16 / (int)sizeof(out_t);
-                if (m < p.M) {
-                    out_t *to = p.out + (size_t)m * p.N + n0;
+            if (tiled_out) {
+                // The sums go to shared memory and leave by TMA while the next tile is added up: a piece is 32 rows x
+                // 128 bytes, and the staging holds two, all of the warp's bf16 columns.
+                constexpr int COLS = 128 / (int)sizeof(out_t), PER = 16 / (int)sizeof(out_t);
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 2 * PER) {
-                        io::Unit<out_t, PER> x[2];
+                for (int c0 = 0; c0 < HALF; c0 += COLS) {
+                    const int piece = c0 / COLS & 1;
+                    if (piece == 0) bulk_wait_read();  // the pieces before have left the staging (lane 0's own copies)
+                    __syncwarp();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float f[PER];
+                    for (int u = 0; u < 8; ++u) {
+                        float f[PER];
 #pragma unroll
-                            for (int e = 0; e < PER; e += 2)
-                                f[e] = acc[(c + h * PER + e) / 2].x, f[e + 1] = acc[(c + h * PER + e) / 2].y;
-                            x[h].set(f);
-                        }
-                        if (store_bytes == 32 && n0 + c + 2 * PER <= p.N) {
-                            store32(to + c, x[0].w, x[1].w);
-                        } else {  // N is a multiple of PER
-                            if (n0 + c < p.N) store16(to + c, x[0].w);
-                            if (n0 + c + PER < p.N) store16(to + c + PER, x[1].w);
-                        }
+                        for (int e = 0; e < PER; e += 2)
+                            f[e] = acc[(c0 + PER * u + e) / 2].x, f[e + 1] = acc[(c0 + PER * u + e) / 2].y;
+                        io::Unit<out_t, PER> x;
+                        x.set(f);
+                        *reinterpret_cast<uint4 *>(stage + piece * L::PIECE + lane * 128 + ((u ^ (lane & 7)) << 4)) = x.w;
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && m0 + quarter * 32 < p.M && n0 + c0 < p.N) {
+                        tma_store_2d(&tm_out, stage_u32 + piece * L::PIECE, n0 + c0, m0 + quarter * 32);
+                        bulk_commit();
                     }
                 }
             } else {  // rows that are not aligned: 32 x 32 sums at a time, transposed through shared memory
+                float *t = reinterpret_cast<float *>(stage);
 #pragma unroll
                 for (int q = 0; q < HALF; q += 32) {
                     if (n0 + q >= p.N) break;
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) stage[lane * 32 + (c ^ lane)] = c & 1 ? acc[(q + c) / 2].y : acc[(q + c) / 2].x;
+                    for (int c = 0; c < 32; ++c) t[lane * 32 + (c ^ lane)] = c & 1 ? acc[(q + c) / 2].y : acc[(q + c) / 2].x;
                     __syncwarp();
                     const int n = n0 + q + lane;
                     out_t *to = p.out + (size_t)(m0 + quarter * 32) * p.N + n;
                     const int rows = n < p.N ? min(32, p.M - m0 - quarter * 32) : 0;
 #pragma unroll 8
-                    for (int r = 0; r < rows; ++r) io::st(to + (size_t)r * p.N, stage[r * 32 + (lane ^ r)]);
+                    for (int r = 0; r < rows; ++r) io::st(to + (size_t)r * p.N, t[r * 32 + (lane ^ r)]);
                 }
             }
         }
+        if (tiled_out) bulk_wait_read();  // before the staging goes
     }
     // drain: after an expired wait, the copies and products in flight land before the CTA exits
     __syncthreads();
@@ -433,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, 2 * BN);
 }
 
-// e4m3 rows of K values as boxes of 128 rows x 128 values
-bool encode(CUtensorMap *map, const void *base, int K, int rows)
+// A row-major matrix as boxes of box_rows rows x 128 bytes, 128-byte swizzled in shared memory
+bool encode(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, int cols, int rows, int box_rows)
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *ptr = nullptr;
@@ -444,23 +442,29 @@ bool encode(CUtensorMap *map, const void *base, int K, int rows)
             ptr = nullptr;
         return (PFN_cuTensorMapEncodeTiled_v12000)ptr;
     }();
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)K};
-    const cuuint32_t box[2] = {kBlock, STAGE_ROWS}, steps[2] = {1, 1};
-    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, steps,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    return fn && fn(map, type, 2, const_cast<void *>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename out_t, int BN>
 cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l)
 {
-    CUtensorMap ma, mw;
-    if (!encode(&ma, p.a, p.K, p.M) || !encode(&mw, p.w, p.K, p.N)) return cudaErrorInvalidValue;
-    const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN), stride = (long long)p.N * sizeof(out_t);
-    const int store_bytes = stride % 32 == 0 && (uintptr_t)p.out % 32 == 0 ? 32 : stride % 16 == 0 ? 16 : 1;
+    CUtensorMap ma, mw, mo;
+    if (!encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.a, p.K, p.M, BM) ||
+        !encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.w, p.K, p.N, STAGE_ROWS))
+        return cudaErrorInvalidValue;
+    const bool tiled = (long long)p.N * sizeof(out_t) % 16 == 0;  // TMA takes rows whose stride is a multiple of 16 bytes
+    if (!tiled)
+        mo = ma;  // not used
+    else if (!encode(&mo, sizeof(out_t) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sizeof(out_t), p.out,
+                     p.N, p.M, 32))
+        return cudaErrorInvalidValue;
+    const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
     const Waits wt{l.d_status, l.wait_ns > 0 ? (unsigned long long)l.wait_ns : 100000000ull};
     product_kernel<out_t, BN><<<(unsigned)(tiles < l.sm_count ? tiles : l.sm_count), kThreads, Layout<BN>::SMEM, l.timer->stream>>>(
-        ma, mw, p, wt, store_bytes);
+        ma, mw, mo, p, wt, tiled ? 1 : 0);
     return cudaGetLastError();
 }
 
