@@ -26,7 +26,7 @@ struct Params {
 };
 
 // ---------------------------------------------------------------------------------------------
-// Few rows (M <= 32): the weights' bytes bound the product, every weight is used M times at most.  A
+// Few rows (M <= 16): the weights' bytes bound the product, every weight is used M times at most.  A
 // warp takes 16 rows of w8 as the A operand of m16n8k32 products straight from global memory to
 // registers (16 bytes of a row per lane and load, four loads for a block of 16 x 128), and 8 NT rows
 // of a8 as B operands.  The products' k order is a free choice as long as both operands share it: the
@@ -152,14 +152,7 @@ void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
 // a_scale[m, b] w_scale[j / 128, b] and add it to the sums in their registers (one row and BN / 2
 // columns per thread, two columns per instruction) while the next block's products run into the other
 // accumulator.  Per block the tensor core needs 128 BN 128 / 8192 cycles and the scaled additions
-// 128 BN / 256.
-//
-// What the tensor cores ask of the L2 is the limit of a lone CTA (16 KB of a8 and 32 KB of w8 for each
-// block of a 128 x 256 tile: loading alone took 110 us of 4096 x 50048 x 768), so two CTAs form a
-// cluster (CL = 2) that works on two tiles of the same columns: each loads its own rows of a8 and half of
-// the w8 tile, which it sends to both.  A stage is free once the products of both have read it.
-//
-// The sums take more registers than an even share, so the four warps of the
+// 128 BN / 256.  The sums take more registers than an even share, so the four warps of the
 // issuing group hand theirs over.
 using namespace prism::tc;
 
@@ -189,29 +182,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
 
 // K-major 128B-swizzled operand: 16-byte core-matrix rows, 1024-byte groups of 8 rows
 __device__ __forceinline__ uint64_t operand(uint32_t addr) { return sdesc(addr, 16, 1024); }
-
-// the same box into both CTAs of a pair, at the same place, counted by the barrier at the same place
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap *map, uint32_t mbar, int c0, int c1)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], "
-        "%5;" ::"r"(dst),
-        "l"((uint64_t)map), "r"(mbar), "r"(c0), "r"(c1), "h"((uint16_t)3)
-        : "memory");
-}
-
-// an arrival on the barrier of both CTAs of a pair once the products issued so far have completed
-__device__ __forceinline__ void mma_commit_both(uint32_t mbar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
 
 // instruction descriptor: e4m3 A and B (format 0), fp32 accumulator
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
@@ -260,7 +230,7 @@ __device__ __forceinline__ void add_scaled(float2 *acc, const uint32_t (&r)[32],
     }
 }
 
-template <typename out_t, int BN, int CL>
+template <typename out_t, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_out, const Params<out_t> p, const Waits wt, int tiled_out)
@@ -274,11 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
-    static_assert(BN / CL % STAGE_ROWS == 0, "a CTA's share of the w8 tile");
-    const int rank = CL > 1 ? blockIdx.x % CL : 0, me = blockIdx.x / CL, all = gridDim.x / CL;
-    const int groups_m = (tiles_m + CL - 1) / CL;  // a pair's second tile may lie behind the last row
-    const long long tiles = (long long)groups_m * tiles_n;
-    const int my_tiles = tiles > me ? (int)((tiles - 1 - me) / all) + 1 : 0;
+    const long long tiles = (long long)tiles_m * tiles_n;
+    const int my_tiles = tiles > blockIdx.x ? (int)((tiles - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
     const long long total = (long long)my_tiles * p.KB;
     const uint32_t sbase = smem_u32(sm);
 
@@ -286,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         abort_s = 0;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&freed[s]), CL);
+            mbar_init(smem_u32(&freed[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
@@ -299,18 +266,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0) tmem_alloc(smem_u32(&tmem_base_s), 2 * BN);
     fence_before_sync();
-    if constexpr (CL > 1)
-        cluster_sync();  // the other CTA's barriers are ready
-    else
-        __syncthreads();
+    __syncthreads();
     fence_after_sync();
     const uint32_t tmem = tmem_base_s;
 
     // tiles of one column of tiles run at the same time on neighbouring CTAs and share w8 in L2
     auto tile_at = [&](int i, int &m0, int &n0) {
-        const long long t = me + (long long)i * all;
-        m0 = ((int)(t % groups_m) * CL + rank) * BM;
-        n0 = (int)(t / groups_m) * BN;
+        const long long t = (long long)blockIdx.x + (long long)i * gridDim.x;
+        m0 = (int)(t % tiles_m) * BM;
+        n0 = (int)(t / tiles_m) * BN;
     };
     auto give_up = [&] {
         atomicCAS(wt.status, 0, kDevTimeout);
@@ -318,64 +282,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     long long issued = 0;  // the issuing threads' counts of steps, for the drain
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (tid == 32) {  // ---- operand loads ----
-            int s = 0, i = 0, b = 0, m0 = 0, n0 = 0;
-            uint32_t round = 0;
-            for (long long g = 0; g < total; ++g) {
-                if (b == 0) tile_at(i, m0, n0);
-                if (round > 0 && !mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns)) {
-                    give_up();
-                    break;
-                }
-                if (*(volatile int *)&abort_s) break;
-                const uint32_t mb = smem_u32(&full[s]), at = sbase + s * L::STAGE;
-                mbar_expect_tx(mb, L::STAGE);
-                tma_load_2d(at, &tm_a, mb, b * kBlock, m0);
-#pragma unroll
-                for (int h = rank; h < BN / STAGE_ROWS; h += CL) {
-                    const uint32_t to = at + L::A_BYTES + h * STAGE_ROWS * kBlock;
-                    if constexpr (CL > 1)
-                        tma_load_2d_both(to, &tm_w, mb, b * kBlock, n0 + h * STAGE_ROWS);
-                    else
-                        tma_load_2d(to, &tm_w, mb, b * kBlock, n0 + h * STAGE_ROWS);
-                }
-                issued = g + 1;
-                if (++s == STAGES) s = 0, ++round;
-                if (++b == p.KB) b = 0, ++i;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (tid == 32) {  // ---- operand loads ----
+        int s = 0, i = 0, b = 0, m0 = 0, n0 = 0;
+        uint32_t round = 0;
+        for (long long g = 0; g < total; ++g) {
+            if (b == 0) tile_at(i, m0, n0);
+            if (round > 0 && !mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns)) {
+                give_up();
+                break;
             }
-            if constexpr (CL > 1)  // the other CTA's last arrivals here, before this CTA may leave
-                for (long long g = max(0LL, issued - STAGES); g < issued; ++g)
-                    if (!mbar_wait(smem_u32(&freed[g % STAGES]), (uint32_t)(g / STAGES) & 1, wt.ns)) {
-                        give_up();
-                        break;
-                    }
-        } else if (tid == 0) {  // ---- products ----
-            int s = 0;
-            uint32_t round = 0;
-            for (long long g = 0; g < total; ++g) {
-                const int buf = (int)(g & 1);
-                bool ok = g < 2 || mbar_wait(smem_u32(&acc_empty[buf]), (uint32_t)((g - 2) >> 1) & 1, wt.ns);
-                ok = ok && mbar_wait(smem_u32(&full[s]), round & 1, wt.ns);
-                if (!ok) {
-                    give_up();
-                    break;
-                }
-                if (*(volatile int *)&abort_s) break;
-                fence_after_sync();
-                const uint64_t da = operand(sbase + s * L::STAGE), db = operand(sbase + s * L::STAGE + L::A_BYTES);
+            if (*(volatile int *)&abort_s) break;
+            const uint32_t mb = smem_u32(&full[s]), at = sbase + s * L::STAGE;
+            mbar_expect_tx(mb, L::STAGE);
+            tma_load_2d(at, &tm_a, mb, b * kBlock, m0);
 #pragma unroll
-                for (int j = 0; j < kBlock / 32; ++j)
-                    mma_f8(tmem + buf * BN, da + 2 * j, db + 2 * j, idesc_e4m3(BM, BN), j > 0);
-                if constexpr (CL > 1)
-                    mma_commit_both(smem_u32(&freed[s]));
-                else
-                    mma_commit(smem_u32(&freed[s]));
-                mma_commit(smem_u32(&acc_full[buf]));
-                issued = g + 1;
-                if (++s == STAGES) s = 0, ++round;
-            }
+            for (int h = 0; h < BN / STAGE_ROWS; ++h)
+                tma_load_2d(at + L::A_BYTES + h * STAGE_ROWS * kBlock, &tm_w, mb, b * kBlock, n0 + h * STAGE_ROWS);
+            issued = g + 1;
+            if (++s == STAGES) s = 0, ++round;
+            if (++b == p.KB) b = 0, ++i;
         }
+    } else if (tid == 0) {  // ---- products ----
+        int s = 0;
+        uint32_t round = 0;
+        for (long long g = 0; g < total; ++g) {
+            const int buf = (int)(g & 1);
+            bool ok = g < 2 || mbar_wait(smem_u32(&acc_empty[buf]), (uint32_t)((g - 2) >> 1) & 1, wt.ns);
+            ok = ok && mbar_wait(smem_u32(&full[s]), round & 1, wt.ns);
+            if (!ok) {
+                give_up();
+                break;
+            }
+            if (*(volatile int *)&abort_s) break;
+            fence_after_sync();
+            const uint64_t da = operand(sbase + s * L::STAGE), db = operand(sbase + s * L::STAGE + L::A_BYTES);
+#pragma unroll
+            for (int j = 0; j < kBlock / 32; ++j)
+                mma_f8(tmem + buf * BN, da + 2 * j, db + 2 * j, idesc_e4m3(BM, BN), j > 0);
+            mma_commit(smem_u32(&freed[s]));
+            mma_commit(smem_u32(&acc_full[buf]));
+            issued = g + 1;
+            if (++s == STAGES) s = 0, ++round;
+        }
+    }
     } else {  // ---- scaled sums: lane quarter warp % 4, columns of half (warp - 4) / 4 ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
         const int quarter = warp & 3, half = (warp - 4) >> 2;
@@ -471,19 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (abort_s && issued > 0) {
         const long long last = issued - 1;
         if (tid == 0)  // products complete in order
-            (void)mbar_wait(smem_u32(&acc_full[last & 1]), (uint32_t)(last >> 1) & 1, 1000000000ull);
+            (void)mbar_wait(smem_u32(&freed[last % STAGES]), (uint32_t)(last / STAGES) & 1, 1000000000ull);
         if (tid == 32)
             for (long long g = last >= STAGES ? last - STAGES + 1 : 0; g <= last; ++g)
                 (void)mbar_wait(smem_u32(&full[g % STAGES]), (uint32_t)(g / STAGES) & 1, 1000000000ull);
-        if (CL > 1 && tid == 32)  // what was sent to the other CTA lands there at about the same time
-            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000ull;) {}
     }
-    __syncwarp();
     fence_before_sync();
-    if constexpr (CL > 1)
-        cluster_sync();  // no copy or arrival of the other CTA is on its way here any more
-    else
-        __syncthreads();
+    __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 2 * BN);
 }
 
@@ -504,7 +448,7 @@ bool encode(CUtensorMap *map, CUtensorMapDataType type, int size, const void *ba
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename out_t, int BN, int CL>
+template <typename out_t, int BN>
 cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l)
 {
     CUtensorMap ma, mw, mo;
@@ -517,20 +461,11 @@ cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l)
     else if (!encode(&mo, sizeof(out_t) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, sizeof(out_t), p.out,
                      p.N, p.M, 32))
         return cudaErrorInvalidValue;
-    const long long tiles = (long long)((p.M + BM * CL - 1) / (BM * CL)) * ((p.N + BN - 1) / BN);
+    const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
     const Waits wt{l.d_status, l.wait_ns > 0 ? (unsigned long long)l.wait_ns : 100000000ull};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < l.sm_count / CL ? tiles : l.sm_count / CL) * CL);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<BN>::SMEM;
-    cfg.stream = l.timer->stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CL;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = CL > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, product_kernel<out_t, BN, CL>, ma, mw, mo, p, wt, tiled ? 1 : 0);
+    product_kernel<out_t, BN><<<(unsigned)(tiles < l.sm_count ? tiles : l.sm_count), kThreads, Layout<BN>::SMEM, l.timer->stream>>>(
+        ma, mw, mo, p, wt, tiled ? 1 : 0);
+    return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -570,40 +505,37 @@ cudaError_t product(const Matmul8Args &a, const TokenLaunch &l)
                           (a.K + kBlock - 1) / kBlock};
     cudaError_t e;
     l.timer->begin("matmul8");
-    if (a.M <= 32) {
+    // Few rows: 8 and 16 of N x K = 50048 x 768 take 11.6 and 18.1 us here, 17 take 15.8 in tiles; of 4096 x 4096 16
+    // take 9.9 here, 17 take 18.6 in tiles.  With four operands of 8 rows the loads wait for registers (32
+    // rows: 22.8 us of 50048 x 768, 57 of 8192 x 8192; in tiles 16.3 and 31).
+    if (a.M <= 16) {
         if (a.M <= 8) launch_skinny<out_t, 1>(p, l.sm_count, l.timer->stream);
-        else if (a.M <= 16) launch_skinny<out_t, 2>(p, l.sm_count, l.timer->stream);
-        else launch_skinny<out_t, 4>(p, l.sm_count, l.timer->stream);
+        else launch_skinny<out_t, 2>(p, l.sm_count, l.timer->stream);
         e = cudaGetLastError();
     } else {
-        // wide tiles halve the reads of a8; narrow ones where wide ones would leave SMs without a tile
-        const int rows = (a.M + BM - 1) / BM;
-        const long long wide = (long long)rows * ((a.N + 255) / 256);
-        if (wide < l.sm_count) e = launch_product<out_t, 128, 1>(p, l);
-        // pairs unless an odd number of row tiles would leave too many second halves empty
-        else if (rows % 2 == 0 || rows >= 8) e = launch_product<out_t, 256, 2>(p, l);
-        else e = launch_product<out_t, 256, 1>(p, l);
+        // The width of tiles that takes less time: turns of the SMs times the rows that a block brings in.
+        const long long rows = (a.M + BM - 1) / BM;
+        auto time = [&](long long bn) { return (rows * ((a.N + bn - 1) / bn) + l.sm_count - 1) / l.sm_count * (bn + BM); };
+        e = time(256) <= time(128) ? launch_product<out_t, 256>(p, l) : launch_product<out_t, 128>(p, l);
     }
     l.timer->end();
     return e;
 }
 
-template <typename out_t, int BN, int CL>
+template <typename out_t, int BN>
 cudaError_t prepare()
 {
-    return cudaFuncSetAttribute(product_kernel<out_t, BN, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<BN>::SMEM);
+    return cudaFuncSetAttribute(product_kernel<out_t, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<BN>::SMEM);
 }
 
 }  // namespace mm8
 
 cudaError_t matmul8_prepare()
 {
-    cudaError_t e = mm8::prepare<float, 128, 1>();
-    if (e == cudaSuccess) e = mm8::prepare<float, 256, 1>();
-    if (e == cudaSuccess) e = mm8::prepare<float, 256, 2>();
-    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 128, 1>();
-    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 256, 1>();
-    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 256, 2>();
+    cudaError_t e = mm8::prepare<float, 128>();
+    if (e == cudaSuccess) e = mm8::prepare<float, 256>();
+    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 128>();
+    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 256>();
     return e;
 }
 

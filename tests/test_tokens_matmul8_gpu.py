@@ -49,7 +49,7 @@ def reference(a8, sa, w8, sw):
 SHAPES = [(1, 1, 16), (1, 64, 64), (1, 1000, 768), (4, 777, 272), (8, 5000, 128), (9, 130, 400), (16, 640, 1040), (17, 129, 144),
           (24, 96, 4096), (31, 3000, 256), (33, 500, 768), (64, 2048, 512), (65, 333, 128), (100, 256, 2064), (127, 129, 144), (128, 128, 128),
           (129, 257, 1040), (200, 40, 768), (256, 512, 384), (300, 4626, 256), (1000, 136, 160), (2050, 264, 768), (5000, 16, 64), (1000, 5000, 400),
-          (1100, 6000, 272), (200, 20000, 144), (384, 30000, 128), (5000, 1111, 400)]
+          (1100, 6000, 272), (200, 20000, 144), (384, 30000, 128), (5000, 1111, 400), (3, 100, 4096), (12, 40, 8192), (2, 20000, 528), (8, 2500, 1024), (16, 33, 2000), (17, 3000, 512)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -85,7 +85,7 @@ def test_sums_keep_32_bits():
         assert torch.all(got == 448.0 * 448.0 + 127 / 64), rows
 
 
-@pytest.mark.parametrize("M,N", [(600, 1000), (1100, 8000)])  # single CTAs; pairs
+@pytest.mark.parametrize("M,N", [(600, 1000), (1100, 8000)])
 def test_an_expired_wait_is_reported(M, N):
     """With a bound of 1 ns every wait runs out: the status says so, and the handle works again after it."""
     a8, sa, w8, sw = draw(M, N, 768, 1)
