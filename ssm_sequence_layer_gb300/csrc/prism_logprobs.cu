@@ -25,7 +25,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.38953139e38f;  // the lowest bfloat16 value
 constexpr float kFar = -1e4f;         // 2^kFar = 0, and kFar times anything in range is finite
 constexpr int kLogClusterMax = 3, kTopMax = 32;
-constexpr int kCandidates = 1024;
+constexpr int kCandidates = 1024, kFew = 160;
 constexpr int kBatchesMax = 96;       // batches of a slice whose largest logits are kept
 
 __device__ __forceinline__ float ex2(float x)
@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
     __shared__ Part mine;                                    // this CTA's part
     __shared__ unsigned long long best[TOP ? kTopMax : 1];   // its first k keys
     __shared__ unsigned long long cand[TOP ? kCandidates : 1];
-    __shared__ float group_top[32];
+    __shared__ float thread_top[TOP ? kWarps : 1][32];
+    __shared__ unsigned long long group_key[TOP ? kWarps : 1][32];
     __shared__ int found;
     __shared__ float threshold;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -262,17 +263,13 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
         *reinterpret_cast<logit_t *>(&x[0].w) = sl.x[single];
         sh.template add<R, 1>(x, c2);
     }
-    // The warp's largest logit, the thread's sums brought onto it, and the warp's sums.  On the way, the
-    // largest logit of each of 32 groups of threads.
-    constexpr int GROUP = kThreads / 32;
+    // the warp's largest logit, the thread's sums brought onto it, and the warp's sums
     float warp_top = sh.top;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        if (TOP && o == GROUP) {
-            if (lane % GROUP == 0) group_top[tid / GROUP] = warp_top;
-            if (tid == 0) found = 0;
-        }
-        warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, o));
+    for (int o = 1; o < 32; o <<= 1) warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, o));
+    if constexpr (TOP) {
+        thread_top[warp][lane] = sh.top;
+        if (tid == 0) found = 0;
     }
     Part r = sh.part(warp_top, c2);
 #pragma unroll
@@ -293,13 +290,15 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
         if (lane == 0) mine = r;
     }
     if constexpr (TOP) {
-        // The k-th largest of the 32 groups' largest logits: at least k of the slice's logits reach it, and
-        // few more.  Those are collected and ordered by counting.
+        // A lane's threads are a group, which holds every 32nd unit.  The k-th largest of the 32 groups' largest
+        // logits: at least k of the slice's logits reach it, and few more (about 130 of any number at k = 32).
+        // Those are collected and ordered by counting.
         if (warp == 1) {
-            const float g = group_top[lane];
+            float g = thread_top[0][lane];
+            for (int w = 1; w < kWarps; ++w) g = fmaxf(g, thread_top[w][lane]);
             int above = 0;
             for (int o = 0; o < 32; ++o) {
-                const float other = group_top[o];
+                const float other = __shfl_sync(0xffffffffu, g, o);
                 above += other > g || (other == g && o < lane);
             }
             if (above == p.k - 1) threshold = g;
@@ -335,7 +334,64 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
         if (single >= 0) offer(io::ld(sl.x + single), single);
         if (tid < kTopMax) best[tid] = 0;
         __syncthreads();
-        const int count = found;
+        int count = found;
+        // The k-th largest of the groups' largest keys, for keys that a thread offers by `mine`; ends with a
+        // barrier.  Keys differ, so at least k of them reach it, however many logits are equal.
+        auto key_threshold = [&](unsigned long long mine) {
+            group_key[warp][lane] = mine;
+            __syncthreads();
+            unsigned long long g = group_key[0][lane];
+            for (int w = 1; w < kWarps; ++w) g = max(g, group_key[w][lane]);
+            int above = 0;
+            for (int o = 0; o < 32; ++o) above += __shfl_sync(0xffffffffu, g, o) > g;
+            // the group that has k - 1 above it; with fewer than k groups that hold a key, 0
+            unsigned long long at = above == p.k - 1 ? g : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) at = max(at, __shfl_xor_sync(0xffffffffu, at, o));
+            if (tid == 0) found = 0;
+            __syncthreads();
+            return at;
+        };
+        auto for_each = [&](auto look) {  // this thread's live logits once more
+            for (int at = sl.u0 + tid; at < sl.u1; at += kThreads) {
+                U x;
+                x.w = __ldg(units + at);
+                float v[R::VEC];
+                x.get(v);
+#pragma unroll
+                for (int e = 0; e < R::VEC; ++e)
+                    if (!(v[e] <= kLowest || v[e] * p.inv_temperature == -INFINITY)) look(key_of(v[e], sl.first + at * R::VEC + e));
+            }
+            if (single >= 0) {
+                const float v = io::ld(sl.x + single);
+                if (!(v <= kLowest || v * p.inv_temperature == -INFINITY)) look(key_of(v, single));
+            }
+        };
+        if (count > kCandidates) {  // many equal logits: by keys instead of by values
+            unsigned long long mine_best = 0;
+            for_each([&](unsigned long long key) { mine_best = max(mine_best, key); });
+            const unsigned long long at = key_threshold(mine_best);
+            for_each([&](unsigned long long key) {
+                if (key < at) return;
+                const int to = atomicAdd(&found, 1);
+                if (to < kCandidates) cand[to] = key;
+            });
+            __syncthreads();
+            count = found;
+        } else if (count > kFew) {  // many candidates: the same choice among them
+            unsigned long long held[kCandidates / kThreads], mine_best = 0;
+#pragma unroll
+            for (int i = 0; i < kCandidates / kThreads; ++i) {
+                held[i] = tid + i * kThreads < count ? cand[tid + i * kThreads] : 0;
+                mine_best = max(mine_best, held[i]);
+            }
+            const unsigned long long at = key_threshold(mine_best);
+#pragma unroll
+            for (int i = 0; i < kCandidates / kThreads; ++i)
+                if (held[i] && held[i] >= at) cand[atomicAdd(&found, 1)] = held[i];
+            __syncthreads();
+            count = found;
+        }
         if (count <= kCandidates) {
             // order by counting; few candidates need one warp only
             if (count > 32 || warp == 0)
@@ -348,24 +404,13 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
             if (count > 32) __syncthreads();
             __syncwarp();
         } else {
-            // many equal logits, or an order that the groups miss: the largest key below the last one, k times
+            // an order that the groups miss: the largest key below the last one, k times
             unsigned long long last = ~0ull;
             for (int i = 0; i < p.k; ++i) {
                 unsigned long long b = 0;
-                auto look = [&](float v, int id) {
-                    if (v <= kLowest || v * p.inv_temperature == -INFINITY) return;
-                    const unsigned long long key = key_of(v, id);
+                for_each([&](unsigned long long key) {
                     if (key < last && key > b) b = key;
-                };
-                for (int at = sl.u0 + tid; at < sl.u1; at += kThreads) {
-                    U x;
-                    x.w = __ldg(units + at);
-                    float v[R::VEC];
-                    x.get(v);
-#pragma unroll
-                    for (int e = 0; e < R::VEC; ++e) look(v[e], sl.first + at * R::VEC + e);
-                }
-                if (single >= 0) look(io::ld(sl.x + single), single);
+                });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
                 __syncthreads();  // cand is free: the round before has been read

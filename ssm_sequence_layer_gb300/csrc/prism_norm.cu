@@ -211,11 +211,12 @@ struct BackwardParams {
 };
 
 // Rows of 16-byte units in registers, as in forward_kernel: one pass gives dx and this block's part of
-// the weight's gradient, which each thread holds for its own columns over all rows of the block.
-template <typename io_t, int WPR, int UPL>
+// the weight's gradient, which each thread holds for its own columns over all rows of the block.  Rows
+// that are not made of 16-byte units go through it one value at a time (VEC = 1).
+template <typename io_t, int WPR, int UPL, int VEC = 16 / (int)sizeof(io_t)>
 __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) backward_kernel(const BackwardParams<io_t> p)
 {
-    constexpr int VEC = 16 / (int)sizeof(io_t), G = 32 * WPR, ROWS = WPR == 1 ? kThreads / 32 : 1;
+    constexpr int G = 32 * WPR, ROWS = WPR == 1 ? kThreads / 32 : 1;
     using U = io::Unit<io_t, VEC>;
     __shared__ float2 parts[2][WPR];
     __shared__ float columns[WPR == 1 ? ROWS : 1][WPR == 1 ? G * UPL * VEC : 1];
@@ -455,15 +456,24 @@ cudaError_t backward(const NormBackwardArgs &a, const NormWorkspace &w, const To
     BackwardParams<io_t> p{(const io_t *)a.sum, (const io_t *)a.weight, (const io_t *)a.dy, (const io_t *)a.dsum,
                            (io_t *)a.dx, w.stats, w.part, a.dweight, a.eps, a.n, a.D, 0};
     cudaStream_t s = l.timer->stream;
-    const bool held = a.n > 0 && pick<2>(a.D, 16 / (int)sizeof(io_t), [&](auto wpr, auto upl) {
-        constexpr int WPR = decltype(wpr)::value, UPL = decltype(upl)::value, threads = WPR == 1 ? kThreads : 32 * WPR;
+    auto go = [&](auto wpr, auto upl, auto vec) {
+        constexpr int WPR = decltype(wpr)::value, UPL = decltype(upl)::value, VEC = decltype(vec)::value;
+        constexpr int threads = WPR == 1 ? kThreads : 32 * WPR;
         const unsigned blocks =
-            resident_blocks<backward_kernel<io_t, WPR, UPL>>(threads, WPR == 1 ? kThreads / 32 : 1, a.n, l.sm_count, kSlabs);
+            resident_blocks<backward_kernel<io_t, WPR, UPL, VEC>>(threads, WPR == 1 ? kThreads / 32 : 1, a.n, l.sm_count, kSlabs);
         p.slabs = (int)blocks;
         l.timer->begin("norm_backward");
-        backward_kernel<io_t, WPR, UPL><<<blocks, threads, 0, s>>>(p);
+        backward_kernel<io_t, WPR, UPL, VEC><<<blocks, threads, 0, s>>>(p);
         l.timer->end();
-    });
+    };
+    constexpr int UNIT = 16 / (int)sizeof(io_t);
+    bool held = a.n > 0 && pick<2>(a.D, UNIT, [&](auto wpr, auto upl) { go(wpr, upl, Int<UNIT>()); });
+    if (!held && a.n > 0 && a.D <= 4096) {  // single values: 8 per thread of one, four or sixteen warps
+        if (a.D <= 256) go(Int<1>(), Int<8>(), Int<1>());
+        else if (a.D <= 1024) go(Int<4>(), Int<8>(), Int<1>());
+        else go(Int<16>(), Int<8>(), Int<1>());
+        held = true;
+    }
     if (!held && a.n > 0) {
         const unsigned rows = (a.n + kThreads / 32 - 1) / (kThreads / 32);
         p.slabs = min(kSlabsAny, a.n);

@@ -81,7 +81,7 @@ def check_forward(out, x, targets, c, k):
     (1, 1, 0, 1, 0, 1.0), (3, 2, 0, 32, 0, 0.7), (5, 33, 0, 5, 0.3, 1.3), (7, 100, 3, 32, 0.9, 1.0), (4, 1000, 0, 8, 0, 1.0),
     (300, 511, 1, 3, 0.1, 1.0), (16, 4099, 0, 20, 0.2, 2.0), (3, 50021, 27, 20, 0.1, 1.25), (2, 131072, 0, 32, 0, 1.0),
     (1, 300007, 0, 8, 0, 1.0), (640, 20000, 0, 4, 0, 1.0), (2, 262144, 5, 0, 0, 1.0), (400, 8193, 0, 0, 0.5, 1.0),
-    (2, 700001, 0, 16, 0, 1.0)])
+    (2, 700001, 0, 16, 0, 1.0), (143, 415, 0, 32, 0, 1.0), (55, 5381, 64, 32, 0, 1.0), (14, 5112, 3, 32, 0.4, 1.0), (9, 260, 0, 32, 0.5, 1.0)])
 def test_token_logprobs(io, n, V, pad, k, masked, c):
     x, targets = draw(n, V, io, n + V, pad, masked)
     with B.Tokens(n, 8, V, io=io) as t:
