@@ -25,7 +25,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.38953139e38f;  // the lowest bfloat16 value
 constexpr float kFar = -1e4f;         // 2^kFar = 0, and kFar times anything in range is finite
 constexpr int kLogClusterMax = 3, kTopMax = 32;
-constexpr int kCandidates = 1024, kFew = 160;
+constexpr int kCandidates = 1024, kFew = 160, kQueue = 1024;
 constexpr int kBatchesMax = 96;       // batches of a slice whose largest logits are kept
 
 __device__ __forceinline__ float ex2(float x)
@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
     __shared__ unsigned long long cand[TOP ? kCandidates : 1];
     __shared__ float thread_top[TOP ? kWarps : 1][32];
     __shared__ unsigned long long group_key[TOP ? kWarps : 1][32];
-    __shared__ int found;
+    __shared__ int queue[TOP ? kQueue : 1];                   // batches to be looked at again
+    __shared__ int found, queued;
     __shared__ float threshold;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cluster = 1 << log_cluster, rank = blockIdx.x & (cluster - 1);
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
     for (int o = 1; o < 32; o <<= 1) warp_top = fmaxf(warp_top, __shfl_xor_sync(0xffffffffu, warp_top, o));
     if constexpr (TOP) {
         thread_top[warp][lane] = sh.top;
-        if (tid == 0) found = 0;
+        if (tid == 0) found = queued = 0;
     }
     Part r = sh.part(warp_top, c2);
 #pragma unroll
@@ -310,26 +311,35 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
             const int at = atomicAdd(&found, 1);
             if (at < kCandidates) cand[at] = key_of(v, id);
         };
-        // only batches that reach the threshold are looked at again (from L2); a thread whose sum is NaN looks
-        // at all of its own
+        // Only batches that reach the threshold are looked at again (from L2), all of them at once: they are
+        // queued, and four threads take one.  A thread whose sum is NaN queues all of its own.
         const bool all = sh.s.x + sh.s.y != sh.s.x + sh.s.y;
         batch = 0;
         for (u = sl.u0; u < sl.u1; u += kBatch, ++batch) {
             if (!all && batch < kept && batch_top[batch * kThreads + tid] < least) continue;
-            U x[kAhead];
+            const int at = atomicAdd(&queued, 1);
+            if (at < kQueue) queue[at] = batch * kThreads + tid;
+        }
+        __syncthreads();
+        auto look_at = [&](int at) {
+            if (at >= sl.u1) return;
+            U x;
+            x.w = __ldg(units + at);
+            if (R::largest_nan(x) < least) return;
+            float v[R::VEC];
+            x.get(v);
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                x[a] = R::nothing();
-                if (u + a * kThreads + tid < sl.u1) x[a].w = __ldg(units + u + a * kThreads + tid);
+            for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + at * R::VEC + e);
+        };
+        const int waiting = queued;
+        if (waiting <= kQueue) {
+            static_assert(kAhead == 4, "four threads a batch");
+            for (int i = tid; i < 4 * waiting; i += kThreads) {
+                const int item = queue[i >> 2];
+                look_at(sl.u0 + item / kThreads * kBatch + (i & 3) * kThreads + item % kThreads);
             }
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                if (R::largest_nan(x[a]) < least) continue;
-                float v[R::VEC];
-                x[a].get(v);
-#pragma unroll
-                for (int e = 0; e < R::VEC; ++e) offer(v[e], sl.first + (u + a * kThreads + tid) * R::VEC + e);
-            }
+        } else {
+            for (int at = sl.u0 + tid; at < sl.u1; at += kThreads) look_at(at);
         }
         if (single >= 0) offer(io::ld(sl.x + single), single);
         if (tid < kTopMax) best[tid] = 0;
