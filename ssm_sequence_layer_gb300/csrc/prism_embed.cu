@@ -616,23 +616,6 @@ constexpr int kSmall = 2048;  // tokens that one CTA sorts
 
 constexpr size_t cluster_smem(int steps) { return sizeof(ClusterShared) + (size_t)steps * kClusterThreads * sizeof(int2); }
 
-// A launch that may begin while the kernel before it in the stream ends (it waits for that kernel's
-// results itself); the first kernel of a call is launched plainly.
-template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Columns are split over warps (32 units each, 64 for the narrow units of unaligned rows): tiles are few
 // when tokens are, and a warp with one unit per lane keeps eight rows in flight.
 template <typename io_t, int VEC>

@@ -9,6 +9,7 @@
 
 #include "io_util.h"
 #include "prism_tokens.h"
+#include "tc_ptx.h"
 
 namespace prism {
 namespace norm {
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) backward_kerne
     const long long step = (long long)gridDim.x * ROWS;
     U w[UPL], x[UPL], a[UPL], b[UPL];
     float acc[UPL][VEC];
+    tc::allow_dependent_launch();
     auto load = [&](long long row) {
 #pragma unroll
         for (int j = 0; j < UPL; ++j)
@@ -375,6 +377,7 @@ __global__ void __launch_bounds__(kJoinThreads) dweight_kernel(const float *__re
 {
     __shared__ float sums[kJoinThreads / 32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    tc::grid_dependency_wait();
     float acc = 0.f;
     if (c < D) {
 #pragma unroll 4
@@ -488,9 +491,9 @@ cudaError_t backward(const NormBackwardArgs &a, const NormWorkspace &w, const To
         l.timer->end();
     }
     l.timer->begin("norm_dweight");
-    dweight_kernel<<<(a.D + 31) / 32, kJoinThreads, 0, s>>>(w.part, a.dweight, p.slabs, a.D);
+    const cudaError_t e = launch_behind(dweight_kernel, dim3((a.D + 31) / 32), kJoinThreads, s, (const float *)w.part, a.dweight, p.slabs, a.D);
     l.timer->end();
-    return cudaGetLastError();
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }

@@ -13,6 +13,23 @@ struct TokenLaunch {
     KernelTimer *timer;
 };
 
+// A launch that may begin while the kernel before it in the stream ends (it waits for that kernel's
+// results itself); the first kernel of a call is launched plainly.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- embedding (prism_embed.cu) ------------------------------------------------------------------
 struct EmbedArgs {
     const long long *ids;
