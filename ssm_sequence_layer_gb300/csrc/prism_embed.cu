@@ -35,7 +35,7 @@ constexpr int kThreads = 256;
 // 768 of 50021 (bf16) and 32768 x 256 of 200003 (fp32): 16 MB 51 and 73 us, 48 MB 48 and 65 us, 80 MB 48 and
 // 57 us, 112 MB 52 and 53 us, all of it 53 and 56 us.
 constexpr long long kBesideSort = 96 << 20;
-constexpr int kTile = 32;  // sorted tokens per warp, at least (tile_of)
+constexpr int kTile = 8;  // sorted tokens per warp, at least (tile_of)
 
 // ---------------------------------------------------------------------------------------------
 // lookup: a warp takes 32 UPL units of one row
@@ -284,6 +284,33 @@ __device__ __forceinline__ void cluster_sync()
         asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
     else
         __syncthreads();
+}
+
+// A few tokens: a token's place is the number of tokens before it in the order, which its thread counts.
+constexpr int kCounted = 512;
+__global__ void __launch_bounds__(kCounted) counted_sort_kernel(const long long *__restrict__ ids, int n, int V, int *__restrict__ key_out,
+                                                               int *__restrict__ pos_out, uint32_t *present, int *status, const Fill f)
+{
+    __shared__ __align__(16) int keys[kCounted];
+    const int tid = threadIdx.x;
+    tc::allow_dependent_launch();
+    if (blockIdx.x > 0) return fill_share(f, blockIdx.x - 1, gridDim.x - 1);
+    const long long id = tid < n ? ids[tid] : -1;
+    if (id >= V) atomicCAS(status, 0, kDevBounds);
+    const int key = tid < n ? key_of(id, V) : 0x7fffffff;
+    keys[tid] = key;
+    for (int i = tid; i <= V / 32; i += kCounted) present[i] = 0;
+    __syncthreads();
+    if (tid >= n) return;
+    int place = 0;
+    for (int o = 0; o < n; o += 4) {  // the padding is larger than every key
+        const int4 k = *reinterpret_cast<const int4 *>(keys + o);
+        place += (k.x < key || (k.x == key && o < tid)) + (k.y < key || (k.y == key && o + 1 < tid)) +
+                 (k.z < key || (k.z == key && o + 2 < tid)) + (k.w < key || (k.w == key && o + 3 < tid));
+    }
+    key_out[place] = key;
+    pos_out[place] = tid;
+    atomicOr(&present[key >> 5], 1u << (key & 31));
 }
 
 template <int CS, int STEPS>
@@ -602,12 +629,14 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumParams p)
 }
 
 // ---------------------------------------------------------------------------------------------
-// Tokens per tile: 32, the lanes of a warp; longer ones for more tokens than 8192 tiles hold, which
-// bounds the workspace.
+// Tokens per tile: 8, the rows that a warp has in flight, up to 1024 tiles; then up to 32, which leaves fewer
+// runs to join (32768 tokens: 8 62 us, 32 54 us); longer ones for more tokens than 8192 tiles hold,
+// which bounds the workspace.
 constexpr int kTilesMax = 8193;
 int tile_of(int n)
 {
     int t = kTile;
+    while (t < 32 && n / t > 1024) t *= 2;
     while (n / t >= kTilesMax) t *= 2;
     return t;
 }
@@ -715,7 +744,7 @@ cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const Emb
     // The sort's kernels clear the table's first rows in equal shares, as many as fit beside them (without
     // tokens there are no sums, and they clear everything).
     const bool in_cluster = a.n <= kCluster * kClusterThreads * kClusterSteps;
-    const int kernels = in_cluster ? 1 : passes + 1, fill_blocks = a.accumulate ? 0 : (in_cluster ? 2 : 4) * l.sm_count;
+    const int kernels = in_cluster ? 1 : passes + 1, fill_blocks = a.accumulate ? 0 : (in_cluster && a.n > kCounted ? 2 : 4) * l.sm_count;
     const long long beside = kernels * kBesideSort / ((long long)a.D * 4);
     const int cleared = a.accumulate || a.n == 0 || beside >= a.V ? a.V : (int)beside;
     const size_t floats = (size_t)cleared * a.D;
@@ -724,7 +753,11 @@ cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const Emb
         return Fill{a.dtable, quads * i / kernels * 4, i == kernels - 1 ? floats : quads * (i + 1) / kernels * 4};
     };
     int result = 0;  // which of the two buffers holds the sorted tokens
-    if (in_cluster) {
+    if (a.n <= kCounted) {
+        l.timer->begin("embed_sort");
+        counted_sort_kernel<<<1 + fill_blocks, kCounted, 0, s>>>(a.ids, a.n, a.V, w.key[0], w.pos[0], w.present, l.d_status, share(0));
+        l.timer->end();
+    } else if (in_cluster) {
         l.timer->begin("embed_sort");
         const int per = a.n <= kSmall ? a.n : (a.n + kCluster - 1) / kCluster;
         auto go = [&](auto cs, auto steps) {
