@@ -63,6 +63,8 @@ def library_path() -> str:
 def lib():
     """Load the CUDA library (raises if it has not been built)."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _lock:
         if _LIB is None:
             path = library_path()

@@ -39,13 +39,41 @@ __device__ __forceinline__ uint16_t e4m3x2(float a, float b)
     return r;
 }
 
-// A block's scale from its largest magnitude, and what the values are multiplied with: a product with
-// the reciprocal is within one unit in the last place of the quotient, far inside e4m3's rounding.
-__device__ __forceinline__ float scale_of(float peak, float &inverse)
+// The 8-bit values of a block of 128.  A value's e4m3 neighbour is decided by y / scale = v / s with v = r w and
+// s = max |v| / 448, in which 1 / rms cancels.  A rounding error there moves values that lie near the middle between
+// two neighbours to the wrong one, so v is held as a product and its rounding error, and the quotient is
+// corrected once with both: what is left are the roundings of s and of the result.  (Of 50 million bf16 values the
+// plain sequence of roundings moves 299, this one 13.)  Values come in pairs: two operations an instruction.
+struct Block {
+    float s, inverse;  // max |v| / 448 and its reciprocal
+    float q, scale;    // 1 / rms; the scale that is stored
+    bool plain;        // the correction does not apply: a scale at its lower bound, or infinite
+
+    __device__ __forceinline__ Block(float peak, float q_) : q(q_)
+    {
+        s = peak / kMaxE4M3;
+        const float raw = s * q;  // NaN where 1 / rms is 0 and the peak infinite: y is 0 or NaN there
+        scale = fmaxf(raw, kMinScale);
+        plain = !(raw > kMinScale) || scale == INFINITY;
+        inverse = plain ? 1.f / scale : 1.f / s;
+    }
+    // v and minus its rounding error
+    __device__ __forceinline__ float2 quotient(float2 v, float2 minus_low) const
+    {
+        using namespace io;
+        const float2 i2 = make_float2(inverse, inverse), q2 = make_float2(q, q);
+        if (plain) return mul2(mul2(v, q2), i2);
+        const float2 t = mul2(v, i2);
+        const float2 rest = fma2(minus_low, make_float2(-1.f, -1.f), fma2(t, make_float2(-s, -s), v));
+        return fma2(rest, i2, t);
+    }
+};
+// v = r w, and minus its rounding error
+__device__ __forceinline__ float2 product(float2 r, float2 w, float2 &minus_low)
 {
-    const float s = fmaxf(peak / kMaxE4M3, kMinScale);
-    inverse = 1.f / s;
-    return s;
+    const float2 v = io::mul2(r, w);
+    minus_low = io::fma2(r, make_float2(-w.x, -w.y), v);
+    return v;
 }
 
 template <typename io_t>
@@ -113,18 +141,21 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel
 #pragma unroll
             for (int o = 0; o < WPR; ++o) ss += parts[turn][o];
         }
-        const float q = rsqrtf(ss / (float)p.D + p.eps);
+        const float q = __frsqrt_rn(ss / (float)p.D + p.eps);
 #pragma unroll
         for (int j = 0; j < UPL; ++j) {
             const int u = t + G * j;
             const bool mine = u < units;
             const size_t at = (size_t)row * p.D + (size_t)u * VEC;
-            float y[VEC], peak = 0.f;
-            if (mine) w[j].get(y);
+            float w4[VEC], peak = 0.f;
+            float2 v[VEC / 2], low[VEC / 2];  // r w and minus its rounding error
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                y[e] = mine ? r[j][e] * q * y[e] : 0.f;
-                peak = fmaxf(peak, fabsf(y[e]));
+            for (int e = 0; e < VEC; ++e) w4[e] = 0.f;
+            if (mine) w[j].get(w4);
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) {
+                v[e / 2] = product(make_float2(r[j][e], r[j][e + 1]), make_float2(w4[e], w4[e + 1]), low[e / 2]);
+                peak = fmaxf(peak, fmaxf(fabsf(v[e / 2].x), fabsf(v[e / 2].y)));
             }
             U o;
             if (mine && p.sum) {
@@ -132,19 +163,24 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel
                 io::store_unit<io_t, VEC>(p.sum + at, o);
             }
             if (mine && p.y) {
+                float y[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; e += 2) y[e] = v[e / 2].x * q, y[e + 1] = v[e / 2].y * q;
                 o.set(y);
                 io::store_unit<io_t, VEC>(p.y + at, o);
             }
             if (p.y8) {
 #pragma unroll
                 for (int o2 = PER / 2; o2 > 0; o2 >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o2));
-                float inverse;
-                const float scale = scale_of(peak, inverse);
+                const Block block(peak, q);
                 if (mine) {
-                    if (lane % PER == 0) p.y_scale[(size_t)row * blocks + u / PER] = scale;
+                    if (lane % PER == 0) p.y_scale[(size_t)row * blocks + u / PER] = block.scale;
                     uint16_t b[VEC / 2];
 #pragma unroll
-                    for (int e = 0; e < VEC; e += 2) b[e / 2] = e4m3x2(y[e] * inverse, y[e + 1] * inverse);
+                    for (int e = 0; e < VEC / 2; ++e) {
+                        const float2 t = block.quotient(v[e], low[e]);
+                        b[e] = e4m3x2(t.x, t.y);
+                    }
                     if constexpr (VEC == 8)
                         *reinterpret_cast<uint2 *>(p.y8 + at) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
                     else
@@ -171,30 +207,39 @@ __global__ void __launch_bounds__(kThreads) forward_any_kernel(const ForwardPara
         const float r = sum_at(c);
         ss = fmaf(r, r, ss);
     }
-    const float q = rsqrtf(warp_sum(ss) / (float)p.D + p.eps);
+    const float q = __frsqrt_rn(warp_sum(ss) / (float)p.D + p.eps);
     const int blocks = (p.D + kBlock - 1) / kBlock;
     for (int b = 0; b < blocks; ++b) {
-        float y[kBlock / 32], peak = 0.f;
+        float2 v[kBlock / 64], low[kBlock / 64];  // columns 64 i + lane and 32 further
+        float peak = 0.f;
 #pragma unroll
-        for (int i = 0; i < kBlock / 32; ++i) {
-            const int c = b * kBlock + 32 * i + lane;
-            y[i] = 0.f;
-            if (c < p.D) {
-                const float r = sum_at(c);
-                y[i] = r * q * io::ld(p.weight + c);
-                if (p.sum) io::st(p.sum + at + c, r);
-                if (p.y) io::st(p.y + at + c, y[i]);
-                peak = fmaxf(peak, fabsf(y[i]));
+        for (int i = 0; i < kBlock / 64; ++i) {
+            float r[2] = {0.f, 0.f}, wt[2] = {0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = b * kBlock + 64 * i + 32 * h + lane;
+                if (c < p.D) r[h] = sum_at(c), wt[h] = io::ld(p.weight + c);
+            }
+            v[i] = product(make_float2(r[0], r[1]), make_float2(wt[0], wt[1]), low[i]);
+            peak = fmaxf(peak, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = b * kBlock + 64 * i + 32 * h + lane;
+                if (c >= p.D) continue;
+                if (p.sum) io::st(p.sum + at + c, r[h]);
+                if (p.y) io::st(p.y + at + c, (h ? v[i].y : v[i].x) * q);
             }
         }
         if (p.y8) {
-            float inverse;
-            const float scale = scale_of(warp_max(peak), inverse);
-            if (lane == 0) p.y_scale[(size_t)row * blocks + b] = scale;
+            const Block block(warp_max(peak), q);
+            if (lane == 0) p.y_scale[(size_t)row * blocks + b] = block.scale;
 #pragma unroll
-            for (int i = 0; i < kBlock / 32; ++i) {
-                const int c = b * kBlock + 32 * i + lane;
-                if (c < p.D) p.y8[at + c] = (uint8_t)e4m3x2(y[i] * inverse, 0.f);
+            for (int i = 0; i < kBlock / 64; ++i) {
+                const float2 t = block.quotient(v[i], low[i]);
+                const uint16_t two = e4m3x2(t.x, t.y);
+                const int c = b * kBlock + 64 * i + lane;
+                if (c < p.D) p.y8[at + c] = (uint8_t)two;
+                if (c + 32 < p.D) p.y8[at + c + 32] = (uint8_t)(two >> 8);
             }
         }
     }
@@ -273,7 +318,7 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) backward_kerne
 #pragma unroll
             for (int o = 0; o < WPR; ++o) s.x += parts[turn][o].x, s.y += parts[turn][o].y;
         }
-        const float q = rsqrtf(s.x / (float)p.D + p.eps), mean = s.y * q / (float)p.D;
+        const float q = __frsqrt_rn(s.x / (float)p.D + p.eps), mean = s.y * q / (float)p.D;
 #pragma unroll
         for (int j = 0; j < UPL; ++j) {
             if (t + G * j >= units) continue;
@@ -328,7 +373,7 @@ __global__ void __launch_bounds__(kThreads) stats_any_kernel(const BackwardParam
         ss = fmaf(r, r, ss);
         along = fmaf(io::ld(p.weight + c) * io::ld(p.dy + at + c), r, along);
     }
-    const float q = rsqrtf(warp_sum(ss) / (float)p.D + p.eps);
+    const float q = __frsqrt_rn(warp_sum(ss) / (float)p.D + p.eps);
     const float mean = warp_sum(along) * q / (float)p.D;
     if (lane == 0) p.stats[row] = make_float2(q, mean);
 }
