@@ -517,16 +517,18 @@ struct BackwardParams {
     int *status;
 };
 
-// A CTA takes kAhead units per thread of one row.  dlogits_j = p_j (B - dentropy log p_j), plus dlogprob at the
+// A CTA takes kAhead units per thread of one row, or 256 / GROUP whole short rows, GROUP threads each.  dlogits_j = p_j (B - dentropy log p_j), plus dlogprob at the
 // target, with inv_temperature in dlogprob and dentropy, and B = -dlogprob - dentropy entropy.
-template <typename logit_t>
+template <typename logit_t, int GROUP>
 __global__ void __launch_bounds__(kThreads, 6) backward_kernel(const BackwardParams<logit_t> p, int chunks)
 {
+    static_assert(GROUP >= 64, "Slice::single takes two warps");
     using R = Row<logit_t>;
     using U = typename R::U;
-    const int tid = threadIdx.x;
-    const long long row = blockIdx.x / chunks;
+    const int tid = threadIdx.x % GROUP;
+    const long long row = (long long)(blockIdx.x / chunks) * (kThreads / GROUP) + threadIdx.x / GROUP;
     const int chunk = (int)(blockIdx.x % chunks);
+    if (row >= p.n) return;
     const Slice<logit_t> sl(p.logits + row * p.ld, p.V, 0, 0);
     logit_t *out = p.dlogits + row * p.ld_d;
     const uint4 *units = sl.units();
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 6) backward_kernel(const BackwardPar
     U x[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
-        if (u0 + a * kThreads < u1) x[a].w = units[u0 + a * kThreads];
+        if (u0 + a * GROUP < u1) x[a].w = units[u0 + a * GROUP];
     const float lse = p.lse[row], c = p.inv_temperature;
     long long t = p.dlogprob ? p.targets[row] : -1;
     if (t >= p.V) {
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 6) backward_kernel(const BackwardPar
     const bool aligned = (((uintptr_t)(out + sl.first)) & 15) == 0;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-        const int u = u0 + a * kThreads;
+        const int u = u0 + a * GROUP;
         if (u >= u1) break;
         const int id = sl.first + u * R::VEC;
         float v[R::VEC], at_hit = 0.f;
@@ -632,7 +634,13 @@ cudaError_t backward(const LogprobBackwardArgs &a, const TokenLaunch &l)
     const int units = a.V / Row<logit_t>::VEC, per = kAhead * kThreads, chunks = units > per ? (units + per - 1) / per : 1;
     l.timer->begin("token_logprobs_backward");
     // n chunks: below 2^31 for any logits that fit the device's memory
-    backward_kernel<logit_t><<<(unsigned)((long long)a.n * chunks), kThreads, 0, l.timer->stream>>>(p, chunks);
+    cudaStream_t s = l.timer->stream;
+    if (units <= kAhead * 64)
+        backward_kernel<logit_t, 64><<<(unsigned)(((long long)a.n + 3) / 4), kThreads, 0, s>>>(p, 1);
+    else if (units <= kAhead * 128)
+        backward_kernel<logit_t, 128><<<(unsigned)(((long long)a.n + 1) / 2), kThreads, 0, s>>>(p, 1);
+    else
+        backward_kernel<logit_t, kThreads><<<(unsigned)((long long)a.n * chunks), kThreads, 0, s>>>(p, chunks);
     l.timer->end();
     return cudaGetLastError();
 }
