@@ -505,6 +505,151 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
     if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// Many short rows: a warp per row and no barriers.  The same steps as in forward_kernel, the lanes being the
+// groups: the k-th largest of their largest logits is the threshold, the second look goes through L1.
+constexpr int kShortUnits = 1024, kShortCandidates = 256;
+
+template <typename logit_t, bool TOP>
+__global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<logit_t> p)
+{
+    using R = Row<logit_t>;
+    using U = typename R::U;
+    __shared__ unsigned long long cand_s[TOP ? kWarps : 1][TOP ? kShortCandidates : 1];
+    __shared__ unsigned long long best_s[TOP ? kWarps : 1][TOP ? kTopMax : 1];
+    __shared__ int found_s[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = (long long)blockIdx.x * kWarps + warp;
+    if (row >= p.n) return;
+    const Slice<logit_t> sl(p.logits + row * p.ld, p.V, 0, 0);
+    const float c = p.inv_temperature, c2 = c * kLog2e;
+    const uint4 *units = sl.units();
+    // single values: the head's on the first lanes, the tail's from lane 16 on (fewer than 8 each)
+    const int single = lane < sl.head ? lane : lane >= 16 && sl.tail0 + lane - 16 < sl.tail1 ? sl.tail0 + lane - 16 : -1;
+
+    Share sh;
+    int u = lane;
+    for (; u + 32 * (kAhead - 1) < sl.u1; u += 32 * kAhead) {
+        U x[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) x[a].w = __ldg(units + u + 32 * a);
+        sh.template add<R, kAhead>(x, c2);
+    }
+    {
+        U x[kAhead];  // what is left, and the single value in the last place
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            x[a] = R::nothing();
+            if (a < kAhead - 1 && u + 32 * a < sl.u1) x[a].w = __ldg(units + u + 32 * a);
+        }
+        if (single >= 0) *reinterpret_cast<logit_t *>(&x[kAhead - 1].w) = sl.x[single];
+        sh.template add<R, kAhead>(x, c2);
+    }
+    float top = sh.top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    Part all = sh.part(top, c2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all.s += __shfl_xor_sync(0xffffffffu, all.s, o);
+        all.t += __shfl_xor_sync(0xffffffffu, all.t, o);
+    }
+    const bool none = all.s == all.s && all.top * c == -INFINITY;
+    const float m = none ? 0.f : all.top, logs = none ? -INFINITY : logf(all.s);
+    if (lane == 0) {
+        if (p.lse) p.lse[row] = fmaf(m, c, logs);
+        if (p.entropy) p.entropy[row] = none ? 0.f : logs - all.t / all.s * kLn2;
+        if (p.logprob) {
+            const long long t = p.targets[row];
+            if (t >= p.V) atomicCAS(p.status, 0, kDevBounds);
+            float v = 0.f;
+            if (t >= 0 && t < p.V) {
+                const float x = io::ld(sl.x + t);
+                v = none || x <= kLowest ? -INFINITY : (x - m) * c - logs;
+                if (all.s != all.s) v = all.s;
+            }
+            p.logprob[row] = v;
+        }
+    }
+    if constexpr (TOP) {
+        unsigned long long *cand = cand_s[warp], *best = best_s[warp];
+        int &found = found_s[warp];
+        auto for_each = [&](float least, auto look) {  // this lane's live logits that reach `least`, and NaN
+            for (int at = lane; at < sl.u1; at += 32) {
+                U x;
+                x.w = __ldg(units + at);
+                if (R::largest_nan(x) < least) continue;
+                float v[R::VEC];
+                x.get(v);
+#pragma unroll
+                for (int e = 0; e < R::VEC; ++e)
+                    if (!(v[e] < least || v[e] <= kLowest || v[e] * c == -INFINITY)) look(key_of(v[e], sl.first + at * R::VEC + e));
+            }
+            if (single >= 0) {
+                const float v = io::ld(sl.x + single);
+                if (!(v < least || v <= kLowest || v * c == -INFINITY)) look(key_of(v, single));
+            }
+        };
+        auto keep = [&](unsigned long long key) {
+            const int at = atomicAdd(&found, 1);
+            if (at < kShortCandidates) cand[at] = key;
+        };
+        auto kth = [&](auto g) {  // the k-th largest of the lanes' values (ties by lane)
+            int above = 0;
+            for (int o = 0; o < 32; ++o) {
+                const auto other = __shfl_sync(0xffffffffu, g, o);
+                above += other > g || (other == g && o < lane);
+            }
+            return __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == p.k - 1)) - 1);
+        };
+        const float least = kth(sh.top);
+        best[lane] = 0;
+        if (lane == 0) found = 0;
+        __syncwarp();
+        for_each(least, keep);
+        __syncwarp();
+        int count = found;
+        __syncwarp();
+        if (count > kShortCandidates) {  // many equal logits: by keys instead of by values
+            unsigned long long mine = 0;
+            for_each(least, [&](unsigned long long key) { mine = max(mine, key); });
+            const unsigned long long at = kth(mine);
+            if (lane == 0) found = 0;
+            __syncwarp();
+            for_each(least, [&](unsigned long long key) {
+                if (key >= at) keep(key);
+            });
+            __syncwarp();
+            count = found;
+        }
+        if (count <= kShortCandidates) {
+            for (int i = lane; i < count; i += 32) {
+                const unsigned long long key = cand[i];
+                int above = 0;
+                for (int o = 0; o < count; ++o) above += cand[o] > key;
+                if (above < p.k) best[above] = key;
+            }
+        } else {  // an order that the lanes miss: the largest key below the last one, k times
+            unsigned long long last = ~0ull;
+            for (int i = 0; i < p.k && last; ++i) {
+                unsigned long long b = 0;
+                for_each(least, [&](unsigned long long key) {
+                    if (key < last && key > b) b = key;
+                });
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+                last = b;
+                if (lane == 0) best[i] = b;
+            }
+        }
+        __syncwarp();
+        if (lane < p.k) {
+            const unsigned long long key = best[lane];
+            if (p.top_ids) p.top_ids[row * p.k + lane] = key ? id_of(key) : -1;
+            if (p.top_logprob) p.top_logprob[row * p.k + lane] = key ? (value_of(key) - m) * c - logs : -INFINITY;
+        }
+    }
+}
+
 template <typename logit_t>
 struct BackwardParams {
     const logit_t *logits;
@@ -613,8 +758,18 @@ cudaError_t forward(const LogprobArgs &a, const TokenLaunch &l)
 {
     const ForwardParams<logit_t> p{(const logit_t *)a.logits, a.targets, a.lse, a.logprob, a.entropy, a.top_logprob, a.top_ids,
                                    a.ld, a.inv_temperature, a.n, a.V, a.k, l.d_status};
-    // Few rows are split over a cluster, down to one unit per thread.
     const long long units = a.V / Row<logit_t>::VEC + 1;
+    // A warp per row where its lanes have one batch at most, and up to 1024 units where there are rows enough for
+    // eight warps an SM.
+    if (units <= 32 * (kAhead - 1) || (units <= kShortUnits && a.n >= 8 * l.sm_count)) {
+        l.timer->begin("token_logprobs");
+        const unsigned grid = (unsigned)((a.n + kWarps - 1) / kWarps);
+        if (a.k == 0) short_kernel<logit_t, false><<<grid, kThreads, 0, l.timer->stream>>>(p);
+        else short_kernel<logit_t, true><<<grid, kThreads, 0, l.timer->stream>>>(p);
+        l.timer->end();
+        return cudaGetLastError();
+    }
+    // Few rows are split over a cluster, down to one unit per thread.
     int log_cluster = 0;
     while (log_cluster < kLogClusterMax && ((long long)a.n << log_cluster) < 2 * l.sm_count && units >> log_cluster > kThreads) ++log_cluster;
     const long long batches = (units >> log_cluster) / kBatch + 1;

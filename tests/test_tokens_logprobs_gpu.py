@@ -81,7 +81,8 @@ def check_forward(out, x, targets, c, k):
     (1, 1, 0, 1, 0, 1.0), (3, 2, 0, 32, 0, 0.7), (5, 33, 0, 5, 0.3, 1.3), (7, 100, 3, 32, 0.9, 1.0), (4, 1000, 0, 8, 0, 1.0),
     (300, 511, 1, 3, 0.1, 1.0), (16, 4099, 0, 20, 0.2, 2.0), (3, 50021, 27, 20, 0.1, 1.25), (2, 131072, 0, 32, 0, 1.0),
     (1, 300007, 0, 8, 0, 1.0), (640, 20000, 0, 4, 0, 1.0), (2, 262144, 5, 0, 0, 1.0), (400, 8193, 0, 0, 0.5, 1.0),
-    (2, 700001, 0, 16, 0, 1.0), (143, 415, 0, 32, 0, 1.0), (55, 5381, 64, 32, 0, 1.0), (14, 5112, 3, 32, 0.4, 1.0), (9, 260, 0, 32, 0.5, 1.0)])
+    (2, 700001, 0, 16, 0, 1.0), (143, 415, 0, 32, 0, 1.0), (55, 5381, 64, 32, 0, 1.0), (14, 5112, 3, 32, 0.4, 1.0), (9, 260, 0, 32, 0.5, 1.0),
+    (1300, 1001, 0, 32, 0.2, 1.0), (1300, 7999, 2, 5, 0, 0.8), (2000, 515, 0, 0, 0.9, 1.0)])
 def test_token_logprobs(io, n, V, pad, k, masked, c):
     x, targets = draw(n, V, io, n + V, pad, masked)
     with B.Tokens(n, 8, V, io=io) as t:
@@ -107,8 +108,15 @@ def test_top_of_ordered_rows(io, V, kind):
            "block": torch.where((at >= V // 2) & (at < V // 2 + 37), at * 0.001, torch.full((V,), -INF)),
            "lowest": torch.where(at % 5 == 0, at * 0.001, torch.full((V,), torch.finfo(DT[io]).min)),
            "zeros": torch.where(at % 2 == 0, torch.tensor(0.0), torch.tensor(-0.0))}[kind]
-    x = row.to(DT[io]).cuda().expand(3, V).contiguous()
+    rows = 1300 if V == 5000 else 3  # a warp per row, or a block or cluster per row
+    x = row.to(DT[io]).cuda().expand(rows, V).contiguous()
     targets = torch.tensor([0, V - 1, V // 2], device="cuda")
+    if rows > 3:
+        with B.Tokens(rows, 8, V, io=io) as t:
+            many = t.token_logprobs(x, k=32)
+            assert torch.equal(many["top_ids"], many["top_ids"][:1].expand(rows, 32))
+            check_forward({key: v[:3] for key, v in many.items()}, f64(x[:3]), None, 1.0, 32)
+        x = x[:3].contiguous()
     with B.Tokens(3, 8, V, io=io) as t:
         for k in (1, 7, 32):
             out = t.token_logprobs(x, targets, k=k)
