@@ -132,10 +132,12 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const Params<
 template <typename out_t, int NT>
 void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
 {
-    // enough warps to keep each SM's loads in flight (16 a SM), as far as the blocks of 128 reach
+    // Enough warps to keep each SM's loads in flight, as far as the blocks of 128 reach: with 16 warps a SM wanted instead
+    // of 40, 8 x 32768 x 4096 takes 38.1 us instead of 32.7 and 16 x 50048 x 768 17.7 instead of 16.6; with 80 the
+    // latter takes 18.5.
     const int tiles = (p.N + 15) / 16;
     int ks = 1;
-    while (ks < 8 && ks < p.KB && tiles * ks < 16 * sm_count) ks *= 2;
+    while (ks < 8 && ks < p.KB && tiles * ks < 40 * sm_count) ks *= 2;
     const int rt = kSkinnyWarps / ks;
     const unsigned grid = (tiles + rt - 1) / rt;
     if (ks == 1) skinny_kernel<out_t, NT, 1><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
@@ -230,10 +232,27 @@ __device__ __forceinline__ void add_scaled(float2 *acc, const uint32_t (&r)[32],
     }
 }
 
-template <typename out_t, int BN>
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The float4 at a shared-memory address of another CTA of the cluster
+__device__ __forceinline__ float4 remote_float4(uint32_t addr, int cta)
+{
+    uint32_t a;
+    float4 x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
+    return x;
+}
+
+// Few tiles: the CTAs of a cluster share a tile and split its blocks of 128 (SPLIT).  Their sums meet in shared
+// memory, where the operands were, and each CTA adds a share of the rows, always in the cluster's order.
+template <typename out_t, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                   const __grid_constant__ CUtensorMap tm_out, const Params<out_t> p, const Waits wt, int tiled_out)
+                   const __grid_constant__ CUtensorMap tm_out, const Params<out_t> p, const Waits wt, int tiled_out, int splits)
 {
     using L = Layout<BN>;
     constexpr int STAGES = L::STAGES, HALF = BN / 2;
@@ -245,8 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
     const long long tiles = (long long)tiles_m * tiles_n;
-    const int my_tiles = tiles > blockIdx.x ? (int)((tiles - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
-    const long long total = (long long)my_tiles * p.KB;
+    const int my_tiles = SPLIT ? 1 : tiles > blockIdx.x ? (int)((tiles - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
+    const int rank = SPLIT ? (int)(blockIdx.x % splits) : 0;
+    const int b_from = SPLIT ? rank * p.KB / splits : 0, b_to = SPLIT ? (rank + 1) * p.KB / splits : p.KB;
+    const long long total = (long long)my_tiles * (b_to - b_from);
     const uint32_t sbase = smem_u32(sm);
 
     if (tid == 0) {
@@ -272,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // tiles of one column of tiles run at the same time on neighbouring CTAs and share w8 in L2
     auto tile_at = [&](int i, int &m0, int &n0) {
-        const long long t = (long long)blockIdx.x + (long long)i * gridDim.x;
+        const long long t = SPLIT ? (long long)(blockIdx.x / splits) : (long long)blockIdx.x + (long long)i * gridDim.x;
         m0 = (int)(t % tiles_m) * BM;
         n0 = (int)(t / tiles_m) * BN;
     };
@@ -284,10 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (tid == 32) {  // ---- operand loads ----
-        int s = 0, i = 0, b = 0, m0 = 0, n0 = 0;
+        int s = 0, i = 0, b = b_from, m0 = 0, n0 = 0;
         uint32_t round = 0;
         for (long long g = 0; g < total; ++g) {
-            if (b == 0) tile_at(i, m0, n0);
+            if (b == b_from) tile_at(i, m0, n0);
             if (round > 0 && !mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns)) {
                 give_up();
                 break;
@@ -301,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_2d(at + L::A_BYTES + h * STAGE_ROWS * kBlock, &tm_w, mb, b * kBlock, n0 + h * STAGE_ROWS);
             issued = g + 1;
             if (++s == STAGES) s = 0, ++round;
-            if (++b == p.KB) b = 0, ++i;
+            if (++b == b_to) b = b_from, ++i;
         }
     } else if (tid == 0) {  // ---- products ----
         int s = 0;
@@ -344,10 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 acc[HALF / 2];
 #pragma unroll
             for (int c = 0; c < HALF / 2; ++c) acc[c] = make_float2(0.f, 0.f);
-            float scale = sa[0] * sw[0];
-            for (int b = 0; b < p.KB; ++b, ++g) {
+            float scale = sa[b_from] * sw[b_from];
+            for (int b = b_from; b < b_to; ++b, ++g) {
                 const int buf = (int)(g & 1);
-                const float next = b + 1 < p.KB ? sa[b + 1] * sw[b + 1] : 0.f;
+                const float next = b + 1 < b_to ? sa[b + 1] * sw[b + 1] : 0.f;
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[buf]), (uint32_t)(g >> 1) & 1, wt.ns));
                 if (!ok) break;
                 fence_after_sync();
@@ -371,7 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) give_up();  // products may still be in flight: the drain below waits for them
                 break;
             }
-            if (tiled_out) {
+            if constexpr (SPLIT) {  // every load has landed and every product has read it: their shared memory is free
+                const int row = quarter * 32 + lane;
+#pragma unroll
+                for (int c = 0; c < HALF / 4; ++c)
+                    *reinterpret_cast<float4 *>(sm + row * BN * 4 + (((half * HALF / 4 + c) ^ (row & 7)) << 4)) =
+                        make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
+            } else if (tiled_out) {
                 // The sums go to shared memory and leave by TMA while the next tile is added up: a piece is 32 rows x
                 // 128 bytes, and the staging holds two, all of the warp's bf16 columns.
                 constexpr int COLS = 128 / (int)sizeof(out_t), PER = 16 / (int)sizeof(out_t);
@@ -414,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (tiled_out) bulk_wait_read();  // before the staging goes
+        if (!SPLIT && tiled_out) bulk_wait_read();  // before the staging goes
     }
     // drain: after an expired wait, the copies and products in flight land before the CTA exits
     __syncthreads();
@@ -429,6 +456,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before_sync();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 2 * BN);
+    if constexpr (SPLIT) {
+        static_assert(BN == 128 && (uint32_t)BM * BN * 4 <= L::OFF_OUT, "a row of sums is one float4 per lane");
+        cluster_barrier();
+        int m0, n0;
+        tile_at(0, m0, n0);
+        const int n = n0 + 4 * lane, each = BM / splits, rows = min(each, p.M - m0 - rank * each);
+        for (int r = warp; r < rows; r += kThreads / 32) {
+            const int row = rank * each + r;
+            const uint32_t at = sbase + row * BN * 4 + ((lane ^ (row & 7)) << 4);
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int c = 0; c < splits; ++c) {
+                const float4 x = remote_float4(at, c);
+                sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+            }
+            out_t *to = p.out + (size_t)(m0 + row) * p.N + n;
+            if (tiled_out && n + 4 <= p.N) {
+                if constexpr (sizeof(out_t) == 4) {
+                    *reinterpret_cast<float4 *>(to) = sum;
+                } else {
+                    using U = io::Unit<out_t, 8>;
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(U::pack(sum.x, sum.y), U::pack(sum.z, sum.w));
+                }
+            } else {
+                const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < p.N) io::st(to + e, f[e]);
+            }
+        }
+        cluster_barrier();  // the others may still read this CTA's sums
+    }
 }
 
 // A row-major matrix as boxes of box_rows rows x 128 bytes, 128-byte swizzled in shared memory
@@ -448,8 +507,8 @@ bool encode(CUtensorMap *map, CUtensorMapDataType type, int size, const void *ba
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename out_t, int BN>
-cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l)
+template <typename out_t, int BN, bool SPLIT>
+cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l, int splits)
 {
     CUtensorMap ma, mw, mo;
     if (!encode(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.a, p.K, p.M, BM) ||
@@ -463,9 +522,18 @@ cudaError_t launch_product(const Params<out_t> &p, const TokenLaunch &l)
         return cudaErrorInvalidValue;
     const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
     const Waits wt{l.d_status, l.wait_ns > 0 ? (unsigned long long)l.wait_ns : 100000000ull};
-    product_kernel<out_t, BN><<<(unsigned)(tiles < l.sm_count ? tiles : l.sm_count), kThreads, Layout<BN>::SMEM, l.timer->stream>>>(
-        ma, mw, mo, p, wt, tiled ? 1 : 0);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * splits : tiles < l.sm_count ? tiles : l.sm_count));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<BN>::SMEM;
+    cfg.stream = l.timer->stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, product_kernel<out_t, BN, SPLIT>, ma, mw, mo, p, wt, tiled ? 1 : 0, splits);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -505,8 +573,8 @@ cudaError_t product(const Matmul8Args &a, const TokenLaunch &l)
                           (a.K + kBlock - 1) / kBlock};
     cudaError_t e;
     l.timer->begin("matmul8");
-    // Few rows: 8 and 16 of N x K = 50048 x 768 take 11.6 and 18.1 us here, 17 take 15.8 in tiles; of 4096 x 4096 16
-    // take 9.9 here, 17 take 18.6 in tiles.  With four operands of 8 rows the loads wait for registers (32
+    // Few rows: 8 and 16 of N x K = 50048 x 768 take 11.6 and 16.6 us here, 17 take 15.8 in tiles; of 4096 x 4096 16
+    // take 9.8 here, 17 take 12.4 in tiles.  With four operands of 8 rows the loads wait for registers (32
     // rows: 22.8 us of 50048 x 768, 57 of 8192 x 8192; in tiles 16.3 and 31).
     if (a.M <= 16) {
         if (a.M <= 8) launch_skinny<out_t, 1>(p, l.sm_count, l.timer->stream);
@@ -516,26 +584,36 @@ cudaError_t product(const Matmul8Args &a, const TokenLaunch &l)
         // The width of tiles that takes less time: turns of the SMs times the rows that a block brings in.
         const long long rows = (a.M + BM - 1) / BM;
         auto time = [&](long long bn) { return (rows * ((a.N + bn - 1) / bn) + l.sm_count - 1) / l.sm_count * (bn + BM); };
-        e = time(256) <= time(128) ? launch_product<out_t, 256>(p, l) : launch_product<out_t, 128>(p, l);
+        // Few tiles: the CTAs of a cluster split the blocks of 128, as many as the machine holds at once.  Meeting costs
+        // about 2 us and a block about 0.4, so there have to be some: 64 x 6144 x 1024 (8 blocks) takes 8.5 us
+        // whole and 10.6 split, 17 x 768 x 2304 (18) 12.4 and 10.0, 128 x 4096 x 4096 (32) 18.7 and 12.5,
+        // 64 x 8192 x 8192 31.3 and 23.1, 64 x 1024 x 16384 55.7 and 14.6.
+        const long long tiles = rows * ((a.N + 127) / 128);
+        int splits = 1;
+        while (p.KB >= 12 && splits < 8 && 2 * splits <= p.KB && tiles * 2 * splits <= l.sm_count) splits *= 2;
+        e = splits > 1 ? launch_product<out_t, 128, true>(p, l, splits)
+            : time(256) <= time(128) ? launch_product<out_t, 256, false>(p, l, 1) : launch_product<out_t, 128, false>(p, l, 1);
     }
     l.timer->end();
     return e;
 }
 
-template <typename out_t, int BN>
+template <typename out_t, int BN, bool SPLIT>
 cudaError_t prepare()
 {
-    return cudaFuncSetAttribute(product_kernel<out_t, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<BN>::SMEM);
+    return cudaFuncSetAttribute(product_kernel<out_t, BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<BN>::SMEM);
 }
 
 }  // namespace mm8
 
 cudaError_t matmul8_prepare()
 {
-    cudaError_t e = mm8::prepare<float, 128>();
-    if (e == cudaSuccess) e = mm8::prepare<float, 256>();
-    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 128>();
-    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 256>();
+    cudaError_t e = mm8::prepare<float, 128, false>();
+    if (e == cudaSuccess) e = mm8::prepare<float, 128, true>();
+    if (e == cudaSuccess) e = mm8::prepare<float, 256, false>();
+    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 128, false>();
+    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 128, true>();
+    if (e == cudaSuccess) e = mm8::prepare<__nv_bfloat16, 256, false>();
     return e;
 }
 
