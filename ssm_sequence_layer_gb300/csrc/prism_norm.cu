@@ -436,7 +436,11 @@ __global__ void __launch_bounds__(kJoinThreads) dweight_kernel(const float *__re
     }
 }
 
-constexpr int kSlabs = 320;    // blocks of backward_kernel, at most
+// Blocks of backward_kernel, each with its own part of the weight's gradient: as many as are resident, which takes up
+// to 960 blocks of four warps (16384 x 768 fp32: 320 58 us, 640 43 us, 960 41 us), but a part only for rows enough
+// (700 x 768 fp32: 320 16.3 us, 700 17.9 us).
+constexpr int kSlabs = 320;
+constexpr int slabs_max(int D) { return D <= 4096 ? 3 * kSlabs : kSlabs; }
 constexpr int kSlabsAny = 64;  // slabs of rows of dweight_part_kernel
 
 // The variant of a width: WPR warps per row and UPL units per lane hold a row of D / VEC units.
@@ -452,7 +456,11 @@ bool pick(int D, int vec, F f)
     if (units <= 32) f(Int<1>(), Int<1>());
     else if (units <= 64) f(Int<1>(), Int<2>());
     else if (units <= 96) f(Int<1>(), Int<3>());
-    else if (units <= 128) f(Int<1>(), Int<4>());
+    else if (units <= 128) {
+        // the gradient of four units per lane keeps one block per SM (16384 x 512 fp32: 51 us, four warps a row 30 us)
+        if constexpr (WIDEST >= 4) f(Int<1>(), Int<4>());
+        else f(Int<4>(), Int<1>());
+    }
     else if (units <= 256) f(Int<4>(), Int<2>());
     else if (units <= 384) f(Int<4>(), Int<3>());
     else if (units <= 512) f(Int<4>(), Int<4>());
@@ -506,9 +514,9 @@ cudaError_t backward(const NormBackwardArgs &a, const NormWorkspace &w, const To
     cudaStream_t s = l.timer->stream;
     auto go = [&](auto wpr, auto upl, auto vec) {
         constexpr int WPR = decltype(wpr)::value, UPL = decltype(upl)::value, VEC = decltype(vec)::value;
-        constexpr int threads = WPR == 1 ? kThreads : 32 * WPR;
+        constexpr int threads = WPR == 1 ? kThreads : 32 * WPR, ROWS = WPR == 1 ? kThreads / 32 : 1;
         const unsigned blocks =
-            resident_blocks<backward_kernel<io_t, WPR, UPL, VEC>>(threads, WPR == 1 ? kThreads / 32 : 1, a.n, l.sm_count, kSlabs);
+            resident_blocks<backward_kernel<io_t, WPR, UPL, VEC>>(threads, ROWS, a.n, l.sm_count, max(kSlabs, min(slabs_max(a.D), a.n / (4 * ROWS))));
         p.slabs = (int)blocks;
         l.timer->begin("norm_backward");
         backward_kernel<io_t, WPR, UPL, VEC><<<blocks, threads, 0, s>>>(p);
@@ -552,7 +560,7 @@ cudaError_t norm_forward(prism_dtype io, const NormArgs &a, const TokenLaunch &l
 
 size_t norm_workspace_bytes(int max_rows, int D)
 {
-    return norm::up256((size_t)max_rows * 8) + norm::up256((size_t)min(norm::kSlabs, max_rows) * D * 4);
+    return norm::up256((size_t)max_rows * 8) + norm::up256((size_t)min(norm::slabs_max(D), max_rows) * D * 4);
 }
 
 void norm_carve(int max_rows, int D, void *base, NormWorkspace *w)
