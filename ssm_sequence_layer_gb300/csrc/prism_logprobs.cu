@@ -506,15 +506,20 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
 }
 
 // Many short rows: a warp per row and no barriers.  The same steps as in forward_kernel, the lanes being the
-// groups: the k-th largest of their largest logits is the threshold, the second look goes through L1.
-constexpr int kShortUnits = 1024, kShortCandidates = 256;
+// groups: the k-th largest of their largest logits is the threshold, and only batches whose largest logit
+// reaches it are looked at again.
+constexpr int kShortUnits = 2048, kShortCandidates = 256, kShortBatches = kShortUnits / (32 * kAhead) + 1;
 
 template <typename logit_t, bool TOP>
 __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<logit_t> p)
 {
     using R = Row<logit_t>;
     using U = typename R::U;
-    __shared__ unsigned long long cand_s[TOP ? kWarps : 1][TOP ? kShortCandidates : 1];
+    // the batches' largest logits, then the candidates
+    __shared__ union {
+        float tops[kShortBatches][32];
+        unsigned long long cand[kShortCandidates];
+    } sh_s[TOP ? kWarps : 1];
     __shared__ unsigned long long best_s[TOP ? kWarps : 1][TOP ? kTopMax : 1];
     __shared__ int found_s[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -527,12 +532,15 @@ __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<
     const int single = lane < sl.head ? lane : lane >= 16 && sl.tail0 + lane - 16 < sl.tail1 ? sl.tail0 + lane - 16 : -1;
 
     Share sh;
-    int u = lane;
+    int u = lane, batches = 0;
+    auto keep_top = [&](float most) {  // u < kShortUnits, so that batches < kShortBatches
+        if constexpr (TOP) sh_s[warp].tops[batches++][lane] = most;
+    };
     for (; u + 32 * (kAhead - 1) < sl.u1; u += 32 * kAhead) {
         U x[kAhead];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) x[a].w = __ldg(units + u + 32 * a);
-        sh.template add<R, kAhead>(x, c2);
+        keep_top(sh.template add<R, kAhead>(x, c2));
     }
     {
         U x[kAhead];  // what is left, and the single value in the last place
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<
             if (a < kAhead - 1 && u + 32 * a < sl.u1) x[a].w = __ldg(units + u + 32 * a);
         }
         if (single >= 0) *reinterpret_cast<logit_t *>(&x[kAhead - 1].w) = sl.x[single];
-        sh.template add<R, kAhead>(x, c2);
+        keep_top(sh.template add<R, kAhead>(x, c2));
     }
     float top = sh.top;
 #pragma unroll
@@ -571,24 +579,8 @@ __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<
         }
     }
     if constexpr (TOP) {
-        unsigned long long *cand = cand_s[warp], *best = best_s[warp];
+        unsigned long long *cand = sh_s[warp].cand, *best = best_s[warp];
         int &found = found_s[warp];
-        auto for_each = [&](float least, auto look) {  // this lane's live logits that reach `least`, and NaN
-            for (int at = lane; at < sl.u1; at += 32) {
-                U x;
-                x.w = __ldg(units + at);
-                if (R::largest_nan(x) < least) continue;
-                float v[R::VEC];
-                x.get(v);
-#pragma unroll
-                for (int e = 0; e < R::VEC; ++e)
-                    if (!(v[e] < least || v[e] <= kLowest || v[e] * c == -INFINITY)) look(key_of(v[e], sl.first + at * R::VEC + e));
-            }
-            if (single >= 0) {
-                const float v = io::ld(sl.x + single);
-                if (!(v < least || v <= kLowest || v * c == -INFINITY)) look(key_of(v, single));
-            }
-        };
         auto keep = [&](unsigned long long key) {
             const int at = atomicAdd(&found, 1);
             if (at < kShortCandidates) cand[at] = key;
@@ -602,20 +594,49 @@ __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<
             return __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == p.k - 1)) - 1);
         };
         const float least = kth(sh.top);
+        uint32_t reach = 0;  // the lane's batches that reach `least`; all where a NaN may hide one
+        for (int b = 0; b < batches; ++b) reach |= (uint32_t)(sh_s[warp].tops[b][lane] >= least || !(sh.s.x + sh.s.y < INFINITY)) << b;
+        auto for_each = [&](auto look) {  // this lane's live logits that reach `least`, and NaN
+            for (uint32_t left = reach; left; left &= left - 1) {
+                const int at = lane + 32 * kAhead * (__ffs(left) - 1);
+                uint32_t in = 0;  // the batch's units that do
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    U x = R::nothing();
+                    if (at + 32 * a < sl.u1) x.w = __ldg(units + at + 32 * a);
+                    in |= (uint32_t)!(R::largest_nan(x) < least) << a;
+                }
+                for (; in; in &= in - 1) {
+                    const int unit = at + 32 * (__ffs(in) - 1);
+                    if (unit >= sl.u1) break;  // nothing is no less than the lowest value
+                    U x;
+                    x.w = __ldg(units + unit);
+                    float v[R::VEC];
+                    x.get(v);
+#pragma unroll
+                    for (int e = 0; e < R::VEC; ++e)
+                        if (!(v[e] < least || v[e] <= kLowest || v[e] * c == -INFINITY)) look(key_of(v[e], sl.first + unit * R::VEC + e));
+                }
+            }
+            if (single >= 0) {
+                const float v = io::ld(sl.x + single);
+                if (!(v < least || v <= kLowest || v * c == -INFINITY)) look(key_of(v, single));
+            }
+        };
         best[lane] = 0;
         if (lane == 0) found = 0;
         __syncwarp();
-        for_each(least, keep);
+        for_each(keep);
         __syncwarp();
         int count = found;
         __syncwarp();
         if (count > kShortCandidates) {  // many equal logits: by keys instead of by values
             unsigned long long mine = 0;
-            for_each(least, [&](unsigned long long key) { mine = max(mine, key); });
+            for_each([&](unsigned long long key) { mine = max(mine, key); });
             const unsigned long long at = kth(mine);
             if (lane == 0) found = 0;
             __syncwarp();
-            for_each(least, [&](unsigned long long key) {
+            for_each([&](unsigned long long key) {
                 if (key >= at) keep(key);
             });
             __syncwarp();
@@ -632,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<
             unsigned long long last = ~0ull;
             for (int i = 0; i < p.k && last; ++i) {
                 unsigned long long b = 0;
-                for_each(least, [&](unsigned long long key) {
+                for_each([&](unsigned long long key) {
                     if (key < last && key > b) b = key;
                 });
 #pragma unroll
@@ -759,8 +780,9 @@ cudaError_t forward(const LogprobArgs &a, const TokenLaunch &l)
     const ForwardParams<logit_t> p{(const logit_t *)a.logits, a.targets, a.lse, a.logprob, a.entropy, a.top_logprob, a.top_ids,
                                    a.ld, a.inv_temperature, a.n, a.V, a.k, l.d_status};
     const long long units = a.V / Row<logit_t>::VEC + 1;
-    // A warp per row where its lanes have one batch at most, and up to 1024 units where there are rows enough for
-    // eight warps an SM.
+    // A warp per row where its lanes have one batch at most, and up to 2048 units where there are rows enough for
+    // eight warps an SM: 2979 x 8892 with 5 alternatives takes 19.2 us so and 27.2 with 256 threads a row, 4096 x
+    // 16000 with 8 33.3 and 41.4, without 27.0 and 29.2; 700 x 8000 with 8 would take 17 us so, 8.7 in clusters.
     if (units <= 32 * (kAhead - 1) || (units <= kShortUnits && a.n >= 8 * l.sm_count)) {
         l.timer->begin("token_logprobs");
         const unsigned grid = (unsigned)((a.n + kWarps - 1) / kWarps);
