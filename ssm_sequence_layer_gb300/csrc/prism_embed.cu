@@ -444,10 +444,11 @@ __device__ __forceinline__ void clear_absent(const SumParams &p, int block, int 
         const bool absent = mine < p.V && !(p.present[mine >> 5] >> (mine & 31) & 1);
         for (uint32_t left = __ballot_sync(0xffffffffu, absent); left; left &= left - 1) {
             float *d = p.dtable + (size_t)(r0 + (long long)(__ffs(left) - 1) * warps) * p.D;
-            if (p.D % 4 == 0)
-                for (int c = lane; c < p.D / 4; c += 32) reinterpret_cast<float4 *>(d)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            else
-                for (int c = lane; c < p.D; c += 32) d[c] = 0.f;
+            // single values up to a 16-byte boundary, units, and what is left behind them
+            const int head = min(p.D, (int)(-((uintptr_t)d >> 2) & 3)), quads = (p.D - head) >> 2, tail = head + 4 * quads;
+            for (int c = lane; c < quads; c += 32) reinterpret_cast<float4 *>(d + head)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < head) d[lane] = 0.f;
+            if (lane < p.D - tail) d[tail + lane] = 0.f;
         }
     }
 }
@@ -818,7 +819,9 @@ cudaError_t embed_backward(prism_dtype io, const EmbedBackwardArgs &a, const Emb
     sp.accumulate = a.accumulate;
     sp.cleared = cleared;
     sp.present = w.present;
-    const int clear_blocks = cleared < a.V ? 2 * l.sm_count : 0;
+    // Blocks that clear, behind those that add: many small shares even out (14309 x 648 of 130295: 2 a SM 83 us, 4 76 us, 8
+    // 72 us, 16 71 us, 32 72 us; 16384 x 768 of 50021 46, 43.6, 43.4, 43.8 and 45.5 us).
+    const int clear_blocks = cleared < a.V ? 16 * l.sm_count : 0;
     l.timer->begin("embed_sum");
     if (io == PRISM_BF16)
         e = a.D % 8 == 0 ? launch_sum<__nv_bfloat16, 8>(a.dout, sp, clear_blocks, s) : launch_sum<__nv_bfloat16, 1>(a.dout, sp, clear_blocks, s);

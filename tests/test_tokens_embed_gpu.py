@@ -113,6 +113,31 @@ def test_ids_of_the_largest_vocabulary():
         del d
 
 
+@pytest.mark.parametrize("n,D", [(300, 131), (5000, 132), (5000, 133), (70000, 134)])
+def test_tables_larger_than_the_sort_clears(n, D):
+    """160 to 420 MB of table: rows without a token are zero wherever they are cleared, rows at any alignment."""
+    V = 300007 if n < 65537 else 800000
+    g = torch.Generator().manual_seed(D)
+    ids = draw_ids(n, V, D, "zipf")
+    ids = torch.where(ids >= 0, torch.randperm(V, generator=g)[ids], ids)
+    dout = torch.randn(n, D, generator=g)
+    with B.Tokens(n, D, V, io="f32") as t:
+        room = torch.full((V * D + 8,), float("nan"), device="cuda")
+        dtable = room[4:4 + V * D].view(V, D)
+        t.embed_backward(ids.cuda(), dout.cuda(), dtable=dtable)
+        torch.cuda.synchronize()
+        t.last_device_status()
+    assert torch.isnan(room[:4]).all() and torch.isnan(room[4 + V * D:]).all()
+    keep = ids >= 0
+    rows, inverse = torch.unique(ids[keep], return_inverse=True)
+    ref = torch.zeros(rows.numel(), D, dtype=torch.float64).index_add_(0, inverse, dout[keep].double())
+    size = torch.zeros(rows.numel(), D, dtype=torch.float64).index_add_(0, inverse, dout[keep].double().abs())
+    count = torch.bincount(inverse)[:, None]
+    assert torch.all((dtable[rows.cuda()].cpu().double() - ref).abs() <= 2.0 ** -24 * (count + 2) * size)
+    dtable[rows.cuda()] = 0
+    assert torch.count_nonzero(dtable).item() == 0
+
+
 def test_embed_gradient_is_the_lookup_transposed():
     """<embed(table), c> = <table, embed_backward(c)> for the linear map that a set of ids defines."""
     n, D, V = 500, 96, 77
