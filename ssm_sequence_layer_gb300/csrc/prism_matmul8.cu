@@ -32,7 +32,10 @@ struct Params {
 // of a8 as B operands.  The products' k order is a free choice as long as both operands share it: the
 // four words of a lane's 16 bytes serve as the k slots (lane % 4) 4 .. + 3 and 16 + (lane % 4) 4 .. + 3 of
 // two products.  KS warps of a CTA share a row tile and split the blocks of 128 among them, so that
-// narrow products still fill the machine; their sums are added in a fixed order.
+// narrow products still fill the machine; their sums are added in a fixed order.  8 x 50048 x 768 takes 11.6 us
+// (3.3 TB/s) and 8 x 32768 x 4096 32.7 us (4.1 TB/s): the loads that two blocks ahead keep in flight bound it, but three or
+// four blocks ahead (14 us), whole lines of one row per load (14.8), rings of bulk copies (16.4) and the weights as
+// the tcgen05 operand (14.1) are all slower.
 constexpr int kSkinnyWarps = 8;
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -153,9 +156,14 @@ void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
 // The accumulator holds c_b of one block only: the eight epilogue warps read it, scale it by
 // a_scale[m, b] w_scale[j / 128, b] and add it to the sums in their registers (one row and BN / 2
 // columns per thread, two columns per instruction) while the next block's products run into the other
-// accumulator.  Per block the tensor core needs 128 BN 128 / 8192 cycles and the scaled additions
-// 128 BN / 256.  The sums take more registers than an even share, so the four warps of the
-// issuing group hand theirs over.
+// accumulator.  The sums take more registers than an even share, so the four warps of the issuing group hand
+// theirs over.
+//
+// 4096 x 50048 x 768 takes 176 us, 1.79 PFLOP/s.  At BN = 256 a block brings 48 KB into the SM, whose port takes 64 bytes
+// a cycle: 768 cycles, 94 us in all (measured with one product per block), against 512 cycles of products and 128 of scaled
+// additions.  Without the sums and the stores it takes 117 us, with the sums 133, with the stores 161: shared
+// memory and the port carry operands in and results out at the same time.  Pairs of CTAs that share operands
+// (one tile per pair: 301 us; multicast: 174 us) do not lift that.
 using namespace prism::tc;
 
 constexpr int BM = 128, STAGE_ROWS = 128;

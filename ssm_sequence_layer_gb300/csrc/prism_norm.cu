@@ -4,7 +4,8 @@
 //   y8 = e4m3(y / s),   s = max(max |y| / 448, 2^-126) over each row's blocks of 128 columns
 //   dx = q (w dy - rh mean_j(w_j dy_j rh_j)) + dsum,   rh = r q,   dweight = sum over rows of dy rh
 //
-// A few operations per value read: HBM bounds both directions.
+// A few operations per value read: HBM bounds both directions.  Sums are fp32 over the unrounded r; outputs are
+// rounded once.
 #include <type_traits>
 
 #include "io_util.h"
@@ -89,7 +90,8 @@ struct ForwardParams {
 // Rows of 16-byte units, held in registers: WPR warps per row, UPL units per lane (unit t + 32 WPR j of a row
 // belongs to thread t, so a block of 128 columns is the same j of 16 (bf16) or 32 (fp32) neighbouring
 // lanes).  Warps walk over the rows; the next row's loads are in flight while a row is worked on, which
-// keeps about 60 KB outstanding per SM.
+// keeps about 60 KB outstanding per SM.  16384 x 768 bf16 with both outputs of the sum and 8 bits: 18.9 us, 4.7 TB/s (a
+// copy of that size reaches about 5; issue slots are 61 % busy); 8192 x 4096 bf16 sum and y 44 us, 6.1 TB/s.
 template <typename io_t, int WPR, int UPL>
 __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel(const ForwardParams<io_t> p)
 {
@@ -192,7 +194,8 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel
 }
 
 // Any width and alignment: a warp per row, one value per lane at a time, two passes over the row (the
-// second one comes from the caches).  Nothing is written before the row has been read to its end, and
+// second one comes from the caches): 16384 x 770 bf16 34 us, 2.9 TB/s, bound by the number of loads.  Nothing is
+// written before the row has been read to its end, and
 // then each value is read before its own place is written, so outputs may take an input's place.
 template <typename io_t>
 __global__ void __launch_bounds__(kThreads) forward_any_kernel(const ForwardParams<io_t> p)
@@ -258,7 +261,9 @@ struct BackwardParams {
 
 // Rows of 16-byte units in registers, as in forward_kernel: one pass gives dx and this block's part of
 // the weight's gradient, which each thread holds for its own columns over all rows of the block.  Rows
-// that are not made of 16-byte units go through it one value at a time (VEC = 1).
+// that are not made of 16-byte units go through it one value at a time (VEC = 1).  HBM bounds it, with two rows of
+// three tensors in flight per warp: 16384 x 768 bf16 21 us and 5 for the join, 16384 x 1024 fp32 47.6 us in all (5.6 TB/s),
+// 16384 x 770 bf16 33 us.
 template <typename io_t, int WPR, int UPL, int VEC = 16 / (int)sizeof(io_t)>
 __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) backward_kernel(const BackwardParams<io_t> p)
 {
