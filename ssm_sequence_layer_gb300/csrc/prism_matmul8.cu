@@ -32,10 +32,10 @@ struct Params {
 // of a8 as B operands.  The products' k order is a free choice as long as both operands share it: the
 // four words of a lane's 16 bytes serve as the k slots (lane % 4) 4 .. + 3 and 16 + (lane % 4) 4 .. + 3 of
 // two products.  KS warps of a CTA share a row tile and split the blocks of 128 among them, so that
-// narrow products still fill the machine; their sums are added in a fixed order.  8 x 50048 x 768 takes 11.6 us
-// (3.3 TB/s) and 8 x 32768 x 4096 32.7 us (4.1 TB/s): the loads that two blocks ahead keep in flight bound it, but three or
-// four blocks ahead (14 us), whole lines of one row per load (14.8), rings of bulk copies (16.4) and the weights as
-// the tcgen05 operand (14.1) are all slower.
+// narrow products still fill the machine; their sums are added in a fixed order.  8 x 50048 x 768 takes 9.9 us
+// (4.0 TB/s) and 8 x 32768 x 4096 31.2 us (4.3 TB/s) among calls of a graph: the loads that two blocks ahead keep in flight bound it, but three or
+// four blocks ahead (14 us, against 12 by single calls), whole lines of one row per load (14.8), rings of bulk copies (16.4)
+// and the weights as the tcgen05 operand (14.1) are all slower.
 constexpr int kSkinnyWarps = 8;
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
@@ -135,12 +135,12 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const Params<
 template <typename out_t, int NT>
 void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
 {
-    // Enough warps to keep each SM's loads in flight, as far as the blocks of 128 reach: with 16 warps a SM wanted instead
-    // of 40, 8 x 32768 x 4096 takes 38.1 us instead of 32.7 and 16 x 50048 x 768 17.7 instead of 16.6; with 80 the
-    // latter takes 18.5.
-    const int tiles = (p.N + 15) / 16;
+    // Enough warps to keep each SM's loads in flight, as far as the blocks of 128 reach.  16, 24 or 40 a SM: 8 x 50048 x
+    // 768 9.9, 10.3 and 10.3 us, 8 x 24576 x 1536 10.2, 10.8, 10.8, but 8 x 30000 x 2048 19.8, 19.9, 16.1 and 8 x 32768 x 4096
+    // 36.8, 36.8, 31.2; 16 x 50048 x 768 16.2, 14.7, 14.8, 16 x 65536 x 256 7.6, 7.6, 8.8.
+    const int tiles = (p.N + 15) / 16, want = p.KB >= 16 ? 40 : NT == 2 ? 24 : 16;
     int ks = 1;
-    while (ks < 8 && ks < p.KB && tiles * ks < 40 * sm_count) ks *= 2;
+    while (ks < 8 && ks < p.KB && tiles * ks < want * sm_count) ks *= 2;
     const int rt = kSkinnyWarps / ks;
     const unsigned grid = (tiles + rt - 1) / rt;
     if (ks == 1) skinny_kernel<out_t, NT, 1><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
@@ -614,7 +614,7 @@ cudaError_t product(const Matmul8Args &a, const TokenLaunch &l)
                           (a.K + kBlock - 1) / kBlock};
     cudaError_t e;
     l.timer->begin("matmul8");
-    // Few rows: 8 and 16 of N x K = 50048 x 768 take 11.6 and 16.6 us here, 17 take 15.8 in tiles; of 4096 x 4096 16
+    // Few rows: 8 and 16 of N x K = 50048 x 768 take 11.6 and 16.5 us here, 17 take 15.8 in tiles; of 4096 x 4096 16
     // take 9.8 here, 17 take 12.4 in tiles.  With four operands of 8 rows the loads wait for registers (32
     // rows: 22.8 us of 50048 x 768, 57 of 8192 x 8192; in tiles 16.3 and 31).
     if (a.M <= 16) {
