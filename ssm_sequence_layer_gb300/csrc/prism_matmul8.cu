@@ -27,13 +27,13 @@ struct Params {
 
 // ---------------------------------------------------------------------------------------------
 // Few rows (M <= 16): the weights' bytes bound the product, every weight is used M times at most.  A
-// warp takes 16 rows of w8 as the A operand of m16n8k32 products straight from global memory to
+// warp takes RPW tiles of 16 rows of w8 as A operands of m16n8k32 products straight from global memory to
 // registers (16 bytes of a row per lane and load, four loads for a block of 16 x 128), and 8 NT rows
 // of a8 as B operands.  The products' k order is a free choice as long as both operands share it: the
 // four words of a lane's 16 bytes serve as the k slots (lane % 4) 4 .. + 3 and 16 + (lane % 4) 4 .. + 3 of
-// two products.  KS warps of a CTA share a row tile and split the blocks of 128 among them, so that
-// narrow products still fill the machine; their sums are added in a fixed order.  8 x 50048 x 768 takes 9.9 us
-// (4.0 TB/s) and 8 x 32768 x 4096 31.2 us (4.3 TB/s) among calls of a graph: the loads that two blocks ahead keep in flight bound it, but three or
+// two products.  KS warps of a CTA share their tiles and split the blocks of 128 among them, so that
+// narrow products still fill the machine; their sums are added in a fixed order.  8 x 50048 x 768 takes 10.0 us
+// (3.9 TB/s) and 8 x 32768 x 4096 24.8 us (5.4 TB/s) among calls of a graph: the loads in flight bound it, but three or
 // four blocks ahead (14 us, against 12 by single calls), whole lines of one row per load (14.8), rings of bulk copies (16.4)
 // and the weights as the tcgen05 operand (14.1) are all slower.
 constexpr int kSkinnyWarps = 8;
@@ -46,31 +46,35 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename out_t, int NT, int KS>
+template <typename out_t, int NT, int KS, int RPW>  // RPW: tiles of 16 rows of a warp, which share a8
 __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const Params<out_t> p)
 {
-    constexpr int RT = kSkinnyWarps / KS;  // row tiles of a CTA
+    constexpr int RT = kSkinnyWarps / KS;  // warps of a CTA with rows of their own
     constexpr int AHEAD = 2;               // blocks of 128 in flight
-    __shared__ float parts[KS > 1 ? kSkinnyWarps : 1][16][8 * NT + 1];
+    __shared__ float parts[KS > 1 ? kSkinnyWarps : 1][16 * RPW][8 * NT + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    const int ks = warp % KS, n0 = (blockIdx.x * RT + warp / KS) * 16;
-    float total[NT][4];
+    const int ks = warp % KS, n0 = (blockIdx.x * RT + warp / KS) * 16 * RPW;
+    float total[RPW][NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int r = 0; r < RPW; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) total[t][i] = 0.f;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) total[r][t][i] = 0.f;
     if (n0 < p.N) {
         // rows beyond the operands' last are read as the last and not stored
-        const uint8_t *wr[2] = {p.w + (size_t)min(n0 + g, p.N - 1) * p.K, p.w + (size_t)min(n0 + g + 8, p.N - 1) * p.K};
+        const uint8_t *wr[2 * RPW];
+#pragma unroll
+        for (int r = 0; r < 2 * RPW; ++r) wr[r] = p.w + (size_t)min(n0 + g + 8 * r, p.N - 1) * p.K;
         const float *ws = p.w_scale + (size_t)(n0 / kBlock) * p.KB;
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        uint4 w[AHEAD][2][2];
+        uint4 w[AHEAD][2 * RPW][2];
         auto load = [&](int slot, int b) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = b * kBlock + h * 64 + q * 16;
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+                for (int r = 0; r < 2 * RPW; ++r)
                     w[slot][r][h] = k < p.K ? __ldcs(reinterpret_cast<const uint4 *>(wr[r] + k)) : zero;
             }
         };
@@ -96,57 +100,74 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) skinny_kernel(const Params<
                 }
                 const float sw = ws[b];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int r = 0; r < RPW; ++r)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        mma_e4m3(c, w[s][0][h].x, w[s][1][h].x, w[s][0][h].y, w[s][1][h].y, a[t][h].x, a[t][h].y);
-                        mma_e4m3(c, w[s][0][h].z, w[s][1][h].z, w[s][0][h].w, w[s][1][h].w, a[t][h].z, a[t][h].w);
+                    for (int t = 0; t < NT; ++t) {
+                        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 lo = w[s][2 * r][h], hi = w[s][2 * r + 1][h];
+                            mma_e4m3(c, lo.x, hi.x, lo.y, hi.y, a[t][h].x, a[t][h].y);
+                            mma_e4m3(c, lo.z, hi.z, lo.w, hi.w, a[t][h].z, a[t][h].w);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) total[r][t][i] = fmaf(c[i], sa[t][i & 1] * sw, total[r][t][i]);
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) total[t][i] = fmaf(c[i], sa[t][i & 1] * sw, total[t][i]);
-                }
                 load(s, b + AHEAD * KS);
             }
         }
     }
     if constexpr (KS > 1) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int r = 0; r < RPW; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) parts[warp][g + 8 * (i >> 1)][8 * t + 2 * q + (i & 1)] = total[t][i];
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) parts[warp][16 * r + g + 8 * (i >> 1)][8 * t + 2 * q + (i & 1)] = total[r][t][i];
         __syncthreads();
         if (ks != 0) return;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int r = 0; r < RPW; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                for (int o = 1; o < KS; ++o) total[t][i] += parts[warp + o][g + 8 * (i >> 1)][8 * t + 2 * q + (i & 1)];
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    for (int o = 1; o < KS; ++o) total[r][t][i] += parts[warp + o][16 * r + g + 8 * (i >> 1)][8 * t + 2 * q + (i & 1)];
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int r = 0; r < RPW; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = 8 * t + 2 * q + (i & 1), n = n0 + g + 8 * (i >> 1);
-            if (m < p.M && n < p.N) io::st(p.out + (size_t)m * p.N + n, total[t][i]);
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = 8 * t + 2 * q + (i & 1), n = n0 + 16 * r + g + 8 * (i >> 1);
+                if (m < p.M && n < p.N) io::st(p.out + (size_t)m * p.N + n, total[r][t][i]);
+            }
 }
 
 template <typename out_t, int NT>
 void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
 {
-    // Enough warps to keep each SM's loads in flight, as far as the blocks of 128 reach.  16, 24 or 40 a SM: 8 x 50048 x
-    // 768 9.9, 10.3 and 10.3 us, 8 x 24576 x 1536 10.2, 10.8, 10.8, but 8 x 30000 x 2048 19.8, 19.9, 16.1 and 8 x 32768 x 4096
-    // 36.8, 36.8, 31.2; 16 x 50048 x 768 16.2, 14.7, 14.8, 16 x 65536 x 256 7.6, 7.6, 8.8.
-    const int tiles = (p.N + 15) / 16, want = p.KB >= 16 ? 40 : NT == 2 ? 24 : 16;
+    // Two tiles of 16 rows per warp share the reads of a8 and keep twice the bytes in flight, where that leaves enough warps:
+    // 8 x 8192 x 8192 takes 21.2 us with one and 14.9 with two, 8 x 32768 x 4096 31.6 and 24.8, 16 x 8192 x 768 5.4 and 4.4, but
+    // 8 x 6144 x 1024 3.4 and 3.7, 8 x 2304 x 768 2.2 and 2.4, 16 x 2304 x 768 2.8 and 3.0 (calls of a graph).
+    const int pairs = (p.N + 31) / 32;
+    constexpr int T = 32 * kSkinnyWarps;
+    if (pairs * 8LL < (NT == 1 ? 12 : 6) * sm_count) {  // few: all warps of a CTA on one tile
+        skinny_kernel<out_t, NT, 8, 1><<<(p.N + 15) / 16, T, 0, s>>>(p);
+        return;
+    }
+    // As many warps as keep each SM's loads in flight, as far as the blocks of 128 reach: 4, 8 or 16 a SM give 30.3, 24.8 and
+    // 26.7 us for 8 x 32768 x 4096, 10.0, 10.0 and 11.5 for 8 x 50048 x 768; 16 x 8192 x 8192 20.2, 22.3 and 22.2, 16 x 16384 x 768
+    // 6.2, 7.7 and 10.5.
     int ks = 1;
-    while (ks < 8 && ks < p.KB && tiles * ks < want * sm_count) ks *= 2;
+    while (ks < 8 && ks < p.KB && (long long)pairs * ks < (NT == 1 ? 8 : 4) * sm_count) ks *= 2;
     const int rt = kSkinnyWarps / ks;
-    const unsigned grid = (tiles + rt - 1) / rt;
-    if (ks == 1) skinny_kernel<out_t, NT, 1><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
-    else if (ks == 2) skinny_kernel<out_t, NT, 2><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
-    else if (ks == 4) skinny_kernel<out_t, NT, 4><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
-    else skinny_kernel<out_t, NT, 8><<<grid, 32 * kSkinnyWarps, 0, s>>>(p);
+    const unsigned grid = (pairs + rt - 1) / rt;
+    if (ks == 1) skinny_kernel<out_t, NT, 1, 2><<<grid, T, 0, s>>>(p);
+    else if (ks == 2) skinny_kernel<out_t, NT, 2, 2><<<grid, T, 0, s>>>(p);
+    else if (ks == 4) skinny_kernel<out_t, NT, 4, 2><<<grid, T, 0, s>>>(p);
+    else skinny_kernel<out_t, NT, 8, 2><<<grid, T, 0, s>>>(p);
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -50,7 +50,8 @@ SHAPES = [(1, 1, 16), (1, 64, 64), (1, 1000, 768), (4, 777, 272), (8, 5000, 128)
           (24, 96, 4096), (31, 3000, 256), (33, 500, 768), (64, 2048, 512), (65, 333, 128), (100, 256, 2064), (127, 129, 144), (128, 128, 128),
           (129, 257, 1040), (200, 40, 768), (256, 512, 384), (300, 4626, 256), (1000, 136, 160), (2050, 264, 768), (5000, 16, 64), (1000, 5000, 400),
           (1100, 6000, 272), (200, 20000, 144), (384, 30000, 128), (5000, 1111, 400), (3, 100, 4096), (12, 40, 8192), (2, 20000, 528), (8, 2500, 1024), (16, 33, 2000), (17, 3000, 512),
-          (40, 130, 2000), (257, 515, 1600), (1000, 1000, 1536), (20, 7, 16384)]
+          (40, 130, 2000), (257, 515, 1600), (1000, 1000, 1536), (20, 7, 16384),
+          (9, 3700, 272), (16, 20011, 1040), (13, 5000, 2064), (8, 9001, 4096), (5, 50048, 160), (11, 40001, 128), (7, 8000, 784)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
