@@ -493,9 +493,10 @@ PRISM_API prism_status prism_matmul8_weights(prism_tokens_t tokens, int N, int K
  * targets [n] int64 may be NULL; each output may be NULL; k in 0 .. 32 (k = 0: no top).
  * Masked tokens: a logit of -inf or of the lowest bfloat16 value and below (either is how masks are
  * written), and a product that overflows to -inf, counts as z = -inf: its probability is zero, it adds
- * nothing to the entropy and is never among the top (missing places hold id -1 and -inf).  Where a whole row is masked, lse is -inf,
- * entropy 0 and logprob -inf.  NaN or +inf in a row gives NaN lse, logprob and entropy, as the
- * formulas do; NaN logits come first among the top.  inv_temperature must be finite and > 0.
+ * nothing to the entropy and is never among the top (missing places hold id -1 and -inf).  Where a whole
+ * row is masked, lse is -inf, entropy 0 and logprob -inf.  NaN or +inf in a row gives NaN lse, logprob
+ * and entropy, as the formulas do; NaN logits come first among the top.  inv_temperature must be finite
+ * and > 0.
  */
 PRISM_API prism_status prism_token_logprobs(prism_tokens_t tokens, int n, const void *logits, long long ld,
                                             const long long *targets, float inv_temperature, int k, float *lse,
@@ -507,7 +508,9 @@ PRISM_API prism_status prism_token_logprobs(prism_tokens_t tokens, int n, const 
  *   dlogits_j = inv_temperature (dlogprob (1_{j=t} - p_j) - dentropy p_j (log p_j + entropy))
  *   dlogprob, dentropy [n] float32 (each may be NULL, not both; dlogprob needs targets, dentropy needs
  *   entropy); dlogits [n, V] with row stride ld_d >= V, dtype of the logits, may be the logits
- *   themselves when ld_d = ld.  Masked tokens and wholly masked rows get zero.
+ *   themselves when ld_d = ld.  Masked tokens and wholly masked rows get zero; a row whose lse is NaN
+ *   gets NaN everywhere.  log p_j is taken as z_j - lse, so p_j is within about 2^-24 (|z_j| + |lse|) of
+ *   itself.
  */
 PRISM_API prism_status prism_token_logprobs_backward(prism_tokens_t tokens, int n, const void *logits, long long ld,
                                                      const long long *targets, float inv_temperature,

@@ -635,9 +635,9 @@ cudaError_t product(const Matmul8Args &a, const TokenLaunch &l)
                           (a.K + kBlock - 1) / kBlock};
     cudaError_t e;
     l.timer->begin("matmul8");
-    // Few rows: 8 and 16 of N x K = 50048 x 768 take 11.6 and 16.5 us here, 17 take 15.8 in tiles; of 4096 x 4096 16
-    // take 9.8 here, 17 take 12.4 in tiles.  With four operands of 8 rows the loads wait for registers (32
-    // rows: 22.8 us of 50048 x 768, 57 of 8192 x 8192; in tiles 16.3 and 31).
+    // Few rows, among calls of a graph: 16 of N x K = 50048 x 768 take 14.9 us here and 17 13.9 in tiles, of 8192 x 8192
+    // 20.1 and 20.1, of 4096 x 4096 7.8 and 10.7; 8 take 10.0, 14.9 and 6.4.  With four operands of 8 rows the loads wait
+    // for registers (32 rows of 50048 x 768 22.8 by single calls, in tiles 16.3).
     if (a.M <= 16) {
         if (a.M <= 8) launch_skinny<out_t, 1>(p, l.sm_count, l.timer->stream);
         else launch_skinny<out_t, 2>(p, l.sm_count, l.timer->stream);
