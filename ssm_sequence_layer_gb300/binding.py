@@ -535,7 +535,8 @@ class Tokens:
     ``max_rows`` is the largest number of rows of a call, ``D`` the model width, ``V`` the vocabulary,
     ``io`` the dtype of activations and tables ("bf16" or "f32"), ``logits`` that of logits (``io``
     unless given).  Rows are tokens; leading axes of the arguments are flattened.  Outputs are
-    allocated unless given.  ``stream`` is torch's current stream unless given.
+    allocated unless given.  ``stream`` (a torch stream or a raw one) is torch's current stream unless
+    given; one that is given is the current stream of the call, for the outputs' memory too.
     """
 
     def __init__(self, max_rows, D, V, io="bf16", logits=None):
@@ -562,8 +563,14 @@ class Tokens:
     def last_device_status(self):
         return prism_tokens_last_device_status(self.handle)
 
-    def _on(self, stream):
-        return self._current_stream(self.device) if stream is None else _stream(stream)
+    @staticmethod
+    def _on(stream, method, *args):
+        """The call with ``stream`` as the current one, whose memory the outputs then come from."""
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return method(*args)
 
     @staticmethod
     def _need(name, t, dtype, numel=None, width=None):
@@ -577,6 +584,8 @@ class Tokens:
         """scale * table[ids] (see prism_embed): ids [...] int64, table [V, D] whose rows may be
         padded (a stride); returns [..., D].  Negative ids give rows of zeros."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.embed, ids, table, scale, out)
         n = ids.numel()
         self._need("ids", ids, torch.int64)
         if table.dtype is not self._io or not table.is_cuda or table.shape != (self.V, self.D) or table.stride(1) != 1:
@@ -585,13 +594,15 @@ class Tokens:
             out = torch.empty(*ids.shape, self.D, dtype=self._io, device=ids.device)
         else:
             self._need("out", out, self._io, n * self.D)
-        prism_embed(self.handle, n, ids, table, table.stride(0), scale, out, self._on(stream))
+        prism_embed(self.handle, n, ids, table, table.stride(0), scale, out, self._current_stream(self.device))
         return out
 
     def embed_backward(self, ids, dout, scale=1.0, dtable=None, accumulate=False, stream=None):
         """The table's gradient [V, D] float32 (see prism_embed_backward); with ``accumulate`` it is
         added to ``dtable``."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.embed_backward, ids, dout, scale, dtable, accumulate)
         n = ids.numel()
         self._need("ids", ids, torch.int64)
         self._need("dout", dout, self._io, n * self.D, self.D)
@@ -601,7 +612,7 @@ class Tokens:
             dtable = torch.empty(self.V, self.D, dtype=torch.float32, device=ids.device)
         else:
             self._need("dtable", dtable, torch.float32, self.V * self.D)
-        prism_embed_backward(self.handle, n, ids, dout, scale, accumulate, dtable, self._on(stream))
+        prism_embed_backward(self.handle, n, ids, dout, scale, accumulate, dtable, self._current_stream(self.device))
         return dtable
 
     def norm(self, x, weight, residual=None, eps=1e-6, want=("y",), out=None, stream=None):
@@ -609,6 +620,8 @@ class Tokens:
         of the outputs that ``want`` names -- "sum" and "y" [..., D], "y8" (float8_e4m3fn) with its
         "y_scale" [..., ceil(D/128)] -- or fills and returns ``out``, a dict of them."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.norm, x, weight, residual, eps, want, out)
         D = self.D
         n = x.numel() // D
         need = self._need
@@ -637,7 +650,7 @@ class Tokens:
                 else:
                     raise ValueError(f"prism_norm has no output {key!r}")
         get = out.get
-        prism_norm(self.handle, n, x, residual, weight, eps, get("sum"), get("y"), get("y8"), get("y_scale"), self._on(stream))
+        prism_norm(self.handle, n, x, residual, weight, eps, get("sum"), get("y"), get("y8"), get("y_scale"), self._current_stream(self.device))
         return out
 
     def norm_backward(self, sum, weight, dy, dsum=None, eps=1e-6, out=None, stream=None):
@@ -645,6 +658,8 @@ class Tokens:
         where there was no residual), dsum the cotangent that reaches it besides the norm's.
         Returns {"dx" [..., D], "dweight" [D] float32}."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.norm_backward, sum, weight, dy, dsum, eps, out)
         D = self.D
         n = sum.numel() // D
         need = self._need
@@ -658,7 +673,7 @@ class Tokens:
         else:
             need("dx", out["dx"], self._io, n * D)
             need("dweight", out["dweight"], torch.float32, D)
-        prism_norm_backward(self.handle, n, sum, weight, eps, dy, dsum, out["dx"], out["dweight"], self._on(stream))
+        prism_norm_backward(self.handle, n, sum, weight, eps, dy, dsum, out["dx"], out["dweight"], self._current_stream(self.device))
         return out
 
     def matmul8(self, a8, a_scale, w8, w_scale, out=None, stream=None):
@@ -666,6 +681,8 @@ class Tokens:
         [..., ceil(K/128)] (norm's "y8" and "y_scale"), w8 [N, K] with w_scale
         [ceil(N/128), ceil(K/128)] (matmul8_weights); returns [..., N] in the logits' dtype."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.matmul8, a8, a_scale, w8, w_scale, out)
         need, f8, f32 = self._need, torch.float8_e4m3fn, torch.float32
         N, K = w8.shape
         M, kb = a8.numel() // K, -(-K // 128)
@@ -677,17 +694,19 @@ class Tokens:
             out = torch.empty(*a8.shape[:-1], N, dtype=self._logits, device=a8.device)
         else:
             need("out", out, self._logits, M * N)
-        prism_matmul8(self.handle, M, N, K, a8, a_scale, w8, w_scale, out, self._on(stream))
+        prism_matmul8(self.handle, M, N, K, a8, a_scale, w8, w_scale, out, self._current_stream(self.device))
         return out
 
     def matmul8_weights(self, W, stream=None):
         """Weights W [N, K] (io dtype) laid out once for matmul8: (w8, w_scale)."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.matmul8_weights, W)
         N, K = W.shape
         self._need("W", W, self._io)
         w8 = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=W.device)
         w_scale = torch.empty(-(-N // 128), -(-K // 128), dtype=torch.float32, device=W.device)
-        prism_matmul8_weights(self.handle, N, K, W, w8, w_scale, self._on(stream))
+        prism_matmul8_weights(self.handle, N, K, W, w8, w_scale, self._current_stream(self.device))
         return w8, w_scale
 
     def _logit_rows(self, name, t):
@@ -707,6 +726,8 @@ class Tokens:
         "entropy" [...], with targets "logprob" [...], with k > 0 "top_ids" [..., k] int64 and
         "top_logprob" [..., k]; or fills and returns ``out``, a dict of those that are wanted."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.token_logprobs, logits, targets, inv_temperature, k, out)
         n, ld = self._logit_rows("logits", logits)
         need, f32, i64 = self._need, torch.float32, torch.int64
         if targets is not None:
@@ -729,7 +750,7 @@ class Tokens:
                     raise ValueError(f"prism_token_logprobs has no output {key!r}")
         get = out.get
         prism_token_logprobs(self.handle, n, logits, ld, targets, inv_temperature, k, get("lse"), get("logprob"), get("entropy"),
-                             get("top_ids"), get("top_logprob"), self._on(stream))
+                             get("top_ids"), get("top_logprob"), self._current_stream(self.device))
         return out
 
     def token_logprobs_backward(self, logits, targets, lse, entropy, dlogprob, dentropy=None, inv_temperature=1.0, dlogits=None,
@@ -737,6 +758,8 @@ class Tokens:
         """The logits' cotangent (see prism_token_logprobs_backward), given the forward's lse and
         entropy (may be None without dentropy); dlogits may be the logits themselves."""
         import torch
+        if stream is not None:
+            return self._on(stream, self.token_logprobs_backward, logits, targets, lse, entropy, dlogprob, dentropy, inv_temperature, dlogits)
         n, ld = self._logit_rows("logits", logits)
         need, f32 = self._need, torch.float32
         for name, t in (("lse", lse), ("entropy", entropy), ("dlogprob", dlogprob), ("dentropy", dentropy)):
@@ -752,7 +775,7 @@ class Tokens:
             if rows != n:
                 raise ValueError("dlogits must have the logits' rows")
         prism_token_logprobs_backward(self.handle, n, logits, ld, targets, inv_temperature, lse, entropy, dlogprob, dentropy,
-                                      dlogits, ld_d, self._on(stream))
+                                      dlogits, ld_d, self._current_stream(self.device))
         return dlogits
 
     def close(self):

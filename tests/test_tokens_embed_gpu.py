@@ -212,3 +212,24 @@ def test_embed_refusals():
             with pytest.raises(B.PrismError) as ei:
                 bad()
             assert ei.value.status == status
+
+
+def test_outputs_come_from_the_given_streams_memory():
+    """A block that the current stream has just freed may still be read by its pending work, so a call on
+    another stream must not get it for its output."""
+    n, D, V = 4096, 1024, 64
+    g = torch.Generator().manual_seed(1)
+    ids, table = draw_ids(n, V, 2, "zipf").cuda(), torch.randn(V, D, generator=g).cuda()
+    s = torch.cuda.Stream()
+    with B.Tokens(n, D, V, io="f32") as t:
+        ref = t.embed(ids, table)
+        torch.cuda.synchronize()
+        freed = torch.empty(n, D, device="cuda")
+        address = freed.data_ptr()
+        del freed
+        outs = [t.embed(ids, table, stream=s), t.embed(ids, table, stream=s.cuda_stream)]
+        assert all(o.data_ptr() != address for o in outs)
+        outs.append(t.embed(ids, table, stream=0))
+        torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, ref)
