@@ -120,7 +120,8 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
         return cuda_fail(e, "workspace allocation");
     }
     t->d_status = (int *)t->ws;
-    if ((e = cudaMemset(t->d_status, 0, sizeof(int))) != cudaSuccess) {
+    // waited for: streams that do not wait for the default one may use the handle at once
+    if ((e = cudaMemset(t->d_status, 0, sizeof(int))) != cudaSuccess || (e = cudaStreamSynchronize(nullptr)) != cudaSuccess) {
         cudaFree(t->ws);
         delete t;
         return cuda_fail(e, "status word init");
@@ -182,7 +183,8 @@ prism_status prism_tokens_last_device_status(prism_tokens_t t)
     cudaError_t e = cudaMemcpy(&word, t->d_status, sizeof(int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "status read");
     if (word == prism::kDevOk) return PRISM_OK;
-    if ((e = cudaMemset(t->d_status, 0, sizeof(int))) != cudaSuccess) return cuda_fail(e, "status clear");
+    if ((e = cudaMemset(t->d_status, 0, sizeof(int))) != cudaSuccess || (e = cudaStreamSynchronize(nullptr)) != cudaSuccess)
+        return cuda_fail(e, "status clear");
     if (word == prism::kDevTimeout) return fail(PRISM_ERR_TIMEOUT, "a bounded device wait expired");
     return fail(PRISM_ERR_DEVICE, "a token id or target was >= V = %d (treated as no token)", t->V);
 }
