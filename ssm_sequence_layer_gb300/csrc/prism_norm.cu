@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel
     }
 }
 
-// Any width and alignment: a warp per row, one value per lane at a time, two passes over the row (the
-// second one comes from the caches): 16384 x 770 bf16 34 us, 2.9 TB/s, bound by the number of loads.  Nothing is
-// written before the row has been read to its end, and
-// then each value is read before its own place is written, so outputs may take an input's place.
+// Any width and alignment: a warp per row, one value per lane at a time, two passes over the row (the second
+// one comes from the caches): 16384 x 770 bf16 34 us, 2.9 TB/s, bound by the instructions per value (with the row held
+// in registers 33 us).  Nothing is written before the row has been read to its end, and then each value is read
+// before its own place is written, so outputs may take an input's place.
 template <typename io_t>
 __global__ void __launch_bounds__(kThreads) forward_any_kernel(const ForwardParams<io_t> p)
 {
