@@ -16,7 +16,7 @@
 // most frequent ones of a text do, is spread over eight warps there).  The sort keeps few SMs busy, so the
 // table's zeros are written beside it.
 //
-// 16384 x 768 bf16 of 50021: 44 us for 179 MB (4.1 TB/s); timed one by one the sort with 96 MB of zeros takes 22, the sums
+// 16384 x 768 bf16 of 50021: 40 us in a graph for 179 MB (4.5 TB/s); timed one by one the sort with 96 MB of zeros takes 22, the sums
 // with the other zeros 20 and the join 10 (onto a table that is not cleared: 15, 16 and 10, 33 in all).  14309 x 648
 // of 130295: 71 us for 356 MB (5.0 TB/s).
 #include <type_traits>
@@ -608,14 +608,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumParams p)
         more = __popc(__ballot_sync(0xffffffffu, same));
         if (next != p.V && last == next && earlier != next) key = next;
     }
-    const bool fits = more < 32;
+    // One warp adds a few parts; more of them are worth the block's eight warps (16384 x 768 of 50021 in a graph: up to 32
+    // parts by one warp 41.1 us, up to 8 39.8).
+    const bool fits = more < 8;
     if (key >= 0 && fits) finish(key, add_parts(a, 0, more + 1));
     if (lane == 0) long_key[warp] = fits ? -1 : key;
     __syncthreads();
     for (int t = 0; t < kThreads / 32; ++t) {  // runs of more tiles: the whole block
         const int from = blockIdx.x * (kThreads / 32) + t, k = long_key[t];
         if (k < 0) continue;
-        int b = from + 33;  // the first tile that does not begin with the key
+        int b = from + 1;  // the first tile that does not begin with the key
         for (;;) {
             const int i = b + tid;
             const int same = __syncthreads_count(i < p.tiles && p.key[(size_t)i * p.tile] == k);
