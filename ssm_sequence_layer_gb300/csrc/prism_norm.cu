@@ -40,40 +40,53 @@ __device__ __forceinline__ uint16_t e4m3x2(float a, float b)
     return r;
 }
 
-// The 8-bit values of a block of 128.  A value's e4m3 neighbour is decided by y / scale = v / s with v = r w and
+// 1 / rms as a power of two and a factor in [1, 2).  Rows are multiplied by the power first, which rounds nothing and
+// brings them to a size of about one, so that v = (power r) w leaves the range of fp32 only where y = factor v does too.
+struct Root {
+    float power, factor;
+    __device__ __forceinline__ explicit Root(float q)
+    {
+        const uint32_t b = __float_as_uint(q);
+        power = q != q ? q : __uint_as_float(b & 0x7f800000u);  // 0 and infinity stay what they are
+        factor = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
+    }
+};
+
+// The 8-bit values of a block of 128.  A value's e4m3 neighbour is decided by y / scale = v / s with
 // s = max |v| / 448, in which 1 / rms cancels.  A rounding error there moves values that lie near the middle between
 // two neighbours to the wrong one, so v is held as a product and its rounding error, and the quotient is
 // corrected once with both: what is left are the roundings of s and of the result.  (Of 50 million bf16 values the
 // plain sequence of roundings moves 299, this one 13.)  Values come in pairs: two operations an instruction.
 struct Block {
-    float s, inverse;  // max |v| / 448 and its reciprocal
-    float q, scale;    // 1 / rms; the scale that is stored
-    bool plain;        // the correction does not apply: a scale at its lower bound, or infinite
+    float s, inverse;     // max |v| / 448 and its reciprocal
+    float factor, scale;  // of the root; the scale that is stored
+    // The correction does not apply: s is so small or so large that its reciprocal, a remainder or a product's rounding
+    // error is not a normal number, or not a number at all
+    bool plain;
 
-    __device__ __forceinline__ Block(float peak, float q_) : q(q_)
+    __device__ __forceinline__ Block(float peak, float factor_) : factor(factor_)
     {
         s = peak / kMaxE4M3;
-        const float raw = s * q;  // NaN where 1 / rms is 0 and the peak infinite: y is 0 or NaN there
-        scale = fmaxf(raw, kMinScale);
-        plain = !(raw > kMinScale) || scale == INFINITY;
+        scale = fmaxf(s * factor, kMinScale);
+        plain = !(s >= 0x1p-80f && s <= 0x1p100f);
         inverse = plain ? 1.f / scale : 1.f / s;
     }
     // v and minus its rounding error
     __device__ __forceinline__ float2 quotient(float2 v, float2 minus_low) const
     {
         using namespace io;
-        const float2 i2 = make_float2(inverse, inverse), q2 = make_float2(q, q);
-        if (plain) return mul2(mul2(v, q2), i2);
+        const float2 i2 = make_float2(inverse, inverse), f2 = make_float2(factor, factor);
+        if (plain) return mul2(mul2(v, f2), i2);
         const float2 t = mul2(v, i2);
         const float2 rest = fma2(minus_low, make_float2(-1.f, -1.f), fma2(t, make_float2(-s, -s), v));
         return fma2(rest, i2, t);
     }
 };
-// v = r w, and minus its rounding error
-__device__ __forceinline__ float2 product(float2 r, float2 w, float2 &minus_low)
+// v = (power r) w, and minus its rounding error
+__device__ __forceinline__ float2 product(float2 r, float2 w, float power, float2 &minus_low)
 {
-    const float2 v = io::mul2(r, w);
-    minus_low = io::fma2(r, make_float2(-w.x, -w.y), v);
+    const float2 a = io::mul2(r, make_float2(power, power)), v = io::mul2(a, w);
+    minus_low = io::fma2(a, make_float2(-w.x, -w.y), v);
     return v;
 }
 
@@ -143,20 +156,20 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel
 #pragma unroll
             for (int o = 0; o < WPR; ++o) ss += parts[turn][o];
         }
-        const float q = __frsqrt_rn(ss / (float)p.D + p.eps);
+        const Root q(__frsqrt_rn(ss / (float)p.D + p.eps));
 #pragma unroll
         for (int j = 0; j < UPL; ++j) {
             const int u = t + G * j;
             const bool mine = u < units;
             const size_t at = (size_t)row * p.D + (size_t)u * VEC;
             float w4[VEC], peak = 0.f;
-            float2 v[VEC / 2], low[VEC / 2];  // r w and minus its rounding error
+            float2 v[VEC / 2], low[VEC / 2];  // y without the root's factor, and minus the product's rounding error
 #pragma unroll
             for (int e = 0; e < VEC; ++e) w4[e] = 0.f;
             if (mine) w[j].get(w4);
 #pragma unroll
             for (int e = 0; e < VEC; e += 2) {
-                v[e / 2] = product(make_float2(r[j][e], r[j][e + 1]), make_float2(w4[e], w4[e + 1]), low[e / 2]);
+                v[e / 2] = product(make_float2(r[j][e], r[j][e + 1]), make_float2(w4[e], w4[e + 1]), q.power, low[e / 2]);
                 peak = fmaxf(peak, fmaxf(fabsf(v[e / 2].x), fabsf(v[e / 2].y)));
             }
             U o;
@@ -167,14 +180,14 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel
             if (mine && p.y) {
                 float y[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; e += 2) y[e] = v[e / 2].x * q, y[e + 1] = v[e / 2].y * q;
+                for (int e = 0; e < VEC; e += 2) y[e] = v[e / 2].x * q.factor, y[e + 1] = v[e / 2].y * q.factor;
                 o.set(y);
                 io::store_unit<io_t, VEC>(p.y + at, o);
             }
             if (p.y8) {
 #pragma unroll
                 for (int o2 = PER / 2; o2 > 0; o2 >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o2));
-                const Block block(peak, q);
+                const Block block(peak, q.factor);
                 if (mine) {
                     if (lane % PER == 0) p.y_scale[(size_t)row * blocks + u / PER] = block.scale;
                     uint16_t b[VEC / 2];
@@ -210,31 +223,34 @@ __global__ void __launch_bounds__(kThreads) forward_any_kernel(const ForwardPara
         const float r = sum_at(c);
         ss = fmaf(r, r, ss);
     }
-    const float q = __frsqrt_rn(warp_sum(ss) / (float)p.D + p.eps);
+    const Root q(__frsqrt_rn(warp_sum(ss) / (float)p.D + p.eps));
     const int blocks = (p.D + kBlock - 1) / kBlock;
     for (int b = 0; b < blocks; ++b) {
-        float2 v[kBlock / 64], low[kBlock / 64];  // columns 64 i + lane and 32 further
-        float peak = 0.f;
+        float r[kBlock / 64][2], wt[kBlock / 64][2];  // columns 64 i + lane and 32 further
 #pragma unroll
-        for (int i = 0; i < kBlock / 64; ++i) {
-            float r[2] = {0.f, 0.f}, wt[2] = {0.f, 0.f};
+        for (int i = 0; i < kBlock / 64; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int c = b * kBlock + 64 * i + 32 * h + lane;
-                if (c < p.D) r[h] = sum_at(c), wt[h] = io::ld(p.weight + c);
+                r[i][h] = wt[i][h] = 0.f;
+                if (c < p.D) r[i][h] = sum_at(c), wt[i][h] = io::ld(p.weight + c);
             }
-            v[i] = product(make_float2(r[0], r[1]), make_float2(wt[0], wt[1]), low[i]);
+        float2 v[kBlock / 64], low[kBlock / 64];
+        float peak = 0.f;
+#pragma unroll
+        for (int i = 0; i < kBlock / 64; ++i) {
+            v[i] = product(make_float2(r[i][0], r[i][1]), make_float2(wt[i][0], wt[i][1]), q.power, low[i]);
             peak = fmaxf(peak, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int c = b * kBlock + 64 * i + 32 * h + lane;
                 if (c >= p.D) continue;
-                if (p.sum) io::st(p.sum + at + c, r[h]);
-                if (p.y) io::st(p.y + at + c, (h ? v[i].y : v[i].x) * q);
+                if (p.sum) io::st(p.sum + at + c, r[i][h]);
+                if (p.y) io::st(p.y + at + c, (h ? v[i].y : v[i].x) * q.factor);
             }
         }
         if (p.y8) {
-            const Block block(warp_max(peak), q);
+            const Block block(warp_max(peak), q.factor);
             if (lane == 0) p.y_scale[(size_t)row * blocks + b] = block.scale;
 #pragma unroll
             for (int i = 0; i < kBlock / 64; ++i) {
