@@ -58,7 +58,10 @@ LOWEST = -3.38953139e38  # bfloat16's: a logit at or below it is masked
 
 
 def z_of(logits, c):
-    return np.where(logits <= LOWEST * (1 - 1e-9), -np.inf, c * logits.astype(np.float64))
+    """c logits; -inf where the logit is a mask's value or the product overflows to -inf in float32."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        overflows = logits.astype(np.float32) * np.float32(c) == -np.inf
+    return np.where((logits <= LOWEST * (1 - 1e-9)) | overflows, -np.inf, c * logits.astype(np.float64))
 
 
 def token_logprobs(logits, targets, c, k):

@@ -99,6 +99,9 @@ struct Row<float> {
     }
 };
 
+// Is it a masked token's logit?  (NaN is none.)
+__device__ __forceinline__ bool masked(float x, float c) { return x <= kLowest || x * c == -INFINITY; }
+
 // A part of a row: its largest logit (-inf: no live token), s and t relative to it
 struct Part {
     float top, s, t;
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
         __syncthreads();
         const float least = threshold;
         auto offer = [&](float v, int id) {
-            if (v < least || v <= kLowest || v * p.inv_temperature == -INFINITY) return;  // NaN passes
+            if (v < least || masked(v, p.inv_temperature)) return;  // NaN passes
             const int at = atomicAdd(&found, 1);
             if (at < kCandidates) cand[at] = key_of(v, id);
         };
@@ -374,11 +377,11 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
                 x.get(v);
 #pragma unroll
                 for (int e = 0; e < R::VEC; ++e)
-                    if (!(v[e] <= kLowest || v[e] * p.inv_temperature == -INFINITY)) look(key_of(v[e], sl.first + at * R::VEC + e));
+                    if (!masked(v[e], p.inv_temperature)) look(key_of(v[e], sl.first + at * R::VEC + e));
             }
             if (single >= 0) {
                 const float v = io::ld(sl.x + single);
-                if (!(v <= kLowest || v * p.inv_temperature == -INFINITY)) look(key_of(v, single));
+                if (!masked(v, p.inv_temperature)) look(key_of(v, single));
             }
         };
         if (count > kCandidates) {  // many equal logits: by keys instead of by values
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 6) forward_kernel(const ForwardParam
                 float v = 0.f;
                 if (t >= 0 && t < p.V) {
                     const float x = io::ld(sl.x + t);
-                    v = none || x <= kLowest ? -INFINITY : (x - top) * c - logs;
+                    v = none || masked(x, c) ? -INFINITY : (x - top) * c - logs;
                     if (all.s != all.s) v = all.s;
                 }
                 p.logprob[row] = v;
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<
             float v = 0.f;
             if (t >= 0 && t < p.V) {
                 const float x = io::ld(sl.x + t);
-                v = none || x <= kLowest ? -INFINITY : (x - m) * c - logs;
+                v = none || masked(x, c) ? -INFINITY : (x - m) * c - logs;
                 if (all.s != all.s) v = all.s;
             }
             p.logprob[row] = v;
@@ -619,12 +622,12 @@ __global__ void __launch_bounds__(kThreads, 4) short_kernel(const ForwardParams<
                     x.get(v);
 #pragma unroll
                     for (int e = 0; e < R::VEC; ++e)
-                        if (!(v[e] < least || v[e] <= kLowest || v[e] * c == -INFINITY)) look(key_of(v[e], sl.first + unit * R::VEC + e));
+                        if (!(v[e] < least || masked(v[e], c))) look(key_of(v[e], sl.first + unit * R::VEC + e));
                 }
             }
             if (single >= 0) {
                 const float v = io::ld(sl.x + single);
-                if (!(v < least || v <= kLowest || v * c == -INFINITY)) look(key_of(v, single));
+                if (!(v < least || masked(v, c))) look(key_of(v, single));
             }
         };
         best[lane] = 0;
@@ -725,27 +728,28 @@ __global__ void __launch_bounds__(kThreads, 6) backward_kernel(const BackwardPar
         const float2 y = mul2(z, both(kLog2e));
         return mul2(make_float2(ex2(y.x), ex2(y.y)), fma2(both(-dh), z, both(Bc)));
     };
-    auto at_target = [&](float v) { return v <= kLowest ? 0.f : dlp; };  // a masked target has no gradient
+    auto at_target = [&](float v) { return masked(v, c) ? 0.f : dlp; };  // a masked target has no gradient
     const bool aligned = (((uintptr_t)(out + sl.first)) & 15) == 0;
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
         const int u = u0 + a * GROUP;
         if (u >= u1) break;
         const int id = sl.first + u * R::VEC;
-        float v[R::VEC], at_hit = 0.f;
+        float v[R::VEC], logit = 0.f;  // at the target
         x[a].get(v);
         const int hit = t >= id && t < id + R::VEC ? (int)t - id : -1;
 #pragma unroll
         for (int e = 0; e < R::VEC; e += 2) {
             const float2 x2 = make_float2(v[e], v[e + 1]), g = grad(x2);
-            if (e == hit) at_hit = at_target(x2.x);
-            if (e + 1 == hit) at_hit = at_target(x2.y);
+            if (e == hit) logit = x2.x;
+            if (e + 1 == hit) logit = x2.y;
             v[e] = g.x, v[e + 1] = g.y;
         }
         if (hit >= 0) {
+            const float more = at_target(logit);
 #pragma unroll
             for (int e = 0; e < R::VEC; ++e)
-                if (e == hit) v[e] += at_hit;
+                if (e == hit) v[e] += more;
         }
         if (aligned) {
             x[a].set(v);

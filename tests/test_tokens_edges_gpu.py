@@ -57,3 +57,40 @@ def test_norm_where_row_times_weight_leaves_the_range(io, D):
     s = got[:, O.blocks_of(D)]
     error = np.abs(f64(out["y8"]) * s - y)
     assert np.all(error <= 2.0 ** -4 * np.abs(y) * 1.0001 + 2.0 ** -10 * s * 1.0001 + 1.125 * (ey + (D / 64 + 14) * u * np.abs(y)))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V,chunk", [(5, 60, 9), (1300, 5000, 97), (5, 50021, 997)])
+def test_a_product_that_overflows_is_masked(io, n, V, chunk):
+    """Logits of -2e38 at an inverse temperature of 2 are -inf: no probability, no place among the top, logprob -inf as a
+    target and no gradient there.  Even rows hold ordinary logits besides, odd ones logits of about -1.6e38, whose z are
+    finite (and so far apart that lse is the largest and one p is 1)."""
+    c = 2.0
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(n, V, generator=g) * 3
+    x[1::2] = -1.6e38 + 1e36 * torch.rand(x[1::2].shape, generator=g)
+    x[:, ::chunk] = -2e38
+    targets = (chunk * torch.randint(0, -(-V // chunk), (n,), generator=g))
+    targets[4::5] += 1  # and one that is not masked
+    x, targets = x.to(DT[io]).cuda(), targets.cuda()
+    with B.Tokens(n, 8, V, io=io) as t:
+        out = t.token_logprobs(x, targets, inv_temperature=c, k=8)
+        ones = torch.ones(n, device="cuda")
+        d = f64(t.token_logprobs_backward(x, targets, out["lse"], None, ones, inv_temperature=c))
+        t.last_device_status()
+    few = slice(0, 20)
+    ref = O.token_logprobs(f64(x[few]), targets[few].cpu().numpy(), c, 8)
+    hit = np.arange(n) % 5 != 4
+    logprob = f64(out["logprob"])
+    assert np.all(np.isneginf(logprob[hit])) and np.all(np.isfinite(logprob[~hit]))
+    assert np.all(np.isneginf(ref["logprob"][hit[few]]))
+    for key in ("lse", "entropy", "top_logprob"):
+        got = f64(out[key][few])
+        assert np.all(np.abs(got - ref[key]) <= 1e-5 * (1 + np.abs(ref[key]))), key
+    assert np.all(f64(x)[np.arange(n)[:, None], out["top_ids"].cpu().numpy()] > -2e38)
+    masked = f64(x) * c < -np.finfo(np.float32).max
+    assert masked.sum() == n * -(-V // chunk) and np.all(d[masked] == 0)
+    # the rest: p within 2^-24 (|z| + |lse|) of itself and the roundings of a few operations and of the output
+    rows = np.arange(0, min(n, 20), 2)
+    want = O.token_logprobs_backward(f64(x[rows]), targets[rows].cpu().numpy(), c, ref["lse"][rows], ref["entropy"][rows], np.ones(rows.size), None)
+    assert np.all(np.abs(d[rows] - want) <= 1e-4 * np.abs(want) + half_ulp(io, want) * 1.001 + 1e-6)
