@@ -495,8 +495,9 @@ PRISM_API prism_status prism_matmul8_weights(prism_tokens_t tokens, int N, int K
  * written), and a product that overflows to -inf, counts as z = -inf: its probability is zero, it adds
  * nothing to the entropy and is never among the top (missing places hold id -1 and -inf).  Where a whole
  * row is masked, lse is -inf, entropy 0 and logprob -inf.  NaN or +inf in a row gives NaN lse, logprob
- * and entropy, as the formulas do; NaN logits come first among the top.  inv_temperature must be finite
- * and > 0.
+ * and entropy, as the formulas do; NaN logits come first among the top.  inv_temperature must be in
+ * 2^-60 .. 2^126 (smaller ones would bring the lowest value near live logits, larger ones overflow); where the
+ * row's largest z passes float32, lse is +inf.
  */
 PRISM_API prism_status prism_token_logprobs(prism_tokens_t tokens, int n, const void *logits, long long ld,
                                             const long long *targets, float inv_temperature, int k, float *lse,
@@ -509,8 +510,8 @@ PRISM_API prism_status prism_token_logprobs(prism_tokens_t tokens, int n, const 
  *   dlogprob, dentropy [n] float32 (each may be NULL, not both; dlogprob needs targets, dentropy needs
  *   entropy); dlogits [n, V] with row stride ld_d >= V, dtype of the logits, may be the logits
  *   themselves when ld_d = ld.  Masked tokens and wholly masked rows get zero; a row whose lse is NaN
- *   gets NaN everywhere.  log p_j is taken as z_j - lse, so p_j is within about 2^-24 (|z_j| + |lse|) of
- *   itself.
+ *   gets NaN everywhere, and one whose lse is +inf has no gradient that float32 could give.  log p_j is
+ *   taken as z_j - lse, so p_j is within about 2^-24 (|z_j| + |lse|) of itself.
  */
 PRISM_API prism_status prism_token_logprobs_backward(prism_tokens_t tokens, int n, const void *logits, long long ld,
                                                      const long long *targets, float inv_temperature,

@@ -68,6 +68,15 @@ prism_status check_sizes8(int N, int K)
     return PRISM_OK;
 }
 
+// Above 2^126 the exponentials' scale inv_temperature log2 e overflows.  Below 2^-60 the lowest values, which stand for
+// masked tokens, would come within the exponentials' reach of live ones: they are 2^103 apart at least, and 2^43 is far.
+prism_status check_temperature(float inv_temperature)
+{
+    if (!(inv_temperature >= 0x1p-60f && inv_temperature <= 0x1p126f))
+        return fail(PRISM_ERR_INVALID_ARG, "inv_temperature must be in 2^-60 .. 2^126 (got %g)", (double)inv_temperature);
+    return PRISM_OK;
+}
+
 prism::TokenLaunch begin(prism_tokens_s *t, struct CUstream_st *stream)
 {
     t->timer.on = t->opt_timing != 0;
@@ -297,8 +306,7 @@ prism_status prism_token_logprobs(prism_tokens_t t, int n, const void *logits, l
         return st;
     if (ld < t->V) return fail(PRISM_ERR_INVALID_ARG, "ld must be >= V = %d (got %lld)", t->V, ld);
     if (k < 0 || k > 32) return fail(PRISM_ERR_INVALID_ARG, "k must be in 0 .. 32 (got %d)", k);
-    if (!std::isfinite(inv_temperature) || inv_temperature <= 0.f)
-        return fail(PRISM_ERR_INVALID_ARG, "inv_temperature must be finite and > 0");
+    if ((st = check_temperature(inv_temperature)) != PRISM_OK) return st;
     if (!top_ids && !top_logprob) k = 0;
     const prism::TokenLaunch l = begin(t, stream);
     if (n == 0) return PRISM_OK;
@@ -319,8 +327,7 @@ prism_status prism_token_logprobs_backward(prism_tokens_t t, int n, const void *
     if (n > 0 && !dlogprob && !dentropy) return fail(PRISM_ERR_INVALID_ARG, "dlogprob and dentropy must not both be NULL");
     if (ld < t->V || ld_d < t->V) return fail(PRISM_ERR_INVALID_ARG, "ld and ld_d must be >= V = %d (got %lld, %lld)", t->V, ld, ld_d);
     if (logits == dlogits && ld != ld_d) return fail(PRISM_ERR_INVALID_ARG, "in place, ld_d must equal ld");
-    if (!std::isfinite(inv_temperature) || inv_temperature <= 0.f)
-        return fail(PRISM_ERR_INVALID_ARG, "inv_temperature must be finite and > 0");
+    if ((st = check_temperature(inv_temperature)) != PRISM_OK) return st;
     const prism::TokenLaunch l = begin(t, stream);
     if (n == 0) return PRISM_OK;
     return launched(prism::logprobs_backward(

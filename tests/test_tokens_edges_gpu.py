@@ -94,3 +94,24 @@ def test_a_product_that_overflows_is_masked(io, n, V, chunk):
     rows = np.arange(0, min(n, 20), 2)
     want = O.token_logprobs_backward(f64(x[rows]), targets[rows].cpu().numpy(), c, ref["lse"][rows], ref["entropy"][rows], np.ones(rows.size), None)
     assert np.all(np.abs(d[rows] - want) <= 1e-4 * np.abs(want) + half_ulp(io, want) * 1.001 + 1e-6)
+
+
+def test_inverse_temperatures_that_the_sums_cannot_take_are_refused():
+    """Beyond 2^126 the scale of the exponentials overflows; below 2^-60 a mask written as the lowest value would not be far
+    enough below the other logits.  At the limits the results are those of the formula."""
+    x = torch.tensor([[1.0, 1.0, 0.5, torch.finfo(torch.float32).min], [0.0, -2.0 ** 60, -2.0 ** 61, torch.finfo(torch.float32).min]], device="cuda")
+    ids = torch.tensor([0, 1], device="cuda")
+    with B.Tokens(2, 8, 4, io="f32") as t:
+        lse = torch.zeros(2, device="cuda")
+        for c in (2.0 ** -61, 1e-40, 2.0 ** 127, 3e38):
+            for call in (lambda: t.token_logprobs(x, ids, inv_temperature=c),
+                         lambda: t.token_logprobs_backward(x, ids, lse, None, lse, inv_temperature=c)):
+                with pytest.raises(B.PrismError) as ei:
+                    call()
+                assert ei.value.status == B.PRISM_ERR_INVALID_ARG
+        out = t.token_logprobs(x[:1].contiguous(), ids[:1], inv_temperature=2.0 ** 126, k=4)
+        assert out["top_ids"].tolist() == [[0, 1, 2, -1]]
+        assert abs(out["logprob"].item() + np.log(2)) < 1e-6 and abs(out["entropy"].item() - np.log(2)) < 1e-6
+        out = t.token_logprobs(x[1:].contiguous(), ids[1:], inv_temperature=2.0 ** -60, k=4)
+        z = torch.tensor([0.0, -1.0, -2.0], dtype=torch.float64)
+        assert abs(out["lse"].item() - torch.logsumexp(z, 0).item()) < 1e-6 and out["top_ids"].tolist() == [[0, 1, 2, -1]]
