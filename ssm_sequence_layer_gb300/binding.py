@@ -756,7 +756,8 @@ class Tokens:
     def token_logprobs_backward(self, logits, targets, lse, entropy, dlogprob, dentropy=None, inv_temperature=1.0, dlogits=None,
                                 stream=None):
         """The logits' cotangent (see prism_token_logprobs_backward), given the forward's lse and
-        entropy (may be None without dentropy); dlogits may be the logits themselves."""
+        entropy (may be None without dentropy); dlogits may be the logits themselves.  Unless given it
+        is contiguous where the logits are, and has rows padded by less than 16 bytes where theirs are."""
         import torch
         if stream is not None:
             return self._on(stream, self.token_logprobs_backward, logits, targets, lse, entropy, dlogprob, dentropy, inv_temperature, dlogits)
@@ -768,8 +769,9 @@ class Tokens:
         if targets is not None:
             need("targets", targets, torch.int64, n)
         if dlogits is None:
-            dlogits = torch.empty(logits.shape, dtype=self._logits, device=logits.device)
-            ld_d = self.V
+            # rows as far from a 16-byte boundary as the logits' are, so that both go in 16-byte units
+            ld_d = self.V + (ld - self.V) % (16 // logits.element_size())
+            dlogits = torch.empty(*logits.shape[:-1], ld_d, dtype=self._logits, device=logits.device)[..., :self.V]
         else:
             rows, ld_d = self._logit_rows("dlogits", dlogits)
             if rows != n:

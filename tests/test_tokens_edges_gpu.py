@@ -115,3 +115,20 @@ def test_inverse_temperatures_that_the_sums_cannot_take_are_refused():
         out = t.token_logprobs(x[1:].contiguous(), ids[1:], inv_temperature=2.0 ** -60, k=4)
         z = torch.tensor([0.0, -1.0, -2.0], dtype=torch.float64)
         assert abs(out["lse"].item() - torch.logsumexp(z, 0).item()) < 1e-6 and out["top_ids"].tolist() == [[0, 1, 2, -1]]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_gradient_of_padded_logits_takes_their_layout(io):
+    """Rows of an odd vocabulary in padded logits: rows of the gradient that the call allocates lie as far from a
+    16-byte boundary, so that both go in 16-byte units; contiguous logits give a contiguous gradient."""
+    n, V, pad = 6, 5001, 7
+    g = torch.Generator().manual_seed(0)
+    full = torch.randn(n, V + pad, generator=g).to(DT[io]).cuda()
+    targets, dlp = torch.randint(0, V, (n,), generator=g).cuda(), torch.randn(n, generator=g).cuda()
+    with B.Tokens(n, 8, V, io=io) as t:
+        lse = t.token_logprobs(full[:, :V])["lse"]
+        got = t.token_logprobs_backward(full[:, :V], targets, lse, None, dlp)
+        dense = full[:, :V].contiguous()
+        ref = t.token_logprobs_backward(dense, targets, lse, None, dlp)
+    assert got.shape == (n, V) and got.stride(1) == 1 and (V + pad - got.stride(0)) * got.element_size() % 16 == 0 and ref.is_contiguous()
+    assert torch.equal(got, ref)
