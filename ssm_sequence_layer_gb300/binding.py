@@ -588,13 +588,14 @@ class Tokens:
             return self._on(stream, self.embed, ids, table, scale, out)
         n = ids.numel()
         self._need("ids", ids, torch.int64)
-        if table.dtype is not self._io or not table.is_cuda or table.shape != (self.V, self.D) or table.stride(1) != 1:
+        dense = table.is_contiguous()  # an axis of one element may have any stride
+        if table.dtype is not self._io or not table.is_cuda or table.shape != (self.V, self.D) or not (dense or table.stride(1) == 1):
             raise ValueError(f"table must be a CUDA tensor [{self.V}, {self.D}] of {self._io} with contiguous rows")
         if out is None:
             out = torch.empty(*ids.shape, self.D, dtype=self._io, device=ids.device)
         else:
             self._need("out", out, self._io, n * self.D)
-        prism_embed(self.handle, n, ids, table, table.stride(0), scale, out, self._current_stream(self.device))
+        prism_embed(self.handle, n, ids, table, self.D if dense else table.stride(0), scale, out, self._current_stream(self.device))
         return out
 
     def embed_backward(self, ids, dout, scale=1.0, dtable=None, accumulate=False, stream=None):

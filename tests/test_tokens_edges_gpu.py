@@ -132,3 +132,15 @@ def test_gradient_of_padded_logits_takes_their_layout(io):
         ref = t.token_logprobs_backward(dense, targets, lse, None, dlp)
     assert got.shape == (n, V) and got.stride(1) == 1 and (V + pad - got.stride(0)) * got.element_size() % 16 == 0 and ref.is_contiguous()
     assert torch.equal(got, ref)
+
+
+def test_tables_of_one_row_or_one_column():
+    """A contiguous table whose axis of one element has any stride."""
+    ids = torch.tensor([0, -1, 0], device="cuda")
+    row = torch.randn(24, device="cuda").as_strided((1, 24), (1, 1))
+    with B.Tokens(3, 24, 1, io="f32") as t:
+        assert torch.equal(t.embed(ids, row)[::2], row.expand(2, 24))
+    column = torch.randn(1, 9, device="cuda").t()
+    ids = torch.tensor([8, -1, 3], device="cuda")
+    with B.Tokens(3, 1, 9, io="f32") as t:
+        assert torch.equal(t.embed(ids, column)[::2], column[[8, 3]])
