@@ -572,11 +572,10 @@ class Tokens:
         with torch.cuda.stream(stream):
             return method(*args)
 
-    @staticmethod
-    def _need(name, t, dtype, numel=None, width=None):
+    def _need(self, name, t, dtype, numel=None, width=None):
         """Refuses a tensor that the library would misread: its device, type, layout and size."""
-        if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+        if t.dtype is not dtype or t.get_device() != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of {dtype} on the handle's device")
         if (numel is not None and t.numel() != numel) or (width is not None and t.shape[-1] != width):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not fit the other arguments")
 
@@ -589,8 +588,8 @@ class Tokens:
         n = ids.numel()
         self._need("ids", ids, torch.int64)
         dense = table.is_contiguous()  # an axis of one element may have any stride
-        if table.dtype is not self._io or not table.is_cuda or table.shape != (self.V, self.D) or not (dense or table.stride(1) == 1):
-            raise ValueError(f"table must be a CUDA tensor [{self.V}, {self.D}] of {self._io} with contiguous rows")
+        if table.dtype is not self._io or table.get_device() != self.device or table.shape != (self.V, self.D) or not (dense or table.stride(1) == 1):
+            raise ValueError(f"table must be [{self.V}, {self.D}] of {self._io} with contiguous rows on the handle's device")
         if out is None:
             out = torch.empty(*ids.shape, self.D, dtype=self._io, device=ids.device)
         else:
@@ -713,8 +712,8 @@ class Tokens:
     def _logit_rows(self, name, t):
         """(rows, row stride) of logits [..., V], or [n, V] with padded rows."""
         V = self.V
-        if t.dtype is not self._logits or not t.is_cuda or t.shape[-1] != V:
-            raise ValueError(f"{name} must be a CUDA tensor [..., {V}] of {self._logits}")
+        if t.dtype is not self._logits or t.get_device() != self.device or t.shape[-1] != V:
+            raise ValueError(f"{name} must be [..., {V}] of {self._logits} on the handle's device")
         if t.is_contiguous():
             return t.numel() // V, V
         if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < V:
