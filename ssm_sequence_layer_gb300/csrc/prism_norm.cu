@@ -54,9 +54,11 @@ struct Root {
 
 // The 8-bit values of a block of 128.  A value's e4m3 neighbour is decided by y / scale = v / s with
 // s = max |v| / 448, in which 1 / rms cancels.  A rounding error there moves values that lie near the middle between
-// two neighbours to the wrong one, so v is held as a product and its rounding error, and the quotient is
-// corrected once with both: what is left are the roundings of s and of the result.  (Of 50 million bf16 values the
-// plain sequence of roundings moves 299, this one 13.)  Values come in pairs: two operations an instruction.
+// two neighbours to the wrong one, so v is held as a product and its rounding error, and the quotient, v times the
+// reciprocal of s, is corrected once by the remainder of both, taken with fused operations (P. W. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): what is left are the
+// roundings of s and of the result.  (Of 50 million bf16 values the plain sequence of roundings moves 299, this
+// one 13.)  Values come in pairs: two operations an instruction.
 struct Block {
     float s, inverse;     // max |v| / 448 and its reciprocal
     float factor, scale;  // of the root; the scale that is stored
