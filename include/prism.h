@@ -393,7 +393,8 @@ typedef struct prism_tokens_s *prism_tokens_t;
  * prism_tokens_plan -- validate the sizes, bind the handle to the current CUDA device and allocate
  * its workspace (no later call allocates, so every call can be captured into a graph).  max_rows:
  * the largest n (or M) of a call, 1 .. 2^24; D in 1 .. 65536; V in 1 .. 2^30.  On error *out_tokens
- * is NULL.  A handle may be used by one stream at a time.
+ * is NULL.  A handle may be used by one stream at a time.  The workspace serves every operator, whichever are called: it
+ * holds 24 bytes a row, V bits and parts of gradients, at most 8193 x 2 x D and 960 x D floats.
  */
 PRISM_API prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism_tokens_t *out_tokens);
 
@@ -426,7 +427,8 @@ PRISM_API prism_status prism_embed(prism_tokens_t tokens, int n, const long long
  * token are not touched (a table shared with the head product, gradients over several calls).
  *   dout [n, D] io   dtable [V, D] float32
  * The tokens are sorted by id (stably) and each row's terms are added in the order of their
- * positions within fixed runs, so the result is reproducible bit for bit.
+ * positions within fixed runs, so the result is reproducible bit for bit.  The sum is scaled, rounded and then added
+ * to dtable; that addition takes numbers below the smallest normal float32 (dtable's own too) for zeros.
  */
 PRISM_API prism_status prism_embed_backward(prism_tokens_t tokens, int n, const long long *ids, const void *dout,
                                             float scale, int accumulate, float *dtable, struct CUstream_st *stream);
@@ -442,7 +444,8 @@ PRISM_API prism_status prism_embed_backward(prism_tokens_t tokens, int n, const 
  *                            columns, y_scale = max(max |y| / 448, 2^-126) and y8 = y / y_scale
  *                            rounded to nearest; y8 and y_scale come together
  * NaN in a row reaches the whole row of y; an infinite y makes its block's scale infinite.
- * eps must be finite and >= 0.  A row of zeros with eps = 0 gives NaN, as the formula does.
+ * eps must be finite and >= 0.  A row of zeros with eps = 0 gives NaN, as the formula does.  The squares
+ * are float32: a row whose length passes 2^64 gives zeros, and with eps = 0 one of values below 2^-75 infinities.
  */
 PRISM_API prism_status prism_norm(prism_tokens_t tokens, int n, const void *x, const void *residual,
                                   const void *weight, float eps, void *sum, void *y, void *y8, float *y_scale,
@@ -467,7 +470,8 @@ PRISM_API prism_status prism_norm_backward(prism_tokens_t tokens, int n, const v
  *   w8 [N, K] e4m3   w_scale [ceil(N/128), ceil(K/128)] float32 (prism_matmul8_weights)
  *   out [M, N], the handle's logits dtype (io, or PRISM_OPT_OUT_DTYPE)
  * K is a multiple of 16, at most 65536; N at most 2^30; M at most max_rows.  N and K need not be the
- * handle's V and D: the product also serves projections.  Products are exact, sums are float32.  An
+ * handle's V and D: the product also serves projections.  Products are exact, sums are float32, and so is the
+ * product of the two scales, which loses bits below the smallest normal float32.  An
  * expired device wait is reported by prism_tokens_last_device_status.
  */
 PRISM_API prism_status prism_matmul8(prism_tokens_t tokens, int M, int N, int K, const void *a8,

@@ -180,11 +180,14 @@ void launch_skinny(const Params<out_t> &p, int sm_count, cudaStream_t s)
 // accumulator.  The sums take more registers than an even share, so the four warps of the issuing group hand
 // theirs over.
 //
-// 4096 x 50048 x 768 takes 176 us, 1.79 PFLOP/s.  At BN = 256 a block brings 48 KB into the SM, whose port takes 64 bytes
-// a cycle: 768 cycles, 94 us in all (measured with one product per block), against 512 cycles of products and 128 of scaled
-// additions.  Without the sums and the stores it takes 117 us, with the sums 133, with the stores 161: shared
-// memory and the port carry operands in and results out at the same time.  Pairs of CTAs that share operands
-// (one tile per pair: 301 us; multicast: 174 us) do not lift that.
+// 4096 x 50048 x 768 takes 172 us among a graph's calls, 1.83 PFLOP/s.  The turn-around of the two accumulators bounds it: from the
+// arrival that frees one to the moment its next sums can be read, the wake-ups of two threads, the products' latency and the
+// reading take a time that neither the bytes nor the other CTAs change, and each block pays half of it.  Tiles of 128
+// columns take 0.39 us a block on 8 CTAs and 0.41 on 80, of which the products are 0.13 and the operands' way into the SM, 64 bytes
+// a cycle, is 0.26; tiles of 256 columns 0.52 us a block (4096 x 8192 x 4096: 116 us) for 0.26 and 0.39.  Without sums and stores
+// 119 us are left.  Other forms: CTAs in pairs that read a shared operand once take 174 us (there, without sums and stores 117, with the
+// sums 133, with the stores 161, and with one product of a block's four and neither 94, so that the other three, 384 cycles, cost half
+// of that); tiles of two SMs, whose accumulators change hands over a longer way, 301.
 using namespace prism::tc;
 
 constexpr int BM = 128, STAGE_ROWS = 128;

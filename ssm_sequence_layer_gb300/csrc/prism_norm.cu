@@ -105,7 +105,7 @@ struct ForwardParams {
 // Rows of 16-byte units, held in registers: WPR warps per row, UPL units per lane (unit t + 32 WPR j of a row
 // belongs to thread t, so a block of 128 columns is the same j of 16 (bf16) or 32 (fp32) neighbouring
 // lanes).  Warps walk over the rows; the next row's loads are in flight while a row is worked on, which
-// keeps about 60 KB outstanding per SM.  16384 x 768 bf16 with both outputs of the sum and 8 bits: 18.9 us, 4.7 TB/s (a
+// keeps about 60 KB outstanding per SM.  16384 x 768 bf16 with the sum and 8 bits: 18.8 us, 4.7 TB/s (a
 // copy of that size reaches about 5; issue slots are 61 % busy); 8192 x 4096 bf16 sum and y 44 us, 6.1 TB/s.
 template <typename io_t, int WPR, int UPL>
 __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel(const ForwardParams<io_t> p)
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(WPR == 1 ? kThreads : 32 * WPR) forward_kernel
 }
 
 // Any width and alignment: a warp per row, one value per lane at a time, two passes over the row (the second
-// one comes from the caches): 16384 x 770 bf16 34 us, 2.9 TB/s, bound by the instructions per value (with the row held
-// in registers 33 us).  Nothing is written before the row has been read to its end, and then each value is read
+// one comes from the caches): 16384 x 770 bf16 33 us, 3.1 TB/s, bound by the instructions that single values take (with the
+// row held in registers as much).  Nothing is written before the row has been read to its end, and then each value is read
 // before its own place is written, so outputs may take an input's place.
 template <typename io_t>
 __global__ void __launch_bounds__(kThreads) forward_any_kernel(const ForwardParams<io_t> p)

@@ -13,8 +13,8 @@ struct TokenLaunch {
     KernelTimer *timer;
 };
 
-// A launch that may begin while the kernel before it in the stream ends (it waits for that kernel's
-// results itself); the first kernel of a call is launched plainly.
+// A launch that may begin while the kernel before it in the stream ends, and waits for that kernel's results itself.
+// A call's first kernel is launched plainly, but for the weight's gradient of a norm of no rows, which waits like any other.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
 {
@@ -45,7 +45,7 @@ cudaError_t embed_forward(prism_dtype io, const EmbedArgs &a, const TokenLaunch 
 // Workspace of the gradient: the tokens sorted by id and the sums of runs that cross a tile's edge.
 struct EmbedWorkspace {
     int *key[2], *pos[2];  // [max_rows] ids (V = no token) and positions, ping-pong of the sort's passes
-    int *hist;             // [kSortPassesMax][kSortBlocks][kSortBins] digit counts
+    int *hist;             // [passes][blocks][bins] digit counts of the sort by a kernel per digit, each at its largest number
     uint32_t *present;     // [V / 32 + 1] a bit for each id that has a token (and for "no token")
     float *part;           // [tiles][2][Dp] sums of a tile's first and last run where it crosses the edge
 };
