@@ -523,6 +523,120 @@ PRISM_API prism_status prism_token_logprobs_backward(prism_tokens_t tokens, int 
                                                      const float *dentropy, void *dlogits, long long ld_d,
                                                      struct CUstream_st *stream);
 
+/*
+ * prism_linear -- a matrix product with what follows it in a block:
+ *   pre = x W^T + bias      y = act(pre) + residual
+ *   x [M, K] io   W [N, K] io   bias [N] io (may be NULL)   residual [M, N] io (may be NULL)
+ *   y [M, N] io (may be residual)   pre [M, N] io (may be NULL): what the gradient of the activation needs
+ * act: the identity, gelu(z) = z Phi(z) with the exact normal distribution function (as in the layer), or
+ * silu(z) = z / (1 + exp(-z)).  M at most max_rows; N and K (1 .. 2^20 each) need not be the handle's V and D, and need no
+ * multiple: rows that are not whole 16-byte units only take longer.  Sums are float32, whatever the io dtype, and y is taken
+ * of the unrounded pre.  An expired device wait is reported by prism_tokens_last_device_status.
+ */
+typedef enum prism_activation {
+    PRISM_ACT_NONE = 0,
+    PRISM_ACT_GELU = 1,
+    PRISM_ACT_SILU = 2
+} prism_activation;
+
+PRISM_API prism_status prism_linear(prism_tokens_t tokens, int M, int N, int K, const void *x, const void *W,
+                                    const void *bias, prism_activation act, const void *residual, void *y, void *pre,
+                                    struct CUstream_st *stream);
+
+/*
+ * prism_linear_backward -- the cotangent of prism_linear's x:
+ *   dx = (dy W) (.) act'(pre) + dsum
+ * act and pre [M, K] io are those of the call that made x, so that the result is the cotangent of that call's pre (for
+ * PRISM_ACT_NONE pre is not read and may be NULL); dsum [M, K] io (may be NULL) is what reaches x besides.
+ *   dy [M, N] io   W [N, K] io   dx [M, K] io (may be dsum or pre)
+ * dy is the cotangent of this product's pre; the residual's cotangent is dy itself.  Sizes and types as prism_linear.
+ */
+PRISM_API prism_status prism_linear_backward(prism_tokens_t tokens, int M, int N, int K, const void *dy, const void *W,
+                                             prism_activation act, const void *pre, const void *dsum, void *dx,
+                                             struct CUstream_st *stream);
+
+/*
+ * prism_linear_weight_backward -- the cotangents of prism_linear's weights and bias:
+ *   dW = dy^T x      dbias = sum over rows of dy
+ * with accumulate != 0 both are added to what is there.
+ *   dy [M, N] io   x [M, K] io   dW [N, K] float32   dbias [N] float32 (may be NULL)
+ * M = 0 gives zeros (or leaves them).  Sizes and types as prism_linear.
+ */
+PRISM_API prism_status prism_linear_weight_backward(prism_tokens_t tokens, int M, int N, int K, const void *dy,
+                                                    const void *x, int accumulate, float *dW, float *dbias,
+                                                    struct CUstream_st *stream);
+
+/*
+ * prism_heads -- from a projection's rows to the layer's queries, keys and values: the norm of each head, the position's
+ * rotation and the layout [B, heads, T, size] in one pass.  A row of x holds Hq query heads and Hk key heads of d values,
+ * then Hv value heads of dv.  For a query or key head x_j, j < d:
+ *   r = 1 (PRISM_HEADS_PLAIN),  1 / sqrt(sum_j x_j^2 + eps) (PRISM_HEADS_UNIT),  1 / sqrt(mean_j x_j^2 + eps) (PRISM_HEADS_RMS)
+ *   y_j = r x_j w_j            w = q_weight or k_weight [d] io (1 where NULL)
+ * and the first rot values of y are turned in pairs, (y_i, y_{i + rot/2}) or, interleaved, (y_{2i}, y_{2i+1}), i < rot/2:
+ *   (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),    t = position inv_freq_i
+ * Values are copied.  positions [B, T] int64 (NULL: 0 .. T-1 in every sequence), of any sign and size up to 2^40; the angle is
+ * reduced in 64-bit fixed point, to 2^-62 turns of the float32 inv_freq times the position.  inv_freq [rot/2] float32 on the
+ * device, each below 2^12 in magnitude.  Scaling for long contexts is a choice of inv_freq and amplitude
+ * (rotary_frequencies of the Python package makes the usual ones).
+ * d and dv in 1 .. 512, rot even, 0 .. d (0: no rotation), eps finite and >= 0; squares are float32 as in prism_norm.
+ */
+typedef enum prism_heads_norm {
+    PRISM_HEADS_PLAIN = 0,
+    PRISM_HEADS_UNIT = 1,
+    PRISM_HEADS_RMS = 2
+} prism_heads_norm;
+
+typedef struct prism_heads_form {
+    int B, T, Hq, Hk, Hv, d, dv;
+    prism_heads_norm norm;
+    float eps;
+    const void *q_weight, *k_weight; /* [d] io, or NULL */
+    int rot, interleaved;
+    const float *inv_freq; /* [rot / 2] */
+    float amplitude;
+    const long long *positions; /* [B, T], or NULL */
+} prism_heads_form;
+
+/*
+ *   x [B, T, ld_x] io (the first Hq d + Hk d + Hv dv columns)
+ *   q [B, Hq, T, d], k [B, Hk, T, d], v [B, Hv, T, dv] io (NULL where there are no such heads)
+ * B T at most max_rows; heads together at most 65535.
+ */
+PRISM_API prism_status prism_heads(prism_tokens_t tokens, const prism_heads_form *form, const void *x, long long ld_x,
+                                   void *q, void *k, void *v, struct CUstream_st *stream);
+
+/*
+ * prism_heads_backward -- the cotangents of prism_heads' x and weights: with g the cotangent of y (dq or dk turned back)
+ *   dx_j = r (w_j g_j - x_j r^2 c sum_i w_i g_i x_i)      c = 0 (plain), 1 (unit), 1/d (rms)      dw_j = sum over heads g_j r x_j
+ *   dq, dk, dv as q, k, v, of type `grads` (float32, as prism_backward leaves them, or the io dtype)
+ *   dx [B, T, ld_dx] io (the same columns; others are not touched)   dq_weight, dk_weight [d] float32 (each may be NULL), overwritten
+ */
+PRISM_API prism_status prism_heads_backward(prism_tokens_t tokens, const prism_heads_form *form, const void *x, long long ld_x,
+                                            prism_dtype grads, const void *dq, const void *dk, const void *dv, void *dx,
+                                            long long ld_dx, float *dq_weight, float *dk_weight, struct CUstream_st *stream);
+
+/*
+ * prism_sample -- draw a token from each row of logits [n, V] (row stride ld >= V), given a number u in [0, 1) for each row.
+ * With z = inv_temperature logits, the tokens ordered by falling logit and at equal logits by rising id, the row keeps the
+ * shortest of the prefixes
+ *   top_k > 0:  the first top_k            top_p < 1:  the fewest whose mass reaches top_p of that of the first top_k
+ *   min_p > 0:  those of at least min_p times the first one's probability
+ * (one token at least; masked tokens never), and the token is the first, by rising id, at which the kept tokens' running mass
+ * exceeds u times their mass.
+ *   u [n] float32 (NaN and below 0 count as 0; 1 and above gives the last kept id)
+ *   inv_temperature [n] float32 (NULL: 1), top_k [n] int32, top_p, min_p [n] float32 (NULL: not used; NaN: not used)
+ *   ids [n] int64   logprob [n] float32: log of the token's share of the kept mass   kept [n] int32: tokens kept (V at most 2^30);
+ *   logprob and kept may be NULL
+ * Masked tokens are those of prism_token_logprobs.  A row without a live token gives id -1, logprob -inf, kept 0; one with NaN
+ * or +inf gives id -1, logprob NaN, kept 0, and so does an inv_temperature outside 2^-60 .. 2^126, which is recorded
+ * (prism_tokens_last_device_status: PRISM_ERR_DEVICE).  Masses are taken to about 2^-40 of the first token's, in sums without
+ * rounding, wherever a choice depends on them, so the choices are those of the formulas in exact arithmetic but for numbers that
+ * lie within that distance of a border.  Tokens of less than 2^-44 of the first one's probability count as having none.
+ */
+PRISM_API prism_status prism_sample(prism_tokens_t tokens, int n, const void *logits, long long ld, const float *u,
+                                    const float *inv_temperature, const int *top_k, const float *top_p, const float *min_p,
+                                    long long *ids, float *logprob, int *kept, struct CUstream_st *stream);
+
 /* Version of this library, "major.minor.patch". */
 PRISM_API const char *prism_version(void);
 

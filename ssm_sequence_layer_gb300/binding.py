@@ -40,7 +40,18 @@ EXPORTED = ("prism_plan", "prism_plan_set_option", "prism_forward", "prism_forwa
             "prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy", "prism_tokens_workspace_bytes",
             "prism_tokens_last_device_status", "prism_tokens_kernel_times", "prism_embed", "prism_embed_backward",
             "prism_norm", "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward",
-            "prism_matmul8", "prism_matmul8_weights")
+            "prism_matmul8", "prism_matmul8_weights", "prism_linear", "prism_linear_backward", "prism_linear_weight_backward",
+            "prism_heads", "prism_heads_backward", "prism_sample")
+
+ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}             # prism_activation
+HEAD_NORMS = {"none": 0, "unit": 1, "rms": 2}               # prism_heads_norm
+
+
+class prism_heads_form(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int) for name in ("B", "T", "Hq", "Hk", "Hv", "d", "dv", "norm")]
+                + [("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rot", ctypes.c_int),
+                   ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_void_p), ("amplitude", ctypes.c_float),
+                   ("positions", ctypes.c_void_p)])
 
 
 class prism_kernel_time(ctypes.Structure):
@@ -114,6 +125,16 @@ def lib():
             L.prism_token_logprobs_backward.argtypes = [vp, i, vp, ll, vp, c_f, vp, vp, vp, vp, vp, ll, vp]
             L.prism_matmul8.argtypes = [vp, i, i, i, vp, vp, vp, vp, vp, vp]
             L.prism_matmul8_weights.argtypes = [vp, i, i, vp, vp, vp, vp]
+            L.prism_linear.argtypes = [vp, i, i, i, vp, vp, vp, i, vp, vp, vp, vp]
+            L.prism_linear_backward.argtypes = [vp, i, i, i, vp, vp, i, vp, vp, vp, vp]
+            L.prism_linear_weight_backward.argtypes = [vp, i, i, i, vp, vp, i, vp, vp, vp]
+            form = ctypes.POINTER(prism_heads_form)
+            L.prism_heads.argtypes = [vp, form, vp, ll, vp, vp, vp, vp]
+            L.prism_heads_backward.argtypes = [vp, form, vp, ll, i, vp, vp, vp, vp, ll, vp, vp, vp]
+            L.prism_sample.argtypes = [vp, i, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+            for name in ("prism_linear", "prism_linear_backward", "prism_linear_weight_backward", "prism_heads",
+                         "prism_heads_backward", "prism_sample"):
+                getattr(L, name).restype = ctypes.c_int
             for name in ("prism_tokens_plan", "prism_tokens_set_option", "prism_tokens_destroy",
                          "prism_tokens_last_device_status", "prism_embed", "prism_embed_backward", "prism_norm",
                          "prism_norm_backward", "prism_token_logprobs", "prism_token_logprobs_backward",
@@ -333,6 +354,35 @@ def prism_token_logprobs_backward(tokens, n, logits, ld, targets, inv_temperatur
     return _check(lib().prism_token_logprobs_backward(tokens, n, _addr(logits), ld, _addr(targets), inv_temperature, _addr(lse),
                                                       _addr(entropy), _addr(dlogprob), _addr(dentropy), _addr(dlogits), ld_d,
                                                       _stream(stream)))
+
+
+def prism_linear(tokens, M, N, K, x, W, bias, act, residual, y, pre, stream=None):
+    return _check(lib().prism_linear(tokens, M, N, K, _addr(x), _addr(W), _addr(bias), act, _addr(residual), _addr(y), _addr(pre),
+                                     _stream(stream)))
+
+
+def prism_linear_backward(tokens, M, N, K, dy, W, act, pre, dsum, dx, stream=None):
+    return _check(lib().prism_linear_backward(tokens, M, N, K, _addr(dy), _addr(W), act, _addr(pre), _addr(dsum), _addr(dx),
+                                              _stream(stream)))
+
+
+def prism_linear_weight_backward(tokens, M, N, K, dy, x, accumulate, dW, dbias, stream=None):
+    return _check(lib().prism_linear_weight_backward(tokens, M, N, K, _addr(dy), _addr(x), int(accumulate), _addr(dW), _addr(dbias),
+                                                     _stream(stream)))
+
+
+def prism_heads(tokens, form, x, ld_x, q, k, v, stream=None):
+    return _check(lib().prism_heads(tokens, ctypes.byref(form), _addr(x), ld_x, _addr(q), _addr(k), _addr(v), _stream(stream)))
+
+
+def prism_heads_backward(tokens, form, x, ld_x, grads, dq, dk, dv, dx, ld_dx, dq_weight, dk_weight, stream=None):
+    return _check(lib().prism_heads_backward(tokens, ctypes.byref(form), _addr(x), ld_x, grads, _addr(dq), _addr(dk), _addr(dv),
+                                             _addr(dx), ld_dx, _addr(dq_weight), _addr(dk_weight), _stream(stream)))
+
+
+def prism_sample(tokens, n, logits, ld, u, inv_temperature, top_k, top_p, min_p, ids, logprob, kept, stream=None):
+    return _check(lib().prism_sample(tokens, n, _addr(logits), ld, _addr(u), _addr(inv_temperature), _addr(top_k), _addr(top_p),
+                                     _addr(min_p), _addr(ids), _addr(logprob), _addr(kept), _stream(stream)))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -779,6 +829,248 @@ class Tokens:
         prism_token_logprobs_backward(self.handle, n, logits, ld, targets, inv_temperature, lse, entropy, dlogprob, dentropy,
                                       dlogits, ld_d, self._current_stream(self.device))
         return dlogits
+
+    def linear(self, x, W, bias=None, activation="none", residual=None, want=("y",), out=None, stream=None):
+        """act(x W^T + bias) + residual (see prism_linear): x [..., K], W [N, K], bias [N], residual [..., N];
+        activation "none", "gelu" or "silu".  Returns a dict of the outputs that ``want`` names -- "y" and "pre",
+        the activation's argument, [..., N] -- or fills and returns ``out``, a dict of them ("y" among them)."""
+        import torch
+        if stream is not None:
+            return self._on(stream, self.linear, x, W, bias, activation, residual, want, out)
+        need, io = self._need, self._io
+        N, K = self._weights_shape(W)
+        M = self._rows("x", x, K)
+        if bias is not None:
+            need("bias", bias, io, N)
+        if residual is not None:
+            need("residual", residual, io, M * N, N)
+        if out is None:
+            if "y" not in want:
+                raise ValueError("prism_linear's outputs must have y among them")
+            out = {}
+            for key in want:
+                if key not in ("y", "pre"):
+                    raise ValueError(f"prism_linear has no output {key!r}")
+                out[key] = torch.empty(*x.shape[:-1], N, dtype=io, device=x.device)
+        else:
+            for key, t in out.items():
+                if key not in ("y", "pre"):
+                    raise ValueError(f"prism_linear has no output {key!r}")
+                need(key, t, io, M * N, N)
+        prism_linear(self.handle, M, N, K, x, W, bias, self._activation(activation), residual, out["y"], out.get("pre"),
+                     self._current_stream(self.device))
+        return out
+
+    def linear_backward(self, dy, W, activation="none", pre=None, dsum=None, dx=None, stream=None):
+        """The cotangent of linear's x (see prism_linear_backward): (dy W) act'(pre) + dsum, where
+        ``activation`` and ``pre`` [..., K] are those of the product that x came from; dy [..., N], W [N, K],
+        dsum [..., K].  Returns dx [..., K], allocated unless given."""
+        import torch
+        if stream is not None:
+            return self._on(stream, self.linear_backward, dy, W, activation, pre, dsum, dx)
+        need, io = self._need, self._io
+        N, K = self._weights_shape(W)
+        M = self._rows("dy", dy, N)
+        act = self._activation(activation)
+        if act == 0:
+            pre = None
+        elif pre is None:
+            raise ValueError("an activation's gradient needs pre")
+        for name, t in (("pre", pre), ("dsum", dsum)):
+            if t is not None:
+                need(name, t, io, M * K, K)
+        if dx is None:
+            dx = torch.empty(*dy.shape[:-1], K, dtype=io, device=dy.device)
+        else:
+            need("dx", dx, io, M * K, K)
+        prism_linear_backward(self.handle, M, N, K, dy, W, act, pre, dsum, dx, self._current_stream(self.device))
+        return dx
+
+    def linear_weight_backward(self, dy, x, want=("dW",), out=None, accumulate=False, stream=None):
+        """The cotangents of linear's weights and bias (see prism_linear_weight_backward): dy [..., N],
+        x [..., K].  Returns a dict of "dW" [N, K] and, where ``want`` names it, "dbias" [N], float32, or
+        fills (``accumulate``: adds to) and returns ``out``, a dict of them."""
+        import torch
+        if stream is not None:
+            return self._on(stream, self.linear_weight_backward, dy, x, want, out, accumulate)
+        need, f32 = self._need, torch.float32
+        N, K = dy.shape[-1], x.shape[-1]
+        M = self._rows("dy", dy, N)
+        if self._rows("x", x, K) != M:
+            raise ValueError("dy and x must have the same rows")
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs an out to add to")
+            if "dW" not in want:
+                raise ValueError("prism_linear_weight_backward's outputs must have dW among them")
+            out = {}
+            for key in want:
+                if key not in ("dW", "dbias"):
+                    raise ValueError(f"prism_linear_weight_backward has no output {key!r}")
+                out[key] = torch.empty((N, K) if key == "dW" else (N,), dtype=f32, device=dy.device)
+        else:
+            for key, t in out.items():
+                if key not in ("dW", "dbias"):
+                    raise ValueError(f"prism_linear_weight_backward has no output {key!r}")
+                need(key, t, f32, N * K if key == "dW" else N, K if key == "dW" else N)
+        prism_linear_weight_backward(self.handle, M, N, K, dy, x, accumulate, out["dW"], out.get("dbias"),
+                                     self._current_stream(self.device))
+        return out
+
+    @staticmethod
+    def _activation(name):
+        if name not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)} (got {name!r})")
+        return ACTIVATIONS[name]
+
+    def _weights_shape(self, W):
+        if W.dim() != 2:
+            raise ValueError("W must be [N, K]")
+        self._need("W", W, self._io)
+        return W.shape
+
+    def _rows(self, name, t, width):
+        """The rows of a contiguous io tensor [..., width]."""
+        n = 1
+        for size in t.shape[:-1]:
+            n *= size
+        self._need(name, t, self._io, n * width, width)
+        return n
+
+    def _row_stride(self, name, t, width):
+        """(B, T, row stride) of io rows [B, T, width or more], whose rows may be padded."""
+        if t.dim() != 3 or t.dtype is not self._io or t.get_device() != self.device or t.shape[2] < width:
+            raise ValueError(f"{name} must be [B, T, {width} or more] of {self._io} on the handle's device")
+        B, T, W = t.shape
+        if t.is_contiguous():
+            return B, T, W
+        ld = t.stride(1) if T > 1 else t.stride(0) if B > 1 else W
+        if t.stride(2) != 1 or ld < W or (B > 1 and t.stride(0) != T * ld):
+            raise ValueError(f"{name} must have contiguous rows of one stride")
+        return B, T, ld
+
+    def _heads_form(self, x, heads, d, dv, norm, q_weight, k_weight, eps, inv_freq, interleaved, amplitude, positions):
+        import torch
+        Hq, Hk, Hv = heads
+        dv = d if dv is None else dv
+        B, T, ld = self._row_stride("x", x, (Hq + Hk) * d + Hv * dv)
+        need = self._need
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                need(name, w, self._io, d)
+        if inv_freq is not None:
+            need("inv_freq", inv_freq, torch.float32)
+        if positions is not None:
+            need("positions", positions, torch.int64, B * T)
+        if norm is None:
+            norm = "none"
+        if norm not in HEAD_NORMS:
+            raise ValueError(f"norm must be one of {', '.join(HEAD_NORMS)} (got {norm!r})")
+        rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+        return ld, dv, prism_heads_form(B, T, Hq, Hk, Hv, d, dv, HEAD_NORMS[norm], eps, _addr(q_weight), _addr(k_weight), rot,
+                                        int(interleaved), _addr(inv_freq), amplitude, _addr(positions))
+
+    def heads(self, x, heads, d, dv=None, norm="unit", q_weight=None, k_weight=None, eps=1e-6, inv_freq=None, interleaved=False,
+              amplitude=1.0, positions=None, out=None, stream=None):
+        """A projection's rows x [B, T, (Hq + Hk) d + Hv dv], whose rows may be padded, as the layer's "q"
+        [B, Hq, T, d], "k" [B, Hk, T, d] and "v" [B, Hv, T, dv] (see prism_heads), with ``heads`` =
+        (Hq, Hk, Hv), the norm ("none", "unit", "rms") and weights [d] of each query and key head, and the
+        rotation of their first 2 len(inv_freq) values by positions [B, T] int64 (0 .. T-1 unless given) times
+        inv_freq float32 (see rotary_frequencies).  Returns a dict, or fills and returns ``out``."""
+        import torch
+        if stream is not None:
+            return self._on(stream, self.heads, x, heads, d, dv, norm, q_weight, k_weight, eps, inv_freq, interleaved, amplitude, positions, out)
+        ld, dv, form = self._heads_form(x, heads, d, dv, norm, q_weight, k_weight, eps, inv_freq, interleaved, amplitude, positions)
+        B, T = form.B, form.T
+        shapes = {key: (B, H, T, size) for key, H, size in (("q", form.Hq, d), ("k", form.Hk, d), ("v", form.Hv, dv)) if H > 0}
+        if out is None:
+            out = {key: torch.empty(shape, dtype=self._io, device=x.device) for key, shape in shapes.items()}
+        else:
+            self._need_exactly("prism_heads", out, shapes, self._io)
+        get = out.get
+        prism_heads(self.handle, form, x, ld, get("q"), get("k"), get("v"), self._current_stream(self.device))
+        return out
+
+    def heads_backward(self, x, grads, heads, d, dv=None, norm="unit", q_weight=None, k_weight=None, eps=1e-6, inv_freq=None,
+                       interleaved=False, amplitude=1.0, positions=None, out=None, stream=None):
+        """The cotangents of heads' x and weights (see prism_heads_backward): ``grads`` holds "dq", "dk", "dv"
+        with the layout of q, k, v, all float32 (Plan.backward's dict serves) or all of the io dtype.  Returns a
+        dict of "dx" [B, T, ...] and, with weights, "dq_weight", "dk_weight" [d] float32, or fills and returns
+        ``out``, a dict of "dx", whose rows may be padded, and those that are wanted."""
+        import torch
+        if stream is not None:
+            return self._on(stream, self.heads_backward, x, grads, heads, d, dv, norm, q_weight, k_weight, eps, inv_freq, interleaved,
+                            amplitude, positions, out)
+        ld, dv, form = self._heads_form(x, heads, d, dv, norm, q_weight, k_weight, eps, inv_freq, interleaved, amplitude, positions)
+        B, T = form.B, form.T
+        width = (form.Hq + form.Hk) * d + form.Hv * dv
+        shapes = {key: (B, H, T, size) for key, H, size in (("dq", form.Hq, d), ("dk", form.Hk, d), ("dv", form.Hv, dv)) if H > 0}
+        given = {key: grads[key] for key in shapes}
+        dtype = next(iter(given.values())).dtype
+        if dtype not in (torch.float32, self._io):
+            raise ValueError(f"the cotangents must be of float32 or {self._io}")
+        self._need_exactly("prism_heads_backward", given, shapes, dtype)
+        f32 = torch.float32
+        if out is None:
+            out = {"dx": torch.empty(B, T, width, dtype=self._io, device=x.device)}
+            for key, w, H in (("dq_weight", q_weight, form.Hq), ("dk_weight", k_weight, form.Hk)):
+                if w is not None and H > 0:
+                    out[key] = torch.empty(d, dtype=f32, device=x.device)
+        else:
+            for key, t in out.items():
+                if key in ("dq_weight", "dk_weight"):
+                    self._need(key, t, f32, d)
+                elif key != "dx":
+                    raise ValueError(f"prism_heads_backward has no output {key!r}")
+        Bd, Td, ld_dx = self._row_stride("dx", out["dx"], width)
+        if (Bd, Td) != (B, T):
+            raise ValueError("dx must have x's rows")
+        get = given.get
+        prism_heads_backward(self.handle, form, x, ld, PRISM_F32 if dtype is f32 else PRISM_BF16, get("dq"), get("dk"), get("dv"),
+                             out["dx"], ld_dx, out.get("dq_weight"), out.get("dk_weight"), self._current_stream(self.device))
+        return out
+
+    def _need_exactly(self, what, tensors, shapes, dtype):
+        if set(tensors) != set(shapes):
+            raise ValueError(f"{what} takes {', '.join(shapes)} (got {', '.join(tensors)})")
+        for key, t in tensors.items():
+            self._need(key, t, dtype)
+            if tuple(t.shape) != shapes[key]:
+                raise ValueError(f"{key} must be {list(shapes[key])} (got {list(t.shape)})")
+
+    def sample(self, logits, u, inv_temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+        """A token for each row of logits [..., V] (or [n, V] with padded rows) from the numbers u [...] float32
+        in [0, 1) (see prism_sample).  inv_temperature, top_p, min_p [...] float32 and top_k [...] int32 hold a
+        rule for each row; a plain number is the rule of all rows (filled into a tensor by the call), None is
+        none.  Returns a dict of "ids" [...] int64, "logprob" [...] float32 and "kept" [...] int32, or fills and
+        returns ``out``, a dict of "ids" and those that are wanted."""
+        import torch
+        args = (logits, u, inv_temperature, top_k, top_p, min_p, out)
+        if stream is not None:
+            return self._on(stream, self.sample, *args)
+        n, ld = self._logit_rows("logits", logits)
+        need, f32, i32 = self._need, torch.float32, torch.int32
+        need("u", u, f32, n)
+        rules = []
+        for name, rule, dtype in (("inv_temperature", inv_temperature, f32), ("top_k", top_k, i32), ("top_p", top_p, f32), ("min_p", min_p, f32)):
+            if isinstance(rule, (int, float)):
+                rule = torch.full((n,), rule, dtype=dtype, device=logits.device)
+            elif rule is not None:
+                need(name, rule, dtype, n)
+            rules.append(rule)
+        if out is None:
+            lead, dev = logits.shape[:-1], logits.device
+            out = {"ids": torch.empty(lead, dtype=torch.int64, device=dev), "logprob": torch.empty(lead, dtype=f32, device=dev),
+                   "kept": torch.empty(lead, dtype=i32, device=dev)}
+        else:
+            types = {"ids": torch.int64, "logprob": f32, "kept": i32}
+            for key, t in out.items():
+                if key not in types:
+                    raise ValueError(f"prism_sample has no output {key!r}")
+                need(key, t, types[key], n)
+        prism_sample(self.handle, n, logits, ld, u, *rules, out["ids"], out.get("logprob"), out.get("kept"),
+                     self._current_stream(self.device))
+        return out
 
     def close(self):
         if self.handle:

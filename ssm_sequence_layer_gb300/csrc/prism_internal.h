@@ -18,6 +18,7 @@ enum DeviceStatus : int {
     kDevOk = 0,
     kDevBounds = 1,   // an internal index check failed
     kDevTimeout = 2,  // a bounded wait expired
+    kDevTemperature = 3,  // a row's inverse temperature is out of range (written by the draw only)
 };
 
 // Pointers of one forward call (device memory, layouts as in prism.h).  v_hist .. v_hist_out

@@ -77,6 +77,44 @@ prism_status check_temperature(float inv_temperature)
     return PRISM_OK;
 }
 
+prism_status check_linear(int N, int K, prism_activation act)
+{
+    if (N < 1 || K < 1) return fail(PRISM_ERR_INVALID_ARG, "N and K must be >= 1 (got %d, %d)", N, K);
+    if (N > (1 << 20) || K > (1 << 20)) return fail(PRISM_ERR_UNSUPPORTED, "N and K are at most 2^20 (got %d, %d)", N, K);
+    if (act != PRISM_ACT_NONE && act != PRISM_ACT_GELU && act != PRISM_ACT_SILU)
+        return fail(PRISM_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+    return PRISM_OK;
+}
+
+// The form of prism_heads and its backward; fills in what NULL stands for.
+prism_status check_heads(const prism_tokens_s *t, const prism_heads_form *f, long long ld, const char *ld_name)
+{
+    if (!t) return fail(PRISM_ERR_INVALID_ARG, "tokens is NULL");
+    if (!f) return fail(PRISM_ERR_INVALID_ARG, "form must not be NULL");
+    if (f->B < 0 || f->T < 0 || (long long)f->B * f->T > t->max_rows)
+        return fail(PRISM_ERR_INVALID_ARG, "B T must be in 0 .. max_rows = %d (got %d x %d)", t->max_rows, f->B, f->T);
+    const prism_status st = check_call(t, f->B * f->T, "B T");
+    if (st != PRISM_OK) return st;
+    if (f->Hq < 0 || f->Hk < 0 || f->Hv < 0 || (long long)f->Hq + f->Hk + f->Hv < 1)
+        return fail(PRISM_ERR_INVALID_ARG, "heads must be >= 0, and one at least (got %d, %d, %d)", f->Hq, f->Hk, f->Hv);
+    if ((long long)f->Hq + f->Hk + f->Hv > 65535)
+        return fail(PRISM_ERR_UNSUPPORTED, "heads are at most 65535 together (got %d, %d, %d)", f->Hq, f->Hk, f->Hv);
+    const bool rows = f->Hq + f->Hk > 0, values = f->Hv > 0;
+    if ((rows && f->d < 1) || (values && f->dv < 1)) return fail(PRISM_ERR_INVALID_ARG, "d and dv must be >= 1 (got %d, %d)", f->d, f->dv);
+    if ((rows && f->d > prism::kMaxHeadSize) || (values && f->dv > prism::kMaxHeadSize))
+        return fail(PRISM_ERR_UNSUPPORTED, "d and dv are at most %d (got %d, %d)", prism::kMaxHeadSize, f->d, f->dv);
+    if (f->norm != PRISM_HEADS_PLAIN && f->norm != PRISM_HEADS_UNIT && f->norm != PRISM_HEADS_RMS)
+        return fail(PRISM_ERR_INVALID_ARG, "unknown norm %d", (int)f->norm);
+    if (!std::isfinite(f->eps) || f->eps < 0.f) return fail(PRISM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (f->rot < 0 || f->rot % 2 != 0 || (rows && f->rot > f->d))
+        return fail(PRISM_ERR_INVALID_ARG, "rot must be even and in 0 .. d = %d (got %d)", f->d, f->rot);
+    if (f->rot > 0 && !std::isfinite(f->amplitude)) return fail(PRISM_ERR_INVALID_ARG, "amplitude must be finite");
+    const long long width = (rows ? (long long)(f->Hq + f->Hk) * f->d : 0) + (values ? (long long)f->Hv * f->dv : 0);
+    if (ld < width) return fail(PRISM_ERR_INVALID_ARG, "%s must be >= the heads' %lld columns (got %lld)", ld_name, width, ld);
+    return check_pointers<4>({{"q_weight", f->q_weight, 16, false}, {"k_weight", f->k_weight, 16, false},
+                              {"inv_freq", f->inv_freq, 4, f->rot > 0}, {"positions", f->positions, 8, false}});
+}
+
 prism::TokenLaunch begin(prism_tokens_s *t, struct CUstream_st *stream)
 {
     t->timer.on = t->opt_timing != 0;
@@ -112,6 +150,8 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
     e = prism::embed_prepare();
     if (e == cudaSuccess) e = prism::matmul8_prepare();
     if (e == cudaSuccess) e = prism::logprobs_prepare();
+    if (e == cudaSuccess) e = prism::linear_prepare();
+    if (e == cudaSuccess) e = prism::sample_prepare();
     if (e != cudaSuccess) return cuda_fail(e, "kernel attribute setup");
     prism_tokens_s *t = new (std::nothrow) prism_tokens_s();
     if (!t) return fail(PRISM_ERR_INVALID_ARG, "out of host memory");
@@ -123,7 +163,8 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
     t->sm_count = sms;
     // one allocation: the status word, then the operators' workspaces
     const size_t embed_bytes = prism::embed_workspace_bytes(max_rows, D, V);
-    t->ws_bytes = 256 + embed_bytes + prism::norm_workspace_bytes(max_rows, D);
+    const size_t norm_bytes = (prism::norm_workspace_bytes(max_rows, D) + 255) & ~(size_t)255;
+    t->ws_bytes = 256 + embed_bytes + norm_bytes + prism::heads_workspace_bytes();
     if ((e = cudaMalloc(&t->ws, t->ws_bytes)) != cudaSuccess) {
         delete t;
         return cuda_fail(e, "workspace allocation");
@@ -137,6 +178,7 @@ prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism
     }
     prism::embed_carve(max_rows, V, (char *)t->ws + 256, &t->embed);
     prism::norm_carve(max_rows, D, (char *)t->ws + 256 + embed_bytes, &t->norm);
+    t->heads = (float *)((char *)t->ws + 256 + embed_bytes + norm_bytes);
     *out_tokens = t;
     return PRISM_OK;
 }
@@ -195,6 +237,7 @@ prism_status prism_tokens_last_device_status(prism_tokens_t t)
     if ((e = cudaMemset(t->d_status, 0, sizeof(int))) != cudaSuccess || (e = cudaStreamSynchronize(nullptr)) != cudaSuccess)
         return cuda_fail(e, "status clear");
     if (word == prism::kDevTimeout) return fail(PRISM_ERR_TIMEOUT, "a bounded device wait expired");
+    if (word == prism::kDevTemperature) return fail(PRISM_ERR_DEVICE, "a row's inv_temperature was outside 2^-60 .. 2^126 (no token drawn)");
     return fail(PRISM_ERR_DEVICE, "a token id or target was >= V = %d (treated as no token)", t->V);
 }
 
@@ -332,6 +375,108 @@ prism_status prism_token_logprobs_backward(prism_tokens_t t, int n, const void *
     if (n == 0) return PRISM_OK;
     return launched(prism::logprobs_backward(
         t->logits, {logits, ld, targets, inv_temperature, lse, entropy, dlogprob, dentropy, dlogits, ld_d, n, t->V}, l));
+}
+
+prism_status prism_linear(prism_tokens_t t, int M, int N, int K, const void *x, const void *W, const void *bias,
+                          prism_activation act, const void *residual, void *y, void *pre, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, M, "M");
+    if (st != PRISM_OK) return st;
+    if ((st = check_linear(N, K, act)) != PRISM_OK) return st;
+    if ((st = check_pointers<6>({{"x", x, 16, M > 0}, {"W", W, 16, true}, {"bias", bias, 16, false}, {"residual", residual, 16, false},
+                                 {"y", y, 16, M > 0}, {"pre", pre, 16, false}})) != PRISM_OK)
+        return st;
+    if (y && y == pre) return fail(PRISM_ERR_INVALID_ARG, "y and pre must differ");
+    const prism::TokenLaunch l = begin(t, stream);
+    if (M == 0) return PRISM_OK;
+    prism::LinearArgs a{prism::LinearOp::forward, x, W, M, N, K, act};
+    a.bias = bias, a.add = residual, a.out = y, a.pre_out = pre;
+    return launched(prism::linear(t->io, a, l));
+}
+
+prism_status prism_linear_backward(prism_tokens_t t, int M, int N, int K, const void *dy, const void *W, prism_activation act,
+                                   const void *pre, const void *dsum, void *dx, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, M, "M");
+    if (st != PRISM_OK) return st;
+    if ((st = check_linear(N, K, act)) != PRISM_OK) return st;
+    if ((st = check_pointers<5>({{"dy", dy, 16, M > 0}, {"W", W, 16, true}, {"pre", pre, 16, M > 0 && act != PRISM_ACT_NONE},
+                                 {"dsum", dsum, 16, false}, {"dx", dx, 16, M > 0}})) != PRISM_OK)
+        return st;
+    const prism::TokenLaunch l = begin(t, stream);
+    if (M == 0) return PRISM_OK;
+    prism::LinearArgs a{prism::LinearOp::backward, dy, W, M, N, K, act};
+    a.pre_in = pre, a.add = dsum, a.out = dx;
+    return launched(prism::linear(t->io, a, l));
+}
+
+prism_status prism_linear_weight_backward(prism_tokens_t t, int M, int N, int K, const void *dy, const void *x, int accumulate,
+                                          float *dW, float *dbias, struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, M, "M");
+    if (st != PRISM_OK) return st;
+    if ((st = check_linear(N, K, PRISM_ACT_NONE)) != PRISM_OK) return st;
+    if ((st = check_pointers<4>({{"dy", dy, 16, M > 0}, {"x", x, 16, M > 0}, {"dW", dW, 16, true}, {"dbias", dbias, 16, false}})) != PRISM_OK)
+        return st;
+    const prism::TokenLaunch l = begin(t, stream);
+    if (M == 0) {
+        if (accumulate) return PRISM_OK;
+        cudaError_t e = cudaMemsetAsync(dW, 0, sizeof(float) * (size_t)N * K, (cudaStream_t)stream);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)N, (cudaStream_t)stream);
+        return e == cudaSuccess ? PRISM_OK : cuda_fail(e, "gradient clear");
+    }
+    prism::LinearArgs a{prism::LinearOp::weights, dy, x, M, N, K, PRISM_ACT_NONE};
+    a.out = dW, a.dbias = dbias, a.accumulate = accumulate != 0;
+    return launched(prism::linear(t->io, a, l));
+}
+
+prism_status prism_heads(prism_tokens_t t, const prism_heads_form *form, const void *x, long long ld_x, void *q, void *k, void *v,
+                         struct CUstream_st *stream)
+{
+    prism_status st = check_heads(t, form, ld_x, "ld_x");
+    if (st != PRISM_OK) return st;
+    const bool rows = form->B * form->T > 0;
+    if ((st = check_pointers<4>({{"x", x, 16, rows}, {"q", q, 16, rows && form->Hq > 0}, {"k", k, 16, rows && form->Hk > 0},
+                                 {"v", v, 16, rows && form->Hv > 0}})) != PRISM_OK)
+        return st;
+    const prism::TokenLaunch l = begin(t, stream);
+    if (!rows) return PRISM_OK;
+    return launched(prism::heads_forward(t->io, {*form, x, ld_x, q, k, v}, l));
+}
+
+prism_status prism_heads_backward(prism_tokens_t t, const prism_heads_form *form, const void *x, long long ld_x, prism_dtype grads,
+                                  const void *dq, const void *dk, const void *dv, void *dx, long long ld_dx, float *dq_weight,
+                                  float *dk_weight, struct CUstream_st *stream)
+{
+    prism_status st = check_heads(t, form, ld_x, "ld_x");
+    if (st == PRISM_OK) st = check_heads(t, form, ld_dx, "ld_dx");
+    if (st != PRISM_OK) return st;
+    if (grads != PRISM_F32 && grads != t->io) return fail(PRISM_ERR_INVALID_ARG, "grads must be float32 or the io dtype");
+    const bool rows = form->B * form->T > 0;
+    if ((st = check_pointers<7>({{"x", x, 16, rows}, {"dq", dq, 16, rows && form->Hq > 0}, {"dk", dk, 16, rows && form->Hk > 0},
+                                 {"dv", dv, 16, rows && form->Hv > 0}, {"dx", dx, 16, rows}, {"dq_weight", dq_weight, 4, false},
+                                 {"dk_weight", dk_weight, 4, false}})) != PRISM_OK)
+        return st;
+    if ((dq_weight && form->Hq == 0) || (dk_weight && form->Hk == 0))
+        return fail(PRISM_ERR_INVALID_ARG, "dq_weight and dk_weight need heads of their kind");
+    const prism::TokenLaunch l = begin(t, stream);
+    return launched(prism::heads_backward(t->io, {*form, x, ld_x, grads, dq, dk, dv, dx, ld_dx, dq_weight, dk_weight}, t->heads, l));
+}
+
+prism_status prism_sample(prism_tokens_t t, int n, const void *logits, long long ld, const float *u, const float *inv_temperature,
+                          const int *top_k, const float *top_p, const float *min_p, long long *ids, float *logprob, int *kept,
+                          struct CUstream_st *stream)
+{
+    prism_status st = check_call(t, n, "n");
+    if (st != PRISM_OK) return st;
+    if ((st = check_pointers<9>({{"logits", logits, 16, n > 0}, {"u", u, 4, n > 0}, {"inv_temperature", inv_temperature, 4, false},
+                                 {"top_k", top_k, 4, false}, {"top_p", top_p, 4, false}, {"min_p", min_p, 4, false},
+                                 {"ids", ids, 8, n > 0}, {"logprob", logprob, 4, false}, {"kept", kept, 4, false}})) != PRISM_OK)
+        return st;
+    if (ld < t->V) return fail(PRISM_ERR_INVALID_ARG, "ld must be >= V = %d (got %lld)", t->V, ld);
+    const prism::TokenLaunch l = begin(t, stream);
+    if (n == 0) return PRISM_OK;
+    return launched(prism::sample(t->logits, {logits, ld, u, inv_temperature, top_k, top_p, min_p, ids, logprob, kept, n, t->V}, l));
 }
 
 }  // extern "C"

@@ -1,4 +1,5 @@
-// Internal declarations of the token operators (embedding, norm, 8-bit product, log probabilities).
+// Internal declarations of the token operators (embedding, norm, 8-bit product, log probabilities, product with bias,
+// activation and residual, heads, draw).
 #pragma once
 
 #include "prism_internal.h"
@@ -124,6 +125,61 @@ struct LogprobBackwardArgs {
 };
 cudaError_t logprobs_backward(prism_dtype logits, const LogprobBackwardArgs &a, const TokenLaunch &l);
 
+// ---- product with bias, activation and residual, and its gradients (prism_linear.cu) -----------------
+// C[i, j] = sum_k A(i, k) B(j, k) with what follows it: i < M, j < N, k < K of the product at hand
+enum class LinearOp { forward, backward, weights };
+struct LinearArgs {
+    LinearOp op;
+    const void *a, *b;    // forward: x, W; backward: dy, W; weights: dy, x
+    int M, N, K;          // of prism_linear, whatever the product at hand
+    prism_activation act;
+    const void *bias;     // [N] (forward)
+    const void *pre_in;   // [M, K] (backward)
+    const void *add;      // residual or dsum, of the output's shape
+    void *out, *pre_out;  // y and pre, dx, or dW (float32)
+    float *dbias;
+    bool accumulate;
+};
+cudaError_t linear_prepare();
+cudaError_t linear(prism_dtype io, const LinearArgs &a, const TokenLaunch &l);
+
+// ---- heads (prism_heads.cu) --------------------------------------------------------------------------
+constexpr int kMaxHeadSize = 512;
+struct HeadsArgs {
+    prism_heads_form form;
+    const void *x;
+    long long ld_x;
+    void *q, *k, *v;
+};
+cudaError_t heads_forward(prism_dtype io, const HeadsArgs &a, const TokenLaunch &l);
+struct HeadsBackwardArgs {
+    prism_heads_form form;
+    const void *x;
+    long long ld_x;
+    prism_dtype grads;
+    const void *dq, *dk, *dv;
+    void *dx;
+    long long ld_dx;
+    float *dq_weight, *dk_weight;
+};
+size_t heads_workspace_bytes();  // parts of the weights' gradients
+cudaError_t heads_backward(prism_dtype io, const HeadsBackwardArgs &a, float *ws, const TokenLaunch &l);
+
+// ---- draw (prism_sample.cu) --------------------------------------------------------------------------
+struct SampleArgs {
+    const void *logits;
+    long long ld;
+    const float *u, *inv_temperature;
+    const int *top_k;
+    const float *top_p, *min_p;
+    long long *ids;
+    float *logprob;
+    int *kept;
+    int n, V;
+};
+cudaError_t sample_prepare();
+cudaError_t sample(prism_dtype logits, const SampleArgs &a, const TokenLaunch &l);
+
 }  // namespace prism
 
 struct prism_tokens_s {
@@ -138,4 +194,5 @@ struct prism_tokens_s {
     size_t ws_bytes;
     prism::EmbedWorkspace embed;
     prism::NormWorkspace norm;
+    float *heads;  // parts of the head weights' gradients
 };
