@@ -1,0 +1,907 @@
+// The tile kernel of the product with bias, activation and residual and of its gradients: tcgen05 (kind::f16, bf16 operands),
+// one output tile of 128 x BN at a time, blocks of 64 in the sum.
+//
+//   op         A(i, k)          B(j, k)         C(i, j)
+//   forward    x[m, k]          W[n, k]         [m, n]   both operands' rows run along the sum (K-major)
+//   backward   dy[m, n]         W[n, k]         [m, k]   B's rows run across it (MN-major)
+//   weights    dy[m, n]         x[m, k]         [n, k]   both operands' rows run across it
+//
+// Operands reach shared memory by TMA (bf16 rows whose stride is a multiple of 16 bytes) or through the registers of eight
+// warps (SOFT: every other stride, and float32).  A float32 value enters as three bf16 parts, its leading 8 bits, the next 8
+// and the last 8, which hold it exactly; of the nine products of parts the six larger ones are summed, so that a product
+// is within 2^-21 of itself.
+//
+// The tensor core cuts its sums off towards zero at each step of 16 terms, which costs long float32 results their last bits (sums over
+// 2048 terms in one accumulator: 2 10^-6 off, 256 terms: 3 10^-7, a plain float32 product 2 10^-7).  Where the outputs or the operands
+// are float32 an accumulator therefore holds four blocks at most, and the warps that finish a tile add it to sums in their
+// registers while the next four run into the other accumulator; the five small products of a float32 block have an
+// accumulator of their own, whose steps cut off 2^-8 times less.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "io_util.h"
+#include "prism_tokens.h"
+#include "tc_ptx.h"
+
+namespace prism {
+namespace lin {
+
+using namespace prism::tc;
+
+// ---- activations ----------------------------------------------------------------------------------
+// Both are within 2^-20 of themselves in relative terms wherever they are normal numbers, also where they are tiny.
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// 2^(h + l), l small
+__device__ __forceinline__ float exp2_of(float h, float l)
+{
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(h));
+    return fmaf(e, l * 0.69314718f, e);
+}
+// With a = |z| (cut at 40, where all is decided), E = e^(-a^2 / 2) and Phi(-a) = E R(a): gelu(z) = max(z, 0) - a E R(a) and
+// gelu'(z) = [z > 0] -+ E (R(a) - a / sqrt(2 pi)).  R(a) = t P(t), t = 1 / (1 + 0.275 a), P of degree 8 fitted to the scaled complementary error
+// function with the least largest relative error, 2^-24; the square's rounding error is carried into the exponential.
+__device__ __forceinline__ void gelu_parts(float z, float &a, float &E, float &R)
+{
+    a = min_nan(fabsf(z), 40.f);
+    const float s = a * a, y = s * -0.72134752f;
+    E = exp2_of(y, fmaf(s, -0.72134752f, -y) + fmaf(s, -9.6298175e-9f, fmaf(a, a, -s) * -0.72134752f));
+    const float t = __fdividef(1.f, fmaf(a, 0.275f, 1.f));
+    float q = fmaf(t, 0.027167636901140213f, -0.11067406088113785f);
+    q = fmaf(t, q, 0.1301683485507965f);
+    q = fmaf(t, q, -0.03515997529029846f);
+    q = fmaf(t, q, 0.08800629526376724f);
+    q = fmaf(t, q, 0.07893631607294083f);
+    q = fmaf(t, q, 0.10219038277864456f);
+    q = fmaf(t, q, 0.10965436697006226f);
+    q = fmaf(t, q, 0.1097106859087944f);
+    R = q * t;
+}
+// With e = e^-|z| (cut at 120): silu(z) = z / (1 + e) or z e / (1 + e), silu'(z) = that over z + z e / (1 + e)^2
+__device__ __forceinline__ void silu_parts(float z, float &a, float &e, float &r)
+{
+    a = min_nan(fabsf(z), 120.f);
+    const float y = a * -1.44269504f;
+    e = exp2_of(y, fmaf(a, -1.44269504f, -y) + a * -1.9259630e-8f);
+    r = __fdividef(1.f, 1.f + e);
+}
+template <prism_activation ACT>
+__device__ __forceinline__ float act_value(float z)
+{
+    float a, e, r;
+    if constexpr (ACT == PRISM_ACT_GELU) {
+        gelu_parts(z, a, e, r);
+        return fmaf(-a * e, r, z > 0.f ? z : 0.f);
+    } else if constexpr (ACT == PRISM_ACT_SILU) {
+        silu_parts(z, a, e, r);
+        return z > 0.f ? z * r : -a * e * r;
+    } else {
+        return z;
+    }
+}
+template <prism_activation ACT>
+__device__ __forceinline__ float act_slope(float z)
+{
+    float a, e, r;
+    if constexpr (ACT == PRISM_ACT_GELU) {
+        gelu_parts(z, a, e, r);
+        const float d = e * fmaf(a, -0.39894228f, r);
+        return z > 0.f ? 1.f - d : d;
+    } else if constexpr (ACT == PRISM_ACT_SILU) {
+        silu_parts(z, a, e, r);
+        const float d = a * e * r * r;
+        return z > 0.f ? r + d : e * r - d;
+    } else {
+        return 1.f;
+    }
+}
+
+// ---- the product at hand -----------------------------------------------------------------------------
+template <typename io_t>
+struct Params {
+    const io_t *a, *b;
+    long long lda, ldb;  // their row strides
+    int I, J, K;         // C is [I, J], the sum runs over K
+    prism_activation act;
+    const io_t *bias;    // [J]
+    const io_t *pre_in;  // [I, J]: C is multiplied by the activation's slope there
+    const io_t *add;     // [I, J]
+    void *out;           // io, or float32 for the weights' gradient
+    io_t *pre_out;
+    float *dbias;        // [I]
+    int accumulate;
+    int tiled;           // the outputs' rows are whole 16-byte units: they leave by TMA
+    int splits;          // CTAs of a cluster that share a tile and split the sum
+};
+
+struct Waits {
+    int *status;
+    unsigned long long ns;
+};
+
+constexpr int BM = 128, BK = 64;
+constexpr int kEpilogueWarps = 8, kLoaderWarps = 4;
+constexpr int kGroup = 4;  // blocks that share an accumulator where its sums go on in registers
+constexpr uint32_t kPanel = BK * 128;  // an MN-major panel: 64 rows (of the sum) x 64 values
+
+template <typename io_t, LinearOp OP, bool SOFT, int BN>
+struct Layout {
+    static constexpr int PARTS = sizeof(io_t) == 4 ? 3 : 1;
+    static constexpr bool GROUPED = PARTS == 3 || OP == LinearOp::weights;  // sums go on in registers
+    static constexpr uint32_t A_PART = BM * 128, B_PART = BN * 128, STAGE = PARTS * (A_PART + B_PART);
+    static constexpr int STAGES = 196608 / STAGE;
+    static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging of outputs: 32 x 32 values of 4 bytes, or two times 2 bytes
+    static constexpr uint32_t OFF_OUT = STAGES * STAGE;
+    static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 0 : kEpilogueWarps * OUT_WARP) + 1024;  // + alignment slack
+    static constexpr int THREADS = 128 + 32 * kEpilogueWarps + (SOFT ? 32 * kLoaderWarps : 0);
+    static constexpr int kColumns = SOFT || OP != LinearOp::weights || BN == 256 ? 512 : 256;  // of tensor memory
+    // registers handed over to the warps that finish tiles, from the issuing ones
+    static constexpr int kLaunchRegs = SOFT ? 128 : 168, kIssueRegs = SOFT ? 40 : 56, kEpilogueRegs = SOFT ? 168 : 224;
+    static constexpr bool HAND_OVER = SOFT || GROUPED;
+    static_assert(128 * kIssueRegs + 32 * kEpilogueWarps * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLaunchRegs : 0) <= THREADS * kLaunchRegs, "registers");
+    static_assert(STAGES >= 2 && SMEM + (OP == LinearOp::weights ? 3072 : 1024) <= 232448 && OFF_OUT % 1024 == 0, "layout");
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return io::Unit<__nv_bfloat16, 8>::pack(a, b); }
+// the leading halves of two floats, the first in the low half
+__device__ __forceinline__ uint32_t leading(float a, float b)
+{
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float without_leading(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+
+// ---- operands through registers ------------------------------------------------------------------------
+// A tile of R rows x C values of a row-major matrix, cut to (rows, cols), four values of a row a thread and step
+template <typename io_t, int R, int C>
+struct SoftTile {
+    static constexpr int GROUPS = R * C / 4, STEPS = GROUPS / (32 * kLoaderWarps) / 2, PER_ROW = C / 4;  // steps of half a tile
+    static constexpr int WORDS = sizeof(io_t) == 4 ? 4 : 2;
+    uint32_t v[STEPS][WORDS];
+
+    __device__ __forceinline__ void load(const io_t *base, long long ld, int r0, int rows, int c0, int cols, int thread, int half)
+    {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int g = thread + (half * STEPS + i) * 32 * kLoaderWarps, r = r0 + g / PER_ROW, c = c0 + g % PER_ROW * 4;
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) v[i][w] = 0;
+            if (r >= rows || c >= cols) continue;
+            const io_t *p = base + (long long)r * ld + c;
+            if (c + 4 <= cols && ld % 4 == 0) {
+                if constexpr (WORDS == 4) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                } else {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+                    v[i][0] = x.x, v[i][1] = x.y;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) {
+                        if constexpr (WORDS == 4) v[i][e] = __ldg(reinterpret_cast<const uint32_t *>(p + e));
+                        else v[i][e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p + e)) << (e % 2 * 16);
+                    }
+            }
+        }
+    }
+    // adds to the sums of the columns that this thread holds in every block (C = 128: the same four)
+    __device__ __forceinline__ void add_columns(float (&sums)[4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            if constexpr (WORDS == 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums[e] += __uint_as_float(v[i][e]);
+            } else {
+                float a, b, c, d;
+                io::Unit<__nv_bfloat16, 8>::two(v[i][0], a, b), io::Unit<__nv_bfloat16, 8>::two(v[i][1], c, d);
+                sums[0] += a, sums[1] += b, sums[2] += c, sums[3] += d;
+            }
+        }
+    }
+    // into panels of 64 columns, 128-byte swizzled; the parts of float32 are part_bytes apart
+    __device__ __forceinline__ void store(uint8_t *to, uint32_t part_bytes, int thread, int half) const
+    {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int g = thread + (half * STEPS + i) * 32 * kLoaderWarps, r = g / PER_ROW, c = g % PER_ROW * 4;
+            uint8_t *at = to + (c >> 6) * R * 128 + sw128(r, c & 63);
+            if constexpr (WORDS == 2) {
+                *reinterpret_cast<uint2 *>(at) = make_uint2(v[i][0], v[i][1]);
+            } else {
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(v[i][e]);
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+                    *reinterpret_cast<uint2 *>(at + part * part_bytes) = make_uint2(leading(f[0], f[1]), leading(f[2], f[3]));
+                    if (part < 2) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[e] = without_leading(f[e]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// ---- outputs --------------------------------------------------------------------------------------------
+// 32 lanes x 32 columns of an accumulator; the values may be used after ld_wait, which takes them as operands
+__device__ __forceinline__ void ld_issue(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+
+template <typename F>
+__device__ __forceinline__ void with_activation(prism_activation act, F f)
+{
+    if (act == PRISM_ACT_GELU) f(std::integral_constant<prism_activation, PRISM_ACT_GELU>());
+    else if (act == PRISM_ACT_SILU) f(std::integral_constant<prism_activation, PRISM_ACT_SILU>());
+    else f(std::integral_constant<prism_activation, PRISM_ACT_NONE>());
+}
+
+// N neighbouring values of a row, as floats; beyond `cols` zeros.  `whole`: rows are whole 16-byte units and at is one's start.
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const T *p, int at, int cols, bool whole, float (&f)[N])
+{
+    constexpr int VEC = 16 / (int)sizeof(T);
+    if constexpr (N % VEC == 0) {
+        if (whole && at + N <= cols) {
+#pragma unroll
+            for (int u = 0; u < N / VEC; ++u) {
+                float g[VEC];
+                io::load_unit<T, VEC>(p + at + u * VEC).get(g);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[u * VEC + e] = g[e];
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = at + e < cols ? io::ld(p + at + e) : 0.f;
+}
+
+// A warp's 32 rows x 32 columns of an output or an addend: lane l holds row l.
+template <typename T>
+struct Patch {
+    static constexpr int VEC = 16 / (int)sizeof(T), BUFFERS = 4 / (int)sizeof(T);
+    // rows that are not whole units come and go through shared memory, a row by all lanes
+    static __device__ __forceinline__ void get(const T *p, int J, int rows, int j0, bool whole, float *t, int lane, float (&f)[32])
+    {
+        if (whole) {
+            load_row<T, 32>(p + (size_t)min(lane, rows - 1) * J, j0, J, true, f);
+            return;
+        }
+        __syncwarp();
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) t[r * 32 + (lane ^ r)] = r < rows && j0 + lane < J ? io::ld(p + (size_t)r * J + j0 + lane) : 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) f[c] = t[lane * 32 + (c ^ lane)];
+    }
+    static __device__ __forceinline__ void put_rows(T *p, int J, int rows, int j0, float *t, int lane, const float (&f)[32])
+    {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) t[lane * 32 + (c ^ lane)] = f[c];
+        __syncwarp();
+        if (j0 + lane >= J) return;
+        T *to = p + j0 + lane;
+        if (rows == 32) {  // eight rows' loads before their stores
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                float g[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) g[r] = t[(r0 + r) * 32 + (lane ^ (r0 + r))];
+#pragma unroll
+                for (int r = 0; r < 8; ++r, to += J) io::st(to, g[r]);
+            }
+        } else {
+            for (int r = 0; r < rows; ++r, to += J) io::st(to, t[r * 32 + (lane ^ r)]);
+        }
+    }
+    // by TMA: a piece of 32 rows x 32 columns, swizzled as the tensor map says (64 bytes a row: 16-byte chunk XOR (row / 2) mod 4;
+    // 128 bytes a row: XOR row mod 8); with two buffers one piece leaves while the next is written
+    static __device__ __forceinline__ void put_tiled(const CUtensorMap *tm, uint8_t *stage, int &turn, int row0, int j0, int lane,
+                                                     const float (&f)[32])
+    {
+        constexpr uint32_t PIECE = 1024 * sizeof(T), ROW = 32 * sizeof(T);
+        uint8_t *to = stage + (turn % BUFFERS) * PIECE;
+        if (BUFFERS == 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        else bulk_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 32 / VEC; ++u) {
+            float g[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g[e] = f[u * VEC + e];
+            io::Unit<T, VEC> x;
+            x.set(g);
+            const int chunk = sizeof(T) == 2 ? u ^ (lane >> 1 & 3) : u ^ (lane & 7);
+            *reinterpret_cast<uint4 *>(to + lane * ROW + chunk * 16) = x.w;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tm, smem_u32(to), j0, row0);
+            bulk_commit();
+        }
+        ++turn;
+    }
+};
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+template <typename V>
+__device__ __forceinline__ V remote(uint32_t addr, int cta);
+template <>
+__device__ __forceinline__ float4 remote<float4>(uint32_t addr, int cta)
+{
+    uint32_t a;
+    float4 x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
+    return x;
+}
+template <>
+__device__ __forceinline__ float remote<float>(uint32_t addr, int cta)
+{
+    uint32_t a;
+    float x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+    return x;
+}
+
+// SPLIT: one tile a cluster, whose CTAs (one or more) split the sum.  Their sums meet in shared memory, where the operands
+// were, and each CTA finishes a share of the rows, always adding in the cluster's order.
+// Otherwise persistent: the next tile's products run into the other of two accumulators while this one is finished.
+template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT>
+__global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_out,
+                const __grid_constant__ CUtensorMap tm_pre, const Params<io_t> p, const Waits wt)
+{
+    using L = Layout<io_t, OP, SOFT, BN>;
+    using out_t = std::conditional_t<OP == LinearOp::weights, float, io_t>;
+    constexpr int STAGES = L::STAGES, HALF = BN / 2, PARTS = L::PARTS;
+    constexpr bool A_MN = OP == LinearOp::weights, B_MN = OP != LinearOp::forward, GROUPED = L::GROUPED;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ uint32_t tmem_base_s;
+    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2];
+    __shared__ int abort_s;
+    __shared__ __align__(16) float column_sums[OP == LinearOp::weights ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tiles_i = (p.I + BM - 1) / BM, tiles_j = (p.J + BN - 1) / BN, blocks = (p.K + BK - 1) / BK;
+    const long long tiles = (long long)tiles_i * tiles_j;
+    const int my_tiles = SPLIT ? 1 : tiles > blockIdx.x ? (int)((tiles - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
+    const int rank = SPLIT ? (int)(blockIdx.x % p.splits) : 0;
+    const int b_from = SPLIT ? (int)((long long)rank * blocks / p.splits) : 0, b_to = SPLIT ? (int)((long long)(rank + 1) * blocks / p.splits) : blocks;
+    const long long total = (long long)my_tiles * (b_to - b_from);
+    const int groups = GROUPED ? (b_to - b_from + kGroup - 1) / kGroup : 1;  // of a tile's blocks, an accumulator each
+    const uint32_t sbase = smem_u32(sm);
+
+    // tiles of one column of tiles run at the same time on neighbouring CTAs and share B in L2
+    auto tile_at = [&](int i, int &i0, int &j0) {
+        const long long t = SPLIT ? (long long)(blockIdx.x / p.splits) : (long long)blockIdx.x + (long long)i * gridDim.x;
+        i0 = (int)(t % tiles_i) * BM;
+        j0 = (int)(t / tiles_i) * BN;
+    };
+    // the sums over dy's rows: two warps add them up from shared memory, or the loaders from their registers
+    bool sums = false;
+    if constexpr (OP == LinearOp::weights) {
+        int i0, j0;
+        tile_at(0, i0, j0);
+        sums = p.dbias && j0 == 0;
+    }
+    auto load_block = [&](int s, int b, int i0, int j0) {
+        const uint32_t mb = smem_u32(&full[s]), at = sbase + s * L::STAGE;
+        mbar_expect_tx(mb, L::STAGE);
+        if constexpr (A_MN) {
+#pragma unroll
+            for (int h = 0; h < BM / 64; ++h) tma_load_2d(at + h * kPanel, &tm_a, mb, i0 + 64 * h, b * BK);
+        } else {
+            tma_load_2d(at, &tm_a, mb, b * BK, i0);
+        }
+        if constexpr (B_MN) {
+#pragma unroll
+            for (int h = 0; h < BN / 64; ++h) tma_load_2d(at + L::A_PART + h * kPanel, &tm_b, mb, j0 + 64 * h, b * BK);
+        } else {
+#pragma unroll
+            for (int h = 0; h < BN / 128; ++h) tma_load_2d(at + L::A_PART + h * 16384, &tm_b, mb, b * BK, j0 + 128 * h);
+        }
+    };
+    const int early = !SOFT && my_tiles > 0 ? min(STAGES, b_to - b_from) : 0;  // on their way while the tensor memory is allocated
+    if (tid == 32) {
+        abort_s = 0;
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), SOFT ? kLoaderWarps : 1);
+            mbar_init(smem_u32(&freed[s]), !SOFT && sums ? 3 : 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&acc_full[s]), 1);
+            mbar_init(smem_u32(&acc_empty[s]), kEpilogueWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+        if constexpr (!SOFT) {
+            int i0, j0;
+            tile_at(0, i0, j0);
+            for (int s = 0; s < early; ++s) load_block(s, b_from + s, i0, j0);
+        }
+        if (!SPLIT && p.tiled) prefetch_tmap(&tm_out);
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_base_s), L::kColumns);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = tmem_base_s;
+
+    auto give_up = [&] {
+        atomicCAS(wt.status, 0, kDevTimeout);
+        *(volatile int *)&abort_s = 1;
+    };
+    long long issued = 0;  // the issuing threads' counts of steps, for the drain
+    if (warp < 4) {
+        if constexpr (L::HAND_OVER) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kIssueRegs));
+        if (!SOFT && tid == 32) {  // ---- operand loads ----
+            int s = early % STAGES, i = b_from + early == b_to ? 1 : 0, b = i > 0 ? b_from : b_from + early, i0 = 0, j0 = 0;
+            uint32_t round = early / STAGES;
+            issued = early;
+            tile_at(0, i0, j0);
+            for (long long g = early; g < total; ++g) {
+                if (b == b_from) tile_at(i, i0, j0);
+                if (round > 0 && !mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns)) {
+                    give_up();
+                    break;
+                }
+                if (*(volatile int *)&abort_s) break;
+                load_block(s, b, i0, j0);
+                issued = g + 1;
+                if (++s == STAGES) s = 0, ++round;
+                if (++b == b_to) b = b_from, ++i;
+            }
+        } else if (tid == 0) {  // ---- products ----
+            int s = 0;
+            uint32_t round = 0, acc = 0;  // accumulators taken so far
+            bool ok = true;
+            for (int i = 0; i < my_tiles && ok; ++i) {
+                for (int b = b_from; ok && b < b_to; ++b) {
+                    const int in_group = GROUPED ? (b - b_from) % kGroup : b - b_from;
+                    const uint32_t buf = acc & 1;
+                    if (in_group == 0) ok = acc < 2 || mbar_wait(smem_u32(&acc_empty[buf]), ((acc - 2) >> 1) & 1, wt.ns);
+                    ok = ok && mbar_wait(smem_u32(&full[s]), round & 1, wt.ns);
+                    if (!ok) give_up();
+                    if (!ok || *(volatile int *)&abort_s) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after_sync();
+                    const uint32_t at = sbase + s * L::STAGE, bt = at + PARTS * L::A_PART, d = tmem + buf * BN;
+                    const uint64_t da = A_MN ? sdesc(at, kPanel, 1024) : sdesc(at, 16, 1024), db = B_MN ? sdesc(bt, kPanel, 1024) : sdesc(bt, 16, 1024);
+                    constexpr uint64_t SA = (A_MN ? 2048 : 32) >> 4, SB = (B_MN ? 2048 : 32) >> 4;
+                    constexpr uint32_t ID = idesc_bf16(BM, BN, A_MN, B_MN);
+                    const uint32_t small = tmem + 2 * BN + (i & 1) * BN;  // the small products' accumulator, for the whole tile
+#pragma unroll
+                    for (int pa = 0; pa < PARTS; ++pa)
+#pragma unroll
+                        for (int pb = 0; pa + pb < PARTS; ++pb)
+#pragma unroll
+                            for (int k = 0; k < BK / 16; ++k)
+                                mma_f16(pa + pb == 0 ? d : small, da + (uint64_t)(pa * L::A_PART >> 4) + SA * k, db + (uint64_t)(pb * L::B_PART >> 4) + SB * k,
+                                        ID, pa + pb == 0 ? in_group > 0 || k > 0 : b > b_from || pa > 0 || pb > 1 || k > 0);
+                    mma_commit(smem_u32(&freed[s]));
+                    if (b + 1 == b_to || (GROUPED && in_group + 1 == kGroup)) {
+                        mma_commit(smem_u32(&acc_full[buf]));
+                        ++acc;
+                    }
+                    ++issued;
+                    if (++s == STAGES) s = 0, ++round;
+                }
+            }
+        } else if (!SOFT && sums && warp >= 2) {  // ---- sums over dy's rows, a pair of columns a lane ----
+            int s = 0;
+            uint32_t round = 0;
+            float2 sum = make_float2(0.f, 0.f);
+            const uint8_t *panel = sm + (warp - 2) * kPanel + (lane & 3) * 4;
+            for (long long g = 0; g < total; ++g) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), round & 1, wt.ns))) {
+                    if (lane == 0) give_up();
+                    break;
+                }
+                if (__any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
+                float2 part[4] = {};
+#pragma unroll 16
+                for (int r = 0; r < BK; ++r) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(panel + s * L::STAGE + r * 128 + (((lane >> 2) ^ r) & 7) * 16);
+                    float a, b;
+                    io::Unit<__nv_bfloat16, 8>::two(w, a, b);
+                    part[r & 3] = io::add2(part[r & 3], make_float2(a, b));
+                }
+                sum = io::add2(sum, io::add2(io::add2(part[0], part[1]), io::add2(part[2], part[3])));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&freed[s]));
+                if (++s == STAGES) s = 0, ++round;
+            }
+            if constexpr (OP == LinearOp::weights)
+                *reinterpret_cast<float2 *>(&column_sums[0][(warp - 2) * 64 + 2 * lane]) = sum;
+            asm volatile("bar.arrive 1, %0;" ::"n"(64 + 32 * kEpilogueWarps) : "memory");  // nothing is read here any more
+        }
+    } else if (SOFT && warp >= 4 + kEpilogueWarps) {  // ---- operands through registers ----
+        const int thread = tid - 128 - 32 * kEpilogueWarps;
+        SoftTile<io_t, A_MN ? BK : BM, A_MN ? BM : BK> ta;
+        SoftTile<io_t, B_MN ? BK : BN, B_MN ? BN : BK> tb;
+        float column[4] = {};
+        int i = 0, b = b_from, i0, j0;  // of the block that the registers hold next
+        tile_at(0, i0, j0);
+        auto load_a = [&](int half) {
+            if (A_MN) ta.load(p.a, p.lda, b * BK, p.K, i0, p.I, thread, half);
+            else ta.load(p.a, p.lda, i0, p.I, b * BK, p.K, thread, half);
+        };
+        auto load_b = [&](int half) {
+            if (B_MN) tb.load(p.b, p.ldb, b * BK, p.K, j0, p.J, thread, half);
+            else tb.load(p.b, p.ldb, j0, p.J, b * BK, p.K, thread, half);
+        };
+        if (total > 0) load_a(0), load_b(0);
+        int s = 0;
+        uint32_t round = 0;
+        for (long long g = 0; g < total; ++g) {
+            const bool ok = round == 0 || mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) give_up();
+                break;
+            }
+            if (__any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
+            // half a tile of each operand in registers: while one is stored the other is on its way
+            uint8_t *at = sm + s * L::STAGE;
+            auto store_a = [&](int half) {
+                if (sums) ta.add_columns(column);
+                ta.store(at, L::A_PART, thread, half);
+            };
+            store_a(0);
+            load_a(1);
+            tb.store(at + PARTS * L::A_PART, L::B_PART, thread, 0);
+            load_b(1);
+            store_a(1);
+            if (++b == b_to) {
+                b = b_from;
+                if (++i < my_tiles) tile_at(i, i0, j0);
+            }
+            if (g + 1 < total) load_a(0);
+            tb.store(at + PARTS * L::A_PART, L::B_PART, thread, 1);
+            if (g + 1 < total) load_b(0);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full[s]));
+            if (++s == STAGES) s = 0, ++round;
+        }
+        if constexpr (OP == LinearOp::weights)
+            *reinterpret_cast<float4 *>(&column_sums[thread / 32][4 * lane]) = make_float4(column[0], column[1], column[2], column[3]);
+    } else {  // ---- what follows: lane quarter warp % 4, columns of half (warp - 4) / 4 ----
+        if constexpr (L::HAND_OVER) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpilogueRegs));
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t from = ((uint32_t)(quarter * 32) << 16) + half * HALF;
+        uint8_t *stage = sm + L::OFF_OUT + (warp - 4) * L::OUT_WARP;
+        float *flat = reinterpret_cast<float *>(stage);
+        const bool whole = (long long)p.J * sizeof(io_t) % 16 == 0;
+        int turn = 0;
+        uint32_t acc = 0;
+        bool ok = true;
+        for (int i = 0; i < my_tiles && ok; ++i) {
+            int i0, j0;
+            tile_at(i, i0, j0);
+            float2 sum[GROUPED ? HALF / 2 : 1];
+            uint32_t buf = 0;
+#pragma unroll 1
+            for (int g = 0; g < groups; ++g, ++acc) {
+                buf = acc & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[buf]), (acc >> 1) & 1, wt.ns));
+                if (!ok) break;
+                fence_after_sync();
+                if constexpr (GROUPED) {
+                    auto add = [&](uint32_t at, bool first) {
+#pragma unroll
+                        for (int c = 0; c < HALF; c += 32) {
+                            uint32_t r[32];
+                            ld_issue(at + c, r);
+                            ld_wait(r);
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) {
+                                const float2 x = make_float2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1]));
+                                sum[c / 2 + q] = first ? x : io::add2(sum[c / 2 + q], x);
+                            }
+                        }
+                    };
+                    add(tmem + buf * BN + from, g == 0);
+                    if (PARTS == 3 && g + 1 == groups) add(tmem + 2 * BN + (i & 1) * BN + from, false);
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+                }
+            }
+            if (!ok) {
+                if (lane == 0) give_up();  // products may still be in flight: the drain below waits for them
+                break;
+            }
+            // 32 columns of the sums, of which the last hand the accumulator back
+            auto piece = [&](int ch, float (&f)[32]) {
+                if constexpr (GROUPED) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) f[2 * q] = sum[16 * ch + q].x, f[2 * q + 1] = sum[16 * ch + q].y;
+                } else {
+                    uint32_t r[32];
+                    ld_issue(tmem + buf * BN + from + 32 * ch, r);
+                    ld_wait(r);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) f[c] = __uint_as_float(r[c]);
+                    if (ch + 1 == HALF / 32) {
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+                    }
+                }
+            };
+            if constexpr (SPLIT) {  // every load has landed and every product has read it: their shared memory is free
+                if (!SOFT && sums) asm volatile("bar.sync 1, %0;" ::"n"(64 + 32 * kEpilogueWarps) : "memory");
+                const int row = quarter * 32 + lane;
+#pragma unroll
+                for (int ch = 0; ch < HALF / 32; ++ch) {
+                    float f[32];
+                    piece(ch, f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<float4 *>(sm + row * BN * 4 + (((half * HALF / 4 + 8 * ch + q) ^ (row & 7)) << 4)) =
+                            make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                }
+            } else {
+                const int r0 = i0 + quarter * 32, rows = min(32, p.I - r0);
+                with_activation(p.act, [&](auto act) {
+                    constexpr prism_activation ACT = decltype(act)::value;
+#pragma unroll (GROUPED ? HALF / 32 : 1)
+                    for (int ch = 0; ch < HALF / 32; ++ch) {
+                        const int j = j0 + half * HALF + ch * 32;
+                        const bool inside = rows > 0 && j < p.J;
+                        float f[32], other[32];
+                        if (inside && OP == LinearOp::backward && ACT != PRISM_ACT_NONE)
+                            Patch<io_t>::get(p.pre_in + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
+                        piece(ch, f);
+                        if (!inside) continue;
+                        if constexpr (OP == LinearOp::forward) {
+                            if (p.bias) {
+                                float bias[32];
+                                load_row<io_t, 32>(p.bias, j, p.J, true, bias);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) f[c] += bias[c];
+                            }
+                            if (p.pre_out) {
+                                if (p.tiled) Patch<io_t>::put_tiled(&tm_pre, stage, turn, r0, j, lane, f);
+                                else Patch<io_t>::put_rows(p.pre_out + (size_t)r0 * p.J, p.J, rows, j, flat, lane, f);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) f[c] = act_value<ACT>(f[c]);
+                        } else if constexpr (OP == LinearOp::backward && ACT != PRISM_ACT_NONE) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) f[c] *= act_slope<ACT>(other[c]);
+                        }
+                        if (p.add) {
+                            Patch<io_t>::get(p.add + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) f[c] += other[c];
+                        }
+                        if (p.tiled) Patch<out_t>::put_tiled(&tm_out, stage, turn, r0, j, lane, f);
+                        else Patch<out_t>::put_rows((out_t *)p.out + (size_t)r0 * p.J, p.J, rows, j, flat, lane, f);
+                    }
+                });
+            }
+        }
+        if (!SPLIT && p.tiled) bulk_wait_read();  // before the staging goes
+    }
+    // drain: after an expired wait, the copies and products in flight land before the CTA exits
+    __syncthreads();
+    if (abort_s && issued > 0) {
+        const long long last = issued - 1;
+        if (tid == 0)  // products complete in order
+            (void)mbar_wait(smem_u32(&freed[last % STAGES]), (uint32_t)(last / STAGES) & 1, 1000000000ull);
+        if (!SOFT && tid == 32)
+            for (long long g = last >= STAGES ? last - STAGES + 1 : 0; g <= last; ++g)
+                (void)mbar_wait(smem_u32(&full[g % STAGES]), (uint32_t)(g / STAGES) & 1, 1000000000ull);
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, L::kColumns);
+    if constexpr (SPLIT) {
+        static_assert((uint32_t)BM * BN * 4 <= L::OFF_OUT, "the sums fit where the operands were");
+        cluster_barrier();
+        int i0, j0;
+        tile_at(0, i0, j0);
+        const int r_from = rank * BM / p.splits, r_to = min((rank + 1) * BM / p.splits, p.I - i0);
+        const bool whole = (long long)p.J * sizeof(out_t) % 16 == 0;
+        with_activation(p.act, [&](auto act) {
+            constexpr prism_activation ACT = decltype(act)::value;
+            for (int e = r_from * (BN / 128) + warp; e < r_to * (BN / 128); e += L::THREADS / 32) {
+                const int row = e / (BN / 128), unit = e % (BN / 128) * 32 + lane, j = j0 + 4 * unit;
+                const uint32_t at = sbase + row * BN * 4 + ((unit ^ (row & 7)) << 4);
+                float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int c = 0; c < p.splits; ++c) {
+                    const float4 x = remote<float4>(at, c);
+                    f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w;
+                }
+                if (j >= p.J) continue;
+                const size_t line = (size_t)(i0 + row) * p.J;
+                // four values of a row that is made of whole units, else one at a time
+                auto four = [&](const io_t *q, float (&g)[4]) {
+                    if (whole) {
+                        if constexpr (sizeof(io_t) == 4) {
+                            io::load_unit<io_t, 4>(q + j).get(g);
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(q + j);
+                            io::Unit<__nv_bfloat16, 8>::two(w.x, g[0], g[1]), io::Unit<__nv_bfloat16, 8>::two(w.y, g[2], g[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) g[x] = j + x < p.J ? io::ld(q + j + x) : 0.f;
+                    }
+                };
+                auto put = [&](auto *q) {
+                    using T = std::remove_pointer_t<decltype(q)>;
+                    if (whole) {
+                        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(q + j) = make_float4(f[0], f[1], f[2], f[3]);
+                        else *reinterpret_cast<uint2 *>(q + j) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (j + x < p.J) io::st(q + j + x, f[x]);
+                    }
+                };
+                float g[4];
+                if constexpr (OP == LinearOp::weights) {
+                    float *to = (float *)p.out + line;
+                    if (p.accumulate) {
+                        load_row<float, 4>(to, j, p.J, whole, g);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) f[x] += g[x];
+                    }
+                    put(to);
+                } else {
+                    if constexpr (OP == LinearOp::forward) {
+                        if (p.bias) {
+                            four(p.bias, g);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) f[x] += g[x];
+                        }
+                        if (p.pre_out) put(p.pre_out + line);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) f[x] = act_value<ACT>(f[x]);
+                    } else if constexpr (ACT != PRISM_ACT_NONE) {
+                        four(p.pre_in + line, g);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) f[x] *= act_slope<ACT>(g[x]);
+                    }
+                    if (p.add) {
+                        four(p.add + line, g);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) f[x] += g[x];
+                    }
+                    put((io_t *)p.out + line);
+                }
+            }
+        });
+        if (OP == LinearOp::weights && p.dbias && j0 == 0) {
+            for (int row = r_from + tid; row < r_to; row += L::THREADS) {
+                float v = 0.f;
+                for (int c = 0; c < p.splits; ++c)
+#pragma unroll
+                    for (int w = 0; w < (SOFT ? kLoaderWarps : 1); ++w)
+                        v += remote<float>(smem_u32(&column_sums[OP == LinearOp::weights ? w : 0][OP == LinearOp::weights ? row : 0]), c);
+                p.dbias[i0 + row] = p.accumulate ? p.dbias[i0 + row] + v : v;
+            }
+        }
+        cluster_barrier();  // the others may still read this CTA's sums
+    }
+}
+
+// A row-major matrix as boxes of box_rows rows x box_cols columns, swizzled by the box's row of 128 or 64 bytes
+inline bool encode(CUtensorMap *map, int size, const void *base, int cols, int rows, int box_cols, int box_rows)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)ptr;
+    }();
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols * size};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+    return fn && fn(map, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides,
+                    box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT>
+cudaError_t launch_tiles(Params<io_t> p, int splits, const TokenLaunch &l)
+{
+    using L = Layout<io_t, OP, SOFT, BN>;
+    constexpr bool A_MN = OP == LinearOp::weights, B_MN = OP != LinearOp::forward;
+    constexpr int OUT = OP == LinearOp::weights ? 4 : (int)sizeof(io_t);
+    CUtensorMap ma = {}, mb = {}, mo = {}, mp = {};
+    if (!SOFT) {  // bf16
+        const bool a = A_MN ? encode(&ma, 2, p.a, p.I, p.K, 64, BK) : encode(&ma, 2, p.a, p.K, p.I, BK, BM);
+        const bool b = B_MN ? encode(&mb, 2, p.b, p.J, p.K, 64, BK) : encode(&mb, 2, p.b, p.K, p.J, BK, 128);
+        if (!a || !b) return cudaErrorInvalidValue;
+    }
+    p.tiled = (long long)p.J * OUT % 16 == 0;
+    if (!SPLIT && p.tiled) {
+        if (!encode(&mo, OUT, p.out, p.J, p.I, 32, 32)) return cudaErrorInvalidValue;
+        if (p.pre_out && !encode(&mp, OUT, p.pre_out, p.J, p.I, 32, 32)) return cudaErrorInvalidValue;
+    }
+    p.splits = splits;
+    const long long tiles = (long long)((p.I + BM - 1) / BM) * ((p.J + BN - 1) / BN);
+    const Waits wt{l.d_status, l.wait_ns > 0 ? (unsigned long long)l.wait_ns : 100000000ull};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * splits : tiles < l.sm_count ? tiles : l.sm_count));
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = L::SMEM;
+    cfg.stream = l.timer->stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, tile_kernel<io_t, OP, SOFT, BN, SPLIT>, ma, mb, mo, mp, p, wt);
+}
+
+template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT>
+cudaError_t prepare_tiles()
+{
+    return cudaFuncSetAttribute(tile_kernel<io_t, OP, SOFT, BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<io_t, OP, SOFT, BN>::SMEM);
+}
+
+// How the product at hand is cut, and the kernel for it (one translation unit each)
+struct Cut {
+    bool soft, split;
+    int bn, splits;
+};
+template <typename io_t>
+cudaError_t forward_tiles(const Params<io_t> &p, const Cut &c, const TokenLaunch &l);
+template <typename io_t>
+cudaError_t backward_tiles(const Params<io_t> &p, const Cut &c, const TokenLaunch &l);
+template <typename io_t>
+cudaError_t weights_tiles(const Params<io_t> &p, const Cut &c, const TokenLaunch &l);
+cudaError_t forward_prepare();
+cudaError_t backward_prepare();
+cudaError_t weights_prepare();
+
+}  // namespace lin
+}  // namespace prism
