@@ -42,9 +42,19 @@ cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
             if (s == 1 || time < best) best = time, c.splits = s;
         }
         c.split = true;
+        // two CTAs a tile of 256 x 256: clusters of up to eight CTAs
+        if (c.bn == 256 && p.I > BM) {
+            c.pair = true, best = 0;
+            const long long pairs = (p.I + 255) / 256 * ((p.J + 255) / 256);
+            for (int s = 1; s <= 4 && s <= blocks; ++s) {
+                const long long time = (pairs * s + l.sm_count / 2 - 1) / (l.sm_count / 2) * ((blocks + s - 1) / s + 12);
+                if (s == 1 || time < best) best = time, c.splits = s;
+            }
+        }
     } else {
         while (c.splits < 8 && 2 * c.splits <= blocks && blocks >= 8 && tiles(128) * 2 * c.splits <= l.sm_count) c.splits *= 2;
         c.split = c.splits > 1;
+        c.pair = !c.split && !c.soft && (p.I + 255) / 256 * ((p.J + 255) / 256) * 2 > l.sm_count;
         if (!c.split && !c.soft && turns(tiles(256)) * (256 + BM) <= turns(tiles(128)) * (128 + BM)) c.bn = 256;
     }
     l.timer->begin(name);

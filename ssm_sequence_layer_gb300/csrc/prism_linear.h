@@ -132,11 +132,11 @@ constexpr int kEpilogueWarps = 8, kLoaderWarps = 4;
 constexpr int kGroup = 4;  // blocks that share an accumulator where its sums go on in registers
 constexpr uint32_t kPanel = BK * 128;  // an MN-major panel: 64 rows (of the sum) x 64 values
 
-template <typename io_t, LinearOp OP, bool SOFT, int BN>
+template <typename io_t, LinearOp OP, bool SOFT, int BN, bool PAIR>
 struct Layout {
     static constexpr int PARTS = sizeof(io_t) == 4 ? 3 : 1;
     static constexpr bool GROUPED = PARTS == 3 || OP == LinearOp::weights;  // sums go on in registers
-    static constexpr uint32_t A_PART = BM * 128, B_PART = BN * 128, STAGE = PARTS * (A_PART + B_PART);
+    static constexpr uint32_t A_PART = BM * 128, B_PART = (PAIR ? BN / 2 : BN) * 128, STAGE = PARTS * (A_PART + B_PART);
     static constexpr int STAGES = 196608 / STAGE;
     static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging of outputs: 32 x 32 values of 4 bytes, or two times 2 bytes
     static constexpr uint32_t OFF_OUT = STAGES * STAGE;
@@ -149,6 +149,17 @@ struct Layout {
     static_assert(128 * kIssueRegs + 32 * kEpilogueWarps * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLaunchRegs : 0) <= THREADS * kLaunchRegs, "registers");
     static_assert(STAGES >= 2 && SMEM + (OP == LinearOp::weights ? 3072 : 1024) <= 232448 && OFF_OUT % 1024 == 0, "layout");
 };
+
+// one look at a barrier's phase
+__device__ __forceinline__ bool mbar_test(uint32_t mbar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(mbar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return io::Unit<__nv_bfloat16, 8>::pack(a, b); }
 // the leading halves of two floats, the first in the low half
@@ -357,6 +368,61 @@ struct Patch {
     }
 };
 
+// one lane of a warp, the same each time
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// a shared-memory address of this CTA in another of the cluster
+__device__ __forceinline__ uint32_t address_in(uint32_t addr, uint32_t cta)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t remote)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+// ---- two CTAs at one tile ----
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum));
+}
+__device__ __forceinline__ void mma_commit_pair(uint32_t mbar, uint16_t ctas)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar), "h"(ctas)
+                 : "memory");
+}
+// into this CTA's shared memory, counted by a barrier of either CTA
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t mbar, int c0, int c1)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(mbar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
@@ -382,41 +448,49 @@ __device__ __forceinline__ float remote<float>(uint32_t addr, int cta)
     return x;
 }
 
-// SPLIT: one tile a cluster, whose CTAs (one or more) split the sum.  Their sums meet in shared memory, where the operands
+// PAIR: two CTAs of neighbouring SMs share a tile of 256 rows (tcgen05 cta_group::2): each brings in and finishes its own 128 rows
+// and brings in half of B, which both read, so that a block's operands are 32 KB an SM and not 48.  One thread of the first CTA issues the
+// products of both; its barriers count the loads of both, and every completion of products arrives in both.
+// SPLIT: one tile a cluster, whose CTAs (or pairs) split the sum (or one does it all).  Their sums meet in shared memory, where the operands
 // were, and each CTA finishes a share of the rows, always adding in the cluster's order.
 // Otherwise persistent: the next tile's products run into the other of two accumulators while this one is finished.
-template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT>
-__global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
+template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT, bool PAIR>
+__global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_out,
                 const __grid_constant__ CUtensorMap tm_pre, const Params<io_t> p, const Waits wt)
 {
-    using L = Layout<io_t, OP, SOFT, BN>;
+    using L = Layout<io_t, OP, SOFT, BN, PAIR>;
     using out_t = std::conditional_t<OP == LinearOp::weights, float, io_t>;
     constexpr int STAGES = L::STAGES, HALF = BN / 2, PARTS = L::PARTS;
     constexpr bool A_MN = OP == LinearOp::weights, B_MN = OP != LinearOp::forward, GROUPED = L::GROUPED;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint32_t tmem_base_s;
-    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2];
+    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], summed[STAGES], acc_full[2], acc_empty[2];
     __shared__ int abort_s;
     __shared__ __align__(16) float column_sums[OP == LinearOp::weights ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
+    constexpr int CTAS = PAIR ? 2 : 1, TM = CTAS * BM;  // of a tile, and its rows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tiles_i = (p.I + BM - 1) / BM, tiles_j = (p.J + BN - 1) / BN, blocks = (p.K + BK - 1) / BK;
+    const int in_tile = PAIR ? (int)(blockIdx.x & 1) : 0;  // the cluster's CTAs are numbered as the grid's
+    const bool leads = in_tile == 0;
+    const int tiles_i = (p.I + TM - 1) / TM, tiles_j = (p.J + BN - 1) / BN, blocks = (p.K + BK - 1) / BK;
     const long long tiles = (long long)tiles_i * tiles_j;
-    const int my_tiles = SPLIT ? 1 : tiles > blockIdx.x ? (int)((tiles - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
-    const int rank = SPLIT ? (int)(blockIdx.x % p.splits) : 0;
+    const unsigned worker = blockIdx.x / CTAS, workers = gridDim.x / CTAS;
+    const int my_tiles = SPLIT ? 1 : tiles > worker ? (int)((tiles - 1 - worker) / workers) + 1 : 0;
+    const int rank = SPLIT ? (int)(worker % p.splits) : 0;
     const int b_from = SPLIT ? (int)((long long)rank * blocks / p.splits) : 0, b_to = SPLIT ? (int)((long long)(rank + 1) * blocks / p.splits) : blocks;
     const long long total = (long long)my_tiles * (b_to - b_from);
     const int groups = GROUPED ? (b_to - b_from + kGroup - 1) / kGroup : 1;  // of a tile's blocks, an accumulator each
-    const uint32_t sbase = smem_u32(sm);
+    const uint32_t sbase = smem_u32(sm), crank = PAIR ? cluster_rank() : 0;
+    const uint32_t leader_full = PAIR ? address_in(smem_u32(&full[0]), crank & ~1) : smem_u32(&full[0]);
 
     // tiles of one column of tiles run at the same time on neighbouring CTAs and share B in L2
     auto tile_at = [&](int i, int &i0, int &j0) {
-        const long long t = SPLIT ? (long long)(blockIdx.x / p.splits) : (long long)blockIdx.x + (long long)i * gridDim.x;
-        i0 = (int)(t % tiles_i) * BM;
+        const long long t = SPLIT ? (long long)(worker / p.splits) : (long long)worker + (long long)i * workers;
+        i0 = (int)(t % tiles_i) * TM + in_tile * BM;
         j0 = (int)(t / tiles_i) * BN;
     };
-    // the sums over dy's rows: two warps add them up from shared memory, or the loaders from their registers
+    // the sums over dy's rows: two warps add them up from shared memory once the products have read it, or the loaders from their registers
     bool sums = false;
     if constexpr (OP == LinearOp::weights) {
         int i0, j0;
@@ -424,45 +498,57 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
         sums = p.dbias && j0 == 0;
     }
     auto load_block = [&](int s, int b, int i0, int j0) {
-        const uint32_t mb = smem_u32(&full[s]), at = sbase + s * L::STAGE;
-        mbar_expect_tx(mb, L::STAGE);
+        const uint32_t at = sbase + s * L::STAGE, mb = leader_full + 8 * s;
+        if (leads) mbar_expect_tx(smem_u32(&full[s]), CTAS * L::STAGE);
+        auto box = [&](uint32_t to, const CUtensorMap *map, int c0, int c1) {
+            if constexpr (PAIR) tma_load_2d_pair(to, map, mb, c0, c1);
+            else tma_load_2d(to, map, mb, c0, c1);
+        };
+        constexpr int OWN = BN / CTAS;  // B's rows (columns) that this CTA brings in
+        j0 += in_tile * OWN;
         if constexpr (A_MN) {
 #pragma unroll
-            for (int h = 0; h < BM / 64; ++h) tma_load_2d(at + h * kPanel, &tm_a, mb, i0 + 64 * h, b * BK);
+            for (int h = 0; h < BM / 64; ++h) box(at + h * kPanel, &tm_a, i0 + 64 * h, b * BK);
         } else {
-            tma_load_2d(at, &tm_a, mb, b * BK, i0);
+            box(at, &tm_a, b * BK, i0);
         }
         if constexpr (B_MN) {
 #pragma unroll
-            for (int h = 0; h < BN / 64; ++h) tma_load_2d(at + L::A_PART + h * kPanel, &tm_b, mb, j0 + 64 * h, b * BK);
+            for (int h = 0; h < OWN / 64; ++h) box(at + L::A_PART + h * kPanel, &tm_b, j0 + 64 * h, b * BK);
         } else {
 #pragma unroll
-            for (int h = 0; h < BN / 128; ++h) tma_load_2d(at + L::A_PART + h * 16384, &tm_b, mb, b * BK, j0 + 128 * h);
+            for (int h = 0; h < OWN / 128; ++h) box(at + L::A_PART + h * 16384, &tm_b, b * BK, j0 + 128 * h);
         }
     };
-    const int early = !SOFT && my_tiles > 0 ? min(STAGES, b_to - b_from) : 0;  // on their way while the tensor memory is allocated
+    // on their way while the tensor memory is allocated; a pair's barriers have to stand first
+    const int early = !SOFT && !PAIR && my_tiles > 0 ? min(STAGES, b_to - b_from) : 0;
     if (tid == 32) {
         abort_s = 0;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), SOFT ? kLoaderWarps : 1);
-            mbar_init(smem_u32(&freed[s]), !SOFT && sums ? 3 : 1);
+            mbar_init(smem_u32(&freed[s]), 1);
+            mbar_init(smem_u32(&summed[s]), 2);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
-            mbar_init(smem_u32(&acc_empty[s]), kEpilogueWarps);
+            mbar_init(smem_u32(&acc_empty[s]), CTAS * kEpilogueWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
-        if constexpr (!SOFT) {
+        if constexpr (!SOFT && !PAIR) {
             int i0, j0;
             tile_at(0, i0, j0);
             for (int s = 0; s < early; ++s) load_block(s, b_from + s, i0, j0);
         }
         if (!SPLIT && p.tiled) prefetch_tmap(&tm_out);
     }
-    if (warp == 0) tmem_alloc(smem_u32(&tmem_base_s), L::kColumns);
+    if (warp == 0) {
+        if constexpr (PAIR) tmem_alloc_pair(smem_u32(&tmem_base_s), L::kColumns);
+        else tmem_alloc(smem_u32(&tmem_base_s), L::kColumns);
+    }
     fence_before_sync();
     __syncthreads();
+    if constexpr (PAIR) cluster_barrier();
     fence_after_sync();
     const uint32_t tmem = tmem_base_s;
 
@@ -473,59 +559,89 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
     long long issued = 0;  // the issuing threads' counts of steps, for the drain
     if (warp < 4) {
         if constexpr (L::HAND_OVER) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kIssueRegs));
-        if (!SOFT && tid == 32) {  // ---- operand loads ----
+        // Whole warps run these loops, so that their counters and descriptors stay in uniform registers, and one lane issues.  Each
+        // looks at its next barrier while it issues: shared memory, busy with operands, takes some hundred cycles to answer
+        // (4096 x 4096 x 4096 took 108 us with one thread a loop and two looks between a block's products and the next).
+        if (!SOFT && warp == 1) {  // ---- operand loads ----
+            const bool one = elect_one();
             int s = early % STAGES, i = b_from + early == b_to ? 1 : 0, b = i > 0 ? b_from : b_from + early, i0 = 0, j0 = 0;
             uint32_t round = early / STAGES;
+            bool ready = false;
             issued = early;
             tile_at(0, i0, j0);
             for (long long g = early; g < total; ++g) {
                 if (b == b_from) tile_at(i, i0, j0);
-                if (round > 0 && !mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns)) {
-                    give_up();
+                if (round > 0 && !ready) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns))) {
+                        if (one) give_up();
+                        break;
+                    }
+                }
+                if (sums && round > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&summed[s]), (round - 1) & 1, wt.ns))) {
+                    if (one) give_up();
                     break;
                 }
-                if (*(volatile int *)&abort_s) break;
-                load_block(s, b, i0, j0);
+                if (s == 0 && __any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
+                const int next = s + 1 == STAGES ? 0 : s + 1;
+                const uint32_t next_round = s + 1 == STAGES ? round + 1 : round;
+                const bool seen = next_round > 0 && mbar_test(smem_u32(&freed[next]), (next_round - 1) & 1);
+                if (one) load_block(s, b, i0, j0);
+                __syncwarp();
+                ready = __all_sync(0xffffffffu, seen);
                 issued = g + 1;
-                if (++s == STAGES) s = 0, ++round;
+                s = next, round = next_round;
                 if (++b == b_to) b = b_from, ++i;
             }
-        } else if (tid == 0) {  // ---- products ----
+        } else if (warp == 0 && leads) {  // ---- products ----
+            const bool one = elect_one();
             int s = 0;
             uint32_t round = 0, acc = 0;  // accumulators taken so far
-            bool ok = true;
+            auto product = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
+                if constexpr (PAIR) mma_f16_pair(d, a, b, id, more);
+                else mma_f16(d, a, b, id, more);
+            };
+            auto done = [&](uint64_t *barrier) {  // arrives once the products so far are complete, in both CTAs of a pair
+                if constexpr (PAIR) mma_commit_pair(smem_u32(barrier), (uint16_t)(3u << (crank & ~1u)));
+                else mma_commit(smem_u32(barrier));
+            };
+            bool ok = true, ready = false;
             for (int i = 0; i < my_tiles && ok; ++i) {
-                for (int b = b_from; ok && b < b_to; ++b) {
+                for (int b = b_from; b < b_to; ++b) {
                     const int in_group = GROUPED ? (b - b_from) % kGroup : b - b_from;
                     const uint32_t buf = acc & 1;
-                    if (in_group == 0) ok = acc < 2 || mbar_wait(smem_u32(&acc_empty[buf]), ((acc - 2) >> 1) & 1, wt.ns);
-                    ok = ok && mbar_wait(smem_u32(&full[s]), round & 1, wt.ns);
-                    if (!ok) give_up();
-                    if (!ok || *(volatile int *)&abort_s) {
-                        ok = false;
+                    if (in_group == 0 && acc >= 2) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_empty[buf]), ((acc - 2) >> 1) & 1, wt.ns));
+                    if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), round & 1, wt.ns));
+                    if (!ok) {
+                        if (one) give_up();
                         break;
                     }
                     fence_after_sync();
+                    const int next = s + 1 == STAGES ? 0 : s + 1;
+                    const uint32_t next_round = s + 1 == STAGES ? round + 1 : round;
+                    const bool seen = mbar_test(smem_u32(&full[next]), next_round & 1);
                     const uint32_t at = sbase + s * L::STAGE, bt = at + PARTS * L::A_PART, d = tmem + buf * BN;
                     const uint64_t da = A_MN ? sdesc(at, kPanel, 1024) : sdesc(at, 16, 1024), db = B_MN ? sdesc(bt, kPanel, 1024) : sdesc(bt, 16, 1024);
                     constexpr uint64_t SA = (A_MN ? 2048 : 32) >> 4, SB = (B_MN ? 2048 : 32) >> 4;
-                    constexpr uint32_t ID = idesc_bf16(BM, BN, A_MN, B_MN);
+                    constexpr uint32_t ID = idesc_bf16(TM, BN, A_MN, B_MN);
                     const uint32_t small = tmem + 2 * BN + (i & 1) * BN;  // the small products' accumulator, for the whole tile
+                    const bool last = b + 1 == b_to || (GROUPED && in_group + 1 == kGroup);
+                    if (one) {
 #pragma unroll
-                    for (int pa = 0; pa < PARTS; ++pa)
+                        for (int pa = 0; pa < PARTS; ++pa)
 #pragma unroll
-                        for (int pb = 0; pa + pb < PARTS; ++pb)
+                            for (int pb = 0; pa + pb < PARTS; ++pb)
 #pragma unroll
-                            for (int k = 0; k < BK / 16; ++k)
-                                mma_f16(pa + pb == 0 ? d : small, da + (uint64_t)(pa * L::A_PART >> 4) + SA * k, db + (uint64_t)(pb * L::B_PART >> 4) + SB * k,
-                                        ID, pa + pb == 0 ? in_group > 0 || k > 0 : b > b_from || pa > 0 || pb > 1 || k > 0);
-                    mma_commit(smem_u32(&freed[s]));
-                    if (b + 1 == b_to || (GROUPED && in_group + 1 == kGroup)) {
-                        mma_commit(smem_u32(&acc_full[buf]));
-                        ++acc;
+                                for (int k = 0; k < BK / 16; ++k)
+                                    product(pa + pb == 0 ? d : small, da + (uint64_t)(pa * L::A_PART >> 4) + SA * k, db + (uint64_t)(pb * L::B_PART >> 4) + SB * k,
+                                            ID, pa + pb == 0 ? in_group > 0 || k > 0 : b > b_from || pa > 0 || pb > 1 || k > 0);
+                        done(&freed[s]);
+                        if (last) done(&acc_full[buf]);
                     }
+                    __syncwarp();
+                    ready = __all_sync(0xffffffffu, seen);
+                    if (last) ++acc;
                     ++issued;
-                    if (++s == STAGES) s = 0, ++round;
+                    s = next, round = next_round;
                 }
             }
         } else if (!SOFT && sums && warp >= 2) {  // ---- sums over dy's rows, a pair of columns a lane ----
@@ -534,7 +650,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
             float2 sum = make_float2(0.f, 0.f);
             const uint8_t *panel = sm + (warp - 2) * kPanel + (lane & 3) * 4;
             for (long long g = 0; g < total; ++g) {
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), round & 1, wt.ns))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&freed[s]), round & 1, wt.ns))) {
                     if (lane == 0) give_up();
                     break;
                 }
@@ -549,7 +665,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
                 }
                 sum = io::add2(sum, io::add2(io::add2(part[0], part[1]), io::add2(part[2], part[3])));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&freed[s]));
+                if (lane == 0) mbar_arrive(smem_u32(&summed[s]));
                 if (++s == STAGES) s = 0, ++round;
             }
             if constexpr (OP == LinearOp::weights)
@@ -616,6 +732,14 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
         int turn = 0;
         uint32_t acc = 0;
         bool ok = true;
+        auto hand_back = [&](uint32_t buf) {
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) mbar_arrive_at(address_in(smem_u32(&acc_empty[buf]), crank & ~1));
+                else mbar_arrive(smem_u32(&acc_empty[buf]));
+            }
+        };
         for (int i = 0; i < my_tiles && ok; ++i) {
             int i0, j0;
             tile_at(i, i0, j0);
@@ -643,9 +767,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
                     };
                     add(tmem + buf * BN + from, g == 0);
                     if (PARTS == 3 && g + 1 == groups) add(tmem + 2 * BN + (i & 1) * BN + from, false);
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+                    hand_back(buf);
                 }
             }
             if (!ok) {
@@ -663,11 +785,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
                     ld_wait(r);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) f[c] = __uint_as_float(r[c]);
-                    if (ch + 1 == HALF / 32) {
-                        fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
-                    }
+                    if (ch + 1 == HALF / 32) hand_back(buf);
                 }
             };
             if constexpr (SPLIT) {  // every load has landed and every product has read it: their shared memory is free
@@ -729,18 +847,21 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
     __syncthreads();
     if (abort_s && issued > 0) {
         const long long last = issued - 1;
-        if (tid == 0)  // products complete in order
+        if (tid == 0 && leads)  // products complete in order
             (void)mbar_wait(smem_u32(&freed[last % STAGES]), (uint32_t)(last / STAGES) & 1, 1000000000ull);
-        if (!SOFT && tid == 32)
+        if (!SOFT && tid == 32 && leads)
             for (long long g = last >= STAGES ? last - STAGES + 1 : 0; g <= last; ++g)
                 (void)mbar_wait(smem_u32(&full[g % STAGES]), (uint32_t)(g / STAGES) & 1, 1000000000ull);
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, L::kColumns);
+    if constexpr (PAIR || SPLIT) cluster_barrier();  // the other CTA's products reach into this one until here; the sums stand in shared memory
+    if (warp == 0) {
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, L::kColumns);
+        else tmem_dealloc(tmem, L::kColumns);
+    }
     if constexpr (SPLIT) {
         static_assert((uint32_t)BM * BN * 4 <= L::OFF_OUT, "the sums fit where the operands were");
-        cluster_barrier();
         int i0, j0;
         tile_at(0, i0, j0);
         const int r_from = rank * BM / p.splits, r_to = min((rank + 1) * BM / p.splits, p.I - i0);
@@ -753,7 +874,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
                 float f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
                 for (int c = 0; c < p.splits; ++c) {
-                    const float4 x = remote<float4>(at, c);
+                    const float4 x = remote<float4>(at, CTAS * c + in_tile);
                     f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w;
                 }
                 if (j >= p.J) continue;
@@ -822,7 +943,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN>::THREADS, 1)
                 for (int c = 0; c < p.splits; ++c)
 #pragma unroll
                     for (int w = 0; w < (SOFT ? kLoaderWarps : 1); ++w)
-                        v += remote<float>(smem_u32(&column_sums[OP == LinearOp::weights ? w : 0][OP == LinearOp::weights ? row : 0]), c);
+                        v += remote<float>(smem_u32(&column_sums[OP == LinearOp::weights ? w : 0][OP == LinearOp::weights ? row : 0]), CTAS * c + in_tile);
                 p.dbias[i0 + row] = p.accumulate ? p.dbias[i0 + row] + v : v;
             }
         }
@@ -848,10 +969,10 @@ inline bool encode(CUtensorMap *map, int size, const void *base, int cols, int r
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT>
+template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT, bool PAIR>
 cudaError_t launch_tiles(Params<io_t> p, int splits, const TokenLaunch &l)
 {
-    using L = Layout<io_t, OP, SOFT, BN>;
+    using L = Layout<io_t, OP, SOFT, BN, PAIR>;
     constexpr bool A_MN = OP == LinearOp::weights, B_MN = OP != LinearOp::forward;
     constexpr int OUT = OP == LinearOp::weights ? 4 : (int)sizeof(io_t);
     CUtensorMap ma = {}, mb = {}, mo = {}, mp = {};
@@ -866,31 +987,32 @@ cudaError_t launch_tiles(Params<io_t> p, int splits, const TokenLaunch &l)
         if (p.pre_out && !encode(&mp, OUT, p.pre_out, p.J, p.I, 32, 32)) return cudaErrorInvalidValue;
     }
     p.splits = splits;
-    const long long tiles = (long long)((p.I + BM - 1) / BM) * ((p.J + BN - 1) / BN);
+    constexpr int CTAS = PAIR ? 2 : 1;
+    const long long tiles = (long long)((p.I + CTAS * BM - 1) / (CTAS * BM)) * ((p.J + BN - 1) / BN), workers = l.sm_count / CTAS;
     const Waits wt{l.d_status, l.wait_ns > 0 ? (unsigned long long)l.wait_ns : 100000000ull};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(SPLIT ? tiles * splits : tiles < l.sm_count ? tiles : l.sm_count));
+    cfg.gridDim = dim3((unsigned)(CTAS * (SPLIT ? tiles * splits : tiles < workers ? tiles : workers)));
     cfg.blockDim = dim3(L::THREADS);
     cfg.dynamicSmemBytes = L::SMEM;
     cfg.stream = l.timer->stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = splits;
+    at[0].val.clusterDim.x = CTAS * splits;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = SPLIT ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tile_kernel<io_t, OP, SOFT, BN, SPLIT>, ma, mb, mo, mp, p, wt);
+    cfg.numAttrs = SPLIT || PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, tile_kernel<io_t, OP, SOFT, BN, SPLIT, PAIR>, ma, mb, mo, mp, p, wt);
 }
 
-template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT>
+template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT, bool PAIR>
 cudaError_t prepare_tiles()
 {
-    return cudaFuncSetAttribute(tile_kernel<io_t, OP, SOFT, BN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<io_t, OP, SOFT, BN>::SMEM);
+    return cudaFuncSetAttribute(tile_kernel<io_t, OP, SOFT, BN, SPLIT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<io_t, OP, SOFT, BN, PAIR>::SMEM);
 }
 
 // How the product at hand is cut, and the kernel for it (one translation unit each)
 struct Cut {
-    bool soft, split;
+    bool soft, split, pair;
     int bn, splits;
 };
 template <typename io_t>

@@ -8,29 +8,31 @@ template <>
 cudaError_t forward_tiles<__nv_bfloat16>(const Params<__nv_bfloat16> &p, const Cut &c, const TokenLaunch &l)
 {
     if (c.soft)
-        return c.split ? launch_tiles<__nv_bfloat16, LinearOp::forward, true, 128, true>(p, c.splits, l)
-                       : launch_tiles<__nv_bfloat16, LinearOp::forward, true, 128, false>(p, 1, l);
-    if (c.split) return launch_tiles<__nv_bfloat16, LinearOp::forward, false, 128, true>(p, c.splits, l);
-    return c.bn == 256 ? launch_tiles<__nv_bfloat16, LinearOp::forward, false, 256, false>(p, 1, l)
-                       : launch_tiles<__nv_bfloat16, LinearOp::forward, false, 128, false>(p, 1, l);
+        return c.split ? launch_tiles<__nv_bfloat16, LinearOp::forward, true, 128, true, false>(p, c.splits, l)
+                       : launch_tiles<__nv_bfloat16, LinearOp::forward, true, 128, false, false>(p, 1, l);
+    if (c.split) return launch_tiles<__nv_bfloat16, LinearOp::forward, false, 128, true, false>(p, c.splits, l);
+    if (c.pair) return launch_tiles<__nv_bfloat16, LinearOp::forward, false, 256, false, true>(p, 1, l);
+    return c.bn == 256 ? launch_tiles<__nv_bfloat16, LinearOp::forward, false, 256, false, false>(p, 1, l)
+                       : launch_tiles<__nv_bfloat16, LinearOp::forward, false, 128, false, false>(p, 1, l);
 }
 
 template <>
 cudaError_t forward_tiles<float>(const Params<float> &p, const Cut &c, const TokenLaunch &l)
 {
-    return c.split ? launch_tiles<float, LinearOp::forward, true, 128, true>(p, c.splits, l)
-                   : launch_tiles<float, LinearOp::forward, true, 128, false>(p, 1, l);
+    return c.split ? launch_tiles<float, LinearOp::forward, true, 128, true, false>(p, c.splits, l)
+                   : launch_tiles<float, LinearOp::forward, true, 128, false, false>(p, 1, l);
 }
 
 cudaError_t forward_prepare()
 {
-    cudaError_t e = prepare_tiles<__nv_bfloat16, LinearOp::forward, false, 256, false>();
-    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, false, 128, false>();
-    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, false, 128, true>();
-    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, true, 128, false>();
-    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, true, 128, true>();
-    if (e == cudaSuccess) e = prepare_tiles<float, LinearOp::forward, true, 128, false>();
-    if (e == cudaSuccess) e = prepare_tiles<float, LinearOp::forward, true, 128, true>();
+    cudaError_t e = prepare_tiles<__nv_bfloat16, LinearOp::forward, false, 256, false, true>();
+    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, false, 256, false, false>();
+    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, false, 128, false, false>();
+    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, false, 128, true, false>();
+    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, true, 128, false, false>();
+    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::forward, true, 128, true, false>();
+    if (e == cudaSuccess) e = prepare_tiles<float, LinearOp::forward, true, 128, false, false>();
+    if (e == cudaSuccess) e = prepare_tiles<float, LinearOp::forward, true, 128, true, false>();
     return e;
 }
 
