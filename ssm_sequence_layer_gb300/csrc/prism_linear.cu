@@ -30,32 +30,30 @@ cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
     Cut c = {};
     // TMA takes rows whose stride is a multiple of 16 bytes
     c.soft = sizeof(io_t) == 4 || p.lda % 8 != 0 || p.ldb % 8 != 0;
-    const long long rows = (p.I + BM - 1) / BM, blocks = (p.K + BK - 1) / BK;
-    auto tiles = [&](long long bn) { return rows * ((p.J + bn - 1) / bn); };
-    auto turns = [&](long long n) { return (n + l.sm_count - 1) / l.sm_count; };
+    const long long blocks = (p.K + BK - 1) / BK;
+    auto tiles = [&](long long bm, long long bn) { return (p.I + bm - 1) / bm * ((p.J + bn - 1) / bn); };
+    auto turns = [&](long long n, int ctas) { return (n + clusters_at_once(ctas) - 1) / clusters_at_once(ctas); };
     c.bn = 128, c.splits = 1;
     if (weights) {
-        if (!c.soft && p.J > 128) c.bn = 256;
-        long long best = 0;
-        for (int s = 1; s <= 8 && s <= blocks; ++s) {
-            const long long time = turns(tiles(c.bn) * s) * ((blocks + s - 1) / s + 12);
-            if (s == 1 || time < best) best = time, c.splits = s;
-        }
+        // The tile, and the CTAs or pairs that split its sum, of least cycles: turns of the clusters that run at once (clusters of six
+        // leave 14 SMs without work, of eight 32) times a share of the blocks, at what a block costs, and about 7000 until the first
+        // products and for the join.
         c.split = true;
-        // two CTAs a tile of 256 x 256: clusters of up to eight CTAs
-        if (c.bn == 256 && p.I > BM) {
-            c.pair = true, best = 0;
-            const long long pairs = (p.I + 255) / 256 * ((p.J + 255) / 256);
-            for (int s = 1; s <= 4 && s <= blocks; ++s) {
-                const long long time = (pairs * s + l.sm_count / 2 - 1) / (l.sm_count / 2) * ((blocks + s - 1) / s + 12);
-                if (s == 1 || time < best) best = time, c.splits = s;
+        long long best = 0;
+        auto consider = [&](bool pair, int bn, long long block) {
+            const int ctas = pair ? 2 : 1;
+            for (int s = 1; s * ctas <= 8 && s <= blocks; ++s) {
+                const long long time = turns(tiles(ctas * BM, bn), s * ctas) * ((blocks + s - 1) / s * block + 7000);
+                if (best == 0 || time < best) best = time, c.pair = pair, c.bn = bn, c.splits = s;
             }
-        }
+        };
+        consider(false, 128, sizeof(io_t) == 4 ? 3000 : c.soft ? 1500 : 540);
+        if (!c.soft) consider(false, 256, 800), consider(true, 256, 560), consider(true, 192, 430);
     } else {
-        while (c.splits < 8 && 2 * c.splits <= blocks && blocks >= 8 && tiles(128) * 2 * c.splits <= l.sm_count) c.splits *= 2;
+        while (c.splits < 8 && 2 * c.splits <= blocks && blocks >= 8 && tiles(BM, 128) <= clusters_at_once(2 * c.splits)) c.splits *= 2;
         c.split = c.splits > 1;
-        c.pair = !c.split && !c.soft && (p.I + 255) / 256 * ((p.J + 255) / 256) * 2 > l.sm_count;
-        if (!c.split && !c.soft && turns(tiles(256)) * (256 + BM) <= turns(tiles(128)) * (128 + BM)) c.bn = 256;
+        c.pair = !c.split && !c.soft && tiles(256, 256) * 2 > l.sm_count;
+        if (!c.split && !c.soft && turns(tiles(BM, 256), 1) * (256 + BM) <= turns(tiles(BM, 128), 1) * (128 + BM)) c.bn = 256;
     }
     l.timer->begin(name);
     const cudaError_t e = weights ? weights_tiles<io_t>(p, c, l) : a.op == LinearOp::forward ? forward_tiles<io_t>(p, c, l) : backward_tiles<io_t>(p, c, l);

@@ -104,6 +104,113 @@ __device__ __forceinline__ float act_slope(float z)
     }
 }
 
+// The same for results that are rounded to bfloat16, two at a time.  R has a polynomial of degree 7 in 1 / (1 + 0.315 a) (2^-21), and the
+// exponent's rounding errors are left alone: 2^-20 of the result where |z| < 4, 2^-15 at |z| = 13, where gelu(z) is 10^-37.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 exp2_of(float2 y)
+{
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+    return e;
+}
+__device__ __forceinline__ float2 reciprocal(float2 x)
+{
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+    return r;
+}
+// a = min(|z|, 40), E and -R
+__device__ __forceinline__ void gelu_parts(float2 z, float2 &a, float2 &E, float2 &minus_R)
+{
+    a = make_float2(min_nan(fabsf(z.x), 40.f), min_nan(fabsf(z.y), 40.f));
+    E = exp2_of(io::mul2(io::mul2(a, a), both(-0.72134752f)));
+    const float2 t = reciprocal(io::fma2(a, both(0.315f), both(1.f)));
+    float2 q = io::fma2(t, both(-0.03444384038448334f), both(0.12904778122901917f));
+    q = io::fma2(t, q, both(-0.1252608746290207f));
+    q = io::fma2(t, q, both(-0.0051743402145802975f));
+    q = io::fma2(t, q, both(-0.10147497057914734f));
+    q = io::fma2(t, q, both(-0.11121252179145813f));
+    q = io::fma2(t, q, both(-0.12581877410411835f));
+    q = io::fma2(t, q, both(-0.12566231191158295f));
+    minus_R = io::mul2(q, t);
+}
+__device__ __forceinline__ void silu_parts(float2 z, float2 &a, float2 &e, float2 &r)
+{
+    a = make_float2(min_nan(fabsf(z.x), 120.f), min_nan(fabsf(z.y), 120.f));
+    e = exp2_of(io::mul2(a, both(-1.44269504f)));
+    r = reciprocal(io::add2(e, both(1.f)));
+}
+template <prism_activation ACT>
+__device__ __forceinline__ float2 act_value(float2 z)
+{
+    float2 a, e, r;
+    if constexpr (ACT == PRISM_ACT_GELU) {
+        gelu_parts(z, a, e, r);
+        return io::fma2(io::mul2(a, e), r, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+    } else if constexpr (ACT == PRISM_ACT_SILU) {
+        silu_parts(z, a, e, r);
+        return io::mul2(r, make_float2(z.x > 0.f ? z.x : -a.x * e.x, z.y > 0.f ? z.y : -a.y * e.y));
+    } else {
+        return z;
+    }
+}
+template <prism_activation ACT>
+__device__ __forceinline__ float2 act_slope(float2 z)
+{
+    float2 a, e, r;
+    if constexpr (ACT == PRISM_ACT_GELU) {
+        gelu_parts(z, a, e, r);
+        const float2 d = io::mul2(e, io::fma2(a, both(0.39894228f), r));  // minus what the precise form calls d
+        return make_float2(z.x > 0.f ? 1.f + d.x : -d.x, z.y > 0.f ? 1.f + d.y : -d.y);
+    } else if constexpr (ACT == PRISM_ACT_SILU) {
+        silu_parts(z, a, e, r);
+        const float2 p = io::mul2(e, r), d = io::mul2(io::mul2(a, p), r);
+        return make_float2(z.x > 0.f ? r.x + d.x : p.x - d.x, z.y > 0.f ? r.y + d.y : p.y - d.y);
+    } else {
+        return both(1.f);
+    }
+}
+// ... of N values, as precise as the type that they go to
+template <typename io_t, prism_activation ACT, int N>
+__device__ __forceinline__ void to_values(float (&f)[N])
+{
+    if constexpr (ACT != PRISM_ACT_NONE) {
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            if constexpr (sizeof(io_t) == 2) {
+                const float2 v = act_value<ACT>(make_float2(f[c], f[c + 1]));
+                f[c] = v.x, f[c + 1] = v.y;
+            } else {
+                f[c] = act_value<ACT>(f[c]), f[c + 1] = act_value<ACT>(f[c + 1]);
+            }
+        }
+    }
+}
+template <typename io_t, prism_activation ACT, int N>
+__device__ __forceinline__ void times_slopes(float (&f)[N], const float (&z)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        if constexpr (sizeof(io_t) == 2) {
+            const float2 v = io::mul2(make_float2(f[c], f[c + 1]), act_slope<ACT>(make_float2(z[c], z[c + 1])));
+            f[c] = v.x, f[c + 1] = v.y;
+        } else {
+            f[c] *= act_slope<ACT>(z[c]), f[c + 1] *= act_slope<ACT>(z[c + 1]);
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void plus(float (&f)[N], const float (&g)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const float2 v = io::add2(make_float2(f[c], f[c + 1]), make_float2(g[c], g[c + 1]));
+        f[c] = v.x, f[c + 1] = v.y;
+    }
+}
+
 // ---- the product at hand -----------------------------------------------------------------------------
 template <typename io_t>
 struct Params {
@@ -136,16 +243,17 @@ template <typename io_t, LinearOp OP, bool SOFT, int BN, bool PAIR>
 struct Layout {
     static constexpr int PARTS = sizeof(io_t) == 4 ? 3 : 1;
     static constexpr bool GROUPED = PARTS == 3 || OP == LinearOp::weights;  // sums go on in registers
-    static constexpr uint32_t A_PART = BM * 128, B_PART = (PAIR ? BN / 2 : BN) * 128, STAGE = PARTS * (A_PART + B_PART);
-    static constexpr int STAGES = 196608 / STAGE;
-    static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging of outputs: 32 x 32 values of 4 bytes, or two times 2 bytes
+    static constexpr uint32_t A_PART = BM * 128, B_PART = ((PAIR ? BN / 2 : BN) + 63) / 64 * 64 * 128, STAGE = PARTS * (A_PART + B_PART);
+    // the addends' pieces of a warp, two on their way
+    static constexpr bool INCOMING = !SOFT && OP != LinearOp::weights;
+    static constexpr int STAGES = (INCOMING && STAGE <= 32768 ? 163840 : 196608) / STAGE - (INCOMING && STAGE > 32768 ? 1 : 0);
+    static constexpr uint32_t OUT_WARP = INCOMING ? 8192 : 4096;  // a warp's staging: outputs of 32 x 32 values of 4 bytes, or two times 2 bytes; addends
     static constexpr uint32_t OFF_OUT = STAGES * STAGE;
     static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 0 : kEpilogueWarps * OUT_WARP) + 1024;  // + alignment slack
     static constexpr int THREADS = 128 + 32 * kEpilogueWarps + (SOFT ? 32 * kLoaderWarps : 0);
     static constexpr int kColumns = SOFT || OP != LinearOp::weights || BN == 256 ? 512 : 256;  // of tensor memory
     // registers handed over to the warps that finish tiles, from the issuing ones
     static constexpr int kLaunchRegs = SOFT ? 128 : 168, kIssueRegs = SOFT ? 40 : 56, kEpilogueRegs = SOFT ? 168 : 224;
-    static constexpr bool HAND_OVER = SOFT || GROUPED;
     static_assert(128 * kIssueRegs + 32 * kEpilogueWarps * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLaunchRegs : 0) <= THREADS * kLaunchRegs, "registers");
     static_assert(STAGES >= 2 && SMEM + (OP == LinearOp::weights ? 3072 : 1024) <= 232448 && OFF_OUT % 1024 == 0, "layout");
 };
@@ -338,6 +446,21 @@ struct Patch {
             for (int r = 0; r < rows; ++r, to += J) io::st(to, t[r * 32 + (lane ^ r)]);
         }
     }
+    // of a bf16 piece that came by TMA, this lane's row
+    static __device__ __forceinline__ void from_tile(const uint8_t *tile, int lane, float (&f)[32])
+    {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                io::Unit<T, 8> x;
+                x.w = *reinterpret_cast<const uint4 *>(tile + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4));
+                float g[8];
+                x.get(g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[8 * u + e] = g[e];
+            }
+        }
+    }
     // by TMA: a piece of 32 rows x 32 columns, swizzled as the tensor map says (64 bytes a row: 16-byte chunk XOR (row / 2) mod 4;
     // 128 bytes a row: XOR row mod 8); with two buffers one piece leaves while the next is written
     static __device__ __forceinline__ void put_tiled(const CUtensorMap *tm, uint8_t *stage, int &turn, int row0, int j0, int lane,
@@ -457,7 +580,7 @@ __device__ __forceinline__ float remote<float>(uint32_t addr, int cta)
 template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT, bool PAIR>
 __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_out,
-                const __grid_constant__ CUtensorMap tm_pre, const Params<io_t> p, const Waits wt)
+                const __grid_constant__ CUtensorMap tm_pre, const __grid_constant__ CUtensorMap tm_add, const Params<io_t> p, const Waits wt)
 {
     using L = Layout<io_t, OP, SOFT, BN, PAIR>;
     using out_t = std::conditional_t<OP == LinearOp::weights, float, io_t>;
@@ -466,7 +589,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint32_t tmem_base_s;
-    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], summed[STAGES], acc_full[2], acc_empty[2];
+    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], summed[STAGES], acc_full[2], acc_empty[2], incoming[2 * kEpilogueWarps];
     __shared__ int abort_s;
     __shared__ __align__(16) float column_sums[OP == LinearOp::weights ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
     constexpr int CTAS = PAIR ? 2 : 1, TM = CTAS * BM;  // of a tile, and its rows
@@ -514,7 +637,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         }
         if constexpr (B_MN) {
 #pragma unroll
-            for (int h = 0; h < OWN / 64; ++h) box(at + L::A_PART + h * kPanel, &tm_b, j0 + 64 * h, b * BK);
+            for (int h = 0; h < (OWN + 63) / 64; ++h) box(at + L::A_PART + h * kPanel, &tm_b, j0 + 64 * h, b * BK);
         } else {
 #pragma unroll
             for (int h = 0; h < OWN / 128; ++h) box(at + L::A_PART + h * 16384, &tm_b, b * BK, j0 + 128 * h);
@@ -529,6 +652,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             mbar_init(smem_u32(&freed[s]), 1);
             mbar_init(smem_u32(&summed[s]), 2);
         }
+        for (int w = 0; w < 2 * kEpilogueWarps; ++w) mbar_init(smem_u32(&incoming[w]), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
             mbar_init(smem_u32(&acc_empty[s]), CTAS * kEpilogueWarps);
@@ -558,7 +682,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     };
     long long issued = 0;  // the issuing threads' counts of steps, for the drain
     if (warp < 4) {
-        if constexpr (L::HAND_OVER) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kIssueRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kIssueRegs));
         // Whole warps run these loops, so that their counters and descriptors stay in uniform registers, and one lane issues.  Each
         // looks at its next barrier while it issues: shared memory, busy with operands, takes some hundred cycles to answer
         // (4096 x 4096 x 4096 took 108 us with one thread a loop and two looks between a block's products and the next).
@@ -723,7 +847,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         if constexpr (OP == LinearOp::weights)
             *reinterpret_cast<float4 *>(&column_sums[thread / 32][4 * lane]) = make_float4(column[0], column[1], column[2], column[3]);
     } else {  // ---- what follows: lane quarter warp % 4, columns of half (warp - 4) / 4 ----
-        if constexpr (L::HAND_OVER) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpilogueRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpilogueRegs));
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t from = ((uint32_t)(quarter * 32) << 16) + half * HALF;
         uint8_t *stage = sm + L::OFF_OUT + (warp - 4) * L::OUT_WARP;
@@ -739,6 +863,50 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                 if constexpr (PAIR) mbar_arrive_at(address_in(smem_u32(&acc_empty[buf]), crank & ~1));
                 else mbar_arrive(smem_u32(&acc_empty[buf]));
             }
+        };
+        // Addends (pre_in, then add) come by TMA where rows are whole units: a warp's pieces of 32 x 32 in the order in which they are used,
+        // two on their way, into the next tile too.
+        const bool has_pre = OP == LinearOp::backward && p.act != PRISM_ACT_NONE, has_add = p.add != nullptr;
+        const int kinds = has_pre + has_add;
+        const bool by_tma = L::INCOMING && !SPLIT && p.tiled && kinds > 0;
+        uint32_t asked = 0, taken = 0;
+        int ask_tile = 0, ask_piece = 0, ask_kind = 0, ask_i0 = 0, ask_j = 0, ask_pieces = 0;
+        auto pieces_of = [&](int i0, int j0) {  // of the warp's columns, those that the matrix has
+            return i0 + quarter * 32 < p.I ? max(0, min(HALF / 32, (p.J - j0 - half * HALF + 31) / 32)) : 0;
+        };
+        auto look = [&] {  // the first tile from ask_tile on with pieces
+            for (; ask_tile < my_tiles; ++ask_tile) {
+                int j0;
+                tile_at(ask_tile, ask_i0, j0);
+                ask_j = j0 + half * HALF;
+                ask_pieces = pieces_of(ask_i0, j0);
+                if (ask_pieces > 0) return;
+            }
+        };
+        auto ask = [&] {
+            if (ask_tile >= my_tiles) return;
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(&incoming[2 * (warp - 4) + (asked & 1)]);
+                mbar_expect_tx(bar, 2048);
+                tma_load_2d(smem_u32(stage + 4096 + (asked & 1) * 2048), has_pre && ask_kind == 0 ? &tm_pre : &tm_add, bar, ask_j + 32 * ask_piece,
+                            ask_i0 + quarter * 32);
+            }
+            ++asked;
+            if (++ask_kind == kinds) {
+                ask_kind = 0;
+                if (++ask_piece == ask_pieces) ask_piece = 0, ++ask_tile, look();
+            }
+        };
+        if (by_tma) look(), ask(), ask();
+        auto take = [&](float (&f)[32]) {  // the next piece; false if it does not come
+            const uint32_t slot = taken & 1;
+            const bool here = __all_sync(0xffffffffu, mbar_wait(smem_u32(&incoming[2 * (warp - 4) + slot]), (taken >> 1) & 1, wt.ns));
+            ++taken;
+            if (!here) return false;
+            Patch<io_t>::from_tile(stage + 4096 + slot * 2048, lane, f);
+            __syncwarp();
+            ask();
+            return true;
         };
         for (int i = 0; i < my_tiles && ok; ++i) {
             int i0, j0;
@@ -809,31 +977,33 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                         const int j = j0 + half * HALF + ch * 32;
                         const bool inside = rows > 0 && j < p.J;
                         float f[32], other[32];
-                        if (inside && OP == LinearOp::backward && ACT != PRISM_ACT_NONE)
-                            Patch<io_t>::get(p.pre_in + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
+                        auto addend = [&](const io_t *from) {
+                            if (by_tma) {
+                                if (ok) ok = take(other);
+                            } else {
+                                Patch<io_t>::get(from + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
+                            }
+                        };
+                        if (inside && has_pre) addend(p.pre_in);
                         piece(ch, f);
                         if (!inside) continue;
                         if constexpr (OP == LinearOp::forward) {
                             if (p.bias) {
                                 float bias[32];
                                 load_row<io_t, 32>(p.bias, j, p.J, true, bias);
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) f[c] += bias[c];
+                                plus(f, bias);
                             }
                             if (p.pre_out) {
                                 if (p.tiled) Patch<io_t>::put_tiled(&tm_pre, stage, turn, r0, j, lane, f);
                                 else Patch<io_t>::put_rows(p.pre_out + (size_t)r0 * p.J, p.J, rows, j, flat, lane, f);
                             }
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) f[c] = act_value<ACT>(f[c]);
+                            to_values<io_t, ACT>(f);
                         } else if constexpr (OP == LinearOp::backward && ACT != PRISM_ACT_NONE) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) f[c] *= act_slope<ACT>(other[c]);
+                            times_slopes<io_t, ACT>(f, other);
                         }
-                        if (p.add) {
-                            Patch<io_t>::get(p.add + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) f[c] += other[c];
+                        if (has_add) {
+                            addend(p.add);
+                            plus(f, other);
                         }
                         if (p.tiled) Patch<out_t>::put_tiled(&tm_out, stage, turn, r0, j, lane, f);
                         else Patch<out_t>::put_rows((out_t *)p.out + (size_t)r0 * p.J, p.J, rows, j, flat, lane, f);
@@ -842,6 +1012,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             }
         }
         if (!SPLIT && p.tiled) bulk_wait_read();  // before the staging goes
+        if (by_tma) {  // after an expired wait: the pieces asked for land before the CTA exits
+            if (!ok && lane == 0) give_up();
+            for (; !ok && taken < asked; ++taken) (void)mbar_wait(smem_u32(&incoming[2 * (warp - 4) + (taken & 1)]), (taken >> 1) & 1, 1000000000ull);
+        }
     }
     // drain: after an expired wait, the copies and products in flight land before the CTA exits
     __syncthreads();
@@ -868,8 +1042,8 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         const bool whole = (long long)p.J * sizeof(out_t) % 16 == 0;
         with_activation(p.act, [&](auto act) {
             constexpr prism_activation ACT = decltype(act)::value;
-            for (int e = r_from * (BN / 128) + warp; e < r_to * (BN / 128); e += L::THREADS / 32) {
-                const int row = e / (BN / 128), unit = e % (BN / 128) * 32 + lane, j = j0 + 4 * unit;
+            for (int e = r_from * (BN / 4) + tid; e < r_to * (BN / 4); e += L::THREADS) {
+                const int row = e / (BN / 4), unit = e % (BN / 4), j = j0 + 4 * unit;
                 const uint32_t at = sbase + row * BN * 4 + ((unit ^ (row & 7)) << 4);
                 float f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -921,17 +1095,14 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                             for (int x = 0; x < 4; ++x) f[x] += g[x];
                         }
                         if (p.pre_out) put(p.pre_out + line);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) f[x] = act_value<ACT>(f[x]);
+                        to_values<io_t, ACT>(f);
                     } else if constexpr (ACT != PRISM_ACT_NONE) {
                         four(p.pre_in + line, g);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) f[x] *= act_slope<ACT>(g[x]);
+                        times_slopes<io_t, ACT>(f, g);
                     }
                     if (p.add) {
                         four(p.add + line, g);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) f[x] += g[x];
+                        plus(f, g);
                     }
                     put((io_t *)p.out + line);
                 }
@@ -975,7 +1146,7 @@ cudaError_t launch_tiles(Params<io_t> p, int splits, const TokenLaunch &l)
     using L = Layout<io_t, OP, SOFT, BN, PAIR>;
     constexpr bool A_MN = OP == LinearOp::weights, B_MN = OP != LinearOp::forward;
     constexpr int OUT = OP == LinearOp::weights ? 4 : (int)sizeof(io_t);
-    CUtensorMap ma = {}, mb = {}, mo = {}, mp = {};
+    CUtensorMap ma = {}, mb = {}, mo = {}, mp = {}, md = {};
     if (!SOFT) {  // bf16
         const bool a = A_MN ? encode(&ma, 2, p.a, p.I, p.K, 64, BK) : encode(&ma, 2, p.a, p.K, p.I, BK, BM);
         const bool b = B_MN ? encode(&mb, 2, p.b, p.J, p.K, 64, BK) : encode(&mb, 2, p.b, p.K, p.J, BK, 128);
@@ -984,7 +1155,9 @@ cudaError_t launch_tiles(Params<io_t> p, int splits, const TokenLaunch &l)
     p.tiled = (long long)p.J * OUT % 16 == 0;
     if (!SPLIT && p.tiled) {
         if (!encode(&mo, OUT, p.out, p.J, p.I, 32, 32)) return cudaErrorInvalidValue;
-        if (p.pre_out && !encode(&mp, OUT, p.pre_out, p.J, p.I, 32, 32)) return cudaErrorInvalidValue;
+        const void *pre = p.pre_out ? (const void *)p.pre_out : p.pre_in;
+        if (pre && !encode(&mp, OUT, pre, p.J, p.I, 32, 32)) return cudaErrorInvalidValue;
+        if (p.add && !encode(&md, OUT, p.add, p.J, p.I, 32, 32)) return cudaErrorInvalidValue;
     }
     p.splits = splits;
     constexpr int CTAS = PAIR ? 2 : 1;
@@ -1001,7 +1174,7 @@ cudaError_t launch_tiles(Params<io_t> p, int splits, const TokenLaunch &l)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = SPLIT || PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tile_kernel<io_t, OP, SOFT, BN, SPLIT, PAIR>, ma, mb, mo, mp, p, wt);
+    return cudaLaunchKernelEx(&cfg, tile_kernel<io_t, OP, SOFT, BN, SPLIT, PAIR>, ma, mb, mo, mp, md, p, wt);
 }
 
 template <typename io_t, LinearOp OP, bool SOFT, int BN, bool SPLIT, bool PAIR>
@@ -1015,6 +1188,7 @@ struct Cut {
     bool soft, split, pair;
     int bn, splits;
 };
+int clusters_at_once(int ctas);  // of so many CTAs, one an SM; after weights_prepare()
 template <typename io_t>
 cudaError_t forward_tiles(const Params<io_t> &p, const Cut &c, const TokenLaunch &l);
 template <typename io_t>

@@ -8,7 +8,9 @@ template <>
 cudaError_t weights_tiles<__nv_bfloat16>(const Params<__nv_bfloat16> &p, const Cut &c, const TokenLaunch &l)
 {
     if (c.soft) return launch_tiles<__nv_bfloat16, LinearOp::weights, true, 128, true, false>(p, c.splits, l);
-    if (c.pair) return launch_tiles<__nv_bfloat16, LinearOp::weights, false, 256, true, true>(p, c.splits, l);
+    if (c.pair)
+        return c.bn == 256 ? launch_tiles<__nv_bfloat16, LinearOp::weights, false, 256, true, true>(p, c.splits, l)
+                           : launch_tiles<__nv_bfloat16, LinearOp::weights, false, 192, true, true>(p, c.splits, l);
     return c.bn == 256 ? launch_tiles<__nv_bfloat16, LinearOp::weights, false, 256, true, false>(p, c.splits, l)
                        : launch_tiles<__nv_bfloat16, LinearOp::weights, false, 128, true, false>(p, c.splits, l);
 }
@@ -19,13 +21,32 @@ cudaError_t weights_tiles<float>(const Params<float> &p, const Cut &c, const Tok
     return launch_tiles<float, LinearOp::weights, true, 128, true, false>(p, c.splits, l);
 }
 
+namespace {
+int at_once[9];  // the same on every device that the library runs on
+}
+
+int clusters_at_once(int ctas) { return at_once[ctas]; }
+
 cudaError_t weights_prepare()
 {
     cudaError_t e = prepare_tiles<__nv_bfloat16, LinearOp::weights, false, 256, true, true>();
+    if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::weights, false, 192, true, true>();
     if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::weights, false, 256, true, false>();
     if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::weights, false, 128, true, false>();
     if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::weights, true, 128, true, false>();
     if (e == cudaSuccess) e = prepare_tiles<float, LinearOp::weights, true, 128, true, false>();
+    using L = Layout<__nv_bfloat16, LinearOp::weights, false, 256, false>;
+    for (int ctas = 1; ctas <= 8 && e == cudaSuccess && at_once[8] == 0; ++ctas) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas), cfg.blockDim = dim3(L::THREADS), cfg.dynamicSmemBytes = L::SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at, cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, tile_kernel<__nv_bfloat16, LinearOp::weights, false, 256, true, false>, &cfg);
+        at_once[ctas] = n > 0 ? n : 1;
+    }
     return e;
 }
 

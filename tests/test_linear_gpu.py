@@ -274,3 +274,51 @@ def test_streams_graphs_and_equal_bits(io):
         for a, c in zip(first, held):
             assert torch.equal(a, c)
         t.last_device_status()
+
+
+@pytest.mark.parametrize("M,N,K", [(5000, 2056, 136), (4608, 2304, 64), (9000, 1000, 520)])
+def test_many_tiles(M, N, K):
+    """Tiles that two SMs share and CTAs that finish several, with last rows and columns that fill a tile in part."""
+    x, W, b, r, pre, dy, ds = tensors("bf16", 17, (M, K), (N, K), (N,), (M, N), (M, N), (M, K), (M, N))
+    W *= K ** -0.5
+    X, WW, bb, rr, P, D, S = (f64(t) for t in (x, W, b, r, pre, dy, ds))
+    with B.Tokens(M, 64, 64) as t:
+        out = t.linear(x, W, bias=b, activation="gelu", residual=r, want=("y", "pre"))
+        # the same sizes for the gradient: its output is [M, N] too, its sum runs over K
+        dx = t.linear_backward(x, W.t().contiguous(), activation="silu", pre=pre, dsum=ds)
+        g = t.linear_weight_backward(ds, x, want=("dW", "dbias"))
+        torch.cuda.synchronize()
+        t.last_device_status()
+    z, y = O.linear(X, WW, bb, "gelu", rr)
+    e = product_error("bf16", X, WW.T, np.abs(bb))
+    close(out["pre"], z, e, "bf16")
+    close(out["y"], y, 1.13 * e + 2.0 ** -19 * np.abs(O.act_value("gelu", z)) + 2.0 ** -126, "bf16")
+    plain, ref = O.linear_backward(X, WW.T, "none", None, None), O.linear_backward(X, WW.T, "silu", P, S)
+    slope = np.abs(O.act_slope("silu", P))
+    close(dx, ref, slope * product_error("bf16", X, WW.T) + 2.0 ** -19 * np.abs(plain) * np.maximum(slope, np.abs(P) * np.exp(-np.abs(P))), "bf16")
+    dW, db = O.linear_weight_backward(S, X)
+    close(g["dW"], dW, product_error("bf16", S.T, X), "f32")
+    close(g["dbias"], db, product_error("bf16", S.T, np.ones((M, 1)))[:, 0], "f32")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(8, 64, 64), (100, 136, 1024), (2500, 2304, 256), (300, 257, 65)])
+def test_an_expired_wait_is_reported(io, M, N, K):
+    """A bound of one nanosecond lets the waits of the tile kernels run out: the call returns, the status says so, and the next
+    call with the bound as it was is right."""
+    x, W, dy, ds = tensors(io, 19, (M, K), (N, K), (M, N), (M, K))
+    with B.Tokens(M, 64, 64, io=io) as t:
+        ref = t.linear(x, W)["y"], t.linear_backward(dy, W, dsum=ds), t.linear_weight_backward(dy, x)["dW"]
+        t.set_option(B.PRISM_OPT_WAIT_NS, 1)
+        for call in (lambda: t.linear(x, W, residual=dy), lambda: t.linear_backward(dy, W, activation="gelu", pre=x, dsum=ds), lambda: t.linear_weight_backward(dy, x, want=("dW", "dbias"))):
+            call()
+            torch.cuda.synchronize()
+            try:
+                t.last_device_status()
+            except B.PrismError as e:
+                assert e.status == B.PRISM_ERR_TIMEOUT
+        t.set_option(B.PRISM_OPT_WAIT_NS, 0)
+        again = t.linear(x, W)["y"], t.linear_backward(dy, W, dsum=ds), t.linear_weight_backward(dy, x)["dW"]
+        torch.cuda.synchronize()
+        t.last_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(ref, again))
