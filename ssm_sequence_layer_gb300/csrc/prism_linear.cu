@@ -48,7 +48,9 @@ cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
             }
         };
         consider(false, 128, sizeof(io_t) == 4 ? 3000 : c.soft ? 1500 : 540);
-        if (!c.soft) consider(false, 256, 800), consider(true, 256, 560), consider(true, 192, 430);
+        // the sums over rows need tensor memory beside the accumulators, which tiles of 256 columns leave none of
+        if (!c.soft) consider(true, 192, 430);
+        if (!c.soft && !p.dbias) consider(false, 256, 800), consider(true, 256, 560);
     } else {
         while (c.splits < 8 && 2 * c.splits <= blocks && blocks >= 8 && tiles(BM, 128) <= clusters_at_once(2 * c.splits)) c.splits *= 2;
         c.split = c.splits > 1;

@@ -249,9 +249,10 @@ struct Layout {
     static constexpr int STAGES = (INCOMING && STAGE <= 32768 ? 163840 : 196608) / STAGE - (INCOMING && STAGE > 32768 ? 1 : 0);
     static constexpr uint32_t OUT_WARP = INCOMING ? 8192 : 4096;  // a warp's staging: outputs of 32 x 32 values of 4 bytes, or two times 2 bytes; addends
     static constexpr uint32_t OFF_OUT = STAGES * STAGE;
-    static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 0 : kEpilogueWarps * OUT_WARP) + 1024;  // + alignment slack
+    static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 2048 : kEpilogueWarps * OUT_WARP) + 1024;  // + alignment slack
     static constexpr int THREADS = 128 + 32 * kEpilogueWarps + (SOFT ? 32 * kLoaderWarps : 0);
-    static constexpr int kColumns = SOFT || OP != LinearOp::weights || BN == 256 ? 512 : 256;  // of tensor memory
+    static constexpr int kColumns = 512;  // of tensor memory: two accumulators, and two for the small products or the sums over rows
+    static constexpr int SUMS = OP == LinearOp::weights && !SOFT && 2 * BN + 32 <= kColumns ? 2 * BN : 0;
     // registers handed over to the warps that finish tiles, from the issuing ones
     static constexpr int kLaunchRegs = SOFT ? 128 : 168, kIssueRegs = SOFT ? 40 : 56, kEpilogueRegs = SOFT ? 168 : 224;
     static_assert(128 * kIssueRegs + 32 * kEpilogueWarps * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLaunchRegs : 0) <= THREADS * kLaunchRegs, "registers");
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint32_t tmem_base_s;
-    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], summed[STAGES], acc_full[2], acc_empty[2], incoming[2 * kEpilogueWarps];
+    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2], incoming[2 * kEpilogueWarps];
     __shared__ int abort_s;
     __shared__ __align__(16) float column_sums[OP == LinearOp::weights ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
     constexpr int CTAS = PAIR ? 2 : 1, TM = CTAS * BM;  // of a tile, and its rows
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         i0 = (int)(t % tiles_i) * TM + in_tile * BM;
         j0 = (int)(t / tiles_i) * BN;
     };
-    // the sums over dy's rows: two warps add them up from shared memory once the products have read it, or the loaders from their registers
+    // the sums over dy's rows: products with ones, 16 columns beside a group's accumulator, or the loaders' registers
     bool sums = false;
     if constexpr (OP == LinearOp::weights) {
         int i0, j0;
@@ -650,7 +651,6 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), SOFT ? kLoaderWarps : 1);
             mbar_init(smem_u32(&freed[s]), 1);
-            mbar_init(smem_u32(&summed[s]), 2);
         }
         for (int w = 0; w < 2 * kEpilogueWarps; ++w) mbar_init(smem_u32(&incoming[w]), 1);
         for (int s = 0; s < 2; ++s) {
@@ -665,6 +665,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             for (int s = 0; s < early; ++s) load_block(s, b_from + s, i0, j0);
         }
         if (!SPLIT && p.tiled) prefetch_tmap(&tm_out);
+    }
+    if (L::SUMS > 0 && warp >= 4 && warp < 8) {  // 16 rows of ones (8 would do where two CTAs bring in half each)
+        *reinterpret_cast<uint4 *>(sm + L::OFF_OUT + (tid - 128) * 16) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        fence_async_smem();
     }
     if (warp == 0) {
         if constexpr (PAIR) tmem_alloc_pair(smem_u32(&tmem_base_s), L::kColumns);
@@ -700,10 +704,6 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                         if (one) give_up();
                         break;
                     }
-                }
-                if (sums && round > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&summed[s]), (round - 1) & 1, wt.ns))) {
-                    if (one) give_up();
-                    break;
                 }
                 if (s == 0 && __any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
                 const int next = s + 1 == STAGES ? 0 : s + 1;
@@ -758,6 +758,14 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                                 for (int k = 0; k < BK / 16; ++k)
                                     product(pa + pb == 0 ? d : small, da + (uint64_t)(pa * L::A_PART >> 4) + SA * k, db + (uint64_t)(pb * L::B_PART >> 4) + SB * k,
                                             ID, pa + pb == 0 ? in_group > 0 || k > 0 : b > b_from || pa > 0 || pb > 1 || k > 0);
+                        if constexpr (OP == LinearOp::weights && !SOFT && L::SUMS > 0) {
+                            if (sums) {
+                                const uint64_t ones = sdesc(sbase + L::OFF_OUT, 16, 1024);
+#pragma unroll
+                                for (int k = 0; k < BK / 16; ++k)
+                                    product(tmem + L::SUMS + 16 * buf, da + SA * k, ones + 2 * k, idesc_bf16(TM, 16, A_MN, 0), in_group > 0 || k > 0);
+                            }
+                        }
                         done(&freed[s]);
                         if (last) done(&acc_full[buf]);
                     }
@@ -768,33 +776,6 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                     s = next, round = next_round;
                 }
             }
-        } else if (!SOFT && sums && warp >= 2) {  // ---- sums over dy's rows, a pair of columns a lane ----
-            int s = 0;
-            uint32_t round = 0;
-            float2 sum = make_float2(0.f, 0.f);
-            const uint8_t *panel = sm + (warp - 2) * kPanel + (lane & 3) * 4;
-            for (long long g = 0; g < total; ++g) {
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&freed[s]), round & 1, wt.ns))) {
-                    if (lane == 0) give_up();
-                    break;
-                }
-                if (__any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
-                float2 part[4] = {};
-#pragma unroll 16
-                for (int r = 0; r < BK; ++r) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(panel + s * L::STAGE + r * 128 + (((lane >> 2) ^ r) & 7) * 16);
-                    float a, b;
-                    io::Unit<__nv_bfloat16, 8>::two(w, a, b);
-                    part[r & 3] = io::add2(part[r & 3], make_float2(a, b));
-                }
-                sum = io::add2(sum, io::add2(io::add2(part[0], part[1]), io::add2(part[2], part[3])));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&summed[s]));
-                if (++s == STAGES) s = 0, ++round;
-            }
-            if constexpr (OP == LinearOp::weights)
-                *reinterpret_cast<float2 *>(&column_sums[0][(warp - 2) * 64 + 2 * lane]) = sum;
-            asm volatile("bar.arrive 1, %0;" ::"n"(64 + 32 * kEpilogueWarps) : "memory");  // nothing is read here any more
         }
     } else if (SOFT && warp >= 4 + kEpilogueWarps) {  // ---- operands through registers ----
         const int thread = tid - 128 - 32 * kEpilogueWarps;
@@ -912,6 +893,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             int i0, j0;
             tile_at(i, i0, j0);
             float2 sum[GROUPED ? HALF / 2 : 1];
+            float over_rows = 0.f;
             uint32_t buf = 0;
 #pragma unroll 1
             for (int g = 0; g < groups; ++g, ++acc) {
@@ -921,19 +903,28 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                 fence_after_sync();
                 if constexpr (GROUPED) {
                     auto add = [&](uint32_t at, bool first) {
+                        uint32_t r[2][32];
+                        ld_issue(at, r[0]);
 #pragma unroll
-                        for (int c = 0; c < HALF; c += 32) {
-                            uint32_t r[32];
-                            ld_issue(at + c, r);
-                            ld_wait(r);
+                        for (int c = 0; c < HALF / 32; ++c) {  // the next columns load while these are added
+                            ld_wait(r[c & 1]);
+                            if (c + 1 < HALF / 32) ld_issue(at + 32 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
                             for (int q = 0; q < 16; ++q) {
-                                const float2 x = make_float2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1]));
-                                sum[c / 2 + q] = first ? x : io::add2(sum[c / 2 + q], x);
+                                const float2 x = make_float2(__uint_as_float(r[c & 1][2 * q]), __uint_as_float(r[c & 1][2 * q + 1]));
+                                sum[16 * c + q] = first ? x : io::add2(sum[16 * c + q], x);
                             }
                         }
                     };
                     add(tmem + buf * BN + from, g == 0);
+                    if constexpr (L::SUMS > 0) {
+                        if (sums && half == 0) {
+                            uint32_t x;
+                            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(tmem + L::SUMS + 16 * buf + ((uint32_t)(quarter * 32) << 16)));
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x)::"memory");
+                            over_rows += __uint_as_float(x);
+                        }
+                    }
                     if (PARTS == 3 && g + 1 == groups) add(tmem + 2 * BN + (i & 1) * BN + from, false);
                     hand_back(buf);
                 }
@@ -956,8 +947,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                     if (ch + 1 == HALF / 32) hand_back(buf);
                 }
             };
+            if constexpr (L::SUMS > 0) {
+                if (half == 0) column_sums[0][quarter * 32 + lane] = over_rows;
+            }
             if constexpr (SPLIT) {  // every load has landed and every product has read it: their shared memory is free
-                if (!SOFT && sums) asm volatile("bar.sync 1, %0;" ::"n"(64 + 32 * kEpilogueWarps) : "memory");
                 const int row = quarter * 32 + lane;
 #pragma unroll
                 for (int ch = 0; ch < HALF / 32; ++ch) {
