@@ -13,8 +13,8 @@
 //
 // The tensor core cuts its sums off towards zero at each step of 16 terms, which costs long float32 results their last bits (sums over
 // 2048 terms in one accumulator: 2 10^-6 off, 256 terms: 3 10^-7, a plain float32 product 2 10^-7).  Where the outputs or the operands
-// are float32 an accumulator therefore holds four blocks at most, and the warps that finish a tile add it to sums in their
-// registers while the next four run into the other accumulator; the five small products of a float32 block have an
+// are float32 an accumulator therefore holds 512 terms at most (256 of float32), and the warps that finish a tile add it to sums in their
+// registers while the next ones run into the other accumulator; the five small products of a float32 block have an
 // accumulator of their own, whose steps cut off 2^-8 times less.
 #pragma once
 
@@ -235,8 +235,7 @@ struct Waits {
 };
 
 constexpr int BM = 128, BK = 64;
-constexpr int kEpilogueWarps = 8, kLoaderWarps = 4;
-constexpr int kGroup = 4;  // blocks that share an accumulator where its sums go on in registers
+constexpr int kEpilogueWarps = 8, kLoaderWarps = 8;
 constexpr uint32_t kPanel = BK * 128;  // an MN-major panel: 64 rows (of the sum) x 64 values
 
 template <typename io_t, LinearOp OP, bool SOFT, int BN, bool PAIR>
@@ -246,16 +245,20 @@ struct Layout {
     static constexpr uint32_t A_PART = BM * 128, B_PART = ((PAIR ? BN / 2 : BN) + 63) / 64 * 64 * 128, STAGE = PARTS * (A_PART + B_PART);
     // the addends' pieces of a warp, two on their way
     static constexpr bool INCOMING = !SOFT && OP != LinearOp::weights;
-    static constexpr int STAGES = (INCOMING && STAGE <= 32768 ? 163840 : 196608) / STAGE - (INCOMING && STAGE > 32768 ? 1 : 0);
+    // SOFT: one stage, whose halves are filled and freed one by one, and raw values on their way for three halves
+    static constexpr int BLOCK = SOFT ? 32 : BK, RAWS = SOFT ? 3 : 0;
+    static constexpr uint32_t RAW = 32768, OFF_RAW = STAGE;
+    static constexpr int GROUP = PARTS == 3 ? 256 / BLOCK : 512 / BLOCK;  // blocks that share an accumulator where its sums go on in registers
+    static constexpr int STAGES = SOFT ? 2 : (INCOMING && STAGE <= 32768 ? 163840 : 196608) / STAGE - (INCOMING && STAGE > 32768 ? 1 : 0);
     static constexpr uint32_t OUT_WARP = INCOMING ? 8192 : 4096;  // a warp's staging: outputs of 32 x 32 values of 4 bytes, or two times 2 bytes; addends
-    static constexpr uint32_t OFF_OUT = STAGES * STAGE;
+    static constexpr uint32_t OFF_OUT = SOFT ? STAGE + RAWS * RAW : STAGES * STAGE;
     static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 2048 : kEpilogueWarps * OUT_WARP) + 1024;  // + alignment slack
     static constexpr int THREADS = 128 + 32 * kEpilogueWarps + (SOFT ? 32 * kLoaderWarps : 0);
     static constexpr int kColumns = 512;  // of tensor memory: two accumulators, and two for the small products or the sums over rows
     static constexpr int SUMS = OP == LinearOp::weights && !SOFT && 2 * BN + 32 <= kColumns ? 2 * BN : 0;
     // registers handed over to the warps that finish tiles, from the issuing ones
-    static constexpr int kLaunchRegs = SOFT ? 128 : 168, kIssueRegs = SOFT ? 40 : 56, kEpilogueRegs = SOFT ? 168 : 224;
-    static_assert(128 * kIssueRegs + 32 * kEpilogueWarps * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLaunchRegs : 0) <= THREADS * kLaunchRegs, "registers");
+    static constexpr int kLaunchRegs = SOFT ? 96 : 168, kIssueRegs = SOFT ? 40 : 56, kEpilogueRegs = SOFT ? 152 : 224, kLoaderRegs = 64;
+    static_assert(128 * kIssueRegs + 32 * kEpilogueWarps * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLoaderRegs : 0) <= THREADS * kLaunchRegs, "registers");
     static_assert(STAGES >= 2 && SMEM + (OP == LinearOp::weights ? 3072 : 1024) <= 232448 && OFF_OUT % 1024 == 0, "layout");
 };
 
@@ -279,68 +282,81 @@ __device__ __forceinline__ uint32_t leading(float a, float b)
 __device__ __forceinline__ float without_leading(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
 
 // ---- operands through registers ------------------------------------------------------------------------
-// A tile of R rows x C values of a row-major matrix, cut to (rows, cols), four values of a row a thread and step
-template <typename io_t, int R, int C>
-struct SoftTile {
-    static constexpr int GROUPS = R * C / 4, STEPS = GROUPS / (32 * kLoaderWarps) / 2, PER_ROW = C / 4;  // steps of half a tile
-    static constexpr int WORDS = sizeof(io_t) == 4 ? 4 : 2;
-    uint32_t v[STEPS][WORDS];
-
-    __device__ __forceinline__ void load(const io_t *base, long long ld, int r0, int rows, int c0, int cols, int thread, int half)
+// Half a stage of an operand: R rows x C values of a row-major matrix (128 x 32 along the sum, or 32 x 128 across it), cut to (rows, cols).
+// A thread copies four values of a row at a time into 16 bytes of its own, two halves ahead and without waiting for them
+// (cp.async: 16 bytes where rows are whole units, else words of 4, of which bfloat16 rows may start in the middle of one), and
+// later brings its values to the form that the tensor core reads.
+template <typename io_t, bool MN>
+struct SoftHalf {
+    static constexpr int C = MN ? 128 : 32, PER_ROW = C / 4, THREADS = 32 * kLoaderWarps, STEPS = 1024 / THREADS;
+    const io_t *base;
+    long long ld, last;  // last: elements of the matrix
+    int rows, cols, thread;
+    bool whole;
+    __device__ __forceinline__ SoftHalf(const io_t *base_, long long ld_, int rows_, int cols_, int thread_)
+        : base(base_), ld(ld_), last(ld_ * rows_), rows(rows_), cols(cols_), thread(thread_), whole(ld_ * sizeof(io_t) % 16 == 0)
+    {
+    }
+    static __device__ __forceinline__ uint32_t raw_of(uint32_t raw, int step, int thread) { return raw + (step * THREADS + thread) * 16; }
+    static __device__ __forceinline__ void copy(uint32_t to, const void *from, int bytes)
+    {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    }
+    __device__ __forceinline__ void ask(uint32_t raw, int r0, int c0) const
     {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            const int g = thread + (half * STEPS + i) * 32 * kLoaderWarps, r = r0 + g / PER_ROW, c = c0 + g % PER_ROW * 4;
-#pragma unroll
-            for (int w = 0; w < WORDS; ++w) v[i][w] = 0;
-            if (r >= rows || c >= cols) continue;
-            const io_t *p = base + (long long)r * ld + c;
-            if (c + 4 <= cols && ld % 4 == 0) {
-                if constexpr (WORDS == 4) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
-                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+            const int g = thread + i * THREADS, r = r0 + g / PER_ROW, c = c0 + g % PER_ROW * 4;
+            const uint32_t to = raw_of(raw, i, thread);
+            const bool in = r < rows && c < cols;
+            const long long at = in ? (long long)r * ld + c : 0;
+            if constexpr (sizeof(io_t) == 4) {
+                if (whole && (!in || c + 4 <= cols)) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(base + at), "r"(in ? 16 : 0) : "memory");
                 } else {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
-                    v[i][0] = x.x, v[i][1] = x.y;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) copy(to + 4 * e, base + (in && c + e < cols ? at + e : 0), in && c + e < cols ? 4 : 0);
                 }
             } else {
+                // the words that hold the four values; the matrix may end in the middle of one
+                const long long word = at & ~1ll;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < cols) {
-                        if constexpr (WORDS == 4) v[i][e] = __ldg(reinterpret_cast<const uint32_t *>(p + e));
-                        else v[i][e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p + e)) << (e % 2 * 16);
-                    }
+                for (int e = 0; e < 3; ++e) {
+                    const bool need = in && word + 2 * e < last && word + 2 * e < at + 4;
+                    copy(to + 4 * e, base + (need ? word + 2 * e : 0), need ? (word + 2 * e + 1 < last ? 4 : 2) : 0);
+                }
             }
         }
     }
-    // adds to the sums of the columns that this thread holds in every block (C = 128: the same four)
-    __device__ __forceinline__ void add_columns(float (&sums)[4]) const
+    // into half `half` of panels of 64 values, 128-byte swizzled; the parts of float32 are part_bytes apart.  sums: of the thread's columns
+    __device__ __forceinline__ void bring(uint8_t *to, uint32_t part_bytes, uint32_t raw, int half, int r0, int c0, bool add, float (&sums)[4]) const
     {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            if constexpr (WORDS == 4) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sums[e] += __uint_as_float(v[i][e]);
+            const int g = thread + i * THREADS, r = g / PER_ROW, c = g % PER_ROW * 4;
+            uint8_t *at = MN ? to + (c >> 6) * kPanel + sw128(r + 32 * half, c & 63) : to + sw128(r, c + 32 * half);
+            uint32_t x[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(raw_of(raw, i, thread)));
+            float f[4];
+            if constexpr (sizeof(io_t) == 2) {
+                const bool odd = (((long long)(r0 + r) * ld + c0 + c) & 1) && r0 + r < rows && c0 + c < cols;
+                uint32_t lo = odd ? __byte_perm(x[0], x[1], 0x5432) : x[0], hi = odd ? __byte_perm(x[1], x[2], 0x5432) : x[1];
+                const int n = cols - c0 - c;  // of the four, those that the row has
+                if (n < 4) {
+                    hi &= n < 3 ? 0u : 0xffffu;
+                    lo &= n < 1 ? 0u : n < 2 ? 0xffffu : ~0u;
+                }
+                *reinterpret_cast<uint2 *>(at) = make_uint2(lo, hi);
+                if (add) io::Unit<__nv_bfloat16, 8>::two(lo, f[0], f[1]), io::Unit<__nv_bfloat16, 8>::two(hi, f[2], f[3]);
             } else {
-                float a, b, c, d;
-                io::Unit<__nv_bfloat16, 8>::two(v[i][0], a, b), io::Unit<__nv_bfloat16, 8>::two(v[i][1], c, d);
-                sums[0] += a, sums[1] += b, sums[2] += c, sums[3] += d;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(x[e]);
             }
-        }
-    }
-    // into panels of 64 columns, 128-byte swizzled; the parts of float32 are part_bytes apart
-    __device__ __forceinline__ void store(uint8_t *to, uint32_t part_bytes, int thread, int half) const
-    {
+            if (add) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int g = thread + (half * STEPS + i) * 32 * kLoaderWarps, r = g / PER_ROW, c = g % PER_ROW * 4;
-            uint8_t *at = to + (c >> 6) * R * 128 + sw128(r, c & 63);
-            if constexpr (WORDS == 2) {
-                *reinterpret_cast<uint2 *>(at) = make_uint2(v[i][0], v[i][1]);
-            } else {
-                float f[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(v[i][e]);
+                for (int e = 0; e < 4; ++e) sums[e] += f[e];
+            }
+            if constexpr (sizeof(io_t) == 4) {
 #pragma unroll
                 for (int part = 0; part < 3; ++part) {
                     *reinterpret_cast<uint2 *>(at + part * part_bytes) = make_uint2(leading(f[0], f[1]), leading(f[2], f[3]));
@@ -597,14 +613,14 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int in_tile = PAIR ? (int)(blockIdx.x & 1) : 0;  // the cluster's CTAs are numbered as the grid's
     const bool leads = in_tile == 0;
-    const int tiles_i = (p.I + TM - 1) / TM, tiles_j = (p.J + BN - 1) / BN, blocks = (p.K + BK - 1) / BK;
+    const int tiles_i = (p.I + TM - 1) / TM, tiles_j = (p.J + BN - 1) / BN, blocks = (p.K + L::BLOCK - 1) / L::BLOCK;
     const long long tiles = (long long)tiles_i * tiles_j;
     const unsigned worker = blockIdx.x / CTAS, workers = gridDim.x / CTAS;
     const int my_tiles = SPLIT ? 1 : tiles > worker ? (int)((tiles - 1 - worker) / workers) + 1 : 0;
     const int rank = SPLIT ? (int)(worker % p.splits) : 0;
     const int b_from = SPLIT ? (int)((long long)rank * blocks / p.splits) : 0, b_to = SPLIT ? (int)((long long)(rank + 1) * blocks / p.splits) : blocks;
     const long long total = (long long)my_tiles * (b_to - b_from);
-    const int groups = GROUPED ? (b_to - b_from + kGroup - 1) / kGroup : 1;  // of a tile's blocks, an accumulator each
+    const int groups = GROUPED ? (b_to - b_from + L::GROUP - 1) / L::GROUP : 1;  // of a tile's blocks, an accumulator each
     const uint32_t sbase = smem_u32(sm), crank = PAIR ? cluster_rank() : 0;
     const uint32_t leader_full = PAIR ? address_in(smem_u32(&full[0]), crank & ~1) : smem_u32(&full[0]);
 
@@ -731,7 +747,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             bool ok = true, ready = false;
             for (int i = 0; i < my_tiles && ok; ++i) {
                 for (int b = b_from; b < b_to; ++b) {
-                    const int in_group = GROUPED ? (b - b_from) % kGroup : b - b_from;
+                    const int in_group = GROUPED ? (b - b_from) % L::GROUP : b - b_from;
                     const uint32_t buf = acc & 1;
                     if (in_group == 0 && acc >= 2) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_empty[buf]), ((acc - 2) >> 1) & 1, wt.ns));
                     if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), round & 1, wt.ns));
@@ -743,21 +759,22 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                     const int next = s + 1 == STAGES ? 0 : s + 1;
                     const uint32_t next_round = s + 1 == STAGES ? round + 1 : round;
                     const bool seen = mbar_test(smem_u32(&full[next]), next_round & 1);
-                    const uint32_t at = sbase + s * L::STAGE, bt = at + PARTS * L::A_PART, d = tmem + buf * BN;
+                    const uint32_t at = sbase + (SOFT ? 0 : s * L::STAGE), bt = at + PARTS * L::A_PART, d = tmem + buf * BN;
                     const uint64_t da = A_MN ? sdesc(at, kPanel, 1024) : sdesc(at, 16, 1024), db = B_MN ? sdesc(bt, kPanel, 1024) : sdesc(bt, 16, 1024);
                     constexpr uint64_t SA = (A_MN ? 2048 : 32) >> 4, SB = (B_MN ? 2048 : 32) >> 4;
                     constexpr uint32_t ID = idesc_bf16(TM, BN, A_MN, B_MN);
                     const uint32_t small = tmem + 2 * BN + (i & 1) * BN;  // the small products' accumulator, for the whole tile
-                    const bool last = b + 1 == b_to || (GROUPED && in_group + 1 == kGroup);
+                    const int from_k = SOFT ? s * L::BLOCK / 16 : 0;  // the half of the stage
+                    const bool last = b + 1 == b_to || (GROUPED && in_group + 1 == L::GROUP);
                     if (one) {
 #pragma unroll
                         for (int pa = 0; pa < PARTS; ++pa)
 #pragma unroll
                             for (int pb = 0; pa + pb < PARTS; ++pb)
 #pragma unroll
-                                for (int k = 0; k < BK / 16; ++k)
-                                    product(pa + pb == 0 ? d : small, da + (uint64_t)(pa * L::A_PART >> 4) + SA * k, db + (uint64_t)(pb * L::B_PART >> 4) + SB * k,
-                                            ID, pa + pb == 0 ? in_group > 0 || k > 0 : b > b_from || pa > 0 || pb > 1 || k > 0);
+                                for (int k = 0; k < L::BLOCK / 16; ++k)
+                                    product(pa + pb == 0 ? d : small, da + (uint64_t)(pa * L::A_PART >> 4) + SA * (k + from_k),
+                                            db + (uint64_t)(pb * L::B_PART >> 4) + SB * (k + from_k), ID, pa + pb == 0 ? in_group > 0 || k > 0 : b > b_from || pa > 0 || pb > 1 || k > 0);
                         if constexpr (OP == LinearOp::weights && !SOFT && L::SUMS > 0) {
                             if (sums) {
                                 const uint64_t ones = sdesc(sbase + L::OFF_OUT, 16, 1024);
@@ -778,53 +795,58 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             }
         }
     } else if (SOFT && warp >= 4 + kEpilogueWarps) {  // ---- operands through registers ----
+        if constexpr (SOFT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoaderRegs));
         const int thread = tid - 128 - 32 * kEpilogueWarps;
-        SoftTile<io_t, A_MN ? BK : BM, A_MN ? BM : BK> ta;
-        SoftTile<io_t, B_MN ? BK : BN, B_MN ? BN : BK> tb;
-        float column[4] = {};
-        int i = 0, b = b_from, i0, j0;  // of the block that the registers hold next
-        tile_at(0, i0, j0);
-        auto load_a = [&](int half) {
-            if (A_MN) ta.load(p.a, p.lda, b * BK, p.K, i0, p.I, thread, half);
-            else ta.load(p.a, p.lda, i0, p.I, b * BK, p.K, thread, half);
+        // rows and columns of the matrices in memory: the sum runs along a row (K-major) or from row to row
+        const SoftHalf<io_t, A_MN> ta(p.a, p.lda, A_MN ? p.K : p.I, A_MN ? p.I : p.K, thread);
+        const SoftHalf<io_t, B_MN> tb(p.b, p.ldb, B_MN ? p.K : p.J, B_MN ? p.J : p.K, thread);
+        float column[4] = {}, unused[4];
+        const uint32_t raws = sbase + L::OFF_RAW;
+        struct At {
+            int i, b, i0, j0;
         };
-        auto load_b = [&](int half) {
-            if (B_MN) tb.load(p.b, p.ldb, b * BK, p.K, j0, p.J, thread, half);
-            else tb.load(p.b, p.ldb, j0, p.J, b * BK, p.K, thread, half);
+        auto step = [&](At &a) {
+            if (++a.b == b_to) {
+                a.b = b_from;
+                if (++a.i < my_tiles) tile_at(a.i, a.i0, a.j0);
+            }
         };
-        if (total > 0) load_a(0), load_b(0);
-        int s = 0;
-        uint32_t round = 0;
+        At next{0, b_from, 0, 0}, now;
+        tile_at(0, next.i0, next.j0);
+        now = next;
+        long long asked = 0;
+        auto ask = [&] {
+            if (asked < total) {
+                const uint32_t raw = raws + (uint32_t)(asked % L::RAWS) * L::RAW;
+                const int k = next.b * L::BLOCK;
+                ta.ask(raw, A_MN ? k : next.i0, A_MN ? next.i0 : k);
+                tb.ask(raw + L::RAW / 2, B_MN ? k : next.j0, B_MN ? next.j0 : k);
+                step(next);
+            }
+            ++asked;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int r = 0; r + 1 < L::RAWS; ++r) ask();
         for (long long g = 0; g < total; ++g) {
-            const bool ok = round == 0 || mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns);
+            const int s = (int)(g & 1);
+            ask();
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::RAWS - 1) : "memory");
+            const bool ok = g < 2 || mbar_wait(smem_u32(&freed[s]), (uint32_t)((g - 2) >> 1) & 1, wt.ns);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) give_up();
                 break;
             }
-            if (__any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
-            // half a tile of each operand in registers: while one is stored the other is on its way
-            uint8_t *at = sm + s * L::STAGE;
-            auto store_a = [&](int half) {
-                if (sums) ta.add_columns(column);
-                ta.store(at, L::A_PART, thread, half);
-            };
-            store_a(0);
-            load_a(1);
-            tb.store(at + PARTS * L::A_PART, L::B_PART, thread, 0);
-            load_b(1);
-            store_a(1);
-            if (++b == b_to) {
-                b = b_from;
-                if (++i < my_tiles) tile_at(i, i0, j0);
-            }
-            if (g + 1 < total) load_a(0);
-            tb.store(at + PARTS * L::A_PART, L::B_PART, thread, 1);
-            if (g + 1 < total) load_b(0);
+            const uint32_t raw = raws + (uint32_t)(g % L::RAWS) * L::RAW;
+            const int k = now.b * L::BLOCK;
+            ta.bring(sm, L::A_PART, raw, s, A_MN ? k : now.i0, A_MN ? now.i0 : k, sums, column);
+            tb.bring(sm + PARTS * L::A_PART, L::B_PART, raw + L::RAW / 2, s, B_MN ? k : now.j0, B_MN ? now.j0 : k, false, unused);
+            step(now);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&full[s]));
-            if (++s == STAGES) s = 0, ++round;
+            if (__any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if constexpr (OP == LinearOp::weights)
             *reinterpret_cast<float4 *>(&column_sums[thread / 32][4 * lane]) = make_float4(column[0], column[1], column[2], column[3]);
     } else {  // ---- what follows: lane quarter warp % 4, columns of half (warp - 4) / 4 ----
