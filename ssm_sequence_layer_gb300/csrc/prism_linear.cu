@@ -9,6 +9,140 @@
 namespace prism {
 namespace lin {
 
+// ---- few rows ---------------------------------------------------------------------------------------------
+// Up to 16 rows of bf16, as a served token of each of some sequences has them: the weights' bytes bound the product, each weight
+// is used M times at most, and tiles of 128 rows would be empty for the most part.  A warp takes RPW tiles of 16 rows of W as A operands
+// of m16n8k16 products straight from global memory to registers (16 bytes of a row per lane and load), and 8 NT rows of x as B
+// operands.  The products' k order is a free choice as long as both operands share it: the four words of a lane's 16 bytes serve as
+// the k slots of two products.  KS warps of a CTA share their tiles and split the sum, so that narrow products still fill the
+// machine; their sums are added in a fixed order.
+constexpr int kFewWarps = 8, kFewBlock = 64;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int NT, int KS, int RPW>
+__global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const Params<__nv_bfloat16> p)
+{
+    constexpr int RT = kFewWarps / KS;  // warps of a CTA with rows of their own
+    constexpr int AHEAD = 2;            // blocks of 64 in flight
+    __shared__ float parts[KS > 1 ? kFewWarps : 1][16 * RPW][8 * NT + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int ks = warp % KS, n0 = (blockIdx.x * RT + warp / KS) * 16 * RPW, blocks = (p.K + kFewBlock - 1) / kFewBlock;
+    float c[RPW][NT][4] = {};
+    if (n0 < p.J) {
+        // rows beyond the operands' last are read as the last and not stored
+        const __nv_bfloat16 *wr[2 * RPW], *xr[NT];
+#pragma unroll
+        for (int r = 0; r < 2 * RPW; ++r) wr[r] = p.b + (size_t)min(n0 + g + 8 * r, p.J - 1) * p.K;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xr[t] = p.a + (size_t)min(8 * t + g, p.I - 1) * p.K;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        uint4 w[AHEAD][2 * RPW][2];
+        auto load = [&](int slot, int b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = b * kFewBlock + h * 32 + q * 8;
+#pragma unroll
+                for (int r = 0; r < 2 * RPW; ++r) w[slot][r][h] = k < p.K ? __ldcs(reinterpret_cast<const uint4 *>(wr[r] + k)) : zero;
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) load(s, ks + s * KS);
+        for (int b0 = ks; b0 < blocks; b0 += AHEAD * KS) {
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) {
+                const int b = b0 + s * KS;
+                if (b >= blocks) break;
+                uint4 x[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = b * kFewBlock + h * 32 + q * 8;
+                        x[t][h] = k < p.K ? __ldg(reinterpret_cast<const uint4 *>(xr[t] + k)) : zero;
+                    }
+#pragma unroll
+                for (int r = 0; r < RPW; ++r)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 lo = w[s][2 * r][h], hi = w[s][2 * r + 1][h];
+                            mma_bf16(c[r][t], lo.x, hi.x, lo.y, hi.y, x[t][h].x, x[t][h].y);
+                            mma_bf16(c[r][t], lo.z, hi.z, lo.w, hi.w, x[t][h].z, x[t][h].w);
+                        }
+                load(s, b + AHEAD * KS);
+            }
+        }
+    }
+    if constexpr (KS > 1) {
+#pragma unroll
+        for (int r = 0; r < RPW; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) parts[warp][16 * r + g + 8 * (i >> 1)][8 * t + 2 * q + (i & 1)] = c[r][t][i];
+        __syncthreads();
+    }
+    // A warp finishes the rows of W that it took (with KS warps a share of them each), a column of its tiles per lane and m: the
+    // stores of neighbouring lanes are neighbours
+    with_activation(p.act, [&](auto act) {
+        constexpr prism_activation ACT = decltype(act)::value;
+        auto finish = [&](int m, int n, float v) {
+            if (m >= p.I || n >= p.J) return;
+            const size_t at = (size_t)m * p.J + n;
+            if (p.bias) v += io::ld(p.bias + n);
+            if (p.pre_out) io::st(p.pre_out + at, v);
+            v = act_value<ACT>(v);
+            if (p.add) v += io::ld(p.add + at);
+            io::st((__nv_bfloat16 *)p.out + at, v);
+        };
+        if constexpr (KS > 1) {
+            for (int e = ks * 32 + lane; e < 16 * RPW * 8 * NT; e += 32 * KS) {
+                const int n = e % (16 * RPW), m = e / (16 * RPW);
+                float v = 0.f;
+#pragma unroll
+                for (int o = 0; o < KS; ++o) v += parts[warp - ks + o][n][m];
+                finish(m, n0 + n, v);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < RPW; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) finish(8 * t + 2 * q + (i & 1), n0 + 16 * r + g + 8 * (i >> 1), c[r][t][i]);
+        }
+    });
+}
+
+template <int NT>
+cudaError_t few_rows(const Params<__nv_bfloat16> &p, const TokenLaunch &l)
+{
+    constexpr int T = 32 * kFewWarps;
+    const int blocks = (p.K + kFewBlock - 1) / kFewBlock, pairs = (p.J + 31) / 32;
+    cudaStream_t s = l.timer->stream;
+    if (pairs * 8LL < 12 * l.sm_count) {  // few rows of W: all warps of a CTA on one tile
+        few_kernel<NT, 8, 1><<<(p.J + 15) / 16, T, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    // as many warps as keep each SM's loads in flight, as far as the blocks of 64 reach
+    int ks = 1;
+    while (ks < 8 && ks < blocks && (long long)pairs * ks < 8 * l.sm_count) ks *= 2;
+    const unsigned grid = (unsigned)((pairs + kFewWarps / ks - 1) / (kFewWarps / ks));
+    if (ks == 1) few_kernel<NT, 1, 2><<<grid, T, 0, s>>>(p);
+    else if (ks == 2) few_kernel<NT, 2, 2><<<grid, T, 0, s>>>(p);
+    else if (ks == 4) few_kernel<NT, 4, 2><<<grid, T, 0, s>>>(p);
+    else few_kernel<NT, 8, 2><<<grid, T, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
 template <typename io_t>
 cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
 {
@@ -26,6 +160,14 @@ cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
     } else {
         name = "linear_weights";
         p.I = a.N, p.J = a.K, p.K = a.M, p.lda = a.N, p.ldb = a.K;
+    }
+    if constexpr (sizeof(io_t) == 2) {
+        if (a.op == LinearOp::forward && a.M <= 16 && a.K % 8 == 0) {
+            l.timer->begin(name);
+            const cudaError_t e = a.M <= 8 ? few_rows<1>(p, l) : few_rows<2>(p, l);
+            l.timer->end();
+            return e;
+        }
     }
     Cut c = {};
     // TMA takes rows whose stride is a multiple of 16 bytes

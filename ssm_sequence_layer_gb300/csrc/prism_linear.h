@@ -283,9 +283,11 @@ __device__ __forceinline__ float without_leading(float a) { return a - __uint_as
 
 // ---- operands through registers ------------------------------------------------------------------------
 // Half a stage of an operand: R rows x C values of a row-major matrix (128 x 32 along the sum, or 32 x 128 across it), cut to (rows, cols).
-// A thread copies four values of a row at a time into 16 bytes of its own, two halves ahead and without waiting for them
+// A thread copies four values of a row at a time into shared memory of its own, two halves ahead and without waiting for them
 // (cp.async: 16 bytes where rows are whole units, else words of 4, of which bfloat16 rows may start in the middle of one), and
-// later brings its values to the form that the tensor core reads.
+// later brings its values to the form that the tensor core reads.  Both ways no two lanes of a phase meet in a bank: words lie
+// beside the other threads' words, and the four rows that a warp brings at once are 0, 1, 4 and 5 of eight, whose swizzled halves
+// fill all banks.
 template <typename io_t, bool MN>
 struct SoftHalf {
     static constexpr int C = MN ? 128 : 32, PER_ROW = C / 4, THREADS = 32 * kLoaderWarps, STEPS = 1024 / THREADS;
@@ -297,7 +299,14 @@ struct SoftHalf {
         : base(base_), ld(ld_), last(ld_ * rows_), rows(rows_), cols(cols_), thread(thread_), whole(ld_ * sizeof(io_t) % 16 == 0)
     {
     }
-    static __device__ __forceinline__ uint32_t raw_of(uint32_t raw, int step, int thread) { return raw + (step * THREADS + thread) * 16; }
+    __device__ __forceinline__ int row_of(int step) const
+    {
+        const int q = thread / PER_ROW;
+        return (MN ? q : (q & ~6) | (q & 2) << 1 | (q & 4) >> 1) + step * (THREADS / PER_ROW);
+    }
+    __device__ __forceinline__ int column() const { return thread % PER_ROW * 4; }
+    __device__ __forceinline__ uint32_t unit_at(uint32_t raw, int step) const { return raw + (step * THREADS + thread) * 16; }
+    __device__ __forceinline__ uint32_t word_at(uint32_t raw, int step, int word) const { return raw + step * THREADS * 16 + word * THREADS * 4 + thread * 4; }
     static __device__ __forceinline__ void copy(uint32_t to, const void *from, int bytes)
     {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
@@ -306,16 +315,15 @@ struct SoftHalf {
     {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            const int g = thread + i * THREADS, r = r0 + g / PER_ROW, c = c0 + g % PER_ROW * 4;
-            const uint32_t to = raw_of(raw, i, thread);
+            const int r = r0 + row_of(i), c = c0 + column();
             const bool in = r < rows && c < cols;
             const long long at = in ? (long long)r * ld + c : 0;
             if constexpr (sizeof(io_t) == 4) {
-                if (whole && (!in || c + 4 <= cols)) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(base + at), "r"(in ? 16 : 0) : "memory");
+                if (whole) {  // columns come in whole units too
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(unit_at(raw, i)), "l"(base + at), "r"(in ? 16 : 0) : "memory");
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) copy(to + 4 * e, base + (in && c + e < cols ? at + e : 0), in && c + e < cols ? 4 : 0);
+                    for (int e = 0; e < 4; ++e) copy(word_at(raw, i, e), base + (in && c + e < cols ? at + e : 0), in && c + e < cols ? 4 : 0);
                 }
             } else {
                 // the words that hold the four values; the matrix may end in the middle of one
@@ -323,7 +331,7 @@ struct SoftHalf {
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
                     const bool need = in && word + 2 * e < last && word + 2 * e < at + 4;
-                    copy(to + 4 * e, base + (need ? word + 2 * e : 0), need ? (word + 2 * e + 1 < last ? 4 : 2) : 0);
+                    copy(word_at(raw, i, e), base + (need ? word + 2 * e : 0), need ? (word + 2 * e + 1 < last ? 4 : 2) : 0);
                 }
             }
         }
@@ -333,10 +341,15 @@ struct SoftHalf {
     {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            const int g = thread + i * THREADS, r = g / PER_ROW, c = g % PER_ROW * 4;
+            const int r = row_of(i), c = column();
             uint8_t *at = MN ? to + (c >> 6) * kPanel + sw128(r + 32 * half, c & 63) : to + sw128(r, c + 32 * half);
             uint32_t x[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(raw_of(raw, i, thread)));
+            if (sizeof(io_t) == 4 && whole) {
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(unit_at(raw, i)));
+            } else {
+#pragma unroll
+                for (int e = 0; e < (sizeof(io_t) == 4 ? 4 : 3); ++e) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[e]) : "r"(word_at(raw, i, e)));
+            }
             float f[4];
             if constexpr (sizeof(io_t) == 2) {
                 const bool odd = (((long long)(r0 + r) * ld + c0 + c) & 1) && r0 + r < rows && c0 + c < cols;
