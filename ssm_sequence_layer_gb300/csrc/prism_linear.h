@@ -235,7 +235,7 @@ struct Waits {
 };
 
 constexpr int BM = 128, BK = 64;
-constexpr int kEpilogueWarps = 8, kLoaderWarps = 8;
+constexpr int kLoaderWarps = 8;
 constexpr uint32_t kPanel = BK * 128;  // an MN-major panel: 64 rows (of the sum) x 64 values
 
 template <typename io_t, LinearOp OP, bool SOFT, int BN, bool PAIR>
@@ -250,15 +250,19 @@ struct Layout {
     static constexpr uint32_t RAW = 32768, OFF_RAW = STAGE;
     static constexpr int GROUP = PARTS == 3 ? 256 / BLOCK : 512 / BLOCK;  // blocks that share an accumulator where its sums go on in registers
     static constexpr int STAGES = SOFT ? 2 : (INCOMING && STAGE <= 32768 ? 163840 : 196608) / STAGE - (INCOMING && STAGE > 32768 ? 1 : 0);
-    static constexpr uint32_t OUT_WARP = INCOMING ? 8192 : 4096;  // a warp's staging: outputs of 32 x 32 values of 4 bytes, or two times 2 bytes; addends
+    // The warps that finish tiles: each element of an activation takes about 25 instructions one after the other, which two warps a
+    // scheduler do not hide; where the sums go on in registers there is room for eight.
+    static constexpr int FINISHERS = INCOMING ? 16 : 8, FINISHED = BN / (FINISHERS / 4);  // and a warp's columns
+    static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging: outputs of 32 x 32 values of 4 bytes, or two times 2 bytes, the second for addends
     static constexpr uint32_t OFF_OUT = SOFT ? STAGE + RAWS * RAW : STAGES * STAGE;
-    static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 2048 : kEpilogueWarps * OUT_WARP) + 1024;  // + alignment slack
-    static constexpr int THREADS = 128 + 32 * kEpilogueWarps + (SOFT ? 32 * kLoaderWarps : 0);
+    static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 2048 : FINISHERS * OUT_WARP) + 1024;  // + alignment slack
+    static constexpr int THREADS = 128 + 32 * FINISHERS + (SOFT ? 32 * kLoaderWarps : 0);
     static constexpr int kColumns = 512;  // of tensor memory: two accumulators, and two for the small products or the sums over rows
     static constexpr int SUMS = OP == LinearOp::weights && !SOFT && 2 * BN + 32 <= kColumns ? 2 * BN : 0;
     // registers handed over to the warps that finish tiles, from the issuing ones
-    static constexpr int kLaunchRegs = SOFT ? 96 : 168, kIssueRegs = SOFT ? 40 : 56, kEpilogueRegs = SOFT ? 152 : 224, kLoaderRegs = 64;
-    static_assert(128 * kIssueRegs + 32 * kEpilogueWarps * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLoaderRegs : 0) <= THREADS * kLaunchRegs, "registers");
+    static constexpr int kLaunchRegs = SOFT || INCOMING ? 96 : 168, kIssueRegs = SOFT || INCOMING ? 40 : 56,
+                         kEpilogueRegs = SOFT ? 152 : INCOMING ? 104 : 224, kLoaderRegs = 64;
+    static_assert(128 * kIssueRegs + 32 * FINISHERS * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLoaderRegs : 0) <= THREADS * kLaunchRegs, "registers");
     static_assert(STAGES >= 2 && SMEM + (OP == LinearOp::weights ? 3072 : 1024) <= 232448 && OFF_OUT % 1024 == 0, "layout");
 };
 
@@ -408,6 +412,16 @@ __device__ __forceinline__ void ld_wait(uint32_t (&r)[32])
     asm volatile("" : "+r"(r[30]), "+r"(r[31]));
 }
 
+// waits for the loads so far and takes 16 values as operands
+__device__ __forceinline__ void wait16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 template <typename F>
 __device__ __forceinline__ void with_activation(prism_activation act, F f)
 {
@@ -437,23 +451,83 @@ __device__ __forceinline__ void load_row(const T *p, int at, int cols, bool whol
     for (int e = 0; e < N; ++e) f[e] = at + e < cols ? io::ld(p + at + e) : 0.f;
 }
 
+// N values of a row as they lie in memory, two at a time
+template <typename T, int N = 32>
+struct Held {
+    uint32_t w[N * sizeof(T) / 4];
+    __device__ __forceinline__ float2 pair(int i) const
+    {
+        float2 v;
+        if constexpr (sizeof(T) == 2) io::Unit<__nv_bfloat16, 8>::two(w[i], v.x, v.y);
+        else v = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        return v;
+    }
+    __device__ __forceinline__ void unit(int u, uint4 x) { w[4 * u] = x.x, w[4 * u + 1] = x.y, w[4 * u + 2] = x.z, w[4 * u + 3] = x.w; }
+    __device__ __forceinline__ void set(const float (&f)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            if constexpr (sizeof(T) == 2) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+            else w[2 * i] = __float_as_uint(f[2 * i]), w[2 * i + 1] = __float_as_uint(f[2 * i + 1]);
+        }
+    }
+    // of a row's values from `at` on; beyond `cols` zeros.  whole: rows are whole 16-byte units and at is one's start
+    __device__ __forceinline__ void load(const T *p, int at, int cols, bool whole)
+    {
+        if (whole && at + N <= cols) {
+#pragma unroll
+            for (int u = 0; u < N * (int)sizeof(T) / 16; ++u) unit(u, reinterpret_cast<const uint4 *>(p + at)[u]);
+            return;
+        }
+        float f[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] = at + e < cols ? io::ld(p + at + e) : 0.f;
+        set(f);
+    }
+};
+template <typename io_t, prism_activation ACT, typename T, int N>
+__device__ __forceinline__ void times_slopes(float (&f)[N], const Held<T, N> &z)
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const float2 x = z.pair(c / 2);
+        if constexpr (sizeof(io_t) == 2) {
+            const float2 v = io::mul2(make_float2(f[c], f[c + 1]), act_slope<ACT>(x));
+            f[c] = v.x, f[c + 1] = v.y;
+        } else {
+            f[c] *= act_slope<ACT>(x.x), f[c + 1] *= act_slope<ACT>(x.y);
+        }
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void plus(float (&f)[N], const Held<T, N> &g)
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const float2 v = io::add2(make_float2(f[c], f[c + 1]), g.pair(c / 2));
+        f[c] = v.x, f[c + 1] = v.y;
+    }
+}
+
 // A warp's 32 rows x 32 columns of an output or an addend: lane l holds row l.
 template <typename T>
 struct Patch {
-    static constexpr int VEC = 16 / (int)sizeof(T), BUFFERS = 4 / (int)sizeof(T);
+    static constexpr int VEC = 16 / (int)sizeof(T);
     // rows that are not whole units come and go through shared memory, a row by all lanes
-    static __device__ __forceinline__ void get(const T *p, int J, int rows, int j0, bool whole, float *t, int lane, float (&f)[32])
+    static __device__ __forceinline__ void get(const T *p, int J, int rows, int j0, bool whole, float *t, int lane, Held<T> &held)
     {
         if (whole) {
-            load_row<T, 32>(p + (size_t)min(lane, rows - 1) * J, j0, J, true, f);
+            held.load(p + (size_t)min(lane, rows - 1) * J, j0, J, true);
             return;
         }
         __syncwarp();
 #pragma unroll 8
         for (int r = 0; r < 32; ++r) t[r * 32 + (lane ^ r)] = r < rows && j0 + lane < J ? io::ld(p + (size_t)r * J + j0 + lane) : 0.f;
         __syncwarp();
+        float f[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) f[c] = t[lane * 32 + (c ^ lane)];
+        held.set(f);
     }
     static __device__ __forceinline__ void put_rows(T *p, int J, int rows, int j0, float *t, int lane, const float (&f)[32])
     {
@@ -476,48 +550,42 @@ struct Patch {
             for (int r = 0; r < rows; ++r, to += J) io::st(to, t[r * 32 + (lane ^ r)]);
         }
     }
-    // of a bf16 piece that came by TMA, this lane's row
-    static __device__ __forceinline__ void from_tile(const uint8_t *tile, int lane, float (&f)[32])
+    // 16 columns of this lane's row of a bf16 piece
+    static __device__ __forceinline__ uint4 *unit_of(uint8_t *piece, int lane, int u) { return reinterpret_cast<uint4 *>(piece + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)); }
+    static __device__ __forceinline__ void get_half(uint8_t *piece, int lane, int half, Held<T, 16> &held)
+    {
+        if constexpr (sizeof(T) == 2) held.unit(0, *unit_of(piece, lane, 2 * half)), held.unit(1, *unit_of(piece, lane, 2 * half + 1));
+    }
+    static __device__ __forceinline__ void put_half(uint8_t *piece, int lane, int half, const float (&f)[16])
     {
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                io::Unit<T, 8> x;
-                x.w = *reinterpret_cast<const uint4 *>(tile + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4));
+            for (int u = 0; u < 2; ++u) {
                 float g[8];
-                x.get(g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[8 * u + e] = g[e];
+                for (int e = 0; e < 8; ++e) g[e] = f[8 * u + e];
+                io::Unit<T, 8> x;
+                x.set(g);
+                *unit_of(piece, lane, 2 * half + u) = x.w;
             }
         }
     }
-    // by TMA: a piece of 32 rows x 32 columns, swizzled as the tensor map says (64 bytes a row: 16-byte chunk XOR (row / 2) mod 4;
-    // 128 bytes a row: XOR row mod 8); with two buffers one piece leaves while the next is written
-    static __device__ __forceinline__ void put_tiled(const CUtensorMap *tm, uint8_t *stage, int &turn, int row0, int j0, int lane,
-                                                     const float (&f)[32])
+    // float32 by TMA: a piece of 32 rows x 32 columns, 128-byte swizzled
+    static __device__ __forceinline__ void put_tiled(const CUtensorMap *tm, uint8_t *stage, int row0, int j0, int lane, const float (&f)[32])
     {
-        constexpr uint32_t PIECE = 1024 * sizeof(T), ROW = 32 * sizeof(T);
-        uint8_t *to = stage + (turn % BUFFERS) * PIECE;
-        if (BUFFERS == 2) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        else bulk_wait_read();
-        __syncwarp();
+        if constexpr (sizeof(T) == 4) {
+            bulk_wait_read();
+            __syncwarp();
 #pragma unroll
-        for (int u = 0; u < 32 / VEC; ++u) {
-            float g[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) g[e] = f[u * VEC + e];
-            io::Unit<T, VEC> x;
-            x.set(g);
-            const int chunk = sizeof(T) == 2 ? u ^ (lane >> 1 & 3) : u ^ (lane & 7);
-            *reinterpret_cast<uint4 *>(to + lane * ROW + chunk * 16) = x.w;
+            for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(tm, smem_u32(stage), j0, row0);
+                bulk_commit();
+            }
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(tm, smem_u32(to), j0, row0);
-            bulk_commit();
-        }
-        ++turn;
     }
 };
 
@@ -614,12 +682,12 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
 {
     using L = Layout<io_t, OP, SOFT, BN, PAIR>;
     using out_t = std::conditional_t<OP == LinearOp::weights, float, io_t>;
-    constexpr int STAGES = L::STAGES, HALF = BN / 2, PARTS = L::PARTS;
+    constexpr int STAGES = L::STAGES, COLS = L::FINISHED, PARTS = L::PARTS;
     constexpr bool A_MN = OP == LinearOp::weights, B_MN = OP != LinearOp::forward, GROUPED = L::GROUPED;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint32_t tmem_base_s;
-    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2], incoming[2 * kEpilogueWarps];
+    __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2], incoming[L::FINISHERS];
     __shared__ int abort_s;
     __shared__ __align__(16) float column_sums[OP == LinearOp::weights ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
     constexpr int CTAS = PAIR ? 2 : 1, TM = CTAS * BM;  // of a tile, and its rows
@@ -681,10 +749,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             mbar_init(smem_u32(&full[s]), SOFT ? kLoaderWarps : 1);
             mbar_init(smem_u32(&freed[s]), 1);
         }
-        for (int w = 0; w < 2 * kEpilogueWarps; ++w) mbar_init(smem_u32(&incoming[w]), 1);
+        for (int w = 0; w < L::FINISHERS; ++w) mbar_init(smem_u32(&incoming[w]), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
-            mbar_init(smem_u32(&acc_empty[s]), CTAS * kEpilogueWarps);
+            mbar_init(smem_u32(&acc_empty[s]), CTAS * L::FINISHERS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
@@ -807,9 +875,9 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                 }
             }
         }
-    } else if (SOFT && warp >= 4 + kEpilogueWarps) {  // ---- operands through registers ----
+    } else if (SOFT && warp >= 4 + L::FINISHERS) {  // ---- operands through registers ----
         if constexpr (SOFT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoaderRegs));
-        const int thread = tid - 128 - 32 * kEpilogueWarps;
+        const int thread = tid - 128 - 32 * L::FINISHERS;
         // rows and columns of the matrices in memory: the sum runs along a row (K-major) or from row to row
         const SoftHalf<io_t, A_MN> ta(p.a, p.lda, A_MN ? p.K : p.I, A_MN ? p.I : p.K, thread);
         const SoftHalf<io_t, B_MN> tb(p.b, p.ldb, B_MN ? p.K : p.J, B_MN ? p.J : p.K, thread);
@@ -862,14 +930,13 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
         if constexpr (OP == LinearOp::weights)
             *reinterpret_cast<float4 *>(&column_sums[thread / 32][4 * lane]) = make_float4(column[0], column[1], column[2], column[3]);
-    } else {  // ---- what follows: lane quarter warp % 4, columns of half (warp - 4) / 4 ----
+    } else {  // ---- what follows: lane quarter warp % 4, share (warp - 4) / 4 of the columns ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpilogueRegs));
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t from = ((uint32_t)(quarter * 32) << 16) + half * HALF;
+        const int quarter = warp & 3, share = (warp - 4) >> 2;
+        const uint32_t from = ((uint32_t)(quarter * 32) << 16) + share * COLS;
         uint8_t *stage = sm + L::OFF_OUT + (warp - 4) * L::OUT_WARP;
         float *flat = reinterpret_cast<float *>(stage);
         const bool whole = (long long)p.J * sizeof(io_t) % 16 == 0;
-        int turn = 0;
         uint32_t acc = 0;
         bool ok = true;
         auto hand_back = [&](uint32_t buf) {
@@ -880,21 +947,21 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                 else mbar_arrive(smem_u32(&acc_empty[buf]));
             }
         };
-        // Addends (pre_in, then add) come by TMA where rows are whole units: a warp's pieces of 32 x 32 in the order in which they are used,
-        // two on their way, into the next tile too.
+        // An addend (pre_in if there is one, else add) comes by TMA where rows are whole units: a warp's pieces of 32 x 32 in the order in which
+        // they are used, the next on its way while one is used, into the next tile too.  Its place is that of the second output.
         const bool has_pre = OP == LinearOp::backward && p.act != PRISM_ACT_NONE, has_add = p.add != nullptr;
-        const int kinds = has_pre + has_add;
-        const bool by_tma = L::INCOMING && !SPLIT && p.tiled && kinds > 0;
+        const bool by_tma = L::INCOMING && !SPLIT && p.tiled && (has_pre || has_add) && !p.pre_out;
+        const CUtensorMap *tm_in = has_pre ? &tm_pre : &tm_add;
         uint32_t asked = 0, taken = 0;
-        int ask_tile = 0, ask_piece = 0, ask_kind = 0, ask_i0 = 0, ask_j = 0, ask_pieces = 0;
+        int ask_tile = 0, ask_piece = 0, ask_i0 = 0, ask_j = 0, ask_pieces = 0;
         auto pieces_of = [&](int i0, int j0) {  // of the warp's columns, those that the matrix has
-            return i0 + quarter * 32 < p.I ? max(0, min(HALF / 32, (p.J - j0 - half * HALF + 31) / 32)) : 0;
+            return i0 + quarter * 32 < p.I ? max(0, min(COLS / 32, (p.J - j0 - share * COLS + 31) / 32)) : 0;
         };
         auto look = [&] {  // the first tile from ask_tile on with pieces
             for (; ask_tile < my_tiles; ++ask_tile) {
                 int j0;
                 tile_at(ask_tile, ask_i0, j0);
-                ask_j = j0 + half * HALF;
+                ask_j = j0 + share * COLS;
                 ask_pieces = pieces_of(ask_i0, j0);
                 if (ask_pieces > 0) return;
             }
@@ -902,32 +969,18 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         auto ask = [&] {
             if (ask_tile >= my_tiles) return;
             if (lane == 0) {
-                const uint32_t bar = smem_u32(&incoming[2 * (warp - 4) + (asked & 1)]);
+                const uint32_t bar = smem_u32(&incoming[warp - 4]);
                 mbar_expect_tx(bar, 2048);
-                tma_load_2d(smem_u32(stage + 4096 + (asked & 1) * 2048), has_pre && ask_kind == 0 ? &tm_pre : &tm_add, bar, ask_j + 32 * ask_piece,
-                            ask_i0 + quarter * 32);
+                tma_load_2d(smem_u32(stage + 2048), tm_in, bar, ask_j + 32 * ask_piece, ask_i0 + quarter * 32);
             }
             ++asked;
-            if (++ask_kind == kinds) {
-                ask_kind = 0;
-                if (++ask_piece == ask_pieces) ask_piece = 0, ++ask_tile, look();
-            }
+            if (++ask_piece == ask_pieces) ask_piece = 0, ++ask_tile, look();
         };
-        if (by_tma) look(), ask(), ask();
-        auto take = [&](float (&f)[32]) {  // the next piece; false if it does not come
-            const uint32_t slot = taken & 1;
-            const bool here = __all_sync(0xffffffffu, mbar_wait(smem_u32(&incoming[2 * (warp - 4) + slot]), (taken >> 1) & 1, wt.ns));
-            ++taken;
-            if (!here) return false;
-            Patch<io_t>::from_tile(stage + 4096 + slot * 2048, lane, f);
-            __syncwarp();
-            ask();
-            return true;
-        };
+        if (by_tma) look(), ask();
         for (int i = 0; i < my_tiles && ok; ++i) {
             int i0, j0;
             tile_at(i, i0, j0);
-            float2 sum[GROUPED ? HALF / 2 : 1];
+            float2 sum[GROUPED ? COLS / 2 : 1];
             float over_rows = 0.f;
             uint32_t buf = 0;
 #pragma unroll 1
@@ -941,9 +994,9 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                         uint32_t r[2][32];
                         ld_issue(at, r[0]);
 #pragma unroll
-                        for (int c = 0; c < HALF / 32; ++c) {  // the next columns load while these are added
+                        for (int c = 0; c < COLS / 32; ++c) {  // the next columns load while these are added
                             ld_wait(r[c & 1]);
-                            if (c + 1 < HALF / 32) ld_issue(at + 32 * (c + 1), r[(c + 1) & 1]);
+                            if (c + 1 < COLS / 32) ld_issue(at + 32 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
                             for (int q = 0; q < 16; ++q) {
                                 const float2 x = make_float2(__uint_as_float(r[c & 1][2 * q]), __uint_as_float(r[c & 1][2 * q + 1]));
@@ -953,7 +1006,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                     };
                     add(tmem + buf * BN + from, g == 0);
                     if constexpr (L::SUMS > 0) {
-                        if (sums && half == 0) {
+                        if (sums && share == 0) {
                             uint32_t x;
                             asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(tmem + L::SUMS + 16 * buf + ((uint32_t)(quarter * 32) << 16)));
                             asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x)::"memory");
@@ -979,50 +1032,103 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                     ld_wait(r);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) f[c] = __uint_as_float(r[c]);
-                    if (ch + 1 == HALF / 32) hand_back(buf);
+                    if (ch + 1 == COLS / 32) hand_back(buf);
                 }
             };
             if constexpr (L::SUMS > 0) {
-                if (half == 0) column_sums[0][quarter * 32 + lane] = over_rows;
+                if (share == 0) column_sums[0][quarter * 32 + lane] = over_rows;
             }
             if constexpr (SPLIT) {  // every load has landed and every product has read it: their shared memory is free
                 const int row = quarter * 32 + lane;
 #pragma unroll
-                for (int ch = 0; ch < HALF / 32; ++ch) {
+                for (int ch = 0; ch < COLS / 32; ++ch) {
                     float f[32];
                     piece(ch, f);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        *reinterpret_cast<float4 *>(sm + row * BN * 4 + (((half * HALF / 4 + 8 * ch + q) ^ (row & 7)) << 4)) =
+                        *reinterpret_cast<float4 *>(sm + row * BN * 4 + (((share * COLS / 4 + 8 * ch + q) ^ (row & 7)) << 4)) =
                             make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
                 }
             } else {
                 const int r0 = i0 + quarter * 32, rows = min(32, p.I - r0);
                 with_activation(p.act, [&](auto act) {
                     constexpr prism_activation ACT = decltype(act)::value;
-#pragma unroll (GROUPED ? HALF / 32 : 1)
-                    for (int ch = 0; ch < HALF / 32; ++ch) {
-                        const int j = j0 + half * HALF + ch * 32;
-                        const bool inside = rows > 0 && j < p.J;
-                        float f[32], other[32];
-                        auto addend = [&](const io_t *from) {
-                            if (by_tma) {
-                                if (ok) ok = take(other);
-                            } else {
-                                Patch<io_t>::get(from + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
+                    if constexpr (!GROUPED) {
+                        if (p.tiled) {  // bf16 pieces of 32 columns through shared memory, 16 at a time through registers
+                            const int row = min(r0 + lane, p.I - 1);
+#pragma unroll 1
+                            for (int ch = 0; ch < COLS / 32; ++ch) {
+                                const int j = j0 + share * COLS + ch * 32;
+                                const bool inside = rows > 0 && j < p.J;
+                                if (inside) {
+                                    if (by_tma) {
+                                        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&incoming[warp - 4]), taken & 1, wt.ns));
+                                        ++taken;
+                                    }
+                                    bulk_wait_read();  // the pieces before have left (two places for them in turn brought nothing)
+                                    __syncwarp();
+                                }
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    uint32_t r[16];
+                                    float f[16];
+                                    tmem_ld_nowait(tmem + buf * BN + from + 32 * ch + 16 * h, r);
+                                    const int at = j + 16 * h;
+                                    Held<io_t, 16> g;
+                                    if (OP == LinearOp::forward && p.bias && inside) g.load(p.bias, at, p.J, true);
+                                    if (OP == LinearOp::backward && has_pre && inside) {
+                                        if (by_tma) Patch<io_t>::get_half(stage + 2048, lane, h, g);
+                                        else g.load(p.pre_in + (size_t)row * p.J, at, p.J, true);
+                                    }
+                                    wait16(r);
+                                    if (h == 1 && ch + 1 == COLS / 32) hand_back(buf);
+                                    if (!inside) continue;
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) f[c] = __uint_as_float(r[c]);
+                                    if constexpr (OP == LinearOp::forward) {
+                                        if (p.bias) plus(f, g);
+                                        if (p.pre_out) Patch<io_t>::put_half(stage + 2048, lane, h, f);
+                                        to_values<io_t, ACT>(f);
+                                    } else if constexpr (ACT != PRISM_ACT_NONE) {
+                                        times_slopes<io_t, ACT>(f, g);
+                                    }
+                                    if (has_add) {
+                                        if (by_tma && !has_pre) Patch<io_t>::get_half(stage + 2048, lane, h, g);
+                                        else g.load(p.add + (size_t)row * p.J, at, p.J, true);
+                                        plus(f, g);
+                                    }
+                                    Patch<io_t>::put_half(stage, lane, h, f);
+                                }
+                                if (!inside) continue;
+                                fence_async_smem();
+                                __syncwarp();
+                                if (lane == 0) {
+                                    tma_store_2d(&tm_out, smem_u32(stage), j, r0);
+                                    if (p.pre_out) tma_store_2d(&tm_pre, smem_u32(stage + 2048), j, r0);
+                                    bulk_commit();
+                                }
+                                if (by_tma) ask();
                             }
-                        };
-                        if (inside && has_pre) addend(p.pre_in);
+                            return;
+                        }
+                    }
+#pragma unroll (GROUPED ? COLS / 32 : 1)
+                    for (int ch = 0; ch < COLS / 32; ++ch) {
+                        const int j = j0 + share * COLS + ch * 32;
+                        const bool inside = rows > 0 && j < p.J;
+                        float f[32];
+                        Held<io_t> other;
+                        if (inside && has_pre) Patch<io_t>::get(p.pre_in + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
                         piece(ch, f);
                         if (!inside) continue;
                         if constexpr (OP == LinearOp::forward) {
                             if (p.bias) {
-                                float bias[32];
-                                load_row<io_t, 32>(p.bias, j, p.J, true, bias);
+                                Held<io_t> bias;
+                                bias.load(p.bias, j, p.J, true);
                                 plus(f, bias);
                             }
                             if (p.pre_out) {
-                                if (p.tiled) Patch<io_t>::put_tiled(&tm_pre, stage, turn, r0, j, lane, f);
+                                if (GROUPED && p.tiled) Patch<io_t>::put_tiled(&tm_pre, stage, r0, j, lane, f);
                                 else Patch<io_t>::put_rows(p.pre_out + (size_t)r0 * p.J, p.J, rows, j, flat, lane, f);
                             }
                             to_values<io_t, ACT>(f);
@@ -1030,10 +1136,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                             times_slopes<io_t, ACT>(f, other);
                         }
                         if (has_add) {
-                            addend(p.add);
+                            Patch<io_t>::get(p.add + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
                             plus(f, other);
                         }
-                        if (p.tiled) Patch<out_t>::put_tiled(&tm_out, stage, turn, r0, j, lane, f);
+                        if (GROUPED && p.tiled) Patch<out_t>::put_tiled(&tm_out, stage, r0, j, lane, f);
                         else Patch<out_t>::put_rows((out_t *)p.out + (size_t)r0 * p.J, p.J, rows, j, flat, lane, f);
                     }
                 });
@@ -1042,7 +1148,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         if (!SPLIT && p.tiled) bulk_wait_read();  // before the staging goes
         if (by_tma) {  // after an expired wait: the pieces asked for land before the CTA exits
             if (!ok && lane == 0) give_up();
-            for (; !ok && taken < asked; ++taken) (void)mbar_wait(smem_u32(&incoming[2 * (warp - 4) + (taken & 1)]), (taken >> 1) & 1, 1000000000ull);
+            for (; !ok && taken < asked; ++taken) (void)mbar_wait(smem_u32(&incoming[warp - 4]), taken & 1, 1000000000ull);
         }
     }
     // drain: after an expired wait, the copies and products in flight land before the CTA exits
