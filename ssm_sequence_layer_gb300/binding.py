@@ -1031,12 +1031,13 @@ class Tokens:
         return out
 
     def _need_exactly(self, what, tensors, shapes, dtype):
-        if set(tensors) != set(shapes):
+        if tensors.keys() != shapes.keys():
             raise ValueError(f"{what} takes {', '.join(shapes)} (got {', '.join(tensors)})")
-        for key, t in tensors.items():
-            self._need(key, t, dtype)
-            if tuple(t.shape) != shapes[key]:
-                raise ValueError(f"{key} must be {list(shapes[key])} (got {list(t.shape)})")
+        device = self.device
+        for key, shape in shapes.items():
+            t = tensors[key]
+            if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+                raise ValueError(f"{key} must be a contiguous tensor {list(shape)} of {dtype} on the handle's device")
 
     def sample(self, logits, u, inv_temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
         """A token for each row of logits [..., V] (or [n, V] with padded rows) from the numbers u [...] float32
