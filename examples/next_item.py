@@ -1,10 +1,11 @@
 """A small next-item model around one recurrent layer: training steps, then serving.
 
 Shows the token operators next to the layer they surround:
-  training   ids -> embed -> norm -> (q, k, v, gates) -> recurrence -> norm(+ residual) -> head -> token_logprobs,
-             and back through token_logprobs_backward, norm_backward, the layer's backward and embed_backward;
-  serving    a prompt carried into the state, then one item at a time: embed -> norm -> decode_step ->
-             norm into 8 bits -> matmul8 (the head's weights laid out once) -> token_logprobs with alternatives.
+  training   ids -> embed -> norm -> linear -> heads (q, k, v) and gates -> recurrence -> linear -> norm(+ residual) ->
+             head (linear) -> token_logprobs, and back through the gradient of each;
+  serving    a prompt carried into the state, then one item at a time: embed -> norm -> linear -> heads ->
+             decode_step -> linear -> norm into 8 bits -> matmul8 (the head's weights laid out once) ->
+             token_logprobs with alternatives, and the next item by sample.
 
     python examples/next_item.py [--steps 60]
 
@@ -52,6 +53,43 @@ class Norm(torch.autograd.Function):
         return None, g["dx"], g["dx"] if ctx.has_residual else None, g["dweight"]
 
 
+class Linear(torch.autograd.Function):
+    """x W^T of rows x [n, K] and weights W [N, K]."""
+
+    @staticmethod
+    def forward(ctx, tokens, x, W):
+        w = W.to(BF16)
+        ctx.tokens = tokens
+        ctx.save_for_backward(x, w)
+        return tokens.linear(x, w)["y"]
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w = ctx.saved_tensors
+        dy = dy.contiguous()
+        return None, ctx.tokens.linear_backward(dy, w), ctx.tokens.linear_weight_backward(dy, x)["dW"]
+
+
+FORM = dict(heads=(H, H, H), d=DK, norm="unit", eps=1e-12)
+
+
+class Heads(torch.autograd.Function):
+    """Rows [B, T, 3 H 64] to the layer's q, k, v [B, H, T, 64], q and k of length one."""
+
+    @staticmethod
+    def forward(ctx, tokens, x):
+        ctx.tokens = tokens
+        ctx.save_for_backward(x)
+        out = tokens.heads(x, **FORM)
+        return out["q"], out["k"], out["v"]
+
+    @staticmethod
+    def backward(ctx, dq, dk, dv):
+        (x,) = ctx.saved_tensors
+        grads = {"dq": dq.contiguous(), "dk": dk.contiguous(), "dv": dv.contiguous()}
+        return None, ctx.tokens.heads_backward(x, grads, **FORM)["dx"]
+
+
 class Recurrence(torch.autograd.Function):
     """The layer with L = 1 (the gated delta rule): q, k, v [B,H,T,64] bf16, beta, alpha [B,H,T] fp32."""
 
@@ -92,21 +130,19 @@ class Model(torch.nn.Module):
         self.gates = p(2 * H, D, std=D ** -0.5)
         self.o = p(D, H * DK, std=D ** -0.5)
 
-    def heads(self, y):
-        """q, k, v [n, H, 64] and the gates [n, H] of normalised inputs y [n, D]."""
-        q, k, v = (y @ self.proj.to(BF16).t()).view(-1, 3, H, DK).unbind(1)
-        unit = lambda x: torch.nn.functional.normalize(x.float(), dim=-1).to(BF16)  # noqa: E731
-        b, a = (y @ self.gates.to(BF16).t()).float().view(-1, 2, H).unbind(1)
-        return unit(q), unit(k), v.contiguous(), torch.sigmoid(b), torch.exp(-torch.nn.functional.softplus(a) / 16)
+    def inputs(self, tokens, y, T_):
+        """The layer's q, k, v [B, H, T_, 64] and gates [B, H, T_] of normalised inputs y [B T_, D]."""
+        q, k, v = Heads.apply(tokens, Linear.apply(tokens, y, self.proj).view(B, T_, -1))
+        b, a = Linear.apply(tokens, y, self.gates).float().view(B, T_, 2, H).permute(2, 0, 3, 1)
+        return q, k, v, torch.sigmoid(b).contiguous(), torch.exp(-torch.nn.functional.softplus(a) / 16).contiguous()
 
     def forward(self, tokens, plan, conv_w, ids):
         e = Embed.apply(tokens, ids, self.table).view(-1, D)
         e, y = Norm.apply(tokens, e, None, self.w_in)
-        q, k, v, beta, alpha = (x.view(B, T, *x.shape[1:]).transpose(1, 2).contiguous() for x in self.heads(y))
-        o = Recurrence.apply(plan, conv_w, q, k, v, beta, alpha)
-        o = o.transpose(1, 2).reshape(-1, H * DK) @ self.o.to(BF16).t()
+        o = Recurrence.apply(plan, conv_w, *self.inputs(tokens, y, T))
+        o = Linear.apply(tokens, o.transpose(1, 2).reshape(-1, H * DK), self.o)
         _, y = Norm.apply(tokens, o, e, self.w_out)
-        return y @ self.table.to(BF16).t()
+        return Linear.apply(tokens, y, self.table)
 
 
 def sequences(follows, g, dev):
@@ -141,9 +177,9 @@ def train(model, steps, dev="cuda"):
 
 
 @torch.no_grad()
-def serve(model, follows, prompt=64, count=16, dev="cuda"):
-    """Greedy continuation of B prompts, one item at a time; returns the items and the top alternatives' log
-    probabilities of every step beside those of the head in bf16."""
+def serve(model, follows, prompt=64, count=16, dev="cuda", top_k=1, top_p=None, inv_temperature=None):
+    """Continuation of B prompts, one item at a time (the likeliest each time unless the rules allow more); returns the items and
+    the top alternatives' log probabilities of every step beside those of the head in bf16."""
     g = torch.Generator(device=dev).manual_seed(2)
     ids = sequences(follows, g, dev)[:, :prompt].contiguous()
     conv_w = torch.zeros(H, 4, DK, dtype=BF16, device=dev)
@@ -155,14 +191,12 @@ def serve(model, follows, prompt=64, count=16, dev="cuda"):
     with binding.Tokens(B * prompt, D, V, io="bf16", logits="f32") as tokens, binding.Plan(B, H, prompt, DK, DK, 1, io="bf16") as plan:
         w8, w_scale = tokens.matmul8_weights(table)  # once
 
-        def layer_inputs(tok):
+        def layer_inputs(tok, T_):
             e = tokens.embed(tok, table).view(-1, D)
-            q, k, v, beta, alpha = model.heads(tokens.norm(e, w_in)["y"])
+            q, k, v, beta, alpha = model.inputs(tokens, tokens.norm(e, w_in)["y"], T_)
             return e, {"q": q, "k": k, "v": v, "beta": beta, "alpha": alpha, "u": None, "gamma": None, "eta": None, "conv_w": conv_w, "L": 1}
 
-        _, inp = layer_inputs(ids)
-        for key in ("q", "k", "v", "beta", "alpha"):
-            inp[key] = inp[key].view(B, prompt, *inp[key].shape[1:]).transpose(1, 2).contiguous()
+        _, inp = layer_inputs(ids, prompt)
         # the last token of the prompt is the first step below: the prompt's others go into the state
         head = {key: (x[:, :, : prompt - 1].contiguous() if key in ("q", "k", "v", "beta", "alpha") else x) for key, x in inp.items()}
         with binding.Plan(B, H, prompt - 1, DK, DK, 1, io="bf16") as before:
@@ -170,15 +204,16 @@ def serve(model, follows, prompt=64, count=16, dev="cuda"):
             torch.cuda.synchronize()
         tok = ids[:, -1].contiguous()
         for _ in range(count):
-            e, inp = layer_inputs(tok)
-            o = plan.decode_step(inp, hist, S, stream=stream).reshape(B, H * DK) @ model.o.to(BF16).t()
+            e, inp = layer_inputs(tok, 1)
+            o = tokens.linear(plan.decode_step(inp, hist, S, stream=stream).reshape(B, H * DK), model.o.to(BF16))["y"]
             y = tokens.norm(o, w_out, residual=e, want=("y", "y8"))
             logits = tokens.matmul8(y["y8"], y["y_scale"], w8, w_scale)
             top = tokens.token_logprobs(logits, k=5)
-            items.append(top["top_ids"][:, 0].clone())
+            drawn = tokens.sample(logits, torch.rand(B, generator=g, device=dev), inv_temperature, top_k, top_p)
+            items.append(drawn["ids"])
             alternatives.append(top["top_logprob"])
             reference.append(torch.log_softmax(y["y"].float() @ table.float().t(), -1).gather(1, top["top_ids"]))
-            tok = top["top_ids"][:, 0].contiguous()
+            tok = drawn["ids"]
         tokens.last_device_status()
         plan.last_device_status()
     return ids[:, -1], torch.stack(items, 1), torch.stack(alternatives), torch.stack(reference)
@@ -195,6 +230,8 @@ def main():
     last, items, alternatives, reference = serve(model, follows)
     chain = torch.cat([last[:, None], items], 1)
     hit = (follows[chain[:, :-1]] == chain[:, 1:]).float().mean().item()
+    drawn = serve(model, follows, top_k=20, top_p=0.9, inv_temperature=0.5)[1]
+    print("drawn with top-k 20, top-p 0.9 at temperature 2:", drawn[0].tolist())
     print("served %d items; %.0f %% follow the rule; 8-bit head against bf16: largest difference of a log probability %.3f"
           % (items.numel(), 100 * hit, (alternatives - reference).abs().max().item()))
 
