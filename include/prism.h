@@ -394,7 +394,7 @@ typedef struct prism_tokens_s *prism_tokens_t;
  * its workspace (no later call allocates, so every call can be captured into a graph).  max_rows:
  * the largest n (or M) of a call, 1 .. 2^24; D in 1 .. 65536; V in 1 .. 2^30.  On error *out_tokens
  * is NULL.  A handle may be used by one stream at a time.  The workspace serves every operator, whichever are called: it
- * holds 24 bytes a row, V bits and parts of gradients, at most 8193 x 2 x D and 960 x D floats.
+ * holds 24 bytes a row, V bits and parts of gradients, at most 8193 x 2 x D and 960 x D floats, and 2.5 MB for those of head weights.
  */
 PRISM_API prism_status prism_tokens_plan(int max_rows, int D, int V, prism_dtype io, prism_tokens_t *out_tokens);
 
@@ -531,7 +531,9 @@ PRISM_API prism_status prism_token_logprobs_backward(prism_tokens_t tokens, int 
  * act: the identity, gelu(z) = z Phi(z) with the exact normal distribution function (as in the layer), or
  * silu(z) = z / (1 + exp(-z)).  M at most max_rows; N and K (1 .. 2^20 each) need not be the handle's V and D, and need no
  * multiple: rows that are not whole 16-byte units only take longer.  Sums are float32, whatever the io dtype, and y is taken
- * of the unrounded pre.  An expired device wait is reported by prism_tokens_last_device_status.
+ * of the unrounded pre.  In float32 a product of two values is within 2^-20 of itself (three bfloat16 parts of each, which hold all
+ * of its bits; the smallest products of parts are left out); parts below the smallest normal number are lost, and an infinite
+ * operand gives NaN.  An expired device wait is reported by prism_tokens_last_device_status.
  */
 typedef enum prism_activation {
     PRISM_ACT_NONE = 0,
@@ -575,7 +577,7 @@ PRISM_API prism_status prism_linear_weight_backward(prism_tokens_t tokens, int M
  * and the first rot values of y are turned in pairs, (y_i, y_{i + rot/2}) or, interleaved, (y_{2i}, y_{2i+1}), i < rot/2:
  *   (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),    t = position inv_freq_i
  * Values are copied.  positions [B, T] int64 (NULL: 0 .. T-1 in every sequence), of any sign and size up to 2^40; the angle is
- * reduced in 64-bit fixed point, to 2^-62 turns of the float32 inv_freq times the position.  inv_freq [rot/2] float32 on the
+ * reduced in 64-bit fixed point, to 2^-62 turns of the float32 inv_freq times the position, and taken to 2^-27 turns.  inv_freq [rot/2] float32 on the
  * device, each below 2^12 in magnitude.  Scaling for long contexts is a choice of inv_freq and amplitude
  * (rotary_frequencies of the Python package makes the usual ones).
  * d and dv in 1 .. 512, rot even, 0 .. d (0: no rotation), eps finite and >= 0; squares are float32 as in prism_norm.
@@ -629,9 +631,10 @@ PRISM_API prism_status prism_heads_backward(prism_tokens_t tokens, const prism_h
  *   logprob and kept may be NULL
  * Masked tokens are those of prism_token_logprobs.  A row without a live token gives id -1, logprob -inf, kept 0; one with NaN
  * or +inf gives id -1, logprob NaN, kept 0, and so does an inv_temperature outside 2^-60 .. 2^126, which is recorded
- * (prism_tokens_last_device_status: PRISM_ERR_DEVICE).  Masses are taken to about 2^-40 of the first token's, in sums without
- * rounding, wherever a choice depends on them, so the choices are those of the formulas in exact arithmetic but for numbers that
- * lie within that distance of a border.  Tokens of less than 2^-44 of the first one's probability count as having none.
+ * (prism_tokens_last_device_status: PRISM_ERR_DEVICE).  Masses are multiples of 2^-44 of the first token's (of 2^-(63 - b) for V up
+ * to 2^b beyond 2^19), added up without rounding.  Wherever a border comes nearer to a token's edge than the machine's exponential
+ * can tell, they are within two of these units, so the choices are those of the formulas in exact arithmetic but for numbers within
+ * some units a token of a border; tokens of less mass than half a unit count as having none.
  */
 PRISM_API prism_status prism_sample(prism_tokens_t tokens, int n, const void *logits, long long ld, const float *u,
                                     const float *inv_temperature, const int *top_k, const float *top_p, const float *min_p,

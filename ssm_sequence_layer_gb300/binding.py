@@ -857,6 +857,8 @@ class Tokens:
                 if key not in ("y", "pre"):
                     raise ValueError(f"prism_linear has no output {key!r}")
                 need(key, t, io, M * N, N)
+            if "y" not in out:
+                raise ValueError("prism_linear's outputs must have y among them")
         prism_linear(self.handle, M, N, K, x, W, bias, self._activation(activation), residual, out["y"], out.get("pre"),
                      self._current_stream(self.device))
         return out
@@ -913,6 +915,8 @@ class Tokens:
                 if key not in ("dW", "dbias"):
                     raise ValueError(f"prism_linear_weight_backward has no output {key!r}")
                 need(key, t, f32, N * K if key == "dW" else N, K if key == "dW" else N)
+            if "dW" not in out:
+                raise ValueError("prism_linear_weight_backward's outputs must have dW among them")
         prism_linear_weight_backward(self.handle, M, N, K, dy, x, accumulate, out["dW"], out.get("dbias"),
                                      self._current_stream(self.device))
         return out
@@ -1022,6 +1026,8 @@ class Tokens:
                     self._need(key, t, f32, d)
                 elif key != "dx":
                     raise ValueError(f"prism_heads_backward has no output {key!r}")
+            if "dx" not in out:
+                raise ValueError("prism_heads_backward's outputs must have dx among them")
         Bd, Td, ld_dx = self._row_stride("dx", out["dx"], width)
         if (Bd, Td) != (B, T):
             raise ValueError("dx must have x's rows")
@@ -1069,6 +1075,8 @@ class Tokens:
                 if key not in types:
                     raise ValueError(f"prism_sample has no output {key!r}")
                 need(key, t, types[key], n)
+            if "ids" not in out:
+                raise ValueError("prism_sample's outputs must have ids among them")
         prism_sample(self.handle, n, logits, ld, u, *rules, out["ids"], out.get("logprob"), out.get("kept"),
                      self._current_stream(self.device))
         return out

@@ -315,19 +315,35 @@ struct SoftHalf {
     {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
     }
-    __device__ __forceinline__ void ask(uint32_t raw, int r0, int c0) const
+    // the thread's row of step 0 and its column, in the matrix, of the half that is copied next
+    int row0, col0;
+    long long from;
+    __device__ __forceinline__ void seek(int r0, int c0)
     {
+        row0 = r0 + row_of(0), col0 = c0 + column();
+        from = (long long)row0 * ld + col0;
+    }
+    __device__ __forceinline__ void advance()  // by a half along the sum
+    {
+        if constexpr (MN) row0 += 32, from += 32 * ld;
+        else col0 += 32, from += 32;
+    }
+    __device__ __forceinline__ void ask(uint32_t raw) const
+    {
+        const bool inside = col0 < cols;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            const int r = r0 + row_of(i), c = c0 + column();
-            const bool in = r < rows && c < cols;
-            const long long at = in ? (long long)r * ld + c : 0;
+            const bool in = inside && row0 + i * (THREADS / PER_ROW) < rows;
+            const long long at = in ? from + i * (THREADS / PER_ROW) * ld : 0;
             if constexpr (sizeof(io_t) == 4) {
                 if (whole) {  // columns come in whole units too
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(unit_at(raw, i)), "l"(base + at), "r"(in ? 16 : 0) : "memory");
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) copy(word_at(raw, i, e), base + (in && c + e < cols ? at + e : 0), in && c + e < cols ? 4 : 0);
+                    for (int e = 0; e < 4; ++e) {
+                        const bool need = in && col0 + e < cols;
+                        copy(word_at(raw, i, e), base + at + (need ? e : 0), need ? 4 : 0);
+                    }
                 }
             } else {
                 // the words that hold the four values; the matrix may end in the middle of one
@@ -340,20 +356,30 @@ struct SoftHalf {
             }
         }
     }
+    // what came, into registers
+    struct Words {
+        uint32_t x[STEPS][4];
+    };
+    __device__ __forceinline__ void fetch(uint32_t raw, Words &w) const
+    {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            if (sizeof(io_t) == 4 && whole) {
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x[i][0]), "=r"(w.x[i][1]), "=r"(w.x[i][2]), "=r"(w.x[i][3]) : "r"(unit_at(raw, i)));
+            } else {
+#pragma unroll
+                for (int e = 0; e < (sizeof(io_t) == 4 ? 4 : 3); ++e) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.x[i][e]) : "r"(word_at(raw, i, e)));
+            }
+        }
+    }
     // into half `half` of panels of 64 values, 128-byte swizzled; the parts of float32 are part_bytes apart.  sums: of the thread's columns
-    __device__ __forceinline__ void bring(uint8_t *to, uint32_t part_bytes, uint32_t raw, int half, int r0, int c0, bool add, float (&sums)[4]) const
+    __device__ __forceinline__ void bring(uint8_t *to, uint32_t part_bytes, const Words &w, int half, int r0, int c0, bool add, float (&sums)[4]) const
     {
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             const int r = row_of(i), c = column();
             uint8_t *at = MN ? to + (c >> 6) * kPanel + sw128(r + 32 * half, c & 63) : to + sw128(r, c + 32 * half);
-            uint32_t x[4];
-            if (sizeof(io_t) == 4 && whole) {
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(unit_at(raw, i)));
-            } else {
-#pragma unroll
-                for (int e = 0; e < (sizeof(io_t) == 4 ? 4 : 3); ++e) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[e]) : "r"(word_at(raw, i, e)));
-            }
+            const uint32_t(&x)[4] = w.x[i];
             float f[4];
             if constexpr (sizeof(io_t) == 2) {
                 const bool odd = (((long long)(r0 + r) * ld + c0 + c) & 1) && r0 + r < rows && c0 + c < cols;
@@ -879,8 +905,8 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         if constexpr (SOFT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoaderRegs));
         const int thread = tid - 128 - 32 * L::FINISHERS;
         // rows and columns of the matrices in memory: the sum runs along a row (K-major) or from row to row
-        const SoftHalf<io_t, A_MN> ta(p.a, p.lda, A_MN ? p.K : p.I, A_MN ? p.I : p.K, thread);
-        const SoftHalf<io_t, B_MN> tb(p.b, p.ldb, B_MN ? p.K : p.J, B_MN ? p.J : p.K, thread);
+        SoftHalf<io_t, A_MN> ta(p.a, p.lda, A_MN ? p.K : p.I, A_MN ? p.I : p.K, thread);
+        SoftHalf<io_t, B_MN> tb(p.b, p.ldb, B_MN ? p.K : p.J, B_MN ? p.J : p.K, thread);
         float column[4] = {}, unused[4];
         const uint32_t raws = sbase + L::OFF_RAW;
         struct At {
@@ -895,14 +921,22 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         At next{0, b_from, 0, 0}, now;
         tile_at(0, next.i0, next.j0);
         now = next;
+        auto seek = [&] {
+            const int k = next.b * L::BLOCK;
+            ta.seek(A_MN ? k : next.i0, A_MN ? next.i0 : k);
+            tb.seek(B_MN ? k : next.j0, B_MN ? next.j0 : k);
+        };
+        seek();
         long long asked = 0;
         auto ask = [&] {
             if (asked < total) {
                 const uint32_t raw = raws + (uint32_t)(asked % L::RAWS) * L::RAW;
-                const int k = next.b * L::BLOCK;
-                ta.ask(raw, A_MN ? k : next.i0, A_MN ? next.i0 : k);
-                tb.ask(raw + L::RAW / 2, B_MN ? k : next.j0, B_MN ? next.j0 : k);
+                ta.ask(raw);
+                tb.ask(raw + L::RAW / 2);
+                const int tile = next.i;
                 step(next);
+                if (next.i == tile) ta.advance(), tb.advance();
+                else seek();
             }
             ++asked;
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -912,15 +946,18 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             const int s = (int)(g & 1);
             ask();
             asm volatile("cp.async.wait_group %0;" ::"n"(L::RAWS - 1) : "memory");
+            const uint32_t raw = raws + (uint32_t)(g % L::RAWS) * L::RAW;
+            typename SoftHalf<io_t, A_MN>::Words wa;
+            typename SoftHalf<io_t, B_MN>::Words wb;
+            ta.fetch(raw, wa), tb.fetch(raw + L::RAW / 2, wb);  // on their way while the half is waited for
             const bool ok = g < 2 || mbar_wait(smem_u32(&freed[s]), (uint32_t)((g - 2) >> 1) & 1, wt.ns);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) give_up();
                 break;
             }
-            const uint32_t raw = raws + (uint32_t)(g % L::RAWS) * L::RAW;
             const int k = now.b * L::BLOCK;
-            ta.bring(sm, L::A_PART, raw, s, A_MN ? k : now.i0, A_MN ? now.i0 : k, sums, column);
-            tb.bring(sm + PARTS * L::A_PART, L::B_PART, raw + L::RAW / 2, s, B_MN ? k : now.j0, B_MN ? now.j0 : k, false, unused);
+            ta.bring(sm, L::A_PART, wa, s, A_MN ? k : now.i0, A_MN ? now.i0 : k, sums, column);
+            tb.bring(sm + PARTS * L::A_PART, L::B_PART, wb, s, B_MN ? k : now.j0, B_MN ? now.j0 : k, false, unused);
             step(now);
             fence_async_smem();
             __syncwarp();

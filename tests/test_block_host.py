@@ -119,7 +119,7 @@ def test_names_and_missing_tensors_are_refused(tokens, monkeypatch):  # noqa: F8
            ("linear_backward", dict(pre=None)), ("linear_backward", dict(activation="tanh")),
            ("linear_weight_backward", dict(out=None, accumulate=True)), ("linear_weight_backward", dict(out=None, want=("dbias",))),
            ("heads", dict(norm="layer")), ("heads", dict(out={"q": plain["heads"]["out"]["q"]})), ("heads_backward", dict(out={"dx": plain["heads"]["x"], "dz": 0})),
-           ("sample", dict(out={"id": 0}))]
+           ("sample", dict(out={"id": 0})), ("sample", dict(out={})), ("linear", dict(out={})), ("linear_weight_backward", dict(out={})), ("heads_backward", dict(out={}))]
     for method, change in bad:
         with pytest.raises(ValueError):
             getattr(tokens, method)(**{**plain[method], **change})
