@@ -150,6 +150,17 @@ struct Mass {
         return close_whole(main, rest);
     }
     __device__ __forceinline__ u64 close_slack(u64 all, int V) const { return (all >> 28) + 4 * (u64)V; }
+    // the logarithm of a token's share of a mass: (l - top) c - log of the mass's power of two, the parts of both kept, - log of its leading bits
+    __device__ __forceinline__ float log_share(float l, u64 all) const
+    {
+        float dh, dl;
+        below(l, dh, dl);
+        const float xh = dh * c, xl = fmaf(dh, c, -xh) + dl * c;
+        const int power = 63 - __clzll(all);
+        const float n = (float)(power - fraction), f = (float)(all << (63 - power)) * 0x1p-63f;
+        const float h = n * 0x1.62ep-1f, a = xh - h, back = a - xh;  // log 2 in two parts, the first product exact
+        return a + (((xh - (a - back)) + (-h - back)) + (xl - fmaf(n, 3.194618495e-05f, logf(f))));
+    }
     // How far sums of rough masses may be off, of tokens V of mass `all`: 2^-22 of the exponential, 2^-22.4 of adding up eight at a
     // time, and 2^-25 times the mean distance in halvings, which is log2 V at most
     __device__ __forceinline__ u64 slack(u64 all, int V) const { return (all >> 20) + (all >> 22) + V; }
@@ -193,6 +204,9 @@ struct Shared {
     union {
         uint32_t count[kBuckets];
         int rank[CANDIDATES];
+        struct {
+            u64 masses[kCounted], below[kCounted];  // of a short list: a token's mass, and that of all up to its id
+        };
     };
     union {
         struct {
@@ -622,11 +636,7 @@ __device__ Drawn draw_token(S &s, const R &row, const Mass &m, const Rules &rule
     Drawn d;
     d.id = s.at, d.sure = s.flag, d.kept = 0;
     d.logprob = 0.f;
-    if (tid == 0) {  // log of the mass: of its leading bits in float32, of its power of two and the token's own in 64 bits
-        const int power = 63 - __clzll(all);
-        const float f = (float)(all << (63 - power)) * 0x1p-63f;  // 1 .. 2
-        d.logprob = (float)(((double)s.top - (double)m.top) * (double)m.c - (double)(power - m.fraction) * 0.69314718055994531 - (double)logf(f));
-    }
+    if (tid == 0) d.logprob = m.log_share(s.top, all);
     __syncthreads();
     return d;
 }
@@ -674,11 +684,44 @@ __device__ __noinline__ Drawn draw_row(S &s, const R &row, const Mass &m, const 
     return d;
 }
 
+// The draw from a short list in order, all of whose first `keep` tokens are kept: each counts the mass up to its id, with all threads at work
+template <int NT, typename S, typename R, int PER>
+__device__ Drawn draw_listed(S &s, const R &row, const Mass &m, const Rules &rules, uint32_t keep, const u64 (&e)[PER], u64 list_before)
+{
+    const int tid = threadIdx.x;
+    u64 at = list_before;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        at += e[i];
+        const uint32_t j = PER * tid + i;
+        if (j < keep) s.masses[j] = e[i], s.below[j] = 0;
+        if (j + 1 == keep) s.mass = at;
+    }
+    __syncthreads();
+    const u64 all = s.mass, target = rules.target(all);
+    int across = 32;
+    while (across < (int)keep) across *= 2;
+    const int i = tid % across, per = ((int)keep + NT / across - 1) / (NT / across), from = tid / across * per;
+    if (i < (int)keep) {
+        const int id = id_in(s.list[i]);
+        u64 sum = 0;
+        for (int o = from; o < min((int)keep, from + per); ++o) sum += id_in(s.list[o]) <= id ? s.masses[o] : 0;
+        if (sum > 0) atomicAdd(&s.below[i], sum);
+    }
+    __syncthreads();
+    if (tid < (int)keep && s.below[tid] > target && s.below[tid] - s.masses[tid] <= target) s.at = id_in(s.list[tid]), s.top = logit_of(order_in(s.list[tid]));
+    __syncthreads();
+    Drawn d;
+    d.id = s.at, d.kept = keep, d.sure = true, d.logprob = 0.f;
+    if (tid == 0) d.logprob = m.log_share(s.top, all);
+    return d;
+}
+
 // The row in three passes where that is enough: its largest logit (the caller); numbers of tokens by distance from it, and the
 // masses' sum if top-p asks for it; the masses of those that are kept for certain, while those among which the borders lie
 // (the window, all candidates where they are few) are listed, to be put in order.
 template <int NT, typename S, typename R>
-__device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, uint32_t &live, bool &done)
+__device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, float own, uint32_t &live, bool &done)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool by_p = rules.p < 1.f, by_min = rules.min_p > 0.f;
@@ -687,17 +730,66 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, uin
     int first = kBuckets, last = kBuckets - 1;  // the window's buckets: empty
     u64 total = 0;                              // of all masses, quick ones
     uint32_t sure_n = 0, listed_n = 0;
-    if (by_p || by_k || by_min) {
+    constexpr int VEC = R::VEC;
+    auto rough_sum = [&](const float (&l)[VEC]) {
+        float e[VEC];
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) e[q] = l[q] > m.mask ? m.rough(l[q]) : 0.f;
+        return m.whole(sum_of<VEC>(e));
+    };
+    // Candidates by a bound where the rules give one: k of the threads' own largest logits that lie above it, or min_p.  (Counting all
+    // tokens' buckets takes 10000 cycles of a row of 50021, the threads' largest 1500.)
+    bool few = false;
+    if ((by_k && rules.k <= NT * 3 / 4) || (by_min && !by_k)) {
+        float low = -INFINITY;
+        bool found = true;
+        if (tid == 0) s.number = 0, s.at = -1;
+        if (by_k) {
+            for (int i = tid; i < kBuckets; i += NT) s.count[i] = 0;
+            __syncthreads();
+            if (own > m.mask) atomicAdd(&s.count[m.bucket(own)], 1u);
+            __syncthreads();
+            uint32_t n[EACH], nn = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) n[i] = s.count[EACH * tid + i], nn += n[i];
+            uint32_t at_n = block_scan<NT>(nn, s.counts) - nn;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                if (at_n < rules.k && at_n + n[i] >= rules.k) s.at = EACH * tid + i;
+                at_n += n[i];
+            }
+            __syncthreads();
+            found = s.at >= 0 && s.at + 1 < kBuckets;  // the last bucket has no lower end
+            low = -((float)s.at + 1.05f) / kPerOctave;
+        }
+        if (by_min && !(by_k && by_p)) low = fmaxf(low, rules.log_min_p * 1.442695f * 1.0001f - 1e-4f);  // the first k are needed for their mass
+        if (found) {
+            if (by_p && !by_k) {
+                row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { total += rough_sum(l); });
+                uint32_t none = 0;
+                block_sums<NT>(s, total, none);
+            }
+            __syncthreads();
+            row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int id) {
+#pragma unroll
+                for (int q = 0; q < VEC; ++q)
+                    if (m.log_of(l[q]) >= low && l[q] > m.mask) {
+                        const uint32_t to = atomicAdd(&s.number, 1u);
+                        if (to < S::kCandidates) s.list[to] = listed(order_of(l[q]), id + q);
+                    }
+            });
+            __syncthreads();
+            listed_n = s.number;
+            few = listed_n <= S::kCandidates;
+            if (few) first = 0, live = row.V + 1;  // k of them at least are live
+            else listed_n = 0, total = 0;
+            __syncthreads();
+        }
+    }
+    if (!few && (by_p || by_k || by_min)) {
         for (int i = tid; i < kBuckets; i += NT) s.count[i] = s.lo[i] = 0;
         if (tid == 0) s.first = 0, s.last = kBuckets - 1, s.number = 0;
         __syncthreads();
-        constexpr int VEC = R::VEC;
-        auto rough_sum = [&](const float (&l)[VEC]) {
-            float e[VEC];
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) e[q] = l[q] > m.mask ? m.rough(l[q]) : 0.f;
-            return m.whole(sum_of<VEC>(e));
-        };
         // with top-p the places within the buckets are added up too, which brings the masses' bounds together
         auto count_places = [&](const float (&l)[VEC]) {
 #pragma unroll
@@ -731,7 +823,11 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, uin
             down[i] = b + 1 == kBuckets ? 0.f : whole * (places ? 1.f - t : 0.97857f), dd += down[i];
         }
         uint32_t at_n = block_scan<NT>(nn, s.counts) - nn;
-        float at_u = block_scan<NT>(uu, reinterpret_cast<float *>(s.sums)) - uu, at_d = block_scan<NT>(dd, reinterpret_cast<float *>(s.more)) - dd;
+        float at_u = 0.f, at_d = 0.f;
+        if (by_p && !by_k) {
+            at_u = block_scan<NT>(uu, reinterpret_cast<float *>(s.sums)) - uu;
+            at_d = block_scan<NT>(dd, reinterpret_cast<float *>(s.more)) - dd;
+        }
         if (tid == NT - 1) s.number_before = at_n + nn;
         __syncthreads();
         live = s.number_before;
@@ -790,7 +886,6 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, uin
     row.range(warp, NT / 32, u0, u1);
     u64 mine = 0;
     uint32_t passed = 0;
-    constexpr int VEC = R::VEC;
     auto list_up = [&](float l, int id) {
         if (l > m.mask) s.list[atomicAdd(&s.number, 1u)] = listed(order_of(l), id);
     };
@@ -804,6 +899,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, uin
             }
             mine += m.whole(sum_of<VEC>(e));
         });
+    } else if (few) {
     } else if (first == 0) {
         row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int id) {
 #pragma unroll
@@ -865,11 +961,14 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, uin
             uint32_t none = 0;
             block_sums<NT>(s, total, none);
         }
-        u64 sure_mass = mine;
-        uint32_t none = 0;
-        block_sums<NT>(s, sure_mass, none);
-        const u64 warp_mass = s.sums[warp];
-        __syncthreads();
+        u64 sure_mass = 0, warp_mass = 0;
+        if (first > 0) {
+            uint32_t none = 0;
+            sure_mass = mine;
+            block_sums<NT>(s, sure_mass, none);
+            warp_mass = s.sums[warp];
+            __syncthreads();
+        }
         // the number of the list's tokens that are kept
         uint32_t keep = listed_n;
         if (listed_n > 0) {
@@ -918,6 +1017,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, uin
             }
             keep = max(keep, 1u);
         }
+        if (first == 0 && keep <= kCounted) return draw_listed<NT>(s, row, m, rules, keep, e, list_before);
         // the warps' masses with the list's share
         Cut cut{INT_MAX, -1, 0};  // of the window's tokens
         if (keep > 0 && listed_n > 0) cut = Cut{order_in(s.list[keep - 1]), id_in(s.list[keep - 1]), 0};
@@ -959,6 +1059,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const Params<T> p
 #pragma unroll
         for (int e = 0; e < R::VEC; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(l[e]));
     });
+    const float own = top;
     // as whole numbers, of which the one NaN that max.NaN gives is the largest
     const int warp_top = __reduce_max_sync(0xffffffffu, order_of(top));
     if (lane == 0) s.counts[warp] = warp_top;
@@ -988,7 +1089,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const Params<T> p
     if (rules.min_p > 1.f) rules.k = 1, rules.p = 1.f, rules.min_p = 0.f;  // nothing reaches it: the first token alone
     uint32_t live = 0;
     bool done = true;
-    Drawn d = draw_window<NT>(s, row, m, rules, live, done);
+    Drawn d = draw_window<NT>(s, row, m, rules, own, live, done);
     if (!done) {
         __syncthreads();
         d = draw_row<NT>(s, row, m, rules, live, false);

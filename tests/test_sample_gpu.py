@@ -111,6 +111,28 @@ def test_flat_rows(io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [300, 5003, 50021])
+def test_orders_and_ties_around_the_kth(io, V):
+    """The kth largest among sorted logits, in a crowd of equal ones, and where only a handful of neighbours is above the mask, for k on both
+    sides of the sizes at which the kernel's ways part; min-p that many tokens, and all of them, reach."""
+    x, u, c, g = rows(12, V, io, 3 * V)
+    x[0] = torch.sort(x[0].float(), descending=True)[0].to(x.dtype)
+    x[1] = torch.sort(x[1].float())[0].to(x.dtype)
+    x[2, 100:] = x[2, 100:].clamp(max=0.5)  # many equal ones below few
+    x[3, 10:] = -float("inf")
+    x[4] = 0.25
+    x[5] = torch.linspace(4, -60, V).to(x.dtype)
+    for k in (1, 2, 10, 11, 191, 192, 193, 256, 257, 383, 384, 385, 767, 768, 769, 1024, 1025):
+        kk = torch.full((12,), k, dtype=torch.int32)
+        check(x, u, c, kk)
+        check(x, u, c, kk, torch.full((12,), 0.9))
+        check(x, u, c, kk, None, torch.full((12,), 0.02))
+    for m in (1e-30, 1e-6, 0.3):
+        check(x, u, c, None, None, torch.full((12,), m))
+        check(x, u, c, None, torch.full((12,), 0.8), torch.full((12,), m))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_ends_of_the_rules(io):
     n, V = 12, 500
     x, u, c, _ = rows(n, V, io, 8)
