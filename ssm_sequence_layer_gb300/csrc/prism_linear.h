@@ -290,8 +290,8 @@ __device__ __forceinline__ float without_leading(float a) { return a - __uint_as
 // A thread copies four values of a row at a time into shared memory of its own, two halves ahead and without waiting for them
 // (cp.async: 16 bytes where rows are whole units, else words of 4, of which bfloat16 rows may start in the middle of one), and
 // later brings its values to the form that the tensor core reads.  Both ways no two lanes of a phase meet in a bank: words lie
-// beside the other threads' words, and the four rows that a warp brings at once are 0, 1, 4 and 5 of eight, whose swizzled halves
-// fill all banks.
+// beside the other threads' words, and along the sum the two rows that half a warp brings at once are four apart, so that their swizzled
+// halves fill all banks.
 template <typename io_t, bool MN>
 struct SoftHalf {
     static constexpr int C = MN ? 128 : 32, PER_ROW = C / 4, THREADS = 32 * kLoaderWarps, STEPS = 1024 / THREADS;
@@ -306,7 +306,7 @@ struct SoftHalf {
     __device__ __forceinline__ int row_of(int step) const
     {
         const int q = thread / PER_ROW;
-        return (MN ? q : (q & ~6) | (q & 2) << 1 | (q & 4) >> 1) + step * (THREADS / PER_ROW);
+        return (MN ? q : (q & ~7) | (q & 1) << 2 | (q & 6) >> 1) + step * (THREADS / PER_ROW);
     }
     __device__ __forceinline__ int column() const { return thread % PER_ROW * 4; }
     __device__ __forceinline__ uint32_t unit_at(uint32_t raw, int step) const { return raw + (step * THREADS + thread) * 16; }
