@@ -189,7 +189,7 @@ cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
                 if (best == 0 || time < best) best = time, c.pair = pair, c.bn = bn, c.splits = s;
             }
         };
-        consider(false, 128, sizeof(io_t) == 4 ? 3000 : c.soft ? 1500 : 540);
+        consider(false, 128, sizeof(io_t) == 4 ? 4700 : c.soft ? 3600 : 540);
         // the sums over rows need tensor memory beside the accumulators, which tiles of 256 columns leave none of
         if (!c.soft) consider(true, 192, 430);
         if (!c.soft && !p.dbias) consider(false, 256, 800), consider(true, 256, 560);

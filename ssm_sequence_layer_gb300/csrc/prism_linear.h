@@ -235,7 +235,7 @@ struct Waits {
 };
 
 constexpr int BM = 128, BK = 64;
-constexpr int kLoaderWarps = 8;
+constexpr int kLoaderWarps = 16;
 constexpr uint32_t kPanel = BK * 128;  // an MN-major panel: 64 rows (of the sum) x 64 values
 
 template <typename io_t, LinearOp OP, bool SOFT, int BN, bool PAIR>
@@ -245,25 +245,27 @@ struct Layout {
     static constexpr uint32_t A_PART = BM * 128, B_PART = ((PAIR ? BN / 2 : BN) + 63) / 64 * 64 * 128, STAGE = PARTS * (A_PART + B_PART);
     // the addends' pieces of a warp, two on their way
     static constexpr bool INCOMING = !SOFT && OP != LinearOp::weights;
-    // SOFT: one stage, whose halves are filled and freed one by one, and raw values on their way for three halves
-    static constexpr int BLOCK = SOFT ? 32 : BK, RAWS = SOFT ? 3 : 0;
+    // SOFT: stages' halves are filled and freed one by one; float32 rows of whole units pass the second stage on their way, which has
+    // room for three halves
+    static constexpr int BLOCK = SOFT ? 32 : BK;
     static constexpr uint32_t RAW = 32768, OFF_RAW = STAGE;
+    static_assert(!SOFT || PARTS == 1 || STAGE == 3 * RAW, "halves on their way");
     static constexpr int GROUP = PARTS == 3 ? 256 / BLOCK : 512 / BLOCK;  // blocks that share an accumulator where its sums go on in registers
-    static constexpr int STAGES = SOFT ? 2 : (INCOMING && STAGE <= 32768 ? 163840 : 196608) / STAGE - (INCOMING && STAGE > 32768 ? 1 : 0);
+    static constexpr int STAGES = SOFT ? (PARTS == 3 ? 4 : 8) : (INCOMING && STAGE <= 32768 ? 163840 : 196608) / STAGE - (INCOMING && STAGE > 32768 ? 1 : 0);
     // The warps that finish tiles: each element of an activation takes about 25 instructions one after the other, which two warps a
     // scheduler do not hide; where the sums go on in registers there is room for eight.
     static constexpr int FINISHERS = INCOMING ? 16 : 8, FINISHED = BN / (FINISHERS / 4);  // and a warp's columns
     static constexpr uint32_t OUT_WARP = 4096;  // a warp's staging: outputs of 32 x 32 values of 4 bytes, or two times 2 bytes, the second for addends
-    static constexpr uint32_t OFF_OUT = SOFT ? STAGE + RAWS * RAW : STAGES * STAGE;
+    static constexpr uint32_t OFF_OUT = SOFT ? STAGES / 2 * STAGE : STAGES * STAGE;
     static constexpr uint32_t SMEM = OFF_OUT + (OP == LinearOp::weights ? 2048 : FINISHERS * OUT_WARP) + 1024;  // + alignment slack
     static constexpr int THREADS = 128 + 32 * FINISHERS + (SOFT ? 32 * kLoaderWarps : 0);
     static constexpr int kColumns = 512;  // of tensor memory: two accumulators, and two for the small products or the sums over rows
     static constexpr int SUMS = OP == LinearOp::weights && !SOFT && 2 * BN + 32 <= kColumns ? 2 * BN : 0;
     // registers handed over to the warps that finish tiles, from the issuing ones
-    static constexpr int kLaunchRegs = SOFT || INCOMING ? 96 : 168, kIssueRegs = SOFT || INCOMING ? 40 : 56,
-                         kEpilogueRegs = SOFT ? 152 : INCOMING ? 104 : 224, kLoaderRegs = 64;
+    static constexpr int kLaunchRegs = SOFT ? 72 : INCOMING ? 96 : 168, kIssueRegs = SOFT || INCOMING ? 40 : 56,
+                         kEpilogueRegs = SOFT ? 136 : INCOMING ? 104 : 224, kLoaderRegs = 48;
     static_assert(128 * kIssueRegs + 32 * FINISHERS * kEpilogueRegs + (SOFT ? 32 * kLoaderWarps * kLoaderRegs : 0) <= THREADS * kLaunchRegs, "registers");
-    static_assert(STAGES >= 2 && SMEM + (OP == LinearOp::weights ? 3072 : 1024) <= 232448 && OFF_OUT % 1024 == 0, "layout");
+    static_assert(STAGES >= 2 && SMEM + (OP == LinearOp::weights && SOFT ? 9216 : 1024) <= 232448 && OFF_OUT % 1024 == 0, "layout");
 };
 
 // one look at a barrier's phase
@@ -286,131 +288,167 @@ __device__ __forceinline__ uint32_t leading(float a, float b)
 __device__ __forceinline__ float without_leading(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
 
 // ---- operands through registers ------------------------------------------------------------------------
-// Half a stage of an operand: R rows x C values of a row-major matrix (128 x 32 along the sum, or 32 x 128 across it), cut to (rows, cols).
-// A thread copies four values of a row at a time into shared memory of its own, two halves ahead and without waiting for them
-// (cp.async: 16 bytes where rows are whole units, else words of 4, of which bfloat16 rows may start in the middle of one), and
-// later brings its values to the form that the tensor core reads.  Both ways no two lanes of a phase meet in a bank: words lie
-// beside the other threads' words, and along the sum the two rows that half a warp brings at once are four apart, so that their swizzled
-// halves fill all banks.
+// Half a stage of an operand: R rows x C values of a row-major matrix (128 x 32 along the sum, or 32 x 128 across it), cut to (rows, cols);
+// what lies outside is zero.  A thread has eight of its values in registers and stores them, in the form that the tensor core reads, when
+// their place is free.  Rows that are whole units of four values come four at a time.  Others come as segments, one value a lane and 32
+// neighbours of a row at once, whatever their alignment; lanes then trade values with their neighbours so that each has two of one row.
+// Either way the two rows that half a warp stores to at once are four apart (or lie across the sum), so that their swizzled halves fill
+// all banks.
+// float32 rows of whole units pass through shared memory of the thread's own, two halves ahead (cp.async of 16 bytes); others are loaded
+// into the registers as soon as these are free.  Microseconds of 4096 x 4096 x 4096 (float32) and 4096 x 4095 x 4097 (float32, bfloat16),
+// forward / dx / dW:
+//   this                                                  1064 / 1138 / 1054    1320 / 1668 / 1087     872 / 921 / 818
+//   all rows straight into registers                      1343 / 1335 / 994     1674 / 1587 / 1216
+//   all by cp.async, of 4 bytes where rows are not whole  1063 / 1215 / 1142    1387 / 1557 / 1633    1282 / 1405 / 1365
+// What bounds it is shared memory: of about 2300 cycles a half of float32, the products' operands take 770 and the values' ways 900.
 template <typename io_t, bool MN>
 struct SoftHalf {
-    static constexpr int C = MN ? 128 : 32, PER_ROW = C / 4, THREADS = 32 * kLoaderWarps, STEPS = 1024 / THREADS;
+    static constexpr int STEP = 32 * kLoaderWarps / (MN ? 32 : 8);  // rows between a thread's two groups of four
     const io_t *base;
-    long long ld, last;  // last: elements of the matrix
-    int rows, cols, thread;
+    long long ld;
+    int rows, cols, warp, lane;
     bool whole;
-    __device__ __forceinline__ SoftHalf(const io_t *base_, long long ld_, int rows_, int cols_, int thread_)
-        : base(base_), ld(ld_), last(ld_ * rows_), rows(rows_), cols(cols_), thread(thread_), whole(ld_ * sizeof(io_t) % 16 == 0)
+    __device__ __forceinline__ SoftHalf(const io_t *base_, long long ld_, int rows_, int cols_, int thread)
+        : base(base_), ld(ld_), rows(rows_), cols(cols_), warp(thread >> 5), lane(thread & 31), whole(ld_ % 4 == 0)
     {
     }
-    __device__ __forceinline__ int row_of(int step) const
+    // the thread's first value in the half
+    __device__ __forceinline__ int own_row() const
     {
-        const int q = thread / PER_ROW;
-        return (MN ? q : (q & ~7) | (q & 1) << 2 | (q & 6) >> 1) + step * (THREADS / PER_ROW);
+        if (whole) return MN ? warp : (warp >> 1) * 8 + (lane >> 3 & 1) * 4 + (warp & 1) * 2 + (lane >> 4);
+        return MN ? (warp & 3) + 8 * (warp >> 2) : 8 * warp;
     }
-    __device__ __forceinline__ int column() const { return thread % PER_ROW * 4; }
-    __device__ __forceinline__ uint32_t unit_at(uint32_t raw, int step) const { return raw + (step * THREADS + thread) * 16; }
-    __device__ __forceinline__ uint32_t word_at(uint32_t raw, int step, int word) const { return raw + step * THREADS * 16 + word * THREADS * 4 + thread * 4; }
-    static __device__ __forceinline__ void copy(uint32_t to, const void *from, int bytes)
-    {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-    }
-    // the thread's row of step 0 and its column, in the matrix, of the half that is copied next
-    int row0, col0;
-    long long from;
+    __device__ __forceinline__ int own_column() const { return whole ? 4 * (MN ? lane : lane & 7) : lane; }
+    // the half that is asked for or loaded next: its block of the sum, its tile, its first row and column in the matrix and the place of
+    // the thread's first value
+    int block, tile, row0, col0;
+    const io_t *at;
     __device__ __forceinline__ void seek(int r0, int c0)
     {
-        row0 = r0 + row_of(0), col0 = c0 + column();
-        from = (long long)row0 * ld + col0;
+        row0 = r0, col0 = c0;
+        at = base + (long long)(r0 + own_row()) * ld + c0 + own_column();
     }
     __device__ __forceinline__ void advance()  // by a half along the sum
     {
-        if constexpr (MN) row0 += 32, from += 32 * ld;
-        else col0 += 32, from += 32;
+        if constexpr (MN) row0 += 32, at += 32 * ld;
+        else col0 += 32, at += 32;
     }
-    __device__ __forceinline__ void ask(uint32_t raw) const
+    __device__ __forceinline__ bool has(int r, int c) const { return row0 + own_row() + r < rows && col0 + own_column() + c < cols; }
+    struct Words {
+        uint32_t x[8];
+    };
+    // straight into registers
+    __device__ __forceinline__ void load(Words &w) const
     {
-        const bool inside = col0 < cols;
+        if (whole) {  // bfloat16
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const bool in = inside && row0 + i * (THREADS / PER_ROW) < rows;
-            const long long at = in ? from + i * (THREADS / PER_ROW) * ld : 0;
-            if constexpr (sizeof(io_t) == 4) {
-                if (whole) {  // columns come in whole units too
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(unit_at(raw, i)), "l"(base + at), "r"(in ? 16 : 0) : "memory");
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool need = in && col0 + e < cols;
-                        copy(word_at(raw, i, e), base + at + (need ? e : 0), need ? 4 : 0);
-                    }
-                }
-            } else {
-                // the words that hold the four values; the matrix may end in the middle of one
-                const long long word = at & ~1ll;
-#pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    const bool need = in && word + 2 * e < last && word + 2 * e < at + 4;
-                    copy(word_at(raw, i, e), base + (need ? word + 2 * e : 0), need ? (word + 2 * e + 1 < last ? 4 : 2) : 0);
-                }
+            for (int i = 0; i < 2; ++i) {
+                const uint2 u = has(i * STEP, 0) ? *reinterpret_cast<const uint2 *>(at + i * STEP * ld) : make_uint2(0, 0);
+                w.x[2 * i] = u.x, w.x[2 * i + 1] = u.y;
             }
+        } else if (row0 + (MN ? 32 : 128) <= rows && col0 + (MN ? 128 : 32) <= cols) {
+            single(w, [&](int, int) { return true; });
+        } else {
+            single(w, [&](int r, int c) { return has(r, c); });
         }
     }
-    // what came, into registers
-    struct Words {
-        uint32_t x[STEPS][4];
-    };
+    template <typename F>
+    __device__ __forceinline__ void single(Words &w, F in) const
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = MN ? 4 * h : j + 4 * h, c = MN ? 32 * j : 0;
+                const io_t *p = at + r * ld + c;
+                uint32_t x = 0;
+                if (in(r, c)) {
+                    if constexpr (sizeof(io_t) == 4) x = *reinterpret_cast<const uint32_t *>(p);
+                    else x = *reinterpret_cast<const uint16_t *>(p);
+                }
+                w.x[2 * j + h] = x;
+            }
+    }
+    // float32 in whole units: into shared memory, a thread's values side by side, and from there into registers
+    __device__ __forceinline__ uint32_t group_at(uint32_t raw, int i) const { return raw + (32 * kLoaderWarps * i + 32 * warp + lane) * 16; }
+    __device__ __forceinline__ void ask(uint32_t raw) const
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool in = has(i * STEP, 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(group_at(raw, i)), "l"(in ? at + i * STEP * ld : base), "r"(in ? 16 : 0) : "memory");
+        }
+    }
     __device__ __forceinline__ void fetch(uint32_t raw, Words &w) const
     {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            if (sizeof(io_t) == 4 && whole) {
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x[i][0]), "=r"(w.x[i][1]), "=r"(w.x[i][2]), "=r"(w.x[i][3]) : "r"(unit_at(raw, i)));
-            } else {
-#pragma unroll
-                for (int e = 0; e < (sizeof(io_t) == 4 ? 4 : 3); ++e) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.x[i][e]) : "r"(word_at(raw, i, e)));
-            }
-        }
+        for (int i = 0; i < 2; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x[4 * i]), "=r"(w.x[4 * i + 1]), "=r"(w.x[4 * i + 2]), "=r"(w.x[4 * i + 3])
+                         : "r"(group_at(raw, i)));
     }
-    // into half `half` of panels of 64 values, 128-byte swizzled; the parts of float32 are part_bytes apart.  sums: of the thread's columns
-    __device__ __forceinline__ void bring(uint8_t *to, uint32_t part_bytes, const Words &w, int half, int r0, int c0, bool add, float (&sums)[4]) const
+    // N values of one row, or their parts, part_bytes apart
+    template <int N>
+    static __device__ __forceinline__ void store_parts(uint8_t *at, uint32_t part_bytes, float (&f)[N])
     {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int r = row_of(i), c = column();
-            uint8_t *at = MN ? to + (c >> 6) * kPanel + sw128(r + 32 * half, c & 63) : to + sw128(r, c + 32 * half);
-            const uint32_t(&x)[4] = w.x[i];
-            float f[4];
-            if constexpr (sizeof(io_t) == 2) {
-                const bool odd = (((long long)(r0 + r) * ld + c0 + c) & 1) && r0 + r < rows && c0 + c < cols;
-                uint32_t lo = odd ? __byte_perm(x[0], x[1], 0x5432) : x[0], hi = odd ? __byte_perm(x[1], x[2], 0x5432) : x[1];
-                const int n = cols - c0 - c;  // of the four, those that the row has
-                if (n < 4) {
-                    hi &= n < 3 ? 0u : 0xffffu;
-                    lo &= n < 1 ? 0u : n < 2 ? 0xffffu : ~0u;
-                }
-                *reinterpret_cast<uint2 *>(at) = make_uint2(lo, hi);
-                if (add) io::Unit<__nv_bfloat16, 8>::two(lo, f[0], f[1]), io::Unit<__nv_bfloat16, 8>::two(hi, f[2], f[3]);
-            } else {
+        for (int part = 0; part < 3; ++part) {
+            if constexpr (N == 4) *reinterpret_cast<uint2 *>(at + part * part_bytes) = make_uint2(leading(f[0], f[1]), leading(f[2], f[3]));
+            else *reinterpret_cast<uint32_t *>(at + part * part_bytes) = leading(f[0], f[1]);
+            if (part < 2) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(x[e]);
-            }
-            if (add) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sums[e] += f[e];
-            }
-            if constexpr (sizeof(io_t) == 4) {
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    *reinterpret_cast<uint2 *>(at + part * part_bytes) = make_uint2(leading(f[0], f[1]), leading(f[2], f[3]));
-                    if (part < 2) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[e] = without_leading(f[e]);
-                    }
-                }
+                for (int e = 0; e < N; ++e) f[e] = without_leading(f[e]);
             }
         }
     }
+    static __device__ __forceinline__ uint8_t *place(uint8_t *to, int r, int c, int half)
+    {
+        return MN ? to + (c >> 6) * kPanel + sw128(r + 32 * half, c & 63) : to + sw128(r, c + 32 * half);
+    }
+    // into half `half` of panels of 64 values, 128-byte swizzled.  sums: of the thread's columns
+    __device__ __forceinline__ void bring(uint8_t *to, uint32_t part_bytes, const Words &w, int half, bool add, float (&sums)[4]) const
+    {
+        const uint32_t(&x)[8] = w.x;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint8_t *at = place(to, own_row() + i * STEP, own_column(), half);
+                float f[4];
+                if constexpr (sizeof(io_t) == 4) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(x[4 * i + e]);
+                } else {
+                    *reinterpret_cast<uint2 *>(at) = make_uint2(x[2 * i], x[2 * i + 1]);
+                    io::Unit<__nv_bfloat16, 8>::two(x[2 * i], f[0], f[1]), io::Unit<__nv_bfloat16, 8>::two(x[2 * i + 1], f[2], f[3]);
+                }
+                if (add) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sums[e] += f[e];
+                }
+                if constexpr (sizeof(io_t) == 4) store_parts(at, part_bytes, f);
+            }
+            return;
+        }
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a = x[2 * j], b = x[2 * j + 1];  // of two rows
+            if (add) {
+                if constexpr (sizeof(io_t) == 4) sums[j] += __uint_as_float(a) + __uint_as_float(b);
+                else sums[j] += __uint_as_float(a << 16) + __uint_as_float(b << 16);
+            }
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1), first = odd ? other : a, second = odd ? b : other;
+            uint8_t *at = place(to, own_row() + (MN ? 0 : j) + (odd ? 4 : 0), (MN ? 32 * j : 0) + (lane & 30), half);
+            if constexpr (sizeof(io_t) == 4) {
+                float f[2] = {__uint_as_float(first), __uint_as_float(second)};
+                store_parts(at, part_bytes, f);
+            } else {
+                *reinterpret_cast<uint32_t *>(at) = first | second << 16;
+            }
+        }
+    }
+    // the column of the half that sums[e] belong to
+    __device__ __forceinline__ int column_of(int e) const { return whole ? own_column() + e : own_column() + 32 * e; }
 };
 
 // ---- outputs --------------------------------------------------------------------------------------------
@@ -715,7 +753,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     __shared__ uint32_t tmem_base_s;
     __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2], incoming[L::FINISHERS];
     __shared__ int abort_s;
-    __shared__ __align__(16) float column_sums[OP == LinearOp::weights ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
+    __shared__ __align__(16) float column_sums[OP == LinearOp::weights && SOFT ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
     constexpr int CTAS = PAIR ? 2 : 1, TM = CTAS * BM;  // of a tile, and its rows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int in_tile = PAIR ? (int)(blockIdx.x & 1) : 0;  // the cluster's CTAs are numbered as the grid's
@@ -728,6 +766,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     const int b_from = SPLIT ? (int)((long long)rank * blocks / p.splits) : 0, b_to = SPLIT ? (int)((long long)(rank + 1) * blocks / p.splits) : blocks;
     const long long total = (long long)my_tiles * (b_to - b_from);
     const int groups = GROUPED ? (b_to - b_from + L::GROUP - 1) / L::GROUP : 1;  // of a tile's blocks, an accumulator each
+    const int stages = SOFT && PARTS == 3 && (p.lda % 4 == 0 || p.ldb % 4 == 0) ? 2 : STAGES;
     const uint32_t sbase = smem_u32(sm), crank = PAIR ? cluster_rank() : 0;
     const uint32_t leader_full = PAIR ? address_in(smem_u32(&full[0]), crank & ~1) : smem_u32(&full[0]);
 
@@ -768,10 +807,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         }
     };
     // on their way while the tensor memory is allocated; a pair's barriers have to stand first
-    const int early = !SOFT && !PAIR && my_tiles > 0 ? min(STAGES, b_to - b_from) : 0;
+    const int early = !SOFT && !PAIR && my_tiles > 0 ? min(stages, b_to - b_from) : 0;
     if (tid == 32) {
         abort_s = 0;
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(smem_u32(&full[s]), SOFT ? kLoaderWarps : 1);
             mbar_init(smem_u32(&freed[s]), 1);
         }
@@ -815,8 +854,8 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         // (4096 x 4096 x 4096 took 108 us with one thread a loop and two looks between a block's products and the next).
         if (!SOFT && warp == 1) {  // ---- operand loads ----
             const bool one = elect_one();
-            int s = early % STAGES, i = b_from + early == b_to ? 1 : 0, b = i > 0 ? b_from : b_from + early, i0 = 0, j0 = 0;
-            uint32_t round = early / STAGES;
+            int s = early % stages, i = b_from + early == b_to ? 1 : 0, b = i > 0 ? b_from : b_from + early, i0 = 0, j0 = 0;
+            uint32_t round = early / stages;
             bool ready = false;
             issued = early;
             tile_at(0, i0, j0);
@@ -829,8 +868,8 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                     }
                 }
                 if (s == 0 && __any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
-                const int next = s + 1 == STAGES ? 0 : s + 1;
-                const uint32_t next_round = s + 1 == STAGES ? round + 1 : round;
+                const int next = s + 1 == stages ? 0 : s + 1;
+                const uint32_t next_round = s + 1 == stages ? round + 1 : round;
                 const bool seen = next_round > 0 && mbar_test(smem_u32(&freed[next]), (next_round - 1) & 1);
                 if (one) load_block(s, b, i0, j0);
                 __syncwarp();
@@ -863,15 +902,15 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                         break;
                     }
                     fence_after_sync();
-                    const int next = s + 1 == STAGES ? 0 : s + 1;
-                    const uint32_t next_round = s + 1 == STAGES ? round + 1 : round;
+                    const int next = s + 1 == stages ? 0 : s + 1;
+                    const uint32_t next_round = s + 1 == stages ? round + 1 : round;
                     const bool seen = mbar_test(smem_u32(&full[next]), next_round & 1);
-                    const uint32_t at = sbase + (SOFT ? 0 : s * L::STAGE), bt = at + PARTS * L::A_PART, d = tmem + buf * BN;
+                    const uint32_t at = sbase + (SOFT ? s >> 1 : s) * L::STAGE, bt = at + PARTS * L::A_PART, d = tmem + buf * BN;
                     const uint64_t da = A_MN ? sdesc(at, kPanel, 1024) : sdesc(at, 16, 1024), db = B_MN ? sdesc(bt, kPanel, 1024) : sdesc(bt, 16, 1024);
                     constexpr uint64_t SA = (A_MN ? 2048 : 32) >> 4, SB = (B_MN ? 2048 : 32) >> 4;
                     constexpr uint32_t ID = idesc_bf16(TM, BN, A_MN, B_MN);
                     const uint32_t small = tmem + 2 * BN + (i & 1) * BN;  // the small products' accumulator, for the whole tile
-                    const int from_k = SOFT ? s * L::BLOCK / 16 : 0;  // the half of the stage
+                    const int from_k = SOFT ? (s & 1) * L::BLOCK / 16 : 0;  // the half of the stage
                     const bool last = b + 1 == b_to || (GROUPED && in_group + 1 == L::GROUP);
                     if (one) {
 #pragma unroll
@@ -908,65 +947,73 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         SoftHalf<io_t, A_MN> ta(p.a, p.lda, A_MN ? p.K : p.I, A_MN ? p.I : p.K, thread);
         SoftHalf<io_t, B_MN> tb(p.b, p.ldb, B_MN ? p.K : p.J, B_MN ? p.J : p.K, thread);
         float column[4] = {}, unused[4];
-        const uint32_t raws = sbase + L::OFF_RAW;
-        struct At {
-            int i, b, i0, j0;
+        auto seek_a = [&] {
+            int i0, j0;
+            tile_at(ta.tile, i0, j0);
+            ta.seek(A_MN ? ta.block * L::BLOCK : i0, A_MN ? i0 : ta.block * L::BLOCK);
         };
-        auto step = [&](At &a) {
-            if (++a.b == b_to) {
-                a.b = b_from;
-                if (++a.i < my_tiles) tile_at(a.i, a.i0, a.j0);
+        auto seek_b = [&] {
+            int i0, j0;
+            tile_at(tb.tile, i0, j0);
+            tb.seek(B_MN ? tb.block * L::BLOCK : j0, B_MN ? j0 : tb.block * L::BLOCK);
+        };
+        auto step = [&](auto &t, auto seek) {
+            t.advance();
+            if (++t.block == b_to) {
+                t.block = b_from;
+                if (++t.tile < my_tiles) seek();
             }
         };
-        At next{0, b_from, 0, 0}, now;
-        tile_at(0, next.i0, next.j0);
-        now = next;
-        auto seek = [&] {
-            const int k = next.b * L::BLOCK;
-            ta.seek(A_MN ? k : next.i0, A_MN ? next.i0 : k);
-            tb.seek(B_MN ? k : next.j0, B_MN ? next.j0 : k);
-        };
-        seek();
-        long long asked = 0;
-        auto ask = [&] {
-            if (asked < total) {
-                const uint32_t raw = raws + (uint32_t)(asked % L::RAWS) * L::RAW;
-                ta.ask(raw);
-                tb.ask(raw + L::RAW / 2);
-                const int tile = next.i;
-                step(next);
-                if (next.i == tile) ta.advance(), tb.advance();
-                else seek();
+        ta.block = tb.block = b_from, ta.tile = tb.tile = 0;
+        seek_a(), seek_b();
+        typename SoftHalf<io_t, A_MN>::Words wa;
+        typename SoftHalf<io_t, B_MN>::Words wb;
+        // float32 rows of whole units are asked for two halves ahead, others loaded when the registers are free
+        const bool ask_a = PARTS == 3 && ta.whole, ask_b = PARTS == 3 && tb.whole;
+        auto ask = [&](long long g) {
+            if constexpr (PARTS == 3) {
+                if (g < total) {
+                    const uint32_t raw = sbase + L::OFF_RAW + (uint32_t)(g % 3) * L::RAW;
+                    if (ask_a) ta.ask(raw), step(ta, seek_a);
+                    if (ask_b) tb.ask(raw + L::RAW / 2), step(tb, seek_b);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
             }
-            ++asked;
-            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        for (int r = 0; r + 1 < L::RAWS; ++r) ask();
+        if (ask_a || ask_b) ask(0), ask(1);
+        if (total > 0 && !ask_a) ta.load(wa), step(ta, seek_a);
+        if (total > 0 && !ask_b) tb.load(wb), step(tb, seek_b);
+        int s = 0;
+        uint32_t round = 0;
         for (long long g = 0; g < total; ++g) {
-            const int s = (int)(g & 1);
-            ask();
-            asm volatile("cp.async.wait_group %0;" ::"n"(L::RAWS - 1) : "memory");
-            const uint32_t raw = raws + (uint32_t)(g % L::RAWS) * L::RAW;
-            typename SoftHalf<io_t, A_MN>::Words wa;
-            typename SoftHalf<io_t, B_MN>::Words wb;
-            ta.fetch(raw, wa), tb.fetch(raw + L::RAW / 2, wb);  // on their way while the half is waited for
-            const bool ok = g < 2 || mbar_wait(smem_u32(&freed[s]), (uint32_t)((g - 2) >> 1) & 1, wt.ns);
+            if (ask_a || ask_b) {
+                ask(g + 2);
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                const uint32_t raw = sbase + L::OFF_RAW + (uint32_t)(g % 3) * L::RAW;
+                if (ask_a) ta.fetch(raw, wa);  // on their way while the half is waited for
+                if (ask_b) tb.fetch(raw + L::RAW / 2, wb);
+            }
+            const bool ok = round == 0 || mbar_wait(smem_u32(&freed[s]), (round - 1) & 1, wt.ns);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) give_up();
                 break;
             }
-            const int k = now.b * L::BLOCK;
-            ta.bring(sm, L::A_PART, wa, s, A_MN ? k : now.i0, A_MN ? now.i0 : k, sums, column);
-            tb.bring(sm + PARTS * L::A_PART, L::B_PART, wb, s, B_MN ? k : now.j0, B_MN ? now.j0 : k, false, unused);
-            step(now);
+            uint8_t *to = sm + (s >> 1) * L::STAGE;
+            ta.bring(to, L::A_PART, wa, s & 1, sums, column);
+            if (!ask_a && g + 1 < total) ta.load(wa), step(ta, seek_a);
+            tb.bring(to + PARTS * L::A_PART, L::B_PART, wb, s & 1, false, unused);
+            if (!ask_b && g + 1 < total) tb.load(wb), step(tb, seek_b);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&full[s]));
             if (__any_sync(0xffffffffu, *(volatile int *)&abort_s)) break;
+            if (++s == stages) s = 0, ++round;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if constexpr (OP == LinearOp::weights)
-            *reinterpret_cast<float4 *>(&column_sums[thread / 32][4 * lane]) = make_float4(column[0], column[1], column[2], column[3]);
+        if constexpr (PARTS == 3) asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (OP == LinearOp::weights) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) column_sums[thread / 32][ta.column_of(e)] = column[e];
+        }
     } else {  // ---- what follows: lane quarter warp % 4, share (warp - 4) / 4 of the columns ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kEpilogueRegs));
         const int quarter = warp & 3, share = (warp - 4) >> 2;
@@ -1028,16 +1075,16 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                 fence_after_sync();
                 if constexpr (GROUPED) {
                     auto add = [&](uint32_t at, bool first) {
-                        uint32_t r[2][32];
-                        ld_issue(at, r[0]);
+                        uint32_t r[2][16];
+                        tmem_ld_nowait(at, r[0]);
 #pragma unroll
-                        for (int c = 0; c < COLS / 32; ++c) {  // the next columns load while these are added
-                            ld_wait(r[c & 1]);
-                            if (c + 1 < COLS / 32) ld_issue(at + 32 * (c + 1), r[(c + 1) & 1]);
+                        for (int c = 0; c < COLS / 16; ++c) {  // the next columns load while these are added
+                            wait16(r[c & 1]);
+                            if (c + 1 < COLS / 16) tmem_ld_nowait(at + 16 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-                            for (int q = 0; q < 16; ++q) {
+                            for (int q = 0; q < 8; ++q) {
                                 const float2 x = make_float2(__uint_as_float(r[c & 1][2 * q]), __uint_as_float(r[c & 1][2 * q + 1]));
-                                sum[16 * c + q] = first ? x : io::add2(sum[16 * c + q], x);
+                                sum[8 * c + q] = first ? x : io::add2(sum[8 * c + q], x);
                             }
                         }
                     };
@@ -1155,7 +1202,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                         const bool inside = rows > 0 && j < p.J;
                         float f[32];
                         Held<io_t> other;
-                        if (inside && has_pre) Patch<io_t>::get(p.pre_in + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
+                        if (!GROUPED && inside && has_pre) Patch<io_t>::get(p.pre_in + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);
                         piece(ch, f);
                         if (!inside) continue;
                         if constexpr (OP == LinearOp::forward) {
@@ -1170,6 +1217,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                             }
                             to_values<io_t, ACT>(f);
                         } else if constexpr (OP == LinearOp::backward && ACT != PRISM_ACT_NONE) {
+                            if (GROUPED) Patch<io_t>::get(p.pre_in + (size_t)r0 * p.J, p.J, rows, j, whole, flat, lane, other);  // the sums hold the registers
                             times_slopes<io_t, ACT>(f, other);
                         }
                         if (has_add) {
@@ -1193,10 +1241,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     if (abort_s && issued > 0) {
         const long long last = issued - 1;
         if (tid == 0 && leads)  // products complete in order
-            (void)mbar_wait(smem_u32(&freed[last % STAGES]), (uint32_t)(last / STAGES) & 1, 1000000000ull);
+            (void)mbar_wait(smem_u32(&freed[last % stages]), (uint32_t)(last / stages) & 1, 1000000000ull);
         if (!SOFT && tid == 32 && leads)
-            for (long long g = last >= STAGES ? last - STAGES + 1 : 0; g <= last; ++g)
-                (void)mbar_wait(smem_u32(&full[g % STAGES]), (uint32_t)(g / STAGES) & 1, 1000000000ull);
+            for (long long g = last >= stages ? last - stages + 1 : 0; g <= last; ++g)
+                (void)mbar_wait(smem_u32(&full[g % stages]), (uint32_t)(g / stages) & 1, 1000000000ull);
     }
     fence_before_sync();
     __syncthreads();
