@@ -686,26 +686,26 @@ __device__ __noinline__ Drawn draw_row(S &s, const R &row, const Mass &m, const 
 
 // The draw from a short list in order, all of whose first `keep` tokens are kept: each counts the mass up to its id, with all threads at work
 template <int NT, typename S, typename R, int PER>
-__device__ Drawn draw_listed(S &s, const R &row, const Mass &m, const Rules &rules, uint32_t keep, const u64 (&e)[PER], u64 list_before)
+__device__ Drawn draw_listed(S &s, const R &row, const Mass &m, const Rules &rules, uint32_t keep, uint32_t per, const u64 (&e)[PER], u64 list_before)
 {
     const int tid = threadIdx.x;
     u64 at = list_before;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         at += e[i];
-        const uint32_t j = PER * tid + i;
-        if (j < keep) s.masses[j] = e[i], s.below[j] = 0;
-        if (j + 1 == keep) s.mass = at;
+        const uint32_t j = per * tid + i;
+        if (i < per && j < keep) s.masses[j] = e[i], s.below[j] = 0;
+        if (i < per && j + 1 == keep) s.mass = at;
     }
     __syncthreads();
     const u64 all = s.mass, target = rules.target(all);
     int across = 32;
     while (across < (int)keep) across *= 2;
-    const int i = tid % across, per = ((int)keep + NT / across - 1) / (NT / across), from = tid / across * per;
+    const int i = tid % across, others = ((int)keep + NT / across - 1) / (NT / across), from = tid / across * others;
     if (i < (int)keep) {
         const int id = id_in(s.list[i]);
         u64 sum = 0;
-        for (int o = from; o < min((int)keep, from + per); ++o) sum += id_in(s.list[o]) <= id ? s.masses[o] : 0;
+        for (int o = from; o < min((int)keep, from + others); ++o) sum += id_in(s.list[o]) <= id ? s.masses[o] : 0;
         if (sum > 0) atomicAdd(&s.below[i], sum);
     }
     __syncthreads();
@@ -730,6 +730,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
     int first = kBuckets, last = kBuckets - 1;  // the window's buckets: empty
     u64 total = 0;                              // of all masses, quick ones
     uint32_t sure_n = 0, listed_n = 0;
+    bool min_ends = by_min;  // the window ends where min_p does, not top-p
     constexpr int VEC = R::VEC;
     auto rough_sum = [&](const float (&l)[VEC]) {
         float e[VEC];
@@ -770,12 +771,14 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
                 block_sums<NT>(s, total, none);
             }
             __syncthreads();
+            bool room = true;  // too many are not counted to the end
             row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int id) {
 #pragma unroll
                 for (int q = 0; q < VEC; ++q)
-                    if (m.log_of(l[q]) >= low && l[q] > m.mask) {
+                    if (m.log_of(l[q]) >= low && l[q] > m.mask && room) {
                         const uint32_t to = atomicAdd(&s.number, 1u);
                         if (to < S::kCandidates) s.list[to] = listed(order_of(l[q]), id + q);
+                        else room = false;
                     }
             });
             __syncthreads();
@@ -788,7 +791,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
     }
     if (!few && (by_p || by_k || by_min)) {
         for (int i = tid; i < kBuckets; i += NT) s.count[i] = s.lo[i] = 0;
-        if (tid == 0) s.first = 0, s.last = kBuckets - 1, s.number = 0;
+        if (tid == 0) s.first = s.last = kBuckets - 1, s.number = 0;
         __syncthreads();
         // with top-p the places within the buckets are added up too, which brings the masses' bounds together
         auto count_places = [&](const float (&l)[VEC]) {
@@ -839,20 +842,22 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
                 block_sums<NT>(s, total, none);
             }
         }
-        // Each rule ends the prefix in a bucket that is known (k), known to a few (p) or not known from below (min_p, together).
-        const bool alone = !by_min && by_k != by_p;
+        // Each rule ends the prefix in a bucket that is known (k) or known to a few (p, min_p); the window reaches from the first of these to
+        // the first by which one of them has ended.  k and p together need the first k's mass: all of them are candidates.
         const float part = by_k ? 0.f : fmaxf(rules.p * (float)total * __int_as_float((127 - m.fraction) << 23), 1e-30f);
-        const int b_min = by_min ? (int)fminf((float)(kBuckets - 1), -rules.log_min_p * (1.442695f * kPerOctave) * 1.00001f + 1.5f) : kBuckets - 1;
+        const float at_min = by_min ? fmaxf(-rules.log_min_p, 0.f) * (1.442695f * kPerOctave) : 0.f;
+        const int b_min = by_min ? (int)fminf((float)(kBuckets - 1), at_min * 1.00001f + 1.5f) : kBuckets - 1;
+        if (tid == 0) {
+            if (by_k && by_p) s.first = 0;
+            else if (by_min) atomicMin(&s.first, (int)fminf((float)(kBuckets - 1), fmaxf(at_min * 0.99999f - 1.5f, 0.f)));
+        }
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             const int b = EACH * tid + i;
-            if (by_k && at_n < rules.k && at_n + n[i] >= rules.k) {
-                atomicMin(&s.last, b);
-                if (alone) s.first = b;
-            }
+            if (by_k && at_n < rules.k && at_n + n[i] >= rules.k) atomicMin(&s.last, b), atomicMin(&s.first, b);
             if (by_p && !by_k) {
                 // the first bucket by whose end the mass may, and the first by whose end it must have been reached
-                if (alone && at_u * 1.00002f < part && (at_u + up[i]) * 1.00002f >= part) s.first = b;
+                if (at_u * 1.00002f < part && (at_u + up[i]) * 1.00002f >= part) atomicMin(&s.first, b);
                 if (at_d * 0.99998f < part && (at_d + down[i]) * 0.99998f >= part) atomicMin(&s.last, b);
             }
             if (by_min && b == b_min && !(by_k && by_p)) atomicMin(&s.last, b);  // the first k are needed for their mass
@@ -860,6 +865,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
         }
         __syncthreads();
         first = s.first, last = s.last;
+        min_ends = by_min && last == b_min;
         __syncthreads();
         // the tokens before and in the window; where all candidates are few, the window begins at the first
         uint32_t before = 0, upto = 0;
@@ -873,7 +879,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
         block_sums<NT>(s, both, none);
         before = (uint32_t)(both >> 32), upto = (uint32_t)both;
         if (!by_p && !by_k && !by_min) first = kBuckets;  // top_k reaches all of them
-        else if (upto <= S::kCandidates) first = 0;
+        else if (upto <= (first == 0 ? S::kCandidates : 1024)) first = 0;  // sorting more takes longer than adding up what is before the window
         else if (first == 0 || upto - before > S::kCandidates) {
             done = false;
             return Drawn{};
@@ -928,10 +934,12 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
     __syncthreads();
     if (listed_n > 0) sort_list<NT>(s, listed_n);
     constexpr int PER = S::kCandidates / NT;
+    const uint32_t per = listed_n <= NT ? 1 : PER;  // neighbouring tokens a thread
+    auto place = [&](int i) { return i < (int)per ? (int)per * tid + i : INT_MAX - 1; };
     u64 e[PER], of_list = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        e[i] = PER * tid + i < (int)listed_n ? m.exact(logit_of(order_in(s.list[PER * tid + i]))) : 0;
+        e[i] = place(i) < (int)listed_n ? m.exact(logit_of(order_in(s.list[place(i)]))) : 0;
         of_list += e[i];
     }
     const u64 list_before = listed_n > 0 ? block_scan<NT>(of_list, s.sums) - of_list : 0;
@@ -975,10 +983,10 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
             if (tid == 0) s.number = listed_n, s.mass = 0;
             __syncthreads();
             if (by_k) keep = min(keep, rules.k - sure_n);
-            if (by_min) {  // the window begins at the first token
+            if (by_min) {  // those before the window reach it all
                 uint32_t reach = 0;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) reach += PER * tid + i < (int)listed_n && rules.reaches_min(m, logit_of(order_in(s.list[PER * tid + i])));
+                for (int i = 0; i < PER; ++i) reach += place(i) < (int)listed_n && rules.reaches_min(m, logit_of(order_in(s.list[place(i)])));
                 u64 zero = 0;
                 block_sums<NT>(s, zero, reach);
                 keep = min(keep, reach);
@@ -989,7 +997,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
                         at += e[i];
-                        if (PER * tid + i + 1 == (int)min(rules.k, listed_n)) s.mass = at;
+                        if (place(i) + 1 == (int)min(rules.k, listed_n)) s.mass = at;
                     }
                     __syncthreads();
                     total = s.mass;
@@ -1000,13 +1008,13 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
                 u64 at = sure_mass + list_before;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int j = PER * tid + i;
+                    const int j = place(i);
                     if (j < (int)listed_n && at + e[i] >= target && (at < target || j == 0)) {
                         s.number = j + 1;
                         if (near && (at + e[i] - target <= near || (at != 0 && target <= at + near))) s.flag = 0;
                         if (j == 0 && at >= target && at != 0) s.flag = 0;  // reached before the window: only for quick masses' errors
                     }
-                    if (j + 1 == (int)listed_n && at + e[i] < target && !by_min && !by_k) s.flag = 0;  // or behind it
+                    if (j + 1 == (int)listed_n && at + e[i] < target && !min_ends && !by_k) s.flag = 0;  // or behind it
                     at += e[i];
                 }
                 __syncthreads();
@@ -1015,9 +1023,9 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
                 __syncthreads();
                 if (!ok) continue;
             }
-            keep = max(keep, 1u);
+            if (sure_n == 0) keep = max(keep, 1u);
         }
-        if (first == 0 && keep <= kCounted) return draw_listed<NT>(s, row, m, rules, keep, e, list_before);
+        if (first == 0 && keep <= kCounted) return draw_listed<NT>(s, row, m, rules, keep, per, e, list_before);
         // the warps' masses with the list's share
         Cut cut{INT_MAX, -1, 0};  // of the window's tokens
         if (keep > 0 && listed_n > 0) cut = Cut{order_in(s.list[keep - 1]), id_in(s.list[keep - 1]), 0};
@@ -1026,7 +1034,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
         const int each = (row.units + NT / 32 - 1) / (NT / 32);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (PER * tid + i < (int)keep) atomicAdd(&s.sums[(id_in(s.list[PER * tid + i]) + row.skew) / R::VEC / each], e[i]);
+            if (place(i) < (int)keep) atomicAdd(&s.sums[(id_in(s.list[place(i)]) + row.skew) / R::VEC / each], e[i]);
         __syncthreads();
         const u64 near = first == 0 || again == 2 ? 0 : again ? m.close_slack(sure_mass, row.V) : m.slack(sure_mass, row.V);
         auto mass = [&](float l, int id) -> u64 {
@@ -1048,7 +1056,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const Params<T> p
 {
     using R = Row<T, RESIDENT>;
     extern __shared__ uint4 copy[];
-    __shared__ Shared<RESIDENT ? 1024 : 2048> s;  // the window of a longer row holds more
+    __shared__ Shared<RESIDENT && NT < 1024 ? 1024 : 2048> s;  // the window of a longer row holds more
     const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     R row(p.logits + (size_t)i * p.ld, p.V);
     if constexpr (RESIDENT) row.template copy_to<NT>(copy);
@@ -1104,7 +1112,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const Params<T> p
 }
 
 // Shared memory for a row where one or two blocks share an SM, beside what the kernel has of its own and the system's 1024 bytes
-constexpr size_t room(int blocks) { return (233472 / blocks - sizeof(Shared<1024>) - 1024) / 16 * 16; }
+constexpr size_t room(int blocks) { return (233472 / blocks - (blocks > 1 ? sizeof(Shared<1024>) : sizeof(Shared<2048>)) - 1024) / 16 * 16; }
 
 template <typename T>
 cudaError_t prepare()
