@@ -10,8 +10,9 @@ namespace prism {
 namespace lin {
 
 // ---- few rows ---------------------------------------------------------------------------------------------
-// Up to 16 rows of bf16, as a served token of each of some sequences has them: the weights' bytes bound the product, each weight
-// is used M times at most, and tiles of 128 rows would be empty for the most part.  A warp takes RPW tiles of 16 rows of W as A operands
+// Few rows of bf16, as a served token of each of some sequences has them: the weights' bytes bound the product, each weight
+// is used M times at most, and tiles of 128 rows would be empty for the most part.  (16 x 2304 x 768: 3.3 us, 1.1 TB/s of weights from a
+// graph's launch to the next one's; 16 x 8192 x 8192: 24, 5.5 TB/s.)  A warp takes RPW tiles of 16 rows of W as A operands
 // of m16n8k16 products straight from global memory to registers (16 bytes of a row per lane and load), and 8 NT rows of x as B
 // operands.  The products' k order is a free choice as long as both operands share it: the four words of a lane's 16 bytes serve as
 // the k slots of two products.  KS warps of a CTA share their tiles and split the sum, so that narrow products still fill the
@@ -122,25 +123,40 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_kernel(const Params<__nv_b
     });
 }
 
+bool few_weights(int J, const TokenLaunch &l) { return (J + 31) / 32 * 8LL < 12 * l.sm_count; }
+
 template <int NT>
-cudaError_t few_rows(const Params<__nv_bfloat16> &p, const TokenLaunch &l)
+cudaError_t launch_few(const Params<__nv_bfloat16> &p, const TokenLaunch &l)
 {
     constexpr int T = 32 * kFewWarps;
     const int blocks = (p.K + kFewBlock - 1) / kFewBlock, pairs = (p.J + 31) / 32;
     cudaStream_t s = l.timer->stream;
-    if (pairs * 8LL < 12 * l.sm_count) {  // few rows of W: all warps of a CTA on one tile
+    if (NT > 2 || few_weights(p.J, l)) {  // all warps of a CTA on one tile
         few_kernel<NT, 8, 1><<<(p.J + 15) / 16, T, 0, s>>>(p);
         return cudaGetLastError();
     }
-    // as many warps as keep each SM's loads in flight, as far as the blocks of 64 reach
-    int ks = 1;
-    while (ks < 8 && ks < blocks && (long long)pairs * ks < 8 * l.sm_count) ks *= 2;
-    const unsigned grid = (unsigned)((pairs + kFewWarps / ks - 1) / (kFewWarps / ks));
-    if (ks == 1) few_kernel<NT, 1, 2><<<grid, T, 0, s>>>(p);
-    else if (ks == 2) few_kernel<NT, 2, 2><<<grid, T, 0, s>>>(p);
-    else if (ks == 4) few_kernel<NT, 4, 2><<<grid, T, 0, s>>>(p);
-    else few_kernel<NT, 8, 2><<<grid, T, 0, s>>>(p);
+    if constexpr (NT <= 2) {
+        // as many warps as keep each SM's loads in flight, as far as the blocks of 64 reach
+        int ks = 1;
+        while (ks < 8 && ks < blocks && (long long)pairs * ks < 8 * l.sm_count) ks *= 2;
+        const unsigned grid = (unsigned)((pairs + kFewWarps / ks - 1) / (kFewWarps / ks));
+        if (ks == 1) few_kernel<NT, 1, 2><<<grid, T, 0, s>>>(p);
+        else if (ks == 2) few_kernel<NT, 2, 2><<<grid, T, 0, s>>>(p);
+        else if (ks == 4) few_kernel<NT, 4, 2><<<grid, T, 0, s>>>(p);
+        else few_kernel<NT, 8, 2><<<grid, T, 0, s>>>(p);
+    }
     return cudaGetLastError();
+}
+
+// Whether M rows are few: up to 16 always (17 rows of 2304 x 768 in tiles: 6.8 us, 16 here 3.3).  More rows only where the weights are small, since
+// each CTA reads all rows again.  Microseconds here / in tiles: 32 rows of 2304 x 768 3.4 / 7.4, of 3584 x 2048 7.5 / 8.6, of 768 x 8192 10.3 / 10.5,
+// of 4096 x 4096 13.6 / 10.9; 64 rows of 2304 x 768 4.7 / 7.2, of 2048 x 2048 6.2 / 8.5, of 768 x 2304 6.9 / 7.9, of 7168 x 768 10.4 / 8.8,
+// of 768 x 8192 14.9 / 10.9.
+bool few_rows(const Params<__nv_bfloat16> &p, const TokenLaunch &l)
+{
+    if (p.K % 8 != 0) return false;
+    const long long weights = (long long)p.J * p.K;
+    return p.I <= 16 || (few_weights(p.J, l) && ((p.I <= 32 && weights <= 1 << 23 && p.K <= 8192) || (p.I <= 64 && weights <= 1 << 22 && p.K <= 2304)));
 }
 
 template <typename io_t>
@@ -162,9 +178,9 @@ cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
         p.I = a.N, p.J = a.K, p.K = a.M, p.lda = a.N, p.ldb = a.K;
     }
     if constexpr (sizeof(io_t) == 2) {
-        if (a.op == LinearOp::forward && a.M <= 16 && a.K % 8 == 0) {
+        if (a.op == LinearOp::forward && few_rows(p, l)) {
             l.timer->begin(name);
-            const cudaError_t e = a.M <= 8 ? few_rows<1>(p, l) : few_rows<2>(p, l);
+            const cudaError_t e = a.M <= 8 ? launch_few<1>(p, l) : a.M <= 16 ? launch_few<2>(p, l) : a.M <= 32 ? launch_few<4>(p, l) : launch_few<8>(p, l);
             l.timer->end();
             return e;
         }
@@ -194,6 +210,11 @@ cudaError_t run(const LinearArgs &a, const TokenLaunch &l)
         if (!c.soft) consider(true, 192, 430);
         if (!c.soft && !p.dbias) consider(false, 256, 800), consider(true, 256, 560);
     } else {
+        // Few tiles split their sum over a cluster as long as all clusters run at once: 32 x 2304 x 768 backward 13.9 us in one piece, 8.6 in four, 7.3
+        // in eight; 256 rows 14.2, 9.3, 9.0; of 1024 rows, which fit in two parts only, 14.3, 11.6 in two, 17.8 in four.  Below eight blocks it is a
+        // draw (7.4 to 8.4).  Many tiles: of 256 columns where that takes no more turns for its width (4096 x 768 x 768: 10.0, of 128 11.7; 2048 rows
+        // 9.8, of 128 8.1), in pairs of SMs where there are as many (8192 x 2304 x 768: 23.3, 26.0 by single SMs; 4096 rows 15.4 and 15.5; 2048 x 768 x 768
+        // 10.6 and 9.8).
         while (c.splits < 8 && 2 * c.splits <= blocks && blocks >= 8 && tiles(BM, 128) <= clusters_at_once(2 * c.splits)) c.splits *= 2;
         c.split = c.splits > 1;
         c.pair = !c.split && !c.soft && tiles(256, 256) * 2 > l.sm_count;

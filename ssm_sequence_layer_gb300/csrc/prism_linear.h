@@ -494,27 +494,6 @@ __device__ __forceinline__ void with_activation(prism_activation act, F f)
     else f(std::integral_constant<prism_activation, PRISM_ACT_NONE>());
 }
 
-// N neighbouring values of a row, as floats; beyond `cols` zeros.  `whole`: rows are whole 16-byte units and at is one's start.
-template <typename T, int N>
-__device__ __forceinline__ void load_row(const T *p, int at, int cols, bool whole, float (&f)[N])
-{
-    constexpr int VEC = 16 / (int)sizeof(T);
-    if constexpr (N % VEC == 0) {
-        if (whole && at + N <= cols) {
-#pragma unroll
-            for (int u = 0; u < N / VEC; ++u) {
-                float g[VEC];
-                io::load_unit<T, VEC>(p + at + u * VEC).get(g);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) f[u * VEC + e] = g[e];
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) f[e] = at + e < cols ? io::ld(p + at + e) : 0.f;
-}
-
 // N values of a row as they lie in memory, two at a time
 template <typename T, int N = 32>
 struct Held {
@@ -576,7 +555,6 @@ __device__ __forceinline__ void plus(float (&f)[N], const Held<T, N> &g)
 // A warp's 32 rows x 32 columns of an output or an addend: lane l holds row l.
 template <typename T>
 struct Patch {
-    static constexpr int VEC = 16 / (int)sizeof(T);
     // rows that are not whole units come and go through shared memory, a row by all lanes
     static __device__ __forceinline__ void get(const T *p, int J, int rows, int j0, bool whole, float *t, int lane, Held<T> &held)
     {
@@ -1273,10 +1251,11 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                 if (j >= p.J) continue;
                 const size_t line = (size_t)(i0 + row) * p.J;
                 // four values of a row that is made of whole units, else one at a time
-                auto four = [&](const io_t *q, float (&g)[4]) {
+                auto four = [&](const auto *q, float (&g)[4]) {
+                    using T = std::remove_cv_t<std::remove_pointer_t<decltype(q)>>;
                     if (whole) {
-                        if constexpr (sizeof(io_t) == 4) {
-                            io::load_unit<io_t, 4>(q + j).get(g);
+                        if constexpr (sizeof(T) == 4) {
+                            io::load_unit<T, 4>(q + j).get(g);
                         } else {
                             const uint2 w = *reinterpret_cast<const uint2 *>(q + j);
                             io::Unit<__nv_bfloat16, 8>::two(w.x, g[0], g[1]), io::Unit<__nv_bfloat16, 8>::two(w.y, g[2], g[3]);
@@ -1301,7 +1280,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                 if constexpr (OP == LinearOp::weights) {
                     float *to = (float *)p.out + line;
                     if (p.accumulate) {
-                        load_row<float, 4>(to, j, p.J, whole, g);
+                        four((const float *)to, g);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) f[x] += g[x];
                     }

@@ -53,12 +53,13 @@ def product_error(io, a, b, extra=0.0):
     return ((K + 8) * u + (2.0 ** -20 if io == "f32" else 0.0)) * (np.abs(a) @ np.abs(b) + extra)
 
 
+FEW = [(17, 768, 768), (24, 2304, 72), (32, 7290, 64), (32, 7296, 64), (32, 1024, 8192), (32, 1024, 8200), (33, 100, 520), (47, 1000, 2304), (63, 257, 2312), (64, 2048, 2048),
+       (64, 2049, 2048), (65, 768, 768)]
 SHAPES = [(1, 1, 1), (1, 64, 64), (2, 130, 72), (5, 7, 3), (16, 2304, 768), (8, 264, 1000), (17, 129, 65), (33, 8, 4096), (64, 96, 128), (128, 256, 64),
           (129, 255, 136), (300, 515, 770), (200, 64, 1041), (1003, 770, 200), (2500, 768, 256), (40, 4096, 48)]
 
 
-@pytest.mark.parametrize("io", ["bf16", "f32"])
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("io,M,N,K", [(io, *shape) for io in ("bf16", "f32") for shape in SHAPES] + [("bf16", *shape) for shape in FEW])
 def test_linear(io, M, N, K):
     x, W, b, r = tensors(io, M + N + K, (M, K), (N, K), (N,), (M, N))
     W *= K ** -0.5
