@@ -203,3 +203,38 @@ def test_a_block_in_serving(io):
             assert torch.allclose(h["q"][:, :, 0], keep["inp"]["q"][:, :, T - 1], atol=1e-6)
         t.last_device_status()
         plan.last_device_status()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_two_handles_on_two_streams(io):
+    """Calls that run beside each other, each with a handle and a stream of its own, leave the bits that they leave alone."""
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[io]
+    g = torch.Generator().manual_seed(3)
+
+    def side(M, N, K, V):
+        new = lambda *s: torch.randn(*s, generator=g).to(dt).cuda()  # noqa: E731
+        t = Bd.Tokens(M, 64, V, io=io)
+        x, W, dy, logits = new(M, K), new(N, K), new(M, N), new(M, V)
+        u, p = torch.rand(M, generator=g).cuda(), torch.full((M,), 0.7, device="cuda")
+
+        def calls(stream=None):
+            out = [t.linear(x, W, activation="gelu", want=("y", "pre"), stream=stream)]
+            out.append({"dx": t.linear_backward(dy, W, stream=stream)})
+            out.append(t.linear_weight_backward(dy, x, stream=stream))
+            out.append(t.sample(logits, u, top_p=p, stream=stream))
+            return {f"{i} {key}": value for i, d in enumerate(out) for key, value in d.items()}
+        return t, calls
+    sides = [side(300, 257, 259, 5003), side(40, 768, 768, 2000)]
+    alone = [calls() for _, calls in sides]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    runs = [[calls(stream) for (_, calls), stream in zip(sides, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for run in runs:
+        for got, want in zip(run, alone):
+            assert all(torch.equal(got[key], want[key]) for key in want)
+    for t, _ in sides:
+        t.last_device_status()
+        t.close()
