@@ -13,7 +13,8 @@
 // Bound: not bandwidth (100 KB a row) but the way of one row through its steps, a barrier or two each, and operations per token in between.
 // Cycles of a row of 50021 bf16, with top-k 50: copy into shared memory 2400, largest logit 2400, candidates by the threads' own largest
 // 7000, sorting 2000, keeping and drawing 5000; counting tokens by their distance from the largest takes 10000 instead, with the places
-// of top-p 20000.  Microseconds: 4 x 50021 bf16, top-k 50: 16, top-p 0.95: 66; 512 x 50021 float32: 68 and 179, no rule 94.
+// of top-p 20000.  Microseconds: 4 x 50021 bf16 with top-k 50 16, top-p 0.95 69 where it keeps 10000 tokens, 22 where it keeps five;
+// 512 x 50021 float32 68, 192 and 98, without a rule 94.
 #pragma once
 
 #include "io_util.h"
@@ -744,38 +745,58 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
         for (int q = 0; q < VEC; ++q) e[q] = l[q] > m.mask ? m.rough(l[q]) : 0.f;
         return m.whole(sum_of<VEC>(e));
     };
-    // Candidates by a bound where the rules give one: k of the threads' own largest logits that lie above it, or min_p.  (Counting all
-    // tokens' buckets takes 10000 cycles of a row of 50021, the threads' largest 1500.)
+    // Candidates by a bound where the rules give one: k of the threads' own largest logits that lie above it, so many of these that they
+    // have top-p's mass, or min_p.  (Counting all tokens' buckets takes 10000 cycles of a row of 50021, the threads' largest 1500.)
+    const bool by_mass = by_p && !by_k;
     bool few = false;
-    if ((by_k && rules.k <= NT * 3 / 4) || (by_min && !by_k)) {
+    if ((by_k && rules.k <= NT * 3 / 4) || by_mass || (by_min && !by_k)) {
         float low = -INFINITY;
         bool found = true;
         if (tid == 0) s.number = 0, s.at = -1;
-        if (by_k) {
+        if (by_mass) {
+            row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { total += rough_sum(l); });
+            uint32_t none = 0;
+            block_sums<NT>(s, total, none);
+        }
+        if (by_k || by_mass) {
             for (int i = tid; i < kBuckets; i += NT) s.count[i] = 0;
             __syncthreads();
-            if (own > m.mask) atomicAdd(&s.count[m.bucket(own)], 1u);
+            // their number, or their mass in 2^-21ths, rounded down
+            if (own > m.mask) atomicAdd(&s.count[m.bucket(own)], by_k ? 1u : __float2uint_rz(m.rough(own) * 2097152.f));
             __syncthreads();
-            uint32_t n[EACH], nn = 0;
+            if (by_k) {
+                uint32_t n[EACH], nn = 0;
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) n[i] = s.count[EACH * tid + i], nn += n[i];
-            uint32_t at_n = block_scan<NT>(nn, s.counts) - nn;
+                for (int i = 0; i < EACH; ++i) n[i] = s.count[EACH * tid + i], nn += n[i];
+                uint32_t at_n = block_scan<NT>(nn, s.counts) - nn;
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) {
-                if (at_n < rules.k && at_n + n[i] >= rules.k) s.at = EACH * tid + i;
-                at_n += n[i];
+                for (int i = 0; i < EACH; ++i) {
+                    if (at_n < rules.k && at_n + n[i] >= rules.k) s.at = EACH * tid + i;
+                    at_n += n[i];
+                }
+            } else {
+                const float part = fmaxf(rules.p * (float)total * __int_as_float((127 - m.fraction) << 23), 1e-30f) * 1.0001f;
+                float d[EACH], dd = 0.f;
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    d[i] = (float)s.count[EACH * tid + i] * (1.f / 2097152.f), dd += d[i];
+                }
+                float at_d = block_scan<NT>(dd, reinterpret_cast<float *>(s.sums)) - dd;
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    if (at_d < part && at_d + d[i] >= part) s.at = EACH * tid + i;
+                    at_d += d[i];
+                }
             }
             __syncthreads();
             found = s.at >= 0 && s.at + 1 < kBuckets;  // the last bucket has no lower end
-            low = -((float)s.at + 1.05f) / kPerOctave;
+            if (found) low = -((float)s.at + 1.05f) / kPerOctave;
         }
-        if (by_min && !(by_k && by_p)) low = fmaxf(low, rules.log_min_p * 1.442695f * 1.0001f - 1e-4f);  // the first k are needed for their mass
+        if (by_min && !(by_k && by_p)) {  // the first k are needed for their mass
+            low = fmaxf(low, rules.log_min_p * 1.442695f * 1.0001f - 1e-4f);
+            found |= by_mass;
+        }
         if (found) {
-            if (by_p && !by_k) {
-                row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { total += rough_sum(l); });
-                uint32_t none = 0;
-                block_sums<NT>(s, total, none);
-            }
             __syncthreads();
             bool room = true;  // too many are not counted to the end
             row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int id) {
@@ -791,7 +812,7 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
             listed_n = s.number;
             few = listed_n <= S::kCandidates;
             if (few) first = 0, live = row.V + 1;  // k of them at least are live
-            else listed_n = 0, total = 0;
+            else listed_n = 0;
             __syncthreads();
         }
     }
@@ -813,10 +834,10 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
             for (int q = 0; q < VEC; ++q)
                 if (l[q] > m.mask) atomicAdd(&s.count[m.bucket(l[q])], 1u);
         };
-        if (by_p && !by_k) row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { count_places(l), total += rough_sum(l); });
+        if (by_mass) row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { count_places(l); });
         else row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { count(l); });
         uint32_t none = 0;
-        block_sums<NT>(s, total, none);
+        __syncthreads();
         // Running numbers, and bounds of the running masses: with t = log 2 / 32 times the tokens' mean place in their bucket b, their mean mass
         // is between (1 - t) and (1 - t + t^2 / 2) 2^(-b / 32) where t may be any in 0 .. log 2 / 32; the last bucket's tokens lie anywhere
         // beyond.  (A sum of places stays below 2^32 for 2^19 tokens of a bucket; longer rows do without.)

@@ -133,14 +133,15 @@ def test_orders_and_ties_around_the_kth(io, V):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
-@pytest.mark.parametrize("V", [20011, 50021])
-def test_borders_among_many_tokens(io, V):
-    """Rules that end within thousands of tokens, each of them first once: nothing is short enough to be sorted from its first token on."""
-    x, u, c, g = rows(8, V, io, 5 * V, std=1.0)
+@pytest.mark.parametrize("V,std", [(20011, 1.0), (50021, 1.0), (50021, 6.0)])
+def test_borders_among_many_tokens(io, V, std):
+    """Rules that end within thousands of tokens, each of them first once, where nothing is short enough to be sorted from its first token on;
+    and in rows with little mass beside a few tokens."""
+    x, u, c, g = rows(8, V, io, 5 * V, std=std)
     full = lambda v, t=torch.float32: torch.full((8,), v, dtype=t)  # noqa: E731
     for k in (None, 3000, 15000):
         kk = None if k is None else full(k, torch.int32)
-        for p in (None, 0.3, 0.9, 0.99):
+        for p in (None, 0.3, 0.9, 0.99, 0.9999):
             for m in (None, 0.2, 0.05, 0.003):
                 check(x, u, c, kk, None if p is None else full(p), None if m is None else full(m))
 
