@@ -829,6 +829,14 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
                     atomicAdd(&s.count[x >> kPlaceBits], 1u), atomicAdd(&s.lo[x >> kPlaceBits], x & ((1 << kPlaceBits) - 1));
                 }
         };
+        auto add_places = [&](const float (&l)[VEC]) {
+#pragma unroll
+            for (int q = 0; q < VEC; ++q)
+                if (l[q] > m.mask) {
+                    const uint32_t x = m.place(l[q]);
+                    atomicAdd(&s.lo[x >> kPlaceBits], x & ((1 << kPlaceBits) - 1));
+                }
+        };
         auto count = [&](const float (&l)[VEC]) {
 #pragma unroll
             for (int q = 0; q < VEC; ++q)
@@ -836,38 +844,40 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
         };
         if (by_mass) row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { count_places(l); });
         else row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { count(l); });
-        uint32_t none = 0;
+        uint32_t none = 0, n[EACH], nn = 0;
         __syncthreads();
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) n[i] = s.count[EACH * tid + i], nn += n[i];
+        uint32_t at_n = block_scan<NT>(nn, s.counts) - nn;
+        if (tid == NT - 1) s.number_before = at_n + nn;
+        __syncthreads();
+        live = s.number_before;
+        // Whether k is a rule has to stand before anything is made for the others: one that reaches all tokens leaves top-p to find its end as
+        // if it were alone, by the mass of all of them, their places and both bounds' running sums.
+        if (by_k && rules.k >= live) {
+            by_k = false;
+            if (by_p) {
+                total = 0;
+                row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { total += rough_sum(l), add_places(l); });
+                block_sums<NT>(s, total, none);
+            }
+        }
         // Running numbers, and bounds of the running masses: with t = log 2 / 32 times the tokens' mean place in their bucket b, their mean mass
         // is between (1 - t) and (1 - t + t^2 / 2) 2^(-b / 32) where t may be any in 0 .. log 2 / 32; the last bucket's tokens lie anywhere
         // beyond.  (A sum of places stays below 2^32 for 2^19 tokens of a bucket; longer rows do without.)
-        uint32_t n[EACH], nn = 0;
         float up[EACH], down[EACH], uu = 0.f, dd = 0.f;
         const bool places = by_p && !by_k && row.V <= (1 << 19);
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             const int b = EACH * tid + i;
-            n[i] = s.count[b], nn += n[i];
             const float whole = (float)n[i] * exp2f(-(float)b / kPerOctave), t = places && n[i] > 0 ? 0.02166085f * (float)s.lo[b] / ((float)(1 << kPlaceBits) * (float)n[i]) : 0.f;
             up[i] = whole * (1.f - t + (places ? 2.4e-4f : 0.f)), uu += up[i];
             down[i] = b + 1 == kBuckets ? 0.f : whole * (places ? 1.f - t : 0.97857f), dd += down[i];
         }
-        uint32_t at_n = block_scan<NT>(nn, s.counts) - nn;
         float at_u = 0.f, at_d = 0.f;
         if (by_p && !by_k) {
             at_u = block_scan<NT>(uu, reinterpret_cast<float *>(s.sums)) - uu;
             at_d = block_scan<NT>(dd, reinterpret_cast<float *>(s.more)) - dd;
-        }
-        if (tid == NT - 1) s.number_before = at_n + nn;
-        __syncthreads();
-        live = s.number_before;
-        if (by_k && rules.k >= live) {
-            by_k = false;
-            if (by_p) {  // the mass of all of them after all
-                total = 0;
-                row.units_of(tid, row.units, NT, [&](const float (&l)[VEC], int) { total += rough_sum(l); });
-                block_sums<NT>(s, total, none);
-            }
         }
         // Each rule ends the prefix in a bucket that is known (k) or known to a few (p, min_p); the window reaches from the first of these to
         // the first by which one of them has ended.  k and p together need the first k's mass: all of them are candidates.
@@ -913,6 +923,10 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
         }
         sure_n = first == kBuckets ? live : first == 0 ? 0 : before;
         listed_n = first == kBuckets ? 0 : upto - sure_n;
+        if (by_p && first > 0 && listed_n == 0 && !min_ends) {  // top-p ends somewhere: without a window that is for the passes to find
+            done = false;
+            return Drawn{};
+        }
     }
     // the masses that are kept for certain, and the window's list
     int u0, u1;
@@ -1121,6 +1135,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const Params<T> p
     rules.min_p = p.min_p ? p.min_p[i] : 0.f;
     if (rules.min_p != rules.min_p) rules.min_p = 0.f;
     rules.log_min_p = rules.min_p > 0.f ? logf(rules.min_p) : 0.f;
+    if (rules.k >= (uint32_t)p.V) rules.k = 0;  // all of them: no rule
     if (rules.min_p > 1.f) rules.k = 1, rules.p = 1.f, rules.min_p = 0.f;  // nothing reaches it: the first token alone
     uint32_t live = 0;
     bool done = true;

@@ -1,0 +1,47 @@
+"""The draw where one rule makes another one idle, against the fp64 oracle (tolerances: tests/test_sample_gpu.py).
+
+No row here has a border nearer to a token's edge than the kernel's units can tell; where the seeds are changed that has to be looked at again."""
+import numpy as np
+import pytest
+import torch
+
+from ssm_sequence_layer_gb300 import build
+from tests.test_sample_gpu import DT, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def combinations(live, V):
+    """Rows of (top_k, top_p, min_p): a top_k around the live tokens' number and far beyond, beside the two others."""
+    ks = [live - 1, live, live + 1, V, 2 ** 31 - 1]
+    return [(k, p, m) for k in ks for p in (0.3, 0.9, 0.9999) for m in (0.0, 0.01)]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1100, 2000, 8193, 50021, 131072])
+@pytest.mark.parametrize("std", [1.0, 2.5, 6.0])
+@pytest.mark.parametrize("masked", [False, True])
+def test_top_k_that_reaches_all_beside_top_p(io, V, std, masked):
+    """top_k of the vocabulary's size, or of more tokens than are live, leaves the row to top-p and min-p.  A deviation of 1 has no token
+    further than 22 below the largest, 6 has many."""
+    g = torch.Generator().manual_seed(V + int(10 * std))
+    row = torch.randn(V, generator=g) * std
+    if masked:
+        row[torch.randperm(V, generator=g)[: V // 3]] = -float("inf")
+    live = int((row != -float("inf")).sum())
+    rules = combinations(live, V)
+    n = len(rules)
+    x = torch.stack([row[torch.randperm(V, generator=g)] for _ in range(n)]).to(DT[io])
+    u = torch.rand(n, generator=g)
+    k, p, m = (torch.tensor([r[i] for r in rules]) for i in range(3))
+    k = k.int()
+    for c in (None, torch.full((n,), 0.8)):
+        with_all = check(x, u, c, k, p, m)
+        without = check(x, u, c, None, p, m)
+        assert np.array_equal(with_all[k.numpy() >= live], without[k.numpy() >= live])
