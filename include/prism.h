@@ -625,7 +625,7 @@ PRISM_API prism_status prism_heads_backward(prism_tokens_t tokens, const prism_h
  *   min_p > 0:  those of at least min_p times the first one's probability
  * (one token at least; masked tokens never), and the token is the first, by rising id, at which the kept tokens' running mass
  * exceeds u times their mass.
- *   u [n] float32 (NaN and below 0 count as 0; 1 and above gives the last kept id)
+ *   u [n] float32 (NaN and below 0 count as 0; 1 and above gives the last kept id, whatever its mass)
  *   inv_temperature [n] float32 (NULL: 1), top_k [n] int32, top_p, min_p [n] float32 (NULL: not used; NaN: not used)
  *   ids [n] int64   logprob [n] float32: log of the token's share of the kept mass   kept [n] int32: tokens kept (V at most 2^30);
  *   logprob and kept may be NULL

@@ -583,7 +583,8 @@ struct Rules {
         if (fabsf(z - log_min_p) > 1e-5f + 1e-5f * fabsf(log_min_p)) return z > log_min_p;
         return ((double)l - (double)m.top) * (double)m.c >= log((double)min_p);
     }
-    __device__ __forceinline__ u64 target(u64 all) const { return u >= 1.f ? all - 1 : share(u > 0.f ? u : 0.f, all, false); }
+    __device__ __forceinline__ bool wants_last() const { return u >= 1.f; }  // the last kept id, whatever its mass
+    __device__ __forceinline__ u64 target(u64 all) const { return share(u > 0.f ? u : 0.f, all, false); }  // u < 1
 };
 
 struct Drawn {
@@ -630,7 +631,7 @@ __device__ Drawn draw_token(S &s, const R &row, const Mass &m, const Rules &rule
                     found = true;
                     s.at = row.first_id(unit + tid) + q;
                     s.top = l[q];
-                    s.flag = near == 0 || rules.u >= 1.f || ((at == 0 || target > at + near) && (at + e[q] == all || at + e[q] > target + near));
+                    s.flag = near == 0 || ((at == 0 || target > at + near) && (at + e[q] == all || at + e[q] > target + near));
                 }
                 at += e[q];
             }
@@ -648,7 +649,8 @@ __device__ Drawn draw_token(S &s, const R &row, const Mass &m, const Rules &rule
     return d;
 }
 
-// Any rules and any number of tokens, in passes over the row for each of them
+// Any rules and any number of tokens, in passes over the row for each of them; u >= 1 always comes this way (the window's ways would carry
+// the search for the last kept id in their registers: 1 to 4 % of every draw)
 template <int NT, typename S, typename R>
 __device__ __noinline__ Drawn draw_row(S &s, const R &row, const Mass &m, const Rules &rules, uint32_t live, bool exact)
 {
@@ -686,6 +688,23 @@ __device__ __noinline__ Drawn draw_row(S &s, const R &row, const Mass &m, const 
     });
     u64 all = mine;
     block_sums<NT>(s, all, kept);  // leaves the warps' masses in s.sums
+    if (rules.wants_last()) {
+        if (threadIdx.x == 0) s.at = -1;
+        __syncthreads();
+        int last = -1;
+        float l_last = 0.f;
+        row.template each<NT>(m.mask, [&](float l, int id) {
+            if (cut.keeps(order_of(l), id) && (!by_min || rules.reaches_min(m, l))) last = id, l_last = l;  // a thread meets its ids in their order
+        });
+        if (last >= 0) atomicMax(&s.at, last);
+        __syncthreads();
+        Drawn d;
+        d.id = s.at, d.logprob = 0.f, d.kept = kept, d.sure = sure;
+        if (last == d.id) s.top = l_last;
+        __syncthreads();
+        if (threadIdx.x == 0) d.logprob = m.log_share(s.top, all);
+        return d;
+    }
     Drawn d = draw_token<NT>(s, row, m, rules, exact ? 0 : m.slack(all, row.V), mass);
     d.kept = kept, d.sure = d.sure && sure;
     return d;
@@ -1138,8 +1157,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const Params<T> p
     if (rules.k >= (uint32_t)p.V) rules.k = 0;  // all of them: no rule
     if (rules.min_p > 1.f) rules.k = 1, rules.p = 1.f, rules.min_p = 0.f;  // nothing reaches it: the first token alone
     uint32_t live = 0;
-    bool done = true;
-    Drawn d = draw_window<NT>(s, row, m, rules, own, live, done);
+    bool done = !rules.wants_last();
+    Drawn d;
+    if (done) {
+        d = draw_window<NT>(s, row, m, rules, own, live, done);
+    } else {
+        row.template each<NT>(mask, [&](float, int) { ++live; });
+        u64 none = 0;
+        block_sums<NT>(s, none, live);
+    }
     if (!done) {
         __syncthreads();
         d = draw_row<NT>(s, row, m, rules, live, false);

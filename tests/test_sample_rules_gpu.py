@@ -1,4 +1,4 @@
-"""The draw where one rule makes another one idle, against the fp64 oracle (tolerances: tests/test_sample_gpu.py).
+"""The draw where one rule makes another one idle, and at the far end of u, against the fp64 oracle (tolerances: tests/test_sample_gpu.py).
 
 No row here has a border nearer to a token's edge than the kernel's units can tell; where the seeds are changed that has to be looked at again."""
 import numpy as np
@@ -45,3 +45,28 @@ def test_top_k_that_reaches_all_beside_top_p(io, V, std, masked):
         with_all = check(x, u, c, k, p, m)
         without = check(x, u, c, None, p, m)
         assert np.array_equal(with_all[k.numpy() >= live], without[k.numpy() >= live])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [40, 700, 5000, 50021, 200000])
+def test_u_of_one_gives_the_last_kept_id(io, V):
+    """... where the last ids are the least likely: below what a sum of the others tells, and below what masses tell at all."""
+    g = torch.Generator().manual_seed(V)
+    lowest = torch.tensor([-16.0, -25.0, -29.0, -40.0, -80.0])
+    flat = torch.randn(V, generator=g)
+    last = V - V // 10  # of the likely ones
+    x = flat.repeat(5, 1)
+    x[:, last:] = lowest[:, None] + 0.1 * torch.rand(5, V - last, generator=g)
+    x = x.to(DT[io])
+    for u in (1.0, 2.0, float("inf")):
+        uu = torch.full((5,), u)
+        from_oracle = lambda *rules: check(x, uu, None, *rules)  # noqa: E731
+        assert (from_oracle() == V).all()
+        from_oracle(torch.full((5,), V - 3).int())
+        from_oracle(torch.full((5,), min(V, 200)).int())
+        from_oracle(None, torch.full((5,), 0.9999))
+        from_oracle(None, None, torch.full((5,), 1e-8))
+        from_oracle(torch.full((5,), V // 2).int(), torch.full((5,), 0.9), torch.full((5,), 1e-3))
+    # a row that falls by one from id to id: all of the first fifty are kept
+    steep = -torch.arange(V).float().repeat(1, 1).to(DT[io])
+    check(steep, torch.ones(1), None, torch.full((1,), min(V, 50)).int())
