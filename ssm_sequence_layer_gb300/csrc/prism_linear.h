@@ -1123,9 +1123,10 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                                 const int j = j0 + share * COLS + ch * 32;
                                 const bool inside = rows > 0 && j < p.J;
                                 if (inside) {
-                                    if (by_tma) {
-                                        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&incoming[warp - 4]), taken & 1, wt.ns));
-                                        ++taken;
+                                    // after an expired wait the piece stays asked for and no other is: the drain below waits for it
+                                    if (by_tma && ok) {
+                                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&incoming[warp - 4]), taken & 1, wt.ns));
+                                        if (ok) ++taken;
                                     }
                                     bulk_wait_read();  // the pieces before have left (two places for them in turn brought nothing)
                                     __syncwarp();
@@ -1169,7 +1170,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                                     if (p.pre_out) tma_store_2d(&tm_pre, smem_u32(stage + 2048), j, r0);
                                     bulk_commit();
                                 }
-                                if (by_tma) ask();
+                                if (by_tma && ok) ask();
                             }
                             return;
                         }
@@ -1209,9 +1210,9 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             }
         }
         if (!SPLIT && p.tiled) bulk_wait_read();  // before the staging goes
-        if (by_tma) {  // after an expired wait: the pieces asked for land before the CTA exits
-            if (!ok && lane == 0) give_up();
-            for (; !ok && taken < asked; ++taken) (void)mbar_wait(smem_u32(&incoming[warp - 4]), taken & 1, 1000000000ull);
+        if (by_tma && !ok) {  // the piece asked for lands before the CTA exits
+            if (lane == 0) give_up();
+            if (taken < asked) (void)mbar_wait(smem_u32(&incoming[warp - 4]), taken & 1, 1000000000ull);
         }
     }
     // drain: after an expired wait, the copies and products in flight land before the CTA exits
