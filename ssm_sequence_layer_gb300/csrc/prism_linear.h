@@ -651,6 +651,20 @@ __device__ __forceinline__ uint32_t address_in(uint32_t addr, uint32_t cta)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
     return a;
 }
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void store_at(uint32_t remote, uint32_t v)
+{
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store_at(uint32_t remote, unsigned long long v)
+{
+    asm volatile("st.relaxed.cluster.shared::cluster.u64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_at(uint32_t remote)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
@@ -731,6 +745,8 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
     __shared__ uint32_t tmem_base_s;
     __shared__ __align__(8) uint64_t full[STAGES], freed[STAGES], acc_full[2], acc_empty[2], incoming[L::FINISHERS];
     __shared__ int abort_s;
+    __shared__ unsigned long long other_issued, products_s;  // after an expired wait: the loads of a pair's other CTA, the products issued
+    __shared__ uint32_t accumulators_s;                       // ... and the accumulators that they have completed
     __shared__ __align__(16) float column_sums[OP == LinearOp::weights && SOFT ? kLoaderWarps : 1][OP == LinearOp::weights ? BM : 1];
     constexpr int CTAS = PAIR ? 2 : 1, TM = CTAS * BM;  // of a tile, and its rows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -822,9 +838,14 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
 
     auto give_up = [&] {
         atomicCAS(wt.status, 0, kDevTimeout);
-        *(volatile int *)&abort_s = 1;
+        if constexpr (PAIR) {  // all of the cluster drain together
+            for (uint32_t c = 0; c < cluster_size(); ++c) store_at(address_in(smem_u32(&abort_s), c), 1u);
+        } else {
+            *(volatile int *)&abort_s = 1;
+        }
     };
-    long long issued = 0;  // the issuing threads' counts of steps, for the drain
+    long long issued = 0;  // the issuing threads' counts of steps and of accumulators filled, also for the drain
+    uint32_t accumulators = 0;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kIssueRegs));
         // Whole warps run these loops, so that their counters and descriptors stay in uniform registers, and one lane issues.  Each
@@ -859,7 +880,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
         } else if (warp == 0 && leads) {  // ---- products ----
             const bool one = elect_one();
             int s = 0;
-            uint32_t round = 0, acc = 0;  // accumulators taken so far
+            uint32_t round = 0;
             auto product = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
                 if constexpr (PAIR) mma_f16_pair(d, a, b, id, more);
                 else mma_f16(d, a, b, id, more);
@@ -872,8 +893,8 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             for (int i = 0; i < my_tiles && ok; ++i) {
                 for (int b = b_from; b < b_to; ++b) {
                     const int in_group = GROUPED ? (b - b_from) % L::GROUP : b - b_from;
-                    const uint32_t buf = acc & 1;
-                    if (in_group == 0 && acc >= 2) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_empty[buf]), ((acc - 2) >> 1) & 1, wt.ns));
+                    const uint32_t buf = accumulators & 1;
+                    if (in_group == 0 && accumulators >= 2) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_empty[buf]), ((accumulators - 2) >> 1) & 1, wt.ns));
                     if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), round & 1, wt.ns));
                     if (!ok) {
                         if (one) give_up();
@@ -912,7 +933,7 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
                     }
                     __syncwarp();
                     ready = __all_sync(0xffffffffu, seen);
-                    if (last) ++acc;
+                    if (last) ++accumulators;
                     ++issued;
                     s = next, round = next_round;
                 }
@@ -1215,19 +1236,52 @@ __global__ void __launch_bounds__(Layout<io_t, OP, SOFT, BN, PAIR>::THREADS, 1)
             if (taken < asked) (void)mbar_wait(smem_u32(&incoming[warp - 4]), taken & 1, 1000000000ull);
         }
     }
-    // drain: after an expired wait, the copies and products in flight land before the CTA exits
+    // drain: after an expired wait, the copies and products in flight land before the CTA exits, and what they signal
+    auto landed = [&](uint64_t *ring, long long to) {  // the last round of steps before `to`
+        for (long long g = to > stages ? to - stages : 0; g < to; ++g) (void)mbar_wait(smem_u32(&ring[g % stages]), (uint32_t)(g / stages) & 1, 1000000000ull);
+    };
+    auto products_landed = [&](long long steps, uint32_t accumulators) {
+        landed(freed, steps);
+        for (uint32_t a = accumulators > 2 ? accumulators - 2 : 0; a < accumulators; ++a) (void)mbar_wait(smem_u32(&acc_full[a & 1]), (a >> 1) & 1, 1000000000ull);
+    };
     __syncthreads();
-    if (abort_s && issued > 0) {
-        const long long last = issued - 1;
-        if (tid == 0 && leads)  // products complete in order
-            (void)mbar_wait(smem_u32(&freed[last % stages]), (uint32_t)(last / stages) & 1, 1000000000ull);
-        if (!SOFT && tid == 32 && leads)
-            for (long long g = last >= stages ? last - stages + 1 : 0; g <= last; ++g)
-                (void)mbar_wait(smem_u32(&full[g % stages]), (uint32_t)(g / stages) & 1, 1000000000ull);
+    if constexpr (!PAIR) {
+        if (abort_s) {
+            if (tid == 0) products_landed(issued, accumulators);
+            if (!SOFT && tid == 32) landed(full, issued);
+        }
     }
     fence_before_sync();
     __syncthreads();
     if constexpr (PAIR || SPLIT) cluster_barrier();  // the other CTA's products reach into this one until here; the sums stand in shared memory
+    if constexpr (PAIR) {
+        // The loads of both CTAs of a pair count in the first one's barriers, and the CTAs stopped where they were.  The one behind brings in
+        // what it lacks (a stage that one of them loaded is free in both, and they are a ring apart at most), so that each barrier gets
+        // all that it expects.  Then the first one waits for the loads, and both for the products, which signal both.  abort_s is the
+        // same in all of the cluster here.
+        if (abort_s) {
+            if (tid == 32) store_at(address_in(smem_u32(&other_issued), crank ^ 1), (unsigned long long)issued);
+            if (tid == 0 && leads)
+                for (uint32_t c = crank; c <= crank + 1; ++c) {
+                    store_at(address_in(smem_u32(&products_s), c), (unsigned long long)issued);
+                    store_at(address_in(smem_u32(&accumulators_s), c), accumulators);
+                }
+            __syncthreads();
+            cluster_barrier();
+            if (tid == 32) {
+                const int of_tile = b_to - b_from;
+                for (const long long to = (long long)other_issued; issued < to; ++issued) {
+                    int i0, j0;
+                    tile_at((int)(issued / of_tile), i0, j0);
+                    load_block((int)(issued % stages), b_from + (int)(issued % of_tile), i0, j0);
+                }
+                if (leads) landed(full, issued);
+            }
+            if (tid == 0) products_landed((long long)products_s, accumulators_s);
+            __syncthreads();
+            cluster_barrier();
+        }
+    }
     if (warp == 0) {
         if constexpr (PAIR) tmem_dealloc_pair(tmem, L::kColumns);
         else tmem_dealloc(tmem, L::kColumns);
