@@ -576,7 +576,8 @@ PRISM_API prism_status prism_linear_weight_backward(prism_tokens_t tokens, int M
  *   y_j = r x_j w_j            w = q_weight or k_weight [d] io (1 where NULL)
  * and the first rot values of y are turned in pairs, (y_i, y_{i + rot/2}) or, interleaved, (y_{2i}, y_{2i+1}), i < rot/2:
  *   (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),    t = position inv_freq_i
- * Values are copied.  positions [B, T] int64 (NULL: 0 .. T-1 in every sequence), of any sign and size up to 2^40; the angle is
+ * Values are copied, and values of queries and keys that are not among the first rot are not turned (an infinity there stays in its place).
+ * positions [B, T] int64 (NULL: 0 .. T-1 in every sequence), of any sign and size up to 2^40; the angle is
  * reduced in 64-bit fixed point, to 2^-62 turns of the float32 inv_freq times the position, and taken to 2^-27 turns.  inv_freq [rot/2] float32 on the
  * device, each below 2^12 in magnitude.  Scaling for long contexts is a choice of inv_freq and amplitude
  * (rotary_frequencies of the Python package makes the usual ones).

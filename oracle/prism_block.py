@@ -109,8 +109,10 @@ def heads_backward(x, grads, heads_, d, dv, norm, eps, q_weight, k_weight, inv_f
         size = _size(y, norm, eps)
         wg = g * (1 if w is None else w.astype(F))
         dws.append((g * y / size).sum((0, 1, 2)))
-        share = {"none": 0.0, "unit": 1.0, "rms": 1.0 / d}[norm]
-        cols.append((wg / size - y * share * (wg * y).sum(-1, keepdims=True) / size ** 3).reshape(B, T, H * d))
+        along = 0.0  # without a norm there is no term along x, be the sum infinite
+        if norm != "none":
+            along = y * (1.0 if norm == "unit" else 1.0 / d) * (wg * y).sum(-1, keepdims=True) / size ** 3
+        cols.append((wg / size - along).reshape(B, T, H * d))
     cols.append(grads[2].astype(F).transpose(0, 2, 1, 3).reshape(B, T, -1))
     return np.concatenate(cols, 2), dws[0], dws[1]
 

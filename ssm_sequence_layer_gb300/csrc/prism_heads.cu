@@ -133,18 +133,20 @@ __device__ __forceinline__ float2 dot(const float (&a)[VEC], const float (&b)[VE
     return sum;
 }
 
-// The pairs' rotation by (c, sign s) on the units a and b: across the units, or within each (interleaved, VEC > 1)
+// The pairs' rotation by (c, sign s) on the units a and b: across the units, or within each (interleaved, VEC > 1).  `pairs` of the slot's VEC
+// pairs are turned, of a slot across the units all or none.  The others are left as they are, which a rotation by no angle would not do to
+// values that are not finite.
 template <int VEC, bool WITHIN>
-__device__ __forceinline__ void turn(float (&a)[VEC], float (&b)[VEC], const float (&c)[VEC], const float (&s)[VEC])
+__device__ __forceinline__ void turn(float (&a)[VEC], float (&b)[VEC], const float (&c)[VEC], const float (&s)[VEC], int pairs)
 {
     if constexpr (WITHIN) {
 #pragma unroll
         for (int e = 0; e < VEC / 2; ++e) {
             const float x = a[2 * e], y = a[2 * e + 1], u = b[2 * e], v = b[2 * e + 1];
-            a[2 * e] = x * c[e] - y * s[e], a[2 * e + 1] = x * s[e] + y * c[e];
-            b[2 * e] = u * c[VEC / 2 + e] - v * s[VEC / 2 + e], b[2 * e + 1] = u * s[VEC / 2 + e] + v * c[VEC / 2 + e];
+            if (e < pairs) a[2 * e] = x * c[e] - y * s[e], a[2 * e + 1] = x * s[e] + y * c[e];
+            if (VEC / 2 + e < pairs) b[2 * e] = u * c[VEC / 2 + e] - v * s[VEC / 2 + e], b[2 * e + 1] = u * s[VEC / 2 + e] + v * c[VEC / 2 + e];
         }
-    } else {
+    } else if (pairs > 0) {
         by_two<VEC>(
             [&](int e) {
                 const float2 x = at2(a + e), y = at2(b + e), c2 = at2(c + e), s2 = at2(s + e);
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, PER == 1 ? 4 : 1) forward_kernel(con
                         if (u.a < units) times<VEC>(a[i], s.w + u.a * VEC);
                         if (u.b < units) times<VEC>(bb[i], s.w + u.b * VEC);
                     }
-                    turn<VEC, WITHIN>(a[i], bb[i], c[i], sn[i]);
+                    turn<VEC, WITHIN>(a[i], bb[i], c[i], sn[i], f.rot / 2 - (lane + i * G) * VEC);
                     io::Unit<io_t, VEC> o;
                     if (u.a < units) o.set(a[i]), io::store_unit<io_t, VEC>(to + k * head + u.a * VEC, o);
                     if (u.b < units) o.set(bb[i]), io::store_unit<io_t, VEC>(to + k * head + u.b * VEC, o);
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, PER == 1 ? (VEC == 8 ? 2 : 3) : 1) b
                     float a[VEC], bb[VEC];
                     raw[k][i][0].get(a), raw[k][i][1].get(bb);
                     grad[k][i][0].get(ga[i]), grad[k][i][1].get(gb[i]);
-                    turn<VEC, WITHIN>(ga[i], gb[i], c[i], sn[i]);
+                    turn<VEC, WITHIN>(ga[i], gb[i], c[i], sn[i], f.rot / 2 - (lane + i * G) * VEC);
                     squares = dot<VEC>(bb, bb, dot<VEC>(a, a, squares));
                     float wa[VEC], wb[VEC];
 #pragma unroll

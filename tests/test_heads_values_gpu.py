@@ -35,7 +35,8 @@ def same(got, ref, tol, io):
     assert np.array_equal(np.isnan(got), np.isnan(ref))
     assert np.array_equal(got[special & ~np.isnan(ref)], ref[special & ~np.isnan(ref)])
     ok = ~special
-    assert np.all(np.abs(got - ref)[ok] <= (tol + half_ulp(io, np.abs(np.where(ok, ref, 0)) + tol) * 1.0001)[ok])
+    got, ref = np.where(ok, got, 0), np.where(ok, ref, 0)
+    assert np.all(np.abs(got - ref)[ok] <= (tol + half_ulp(io, np.abs(ref) + tol) * 1.0001)[ok])
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
