@@ -580,7 +580,8 @@ PRISM_API prism_status prism_linear_weight_backward(prism_tokens_t tokens, int M
  * positions [B, T] int64 (NULL: 0 .. T-1 in every sequence), of any sign and size up to 2^40; the angle is
  * reduced in 64-bit fixed point, to 2^-62 turns of the float32 inv_freq times the position, and taken to 2^-27 turns.  inv_freq [rot/2] float32 on the
  * device, each below 2^12 in magnitude.  Scaling for long contexts is a choice of inv_freq and amplitude
- * (rotary_frequencies of the Python package makes the usual ones).
+ * (rotary_frequencies of the Python package makes the usual ones).  An amplitude other than 1 is for attention's products; the layer's step along
+ * a key is 1 - beta |k|^2 and takes keys of length one, PRISM_HEADS_UNIT with amplitude 1.
  * d and dv in 1 .. 512, rot even, 0 .. d (0: no rotation), eps finite and >= 0; squares are float32 as in prism_norm.
  */
 typedef enum prism_heads_norm {

@@ -1,6 +1,9 @@
 """The position rotation's frequencies for ``Tokens.heads``, also for contexts longer than a model was trained on.
 
 A pair i of the first ``rot`` values of a head is turned by position * inv_freq[i] and multiplied by an amplitude.
+
+An amplitude other than 1 belongs to attention, where it scales the products of queries and keys.  The recurrent layer's step along a
+key is 1 - beta |k|^2: it takes keys of length one, so leave the amplitude out there (with beta = 1 a length above sqrt(2) makes the state grow).
 """
 from __future__ import annotations
 
@@ -15,7 +18,7 @@ def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_len
       "base"      a base larger by factor ** (rot / (rot - 2)): the slowest pair as with "linear", the fastest as before
       "by parts"  pairs that turn at least ``fast`` times within original_length as before, those that turn at most
                   ``slow`` times as with "linear", between them a mix in proportion to the turns; the amplitude is
-                  1 + 0.1 log(factor) (arXiv 2309.00071)
+                  1 + 0.1 log(factor) (arXiv 2309.00071), for attention only: the layer's keys stay of length one without it
     """
     import torch
     if rot < 0 or rot % 2 != 0:
