@@ -1,6 +1,8 @@
 // The tile kernels of dW = dy^T x and the sums over dy's rows (prism_linear.h).
 #include "prism_linear.h"
 
+#include <mutex>
+
 namespace prism {
 namespace lin {
 
@@ -22,8 +24,10 @@ cudaError_t weights_tiles<float>(const Params<float> &p, const Cut &c, const Tok
 }
 
 namespace {
-int at_once[9];  // the same on every device that the library runs on
-}
+// The same on every device that the library runs on.  Written once, under the lock that every plan passes before its handle is used
+int at_once[9];
+std::mutex at_once_lock;
+}  // namespace
 
 int clusters_at_once(int ctas) { return at_once[ctas]; }
 
@@ -36,7 +40,10 @@ cudaError_t weights_prepare()
     if (e == cudaSuccess) e = prepare_tiles<__nv_bfloat16, LinearOp::weights, true, 128, true, false>();
     if (e == cudaSuccess) e = prepare_tiles<float, LinearOp::weights, true, 128, true, false>();
     using L = Layout<__nv_bfloat16, LinearOp::weights, false, 256, false>;
-    for (int ctas = 1; ctas <= 8 && e == cudaSuccess && at_once[8] == 0; ++ctas) {
+    const std::lock_guard<std::mutex> hold(at_once_lock);
+    if (at_once[8] != 0) return e;
+    int counts[9] = {};
+    for (int ctas = 1; ctas <= 8 && e == cudaSuccess; ++ctas) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(ctas), cfg.blockDim = dim3(L::THREADS), cfg.dynamicSmemBytes = L::SMEM;
         cudaLaunchAttribute at[1];
@@ -45,8 +52,9 @@ cudaError_t weights_prepare()
         cfg.attrs = at, cfg.numAttrs = 1;
         int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, tile_kernel<__nv_bfloat16, LinearOp::weights, false, 256, true, false>, &cfg);
-        at_once[ctas] = n > 0 ? n : 1;
+        counts[ctas] = n > 0 ? n : 1;
     }
+    if (e == cudaSuccess) memcpy(at_once, counts, sizeof(at_once));
     return e;
 }
 
