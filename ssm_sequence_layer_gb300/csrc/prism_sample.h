@@ -912,9 +912,11 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
             const int b = EACH * tid + i;
             if (by_k && at_n < rules.k && at_n + n[i] >= rules.k) atomicMin(&s.last, b), atomicMin(&s.first, b);
             if (by_p && !by_k) {
-                // the first bucket by whose end the mass may, and the first by whose end it must have been reached
-                if (at_u * 1.00002f < part && (at_u + up[i]) * 1.00002f >= part) atomicMin(&s.first, b);
-                if (at_d * 0.99998f < part && (at_d + down[i]) * 0.99998f >= part) atomicMin(&s.last, b);
+                // the first bucket by whose end the mass may, and the first by whose end it must have been reached.  Two threads' sums up to the
+                // buckets between them differ in their last bits: what a bucket starts from is told with room for that, so that none is left
+                // out between them, and the first of those told apart by their ends counts.
+                if (at_u * 0.9999f < part && (at_u + up[i]) * 1.00002f >= part) atomicMin(&s.first, b);
+                if (at_d * 0.9999f < part && (at_d + down[i]) * 0.99998f >= part) atomicMin(&s.last, b);
             }
             if (by_min && b == b_min && !(by_k && by_p)) atomicMin(&s.last, b);  // the first k are needed for their mass
             at_n += n[i], at_u += up[i], at_d += down[i];

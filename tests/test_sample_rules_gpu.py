@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from ssm_sequence_layer_gb300 import binding as B
 from ssm_sequence_layer_gb300 import build
 from tests.test_sample_gpu import DT, check
 
@@ -70,3 +71,31 @@ def test_u_of_one_gives_the_last_kept_id(io, V):
     # a row that falls by one from id to id: all of the first fifty are kept
     steep = -torch.arange(V).float().repeat(1, 1).to(DT[io])
     check(steep, torch.ones(1), None, torch.full((1,), min(V, 50)).int())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [2000, 9000, 50021])
+@pytest.mark.parametrize("min_p", [None])
+def test_every_top_p_next_to_one(io, V, min_p):
+    """Every float32 of 1 - 2^-12 .. 1, and as many all over (0, 1), of three rows: wherever the border falls it is found, also between what two
+    threads add up."""
+    g = torch.Generator().manual_seed(V)
+    p = torch.cat([1 - torch.arange(1, 4097) * 2.0 ** -24, torch.rand(4096, generator=g)])
+    n = p.numel()
+    with B.Tokens(n, 64, V, io=io) as t:
+        for _ in range(3):
+            row = (torch.randn(V, generator=g) * 2.5).to(DT[io])
+            out = t.sample(row.cuda().repeat(n, 1), torch.full((n,), 0.5, device="cuda"), None, None, p.cuda(), min_p)
+            torch.cuda.synchronize()
+            t.last_device_status()
+            z = np.sort(row.double().numpy())[::-1]
+            e = np.exp(z - z[0])
+            running = np.cumsum(e)
+            target = p.double().numpy() * running[-1]
+            kept = np.searchsorted(running, target) + 1
+            # where a border is within the kernel's units of a token's edge either side will do
+            near = np.minimum(np.abs(running[np.minimum(kept, V) - 1] - target), np.abs(running[np.maximum(kept - 2, 0)] - target)) <= 2 * V * 2.0 ** -44
+            if min_p is not None:
+                kept = np.minimum(kept, int((z - z[0] >= np.log(np.float32(min_p).astype(np.float64))).sum()))
+            assert near.mean() < 0.5
+            assert np.array_equal(out["kept"].cpu().numpy()[~near], kept[~near])
