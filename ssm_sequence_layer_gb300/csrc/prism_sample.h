@@ -1076,7 +1076,8 @@ __device__ Drawn draw_window(S &s, const R &row, const Mass &m, Rules rules, flo
                         if (near && (at + e[i] - target <= near || (at != 0 && target <= at + near))) s.flag = 0;
                         if (j == 0 && at >= target && at != 0) s.flag = 0;  // reached before the window: only for quick masses' errors
                     }
-                    if (j + 1 == (int)listed_n && at + e[i] < target && !min_ends && !by_k) s.flag = 0;  // or behind it
+                    // or behind it: where min_p ends the window that is as it should be, if it is certain
+                    if (j + 1 == (int)listed_n && at + e[i] < target && !by_k && (!min_ends || target - (at + e[i]) <= near)) s.flag = 0;
                     at += e[i];
                 }
                 __syncthreads();

@@ -74,8 +74,29 @@ def test_u_of_one_gives_the_last_kept_id(io, V):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("V,n", [(7, 400), (42, 400), (494, 400), (3000, 200), (22326, 200)])
+def test_top_p_next_to_one_beside_a_small_min_p(io, V, n):
+    """What top-p leaves out, 2^-24 of the mass, is less than rough masses tell: whether it ends the row before min-p does has to be found with
+    closer ones."""
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(n, V, generator=g) * torch.tensor([2.5, 6.0, 4.0, 2.5]).repeat(n // 4)[:, None]).to(DT[io])
+    p, m = torch.full((n,), 1 - 2.0 ** -24), torch.tensor([1e-10, 1e-20]).repeat(n // 2)
+    # the tokens' masses from the smallest on, against what is left out: only rows in which they are further apart than two units a token
+    e = np.exp(x.double().numpy() - x.double().numpy().max(1, keepdims=True))
+    tail = np.cumsum(np.sort(e, 1), 1)
+    gap = np.abs(tail - ((1 - p.double().numpy()) * tail[:, -1])[:, None]).min(1)
+    clear = torch.from_numpy(gap > 2 * V * 2.0 ** -44)
+    assert clear.sum() >= 50
+    x, p, m, u = x[clear], p[clear], m[clear], torch.rand(n, generator=g)[clear]
+    kept = check(x, u, None, None, p, m)
+    assert (kept < V).any()
+    check(x, u, None, torch.full((x.shape[0],), V).int(), p, m)
+    check(x, u, None, None, p, None)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("V", [2000, 9000, 50021])
-@pytest.mark.parametrize("min_p", [None])
+@pytest.mark.parametrize("min_p", [None, 1e-9])
 def test_every_top_p_next_to_one(io, V, min_p):
     """Every float32 of 1 - 2^-12 .. 1, and as many all over (0, 1), of three rows: wherever the border falls it is found, also between what two
     threads add up."""
