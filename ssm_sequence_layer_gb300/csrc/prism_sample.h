@@ -631,7 +631,7 @@ __device__ Drawn draw_token(S &s, const R &row, const Mass &m, const Rules &rule
                     found = true;
                     s.at = row.first_id(unit + tid) + q;
                     s.top = l[q];
-                    s.flag = near == 0 || ((at == 0 || target > at + near) && (at + e[q] == all || at + e[q] > target + near));
+                    s.flag = near == 0 || ((at == 0 || target > at + near) && at + e[q] > target + near);
                 }
                 at += e[q];
             }

@@ -120,3 +120,21 @@ def test_every_top_p_next_to_one(io, V, min_p):
                 kept = np.minimum(kept, int((z - z[0] >= np.log(np.float32(min_p).astype(np.float64))).sum()))
             assert near.mean() < 0.5
             assert np.array_equal(out["kept"].cpu().numpy()[~near], kept[~near])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_u_next_to_one_where_one_token_has_nearly_all(io):
+    """A row whose other tokens' masses vanish beside the largest one's in float32: u of 1 - 2^-24 falls beyond the largest by half of its distance to
+    one, which rough masses do not show although their sum ends with that token."""
+    row = torch.tensor([9.140625, -7.578125, -8.0859375, -13.046875, -18.28125, -32.0, -52.5])
+    x = row.repeat(4, 1)
+    x[1], x[2] = row[[1, 0, 2, 3, 4, 5, 6]], row[[1, 2, 3, 4, 5, 6, 0]]
+    x[3, 1:3] = -9.0
+    check(x.to(DT[io]), torch.full((4,), 1 - 2.0 ** -24))
+    for V in (900, 30000):
+        g = torch.Generator().manual_seed(V)
+        x = torch.full((50, V), -60.0)
+        x.scatter_(1, torch.randint(0, V, (50, 40), generator=g), -17 - 4 * torch.rand(50, 40, generator=g))
+        x.scatter_(1, torch.randint(0, V // 2, (50, 1), generator=g), 0.0)
+        check(x.to(DT[io]), torch.full((50,), 1 - 2.0 ** -24))
+        check(x.to(DT[io]), torch.full((50,), 1 - 2.0 ** -23))
