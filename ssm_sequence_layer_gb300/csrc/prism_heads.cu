@@ -240,7 +240,7 @@ struct Forward {
     io_t *out[3];
 };
 
-// NB heads of a token at once: their loads are in flight together.  16384 rows of 18 heads of 128 (bf16, 151 MB): 29.5 us, 5.1 TB/s, with
+// NB heads of a token at once: their loads are in flight together.  16384 rows of 18 heads of 128 (bf16, 151 MB): 29.8 us, 5.1 TB/s, with
 // two heads and four blocks an SM; three heads and three blocks 31.5 us.
 template <typename io_t, int VEC, int PER, bool WITHIN, int NB>
 __global__ void __launch_bounds__(kThreads, PER == 1 ? 4 : 1) forward_kernel(const Forward<io_t> p)
@@ -319,8 +319,8 @@ struct Backward {
     float *part[2];  // [blocks][chunks of the kind][d], or NULL where the weight's gradient is not wanted
 };
 
-// 16384 rows of 18 heads of 128 with float32 cotangents (277 MB): 69 us, 4.0 TB/s; 32768 rows of 12 heads of 64 in float32 (269 MB): 51 us,
-// 5.3 TB/s.  The loads in flight bound it: two blocks an SM in bf16, where registers hold 96 bytes a lane on their way (three
+// 16384 rows of 18 heads of 128 with float32 cotangents (277 MB): 62 us, 4.4 TB/s, 67.5 with the join behind it; 32768 rows of 12 heads of 64 in
+// float32 (269 MB): 50 us, 5.4 TB/s.  The loads in flight bound it: two blocks an SM in bf16, where registers hold 96 bytes a lane on their way (three
 // spill: 76 us), three in float32 (two: 62 us).
 template <typename io_t, typename grad_t, int VEC, int PER, bool WITHIN, int NB>
 __global__ void __launch_bounds__(kThreads, PER == 1 ? (VEC == 8 ? 2 : 3) : 1) backward_kernel(const Backward<io_t, grad_t> p)

@@ -11,7 +11,7 @@ namespace lin {
 
 // ---- few rows ---------------------------------------------------------------------------------------------
 // Few rows of bf16, as a served token of each of some sequences has them: the weights' bytes bound the product, each weight
-// is used M times at most, and tiles of 128 rows would be empty for the most part.  (16 x 2304 x 768: 3.3 us, 1.1 TB/s of weights from a
+// is used M times at most, and tiles of 128 rows would be empty for the most part.  (16 x 2304 x 768: 3.2 us, 1.1 TB/s of weights from a
 // graph's launch to the next one's; 16 x 8192 x 8192: 24, 5.5 TB/s.)  A warp takes RPW tiles of 16 rows of W as A operands
 // of m16n8k16 products straight from global memory to registers (16 bytes of a row per lane and load), and 8 NT rows of x as B
 // operands.  The products' k order is a free choice as long as both operands share it: the four words of a lane's 16 bytes serve as
@@ -148,7 +148,7 @@ cudaError_t launch_few(const Params<__nv_bfloat16> &p, const TokenLaunch &l)
     return cudaGetLastError();
 }
 
-// Whether M rows are few: up to 16 always (17 rows of 2304 x 768 in tiles: 6.8 us, 16 here 3.3).  More rows only where the weights are small, since
+// Whether M rows are few: up to 16 always (17 rows of 2304 x 768 in tiles: 6.8 us, 16 here 3.2).  More rows only where the weights are small, since
 // each CTA reads all rows again.  Microseconds here / in tiles: 32 rows of 2304 x 768 3.4 / 7.4, of 3584 x 2048 7.5 / 8.6, of 768 x 8192 10.3 / 10.5,
 // of 4096 x 4096 13.6 / 10.9; 64 rows of 2304 x 768 4.7 / 7.2, of 2048 x 2048 6.2 / 8.5, of 768 x 2304 6.9 / 7.9, of 7168 x 768 10.4 / 8.8,
 // of 768 x 8192 14.9 / 10.9.

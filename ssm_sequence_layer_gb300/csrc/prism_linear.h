@@ -32,7 +32,8 @@ namespace lin {
 using namespace prism::tc;
 
 // ---- activations ----------------------------------------------------------------------------------
-// Both are within 2^-20 of themselves in relative terms wherever they are normal numbers, also where they are tiny.
+// The values are within 2^-20 of themselves in relative terms wherever they are normal numbers, also where they are tiny; the slopes, each a
+// sum of two terms, within 2^-20 of the larger one, so that near their zeros they are no more exact than that.
 __device__ __forceinline__ float min_nan(float a, float b)
 {
     float r;
@@ -105,7 +106,8 @@ __device__ __forceinline__ float act_slope(float z)
 }
 
 // The same for results that are rounded to bfloat16, two at a time.  R has a polynomial of degree 7 in 1 / (1 + 0.315 a) (2^-21), and the
-// exponent's rounding errors are left alone: 2^-20 of the result where |z| < 4, 2^-15 at |z| = 13, where gelu(z) is 10^-37.
+// exponent's rounding errors are left alone: 2^-20 of the result where |z| < 4, 2^-15 at |z| = 13, where gelu(z) is 10^-37.  Exponentials
+// below the smallest normal number are zero, and with them values and slopes below 2^-119 (silu beyond |z| = 87.3, gelu beyond 13.2).
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 exp2_of(float2 y)
 {

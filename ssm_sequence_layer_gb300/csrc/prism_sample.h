@@ -13,8 +13,8 @@
 // Bound: not bandwidth (100 KB a row) but the way of one row through its steps, a barrier or two each, and operations per token in between.
 // Cycles of a row of 50021 bf16, with top-k 50: copy into shared memory 2400, largest logit 2400, candidates by the threads' own largest
 // 7000, sorting 2000, keeping and drawing 5000; counting tokens by their distance from the largest takes 10000 instead, with the places
-// of top-p 20000.  Microseconds: 4 x 50021 bf16 with top-k 50 16, top-p 0.95 69 where it keeps 10000 tokens, 22 where it keeps five;
-// 512 x 50021 float32 68, 192 and 98, without a rule 94.
+// of top-p 20000.  Microseconds: 4 x 50021 bf16 with top-k 50 17, top-p 0.95 70 where it keeps 10000 tokens, 23 where it keeps five;
+// 512 x 50021 float32 70, 193 and 99, without a rule 94.
 #pragma once
 
 #include "io_util.h"
