@@ -531,11 +531,12 @@ PRISM_API prism_status prism_token_logprobs_backward(prism_tokens_t tokens, int 
  * act: the identity, gelu(z) = z Phi(z) with the exact normal distribution function (as in the layer), or
  * silu(z) = z / (1 + exp(-z)).  M at most max_rows; N and K (1 .. 2^20 each) need not be the handle's V and D, and need no
  * multiple: rows that are not whole 16-byte units only take longer.  Sums are float32, whatever the io dtype, and y is taken
- * of the unrounded pre.  With bfloat16 operands one sum runs over all of K in the tensor core, which cuts it off towards zero every 16
- * terms: K / 16 times at most 2^-23 of it (K = 768 2^-17, K = 50021 2^-11 at worst, half of that on average); the weights' gradient goes on in
- * rounded float32 sums every 512 terms.  A bfloat16 y or dx may miss parts below 2^-119 of an activation or its slope.  In float32 a product of two values is within 2^-20 of itself (three bfloat16 parts of each, which hold all
- * of its bits; the smallest products of parts are left out); parts below the smallest normal number are lost, and an infinite
- * operand gives NaN.  An expired device wait is reported by prism_tokens_last_device_status.
+ * of the unrounded pre.  With bfloat16 operands one sum runs over all of K in the tensor core, which cuts it off towards zero
+ * every 16 terms: K / 16 times at most 2^-23 of it (K = 768 2^-17, K = 50021 2^-11 at worst, half of that on average); the
+ * weights' gradient goes on in rounded float32 sums every 512 terms.  A bfloat16 y or dx may miss parts below 2^-119 of an
+ * activation or its slope.  In float32 a product of two values is within 2^-20 of itself (three bfloat16 parts of each, which
+ * hold all of its bits; the smallest products of parts are left out); parts below the smallest normal number are lost, and an
+ * infinite operand gives NaN.  An expired device wait is reported by prism_tokens_last_device_status.
  */
 typedef enum prism_activation {
     PRISM_ACT_NONE = 0,
